@@ -53,7 +53,9 @@ typedef enum {
     SPECDEC_ERR_TIMEOUT = 4        /* specdec_wait gave up */
 } specdec_status_t;
 
-typedef enum { SPECDEC_F32 = 0, SPECDEC_BF16 = 1 } specdec_dtype_t;
+/* The verify takes F32 and BF16 logits; the cache operators below also take F16, and E4M3 (8-bit
+ * floating point, 4 exponent and 3 mantissa bits, no infinity) as a cache's type. */
+typedef enum { SPECDEC_F32 = 0, SPECDEC_BF16 = 1, SPECDEC_F16 = 2, SPECDEC_E4M3 = 3 } specdec_dtype_t;
 
 /* Per-request status bits written to status[b] (0 = clean). The kernel never traps. */
 #define SPECDEC_ST_BAD_DRAFT_ID    1u   /* a draft id outside [0, V): counted invalid, never accepted */
@@ -63,6 +65,9 @@ typedef enum { SPECDEC_F32 = 0, SPECDEC_BF16 = 1 } specdec_dtype_t;
 #define SPECDEC_ST_BAD_OFFSETS    16u   /* cu[0] != 0 or cu[b] > cu[b+1] or cu[b+1] > cu[B]: skipped */
 #define SPECDEC_ST_DEVICE_TIMEOUT 32u   /* an on-chip copy did not land within its time limit */
 #define SPECDEC_ST_BAD_TOP_P      64u   /* top_p not a number in (0, 1]: no top-p filter */
+/* Set by the cache operators (with K_TOO_LARGE, BAD_OFFSETS and DEVICE_TIMEOUT above). */
+#define SPECDEC_ST_BAD_LENGTH    128u   /* a negative length, or one past the request's row of block_table: skipped */
+#define SPECDEC_ST_BAD_PAGE      256u   /* a page id outside [0, num_pages): nothing written there, zeros read */
 
 /*
  * specdec_verify -- verify one batch (stream-ordered, asynchronous).
@@ -296,6 +301,192 @@ specdec_status_t specdec_bitmask_scatter(const int32_t* compact, int64_t compact
                                          const int32_t* constrained, int32_t n,
                                          const int32_t* cu_num_draft, int32_t B, int32_t V,
                                          int32_t* bitmask, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The forward step whose logits specdec_verify reads: rotary positions, the paged key-value
+ * cache (written as the step's rows arrive, optionally quantised, and read back), and the
+ * attention of the step's rows over it. The pages describe the step only from outside ("vLLM
+ * tour part 2": the target model runs over all draft positions and the bonus position of every
+ * request); the operators are this library's, from their formulas.
+ *
+ * Rows. The layout is the verify's: request b owns the k_b + 1 rows t(b, j) = cu[b] + b + j, and
+ * cached_len[b] tokens of it were in the cache before the step. Row j is the request's token
+ * number cached_len[b] + j: its default rotary position, its place in the cache, and the last
+ * token that its attention sees. After the verify the next step's cached_len[b] is
+ * cached_len[b] + out_num_accepted[b] + 1; the cache entries of rejected drafts lie behind it and
+ * are written over. A prompt is a request whose k_b + 1 rows are its tokens (the cache write and
+ * the rotation take any k_b; the attention takes k_b <= max_k <= SPECDEC_KMAX). A request with
+ * cached_len[b] < 0 is skipped. Rows at and behind cu[B] + B are neither read nor written.
+ *
+ * status[b], where a call takes it (NULL: not reported), has bits OR-ed in and is never cleared,
+ * so that one array can collect a step's calls. All pointers are device pointers on the current
+ * device unless said otherwise; nothing is allocated; every call is asynchronous on `stream`
+ * and may be captured into a graph (lengths, offsets and block tables are read on the device, so a
+ * replay uses their values at that time).
+ * ------------------------------------------------------------------------------------------ */
+
+/* A rotary embedding. freq[i] (device) is how far the i-th pair turns per position, in units of
+ * 2^-64 turn (specdec_rope_frequencies): the angle of position p is p * freq[i] modulo 2^64, exact
+ * however far the position. rot_dim (even, 2 <= rot_dim <= head_dim) leading elements of each head
+ * are rotated, the others copied. interleaved = 0: element i pairs with i + rot_dim / 2; 1: 2 i
+ * with 2 i + 1. cosine and sine are multiplied by amplitude. */
+typedef struct {
+    const uint64_t* freq;       /* [rot_dim / 2], device */
+    int32_t rot_dim;
+    int32_t interleaved;
+    float amplitude;
+} specdec_rope_t;
+
+typedef enum { SPECDEC_ROPE_PLAIN = 0, SPECDEC_ROPE_LINEAR = 1, SPECDEC_ROPE_BY_PARTS = 2 } specdec_rope_scaling_t;
+
+/*
+ * specdec_rope_frequencies -- the frequency table of a rotary embedding (host arithmetic in 64
+ * bits; freq is HOST memory: copy it to the device once). Pair i of rot_dim / 2 turns by
+ * f_i = theta^(-2 i / rot_dim) radians per position;
+ *   LINEAR     f_i / factor (position interpolation);
+ *   BY_PARTS   f_i (w + (1 - w) / factor), w = (original_len f_i / 2 pi - beta_slow) /
+ *              (beta_fast - beta_slow) clamped to [0, 1]: pairs that turn more than beta_fast times
+ *              over original_len positions are kept, those under beta_slow are interpolated; and
+ *              *amplitude = 0.1 ln(factor) + 1 (factor > 1).
+ * PLAIN and LINEAR give amplitude 1. amplitude may be NULL. factor is ignored by PLAIN;
+ * original_len, beta_fast and beta_slow matter to BY_PARTS alone.
+ * Errors: INVALID_ARG for rot_dim odd, < 2 or > 256, freq NULL, theta < 1 or not finite, factor
+ * not in (0, inf), an unknown scaling, original_len < 1 or beta_fast <= beta_slow where they matter.
+ */
+specdec_status_t specdec_rope_frequencies(int32_t rot_dim, double theta, specdec_rope_scaling_t scaling,
+                                          double factor, int64_t original_len, double beta_fast,
+                                          double beta_slow, uint64_t* freq, float* amplitude);
+
+/*
+ * specdec_rope -- rotates the heads of `rows` rows: (a, b) -> (a c - b s, b c + a s) for every
+ * pair, c = amplitude cos(angle), s = amplitude sin(angle). inverse != 0 turns the other way
+ * (s -> -s), which is also the gradient: dx = rope(dout) with inverse = 1.
+ *
+ *   x, out     [rows, heads, head_dim] of dtype (F32, BF16 or F16), row and head strides in elements,
+ *              the elements of a head contiguous. out may be x itself (with x's strides: rotation
+ *              in place); any other overlap is undefined. Arithmetic is fp32, rounded once.
+ *   positions  [rows] int32: the position of every row (may be negative); or NULL: row j of request
+ *              b has position cached_len[b] + j, and rows of skipped or malformed requests and
+ *              behind the last request are left as they were.
+ *   cu_num_draft [B+1], cached_len [B] int32: used (and required) when positions is NULL.
+ * Errors: INVALID_ARG for a NULL required pointer, rows or B < 0, heads < 1, a negative stride or a
+ * misaligned pointer; UNSUPPORTED for another dtype, or head_dim odd, < 2 or > 256; CUDA.
+ */
+specdec_status_t specdec_rope(const void* x, void* out, specdec_dtype_t dtype, int32_t rows, int32_t heads,
+                              int32_t head_dim, int64_t x_row_stride, int64_t x_head_stride,
+                              int64_t out_row_stride, int64_t out_head_stride, const specdec_rope_t* rope,
+                              int32_t inverse, const int32_t* positions, const int32_t* cu_num_draft,
+                              const int32_t* cached_len, int32_t B, void* stream);
+
+/* A paged key-value cache. Element (page, head, slot, d) of k and of v lies at
+ * page * page_stride + head * head_stride + slot * slot_stride + d (strides in elements, so heads
+ * and slots may lie in either order). Token i of request b lives in page block_table[b][i / page_size]
+ * at slot i % page_size.
+ * dtype BF16, F16 or E4M3. An E4M3 cache has one power-of-two scale for each token and head in
+ * k_exp and v_exp, [num_pages, num_kv_heads, page_size] contiguous bytes: the element stands for
+ * e4m3 * 2^(byte - 127). Bytes the library writes are in [1, 254]. */
+typedef struct {
+    void* k;
+    void* v;
+    uint8_t* k_exp;             /* E4M3 only, else NULL */
+    uint8_t* v_exp;
+    specdec_dtype_t dtype;
+    int32_t num_pages;
+    int32_t page_size;          /* 16, 32, 64, 128 or 256 */
+    int32_t num_kv_heads;
+    int32_t head_dim;           /* a multiple of 16, at most 128 */
+    int64_t page_stride;
+    int64_t head_stride;
+    int64_t slot_stride;
+} specdec_kv_cache_t;
+
+/*
+ * specdec_kv_write -- puts the keys and values of a step's rows into the cache: row j of request b
+ * as token cached_len[b] + j. With `rope` the keys are rotated on the way, in fp32.
+ *
+ *   k, v         [rows, num_kv_heads, head_dim] of dtype F32, BF16 or F16; row and head strides in
+ *                elements, the same for both (slices of one projection's output, for instance).
+ *   rope         NULL: keys are stored as given. positions [rows] int32 or NULL (NULL:
+ *                cached_len[b] + j); it moves the rotation only, never the place in the cache.
+ *   block_table  [B, max_blocks] int32 with block_stride elements between rows; only entries of
+ *                pages that receive a token are read.
+ * A stored value is the (rotated) value rounded once, to nearest, ties to even. For an E4M3 cache
+ * the scale is the smallest power of two 2^e, e >= -126, with max |finite x| <= 448 * 2^e over the
+ * head's elements (2^0 for a head of zeros): a power of two moves no mantissa bit, so the only
+ * rounding is that to e4m3. Infinities and NaN are stored as NaN.
+ * Two requests of one call that write the same page slot: one of them wins, element by element.
+ * status: BAD_LENGTH (cached_len[b] < 0, or a token past max_blocks pages: none of the request's rows
+ * are written), BAD_PAGE, BAD_OFFSETS.
+ * Errors: INVALID_ARG for a NULL required pointer, a bad size or stride, or a misaligned pointer (k,
+ * v of the cache: 16 bytes, and strides of a multiple of 16 bytes); UNSUPPORTED for a dtype,
+ * page_size or head_dim outside those above; CUDA.
+ */
+specdec_status_t specdec_kv_write(const void* k, const void* v, specdec_dtype_t dtype, int32_t rows,
+                                  int64_t row_stride, int64_t head_stride, const specdec_rope_t* rope,
+                                  const int32_t* positions, const specdec_kv_cache_t* cache,
+                                  const int32_t* block_table, int32_t max_blocks, int64_t block_stride,
+                                  const int32_t* cached_len, const int32_t* cu_num_draft, int32_t B,
+                                  uint32_t* status, void* stream);
+
+/*
+ * specdec_kv_read -- reads tokens back into dense rows: out row cu_len[b] + i takes token
+ * first[b] + i of request b, i in [0, cu_len[b+1] - cu_len[b]), as the value that the cache holds
+ * for it, rounded to out's type (exact where the type holds it).
+ *
+ *   cu_len       [B+1] int64 offsets, cu_len[0] = 0; rows at and behind cu_len[B] are left as they
+ *                were, rows = the row capacity of the outputs.
+ *   first        [B] int32 or NULL (0).
+ *   out_k, out_v [rows, num_kv_heads, head_dim], F32, BF16 or F16; either may be NULL.
+ * status: BAD_LENGTH (first[b] < 0, or a token past max_blocks pages: none of its rows are written),
+ * BAD_PAGE (zeros), BAD_OFFSETS. Errors as specdec_kv_write's.
+ */
+specdec_status_t specdec_kv_read(const specdec_kv_cache_t* cache, const int32_t* block_table,
+                                 int32_t max_blocks, int64_t block_stride, const int32_t* first,
+                                 const int64_t* cu_len, int32_t B, int64_t rows, void* out_k, void* out_v,
+                                 specdec_dtype_t out_dtype, int64_t out_row_stride, int64_t out_head_stride,
+                                 uint32_t* status, void* stream);
+
+/*
+ * specdec_paged_attention -- softmax(scale q K^T) V of a step's rows over the paged cache. Row j of
+ * request b sees tokens 0 .. cached_len[b] + j of its request (the step's own rows must be in the
+ * cache: specdec_kv_write first), or the last `window` of them when window > 0. One row a request
+ * (k_b = 0) is plain decoding. Query head h reads key-value head h / (num_heads / num_kv_heads).
+ *
+ *   q, out       [rows, num_heads, head_dim] of dtype BF16 or F16, each with row and head strides in
+ *                elements (multiples of 8; pointers 16-byte aligned). The cache has dtype's own type or
+ *                E4M3. out must not overlap q.
+ *   lse          [rows, num_heads] fp32 contiguous or NULL: ln(sum exp(scale q k)) of every row and
+ *                head, by which partial results over other keys can be joined.
+ *   max_k        every k_b must be <= max_k <= SPECDEC_KMAX; it chooses the kernel's row tile.
+ *   scale        finite.  window >= 0.
+ *   workspace    specdec_paged_attention_workspace_size(...) bytes, 16-byte aligned, no
+ *                initialisation; it holds nothing between calls, and calls (or captured graphs) that
+ *                share one must not overlap in time.
+ *   wait_limit_us -1: 2 s; 0..2000000: the limit of every wait inside the kernel, after which the
+ *                requests concerned get SPECDEC_ST_DEVICE_TIMEOUT and undefined outputs; nothing
+ *                hangs or traps.
+ * A row's result depends on its own request alone, and equal calls give equal bits. Scores, maxima,
+ * sums and the output are accumulated in fp32; the weights exp(s - m) are rounded to the cache's
+ * 16-bit type (F16 for E4M3) before their product with V. Keys and values that a row does not see
+ * do not reach it, whatever they hold (infinities, NaN, pages never written). A row that sees no
+ * finite score gets zeros and lse = -inf.
+ * status: K_TOO_LARGE, BAD_OFFSETS (rows unknown: not written), BAD_LENGTH (both: zeros,
+ * lse -inf in its rows), BAD_PAGE (its tokens read as zeros), DEVICE_TIMEOUT.
+ * Errors: INVALID_ARG for a NULL required pointer, a bad size or stride, num_heads not a multiple of
+ * num_kv_heads, a workspace too small or misaligned; UNSUPPORTED for types, page_size or head_dim
+ * outside those above; CUDA.
+ */
+size_t specdec_paged_attention_workspace_size(int32_t B, int32_t max_k, int32_t num_heads,
+                                              int32_t num_kv_heads, int32_t head_dim);
+specdec_status_t specdec_paged_attention(const void* q, specdec_dtype_t dtype, int32_t rows, int32_t num_heads,
+                                         int64_t q_row_stride, int64_t q_head_stride,
+                                         const specdec_kv_cache_t* cache, const int32_t* block_table,
+                                         int32_t max_blocks, int64_t block_stride, const int32_t* cached_len,
+                                         const int32_t* cu_num_draft, int32_t B, int32_t max_k, float scale,
+                                         int32_t window, void* out, int64_t out_row_stride,
+                                         int64_t out_head_stride, float* lse, uint32_t* status,
+                                         void* workspace, size_t workspace_bytes, int32_t wait_limit_us,
+                                         void* stream);
 
 /*
  * specdec_wait -- block the calling host thread until all work queued on `stream` has

@@ -18,6 +18,8 @@ SPECDEC_ERR_CUDA = 3
 SPECDEC_ERR_TIMEOUT = 4
 SPECDEC_F32 = 0
 SPECDEC_BF16 = 1
+SPECDEC_F16 = 2
+SPECDEC_E4M3 = 3
 SPECDEC_KMAX = 32
 TELEMETRY_SHAPE = (4, SPECDEC_KMAX + 1)   # rows: drafts, eligible, accepted-through by position; histogram
 
@@ -28,14 +30,34 @@ ST_K_TOO_LARGE = 8
 ST_BAD_OFFSETS = 16
 ST_DEVICE_TIMEOUT = 32
 ST_BAD_TOP_P = 64
+ST_BAD_LENGTH = 128
+ST_BAD_PAGE = 256
 
 EXPORTED = ("specdec_verify", "specdec_verify_noalloc", "specdec_wait", "specdec_status_string",
             "specdec_launch_config", "specdec_workspace_size", "specdec_ngram_propose",
-            "specdec_bitmask_scatter", "specdec_set_launch_options")
+            "specdec_bitmask_scatter", "specdec_set_launch_options", "specdec_rope_frequencies",
+            "specdec_rope", "specdec_kv_write", "specdec_kv_read", "specdec_paged_attention_workspace_size",
+            "specdec_paged_attention")
 NGRAM_MAX_N = 64                        # SPECDEC_NGRAM_MAX_N
 NOALLOC_MAX_REQUESTS = 16384            # SPECDEC_NOALLOC_MAX_REQUESTS
 
+ROPE_SCALINGS = {None: 0, "linear": 1, "by_parts": 2}      # specdec_rope_scaling_t
+
 _lib = None
+
+
+class RopeStruct(ctypes.Structure):
+    """specdec_rope_t"""
+    _fields_ = [("freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("amplitude", ctypes.c_float)]
+
+
+class KVCacheStruct(ctypes.Structure):
+    """specdec_kv_cache_t"""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+                ("dtype", ctypes.c_int), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64)]
 
 
 class SpecdecError(RuntimeError):
@@ -73,6 +95,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.specdec_launch_config.argtypes = [i32, i32, ctypes.c_int, vp, vp, vp, vp, vp, vp]
     lib.specdec_set_launch_options.restype = ctypes.c_int
     lib.specdec_set_launch_options.argtypes = [i32, i32, i32, i32, i32]
+    i64, f64 = ctypes.c_int64, ctypes.c_double
+    lib.specdec_rope_frequencies.restype = ctypes.c_int
+    lib.specdec_rope_frequencies.argtypes = [i32, f64, ctypes.c_int, f64, i64, f64, f64, vp, vp]
+    lib.specdec_rope.restype = ctypes.c_int
+    lib.specdec_rope.argtypes = [vp, vp, ctypes.c_int, i32, i32, i32, i64, i64, i64, i64, vp, i32, vp, vp, vp, i32, vp]
+    lib.specdec_kv_write.restype = ctypes.c_int
+    lib.specdec_kv_write.argtypes = [vp, vp, ctypes.c_int, i32, i64, i64, vp, vp, vp, vp, i32, i64, vp, vp, i32, vp, vp]
+    lib.specdec_kv_read.restype = ctypes.c_int
+    lib.specdec_kv_read.argtypes = [vp, vp, i32, i64, vp, vp, i32, i64, vp, vp, ctypes.c_int, i64, i64, vp, vp]
+    lib.specdec_paged_attention_workspace_size.restype = ctypes.c_size_t
+    lib.specdec_paged_attention_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    lib.specdec_paged_attention.restype = ctypes.c_int
+    lib.specdec_paged_attention.argtypes = [vp, ctypes.c_int, i32, i32, i64, i64, vp, vp, i32, i64, vp, vp, i32, i32,
+                                            ctypes.c_float, i32, vp, i64, i64, vp, vp, vp, ctypes.c_size_t, i32, vp]
     _lib = lib
     return lib
 
@@ -236,3 +272,197 @@ def bitmask_scatter(compact, compact_rows: int, constrained, n: int, cu_num_draf
                                         int(B), int(V), _p(bitmask), stream)
     if rc != SPECDEC_OK:
         raise SpecdecError(rc, "specdec_bitmask_scatter")
+
+
+# ------------------------------------------------------------------ rotary positions, paged cache, attention
+
+def _stream(stream):
+    import torch
+
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _dtype_of(t) -> int:
+    import torch
+
+    types = {torch.float32: SPECDEC_F32, torch.bfloat16: SPECDEC_BF16, torch.float16: SPECDEC_F16}
+    if t.dtype not in types:
+        raise SpecdecError(SPECDEC_ERR_UNSUPPORTED, f"dtype {t.dtype}")
+    return types[t.dtype]
+
+
+def _on_device(*tensors) -> None:
+    """Every (name, tensor) given is on the current CUDA device: the library launches there."""
+    import torch
+
+    for name, t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _ints(name, t, dtype: str, *shape) -> None:
+    """t is None or a contiguous tensor of `dtype` that holds at least `shape` (its first dimension may be longer)."""
+    if t is None:
+        return
+    if str(t.dtype) != f"torch.{dtype}" or t.dim() != len(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {len(shape)} dimension(s)")
+    if t.shape[0] < shape[0] or tuple(t.shape[1:]) != shape[1:]:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, {shape} is needed")
+
+
+def _status_ints(status, B: int) -> None:
+    if status is not None and (status.element_size() != 4 or status.dim() != 1 or not status.is_contiguous() or status.shape[0] < B):
+        raise ValueError("status must be a contiguous 32-bit integer tensor of B elements")
+
+
+def _heads(name, t, like=None) -> None:
+    """t is [rows, heads, head_dim] with the elements of a head contiguous."""
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError(f"{name} must be [rows, heads, head_dim] with the elements of a head contiguous")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+        raise ValueError(f"{name} has shape {tuple(t.shape)} {t.dtype}, {tuple(like.shape)} {like.dtype} is needed")
+
+
+def _table(block_table, B: int):
+    if str(block_table.dtype) != "torch.int32" or block_table.dim() != 2 or block_table.shape[0] < B:
+        raise ValueError("block_table must be int32 [B, max_blocks]")
+    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+        raise ValueError("a request's row of block_table must be contiguous")
+    return block_table.shape[1], block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
+
+
+def rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                     original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """specdec_rope_frequencies: (table, amplitude). The table is a CPU int64 tensor [rot_dim / 2] that holds
+    the unsigned 64-bit units; copy it to the device once. scaling: None, "linear" or "by_parts"."""
+    import torch
+
+    if scaling not in ROPE_SCALINGS:
+        raise SpecdecError(SPECDEC_ERR_INVALID_ARG, f"rope scaling {scaling!r}")
+    table = torch.zeros(max(int(rot_dim) // 2, 1), dtype=torch.int64)
+    amplitude = ctypes.c_float()
+    rc = load().specdec_rope_frequencies(int(rot_dim), float(theta), ROPE_SCALINGS[scaling], float(factor), int(original_len),
+                                         float(beta_fast), float(beta_slow), table.data_ptr(), ctypes.byref(amplitude))
+    if rc != SPECDEC_OK:
+        raise SpecdecError(rc, "specdec_rope_frequencies")
+    return table, amplitude.value
+
+
+def _rope_struct(freqs, rot_dim: int, interleaved: bool = False, amplitude: float = 1.0) -> RopeStruct:
+    _ints("freqs", freqs, "int64", int(rot_dim) // 2)
+    _on_device(("freqs", freqs))
+    return RopeStruct(_p(freqs), int(rot_dim), int(bool(interleaved)), float(amplitude))
+
+
+def rope(x, out, freqs, rot_dim: int, interleaved: bool = False, amplitude: float = 1.0, inverse: bool = False,
+         positions=None, cu_num_draft=None, cached_len=None, B: int = 0, stream=None) -> None:
+    """Queue specdec_rope: x rotated into out (which may be x), both [rows, heads, head_dim] with any row and
+    head strides. Positions are given for every row, or follow from cu_num_draft, cached_len and B."""
+    _heads("x", x)
+    _heads("out", out, x)
+    if positions is None and (cu_num_draft is None or cached_len is None):
+        raise ValueError("rope needs positions, or cu_num_draft and cached_len")
+    _ints("positions", positions, "int32", x.shape[0])
+    _ints("cu_num_draft", cu_num_draft, "int32", int(B) + 1)
+    _ints("cached_len", cached_len, "int32", int(B))
+    _on_device(("x", x), ("out", out), ("positions", positions), ("cu_num_draft", cu_num_draft), ("cached_len", cached_len))
+    r = _rope_struct(freqs, rot_dim, interleaved, amplitude)
+    rc = load().specdec_rope(_p(x), _p(out), _dtype_of(x), x.shape[0], x.shape[1], x.shape[2], x.stride(0), x.stride(1),
+                             out.stride(0), out.stride(1), ctypes.byref(r), int(bool(inverse)), _p(positions),
+                             _p(cu_num_draft), _p(cached_len), int(B), _stream(stream))
+    if rc != SPECDEC_OK:
+        raise SpecdecError(rc, "specdec_rope")
+
+
+def kv_write(k, v, cache, block_table, cached_len, cu_num_draft, B: int, rope=None, positions=None, status=None,
+             stream=None) -> None:
+    """Queue specdec_kv_write: the rows of k and v [rows, num_kv_heads, head_dim] (same strides) into `cache`
+    (kvcache.PagedCache). rope: None, or the keyword arguments of a rotation of the keys: a dict of freqs,
+    rot_dim and, optionally, interleaved and amplitude."""
+    _heads("k", k)
+    _heads("v", v, k)
+    if k.stride() != v.stride():
+        raise ValueError("k and v must have the same strides")
+    if tuple(k.shape[1:]) != (cache.k.shape[1], cache.k.shape[3]):
+        raise ValueError(f"rows of {tuple(k.shape[1:])} do not go into a cache of {(cache.k.shape[1], cache.k.shape[3])}")
+    max_blocks, block_stride = _table(block_table, B)
+    _ints("positions", positions, "int32", k.shape[0])
+    _ints("cu_num_draft", cu_num_draft, "int32", int(B) + 1)
+    _ints("cached_len", cached_len, "int32", int(B))
+    _status_ints(status, B)
+    _on_device(("k", k), ("v", v), ("cache", cache.k), ("block_table", block_table), ("cached_len", cached_len),
+               ("cu_num_draft", cu_num_draft), ("positions", positions), ("status", status))
+    r = None if rope is None else _rope_struct(**rope)
+    c = cache.struct()
+    rc = load().specdec_kv_write(_p(k), _p(v), _dtype_of(k), k.shape[0], k.stride(0), k.stride(1),
+                                 None if r is None else ctypes.byref(r), _p(positions), ctypes.byref(c), _p(block_table),
+                                 max_blocks, block_stride, _p(cached_len), _p(cu_num_draft), int(B), _p(status),
+                                 _stream(stream))
+    if rc != SPECDEC_OK:
+        raise SpecdecError(rc, "specdec_kv_write")
+
+
+def kv_read(cache, block_table, cu_len, B: int, out_k, out_v, first=None, status=None, stream=None) -> None:
+    """Queue specdec_kv_read: tokens first[b] .. of every request into rows cu_len[b] .. of out_k and out_v
+    ([rows, num_kv_heads, head_dim], same strides; either may be None)."""
+    out = out_k if out_k is not None else out_v
+    if out is None:
+        raise ValueError("kv_read needs out_k or out_v")
+    _heads("out_k", out)
+    if out_k is not None and out_v is not None:
+        _heads("out_v", out_v, out_k)
+        if out_k.stride() != out_v.stride():
+            raise ValueError("out_k and out_v must have the same strides")
+    if tuple(out.shape[1:]) != (cache.k.shape[1], cache.k.shape[3]):
+        raise ValueError(f"rows of {tuple(out.shape[1:])} do not hold a cache of {(cache.k.shape[1], cache.k.shape[3])}")
+    max_blocks, block_stride = _table(block_table, B)
+    _ints("cu_len", cu_len, "int64", int(B) + 1)
+    _ints("first", first, "int32", int(B))
+    _status_ints(status, B)
+    _on_device(("out_k", out_k), ("out_v", out_v), ("cache", cache.k), ("block_table", block_table), ("cu_len", cu_len),
+               ("first", first), ("status", status))
+    c = cache.struct()
+    rc = load().specdec_kv_read(ctypes.byref(c), _p(block_table), max_blocks, block_stride, _p(first), _p(cu_len), int(B),
+                                out.shape[0], _p(out_k), _p(out_v), _dtype_of(out), out.stride(0), out.stride(1),
+                                _p(status), _stream(stream))
+    if rc != SPECDEC_OK:
+        raise SpecdecError(rc, "specdec_kv_read")
+
+
+def paged_attention_workspace_size(B: int, max_k: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(load().specdec_paged_attention_workspace_size(int(B), int(max_k), int(num_heads), int(num_kv_heads), int(head_dim)))
+
+
+def paged_attention(q, cache, block_table, cached_len, cu_num_draft, B: int, max_k: int, out, workspace,
+                    scale: Optional[float] = None, window: int = 0, lse=None, status=None,
+                    wait_limit_us: Optional[int] = None, stream=None) -> None:
+    """Queue specdec_paged_attention: q and out [rows, num_heads, head_dim], cache a kvcache.PagedCache, workspace a
+    CUDA tensor of at least paged_attention_workspace_size(...) bytes. scale: default head_dim ** -0.5."""
+    _heads("q", q)
+    _heads("out", out, q)
+    if q.shape[2] != cache.k.shape[3]:
+        raise ValueError(f"head_dim {q.shape[2]} against the cache's {cache.k.shape[3]}")
+    max_blocks, block_stride = _table(block_table, B)
+    _ints("cu_num_draft", cu_num_draft, "int32", int(B) + 1)
+    _ints("cached_len", cached_len, "int32", int(B))
+    _ints("lse", lse, "float32", q.shape[0], q.shape[1])
+    _status_ints(status, B)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _on_device(("q", q), ("out", out), ("cache", cache.k), ("block_table", block_table), ("cached_len", cached_len),
+               ("cu_num_draft", cu_num_draft), ("lse", lse), ("status", status), ("workspace", workspace))
+    c = cache.struct()
+    rc = load().specdec_paged_attention(_p(q), _dtype_of(q), q.shape[0], q.shape[1], q.stride(0), q.stride(1),
+                                        ctypes.byref(c), _p(block_table), max_blocks, block_stride, _p(cached_len),
+                                        _p(cu_num_draft), int(B), int(max_k),
+                                        float(q.shape[2] ** -0.5 if scale is None else scale), int(window), _p(out),
+                                        out.stride(0), out.stride(1), _p(lse), _p(status), _p(workspace), _nbytes(workspace),
+                                        -1 if wait_limit_us is None else int(wait_limit_us), _stream(stream))
+    if rc != SPECDEC_OK:
+        raise SpecdecError(rc, "specdec_paged_attention")

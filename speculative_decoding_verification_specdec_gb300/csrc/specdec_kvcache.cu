@@ -1,0 +1,379 @@
+/*
+ * specdec_kvcache.cu -- the paged key-value cache for GB300 (sm_103a): rows of a step written into
+ * their pages (keys rotated, heads quantised on the way) and tokens read back; C-ABI entry points
+ * in include/specdec.h.
+ *
+ * Quantisation: an e4m3 head (one token, one head) carries the power of two 2^e with
+ * max |x| in (224, 448] 2^e. Scaling by a power of two is exact, so the only rounding is the one to
+ * e4m3's three mantissa bits (relative error at most 2^-4), and the scale takes one byte.
+ *
+ * Both kernels only move data: bound by HBM.
+ */
+#include "specdec_rows.cuh"
+
+namespace {
+
+using namespace specdec;
+
+constexpr int kThreads = 256;
+constexpr int kMaxRows = 32;
+
+struct Table {
+    const int32_t* block_table;
+    int64_t block_stride;
+    int32_t max_blocks;
+};
+
+struct WriteArgs {
+    const void *k, *v;
+    int64_t row_stride, head_stride;
+    int32_t rows, rows_per_cta;
+    int32_t has_rope;
+    specdec_rope_t rope;
+    const int32_t* positions;
+    specdec_kv_cache_t cache;
+    Table table;
+    const int32_t *cached, *cu;
+    int32_t B;
+    uint32_t* status;
+};
+
+struct RowSlot {
+    int64_t at;        // element offset of (page, head 0, slot)
+    int64_t exp_at;    // byte offset of the same in k_exp, v_exp
+    int64_t position;
+    int32_t live;
+};
+
+__device__ __forceinline__ RowSlot no_slot() { return RowSlot{0, 0, 0, 0}; }
+
+// Page and slot of token i of request b; a bad page id is reported and leaves the row dead (-1).
+__device__ __forceinline__ RowSlot slot_of(const specdec_kv_cache_t& c, const Table& t, int b, int64_t i, uint32_t* status)
+{
+    const int page = __ldg(t.block_table + b * t.block_stride + i / c.page_size);
+    RowSlot r = no_slot();
+    if (page < 0 || page >= c.num_pages) {
+        if (status) atomicOr(status + b, SPECDEC_ST_BAD_PAGE);
+        r.live = -1;
+        return r;
+    }
+    const int slot = (int)(i % c.page_size);
+    r.at = page * c.page_stride + slot * c.slot_stride;
+    r.exp_at = (int64_t)page * c.num_kv_heads * c.page_size + slot;
+    r.live = 1;
+    return r;
+}
+
+__device__ __forceinline__ bool fits(const specdec_kv_cache_t& c, const Table& t, int64_t tokens)
+{
+    return tokens <= (int64_t)t.max_blocks * c.page_size;
+}
+
+// The exponent of an e4m3 head: smallest e >= -126 with top <= 448 2^e (0 for a head of zeros).
+// top = m 2^x with m in [0.5, 1), 448 = 0.875 2^9.
+__device__ __forceinline__ int e4m3_exponent(float top)
+{
+    if (top == 0.f) return 0;
+    int x;
+    const float m = frexpf(top, &x);
+    return max(m <= 0.875f ? x - 9 : x - 8, -126);
+}
+
+template <int N> __device__ __forceinline__ void store_e4m3(uint8_t* p, const float* x, float inverse_scale)
+{
+    uint8_t q[N];
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float a = isfinite(x[i]) ? x[i] * inverse_scale : NAN;
+        const float b = i + 1 < N ? (isfinite(x[i + 1]) ? x[i + 1] * inverse_scale : NAN) : 0.f;
+        const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+        q[i] = (uint8_t)(two & 0xff);
+        if (i + 1 < N) q[i + 1] = (uint8_t)(two >> 8);
+    }
+    if constexpr (N % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 8) {
+            uint2 w;
+            w.x = q[i] | q[i + 1] << 8 | q[i + 2] << 16 | (uint32_t)q[i + 3] << 24;
+            w.y = q[i + 4] | q[i + 5] << 8 | q[i + 6] << 16 | (uint32_t)q[i + 7] << 24;
+            *reinterpret_cast<uint2*>(p + i) = w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i] = q[i];
+    }
+}
+
+// A head is held by a group of kLanes lanes, kUnits units of 2V elements a lane, so that its largest
+// magnitude is a shuffle reduction and its elements are read once.
+// V = 8: 16-byte runs, groups of 8 lanes (head_dim <= 128); V = 1 takes any even rot_dim and any
+// alignment of the inputs with a warp a head.
+template <typename T, typename C, int V, int kLanes, int kUnits>
+__global__ void __launch_bounds__(kThreads) specdec_kv_write_kernel(const WriteArgs a)
+{
+    extern __shared__ float2 cs[];                                 // [rows_per_cta][rot_dim / 2]
+    __shared__ RowSlot slots[kMaxRows];
+    const specdec_kv_cache_t& c = a.cache;
+    const int tid = threadIdx.x;
+    const int64_t row0 = (int64_t)blockIdx.x * a.rows_per_cta;
+    const int n = (int)min((int64_t)a.rows_per_cta, a.rows - row0);
+
+    if (a.status)
+        for (int64_t b = (int64_t)blockIdx.x * kThreads + tid; b < a.B; b += (int64_t)gridDim.x * kThreads) {
+            if (!offsets_ok(a.cu, a.B, (int)b)) atomicOr(a.status + b, SPECDEC_ST_BAD_OFFSETS);
+            else if (a.cached[b] < 0 || !fits(c, a.table, (int64_t)a.cached[b] + a.cu[b + 1] - a.cu[b] + 1))
+                atomicOr(a.status + b, SPECDEC_ST_BAD_LENGTH);
+        }
+
+    int b = owner_of<kThreads>(a.B, row0, [&](int i) { return (int64_t)__ldg(a.cu + i) + i; });
+    if (tid < n) {
+        const int64_t t = row0 + tid;
+        b = max(b, 0);
+        while (b < a.B && t > (int64_t)__ldg(a.cu + b + 1) + b) ++b;
+        RowSlot r = no_slot();
+        if (b < a.B && offsets_ok(a.cu, a.B, b)) {
+            const int64_t j = t - __ldg(a.cu + b) - b, k = (int64_t)__ldg(a.cu + b + 1) - __ldg(a.cu + b);
+            const int64_t cached = __ldg(a.cached + b);
+            if (j >= 0 && cached >= 0 && fits(c, a.table, cached + k + 1)) {
+                r = slot_of(c, a.table, b, cached + j, a.status);
+                r.position = a.positions ? a.positions[t] : cached + j;
+            }
+        }
+        slots[tid] = r;
+    }
+    __syncthreads();
+    const int half = a.has_rope ? a.rope.rot_dim / 2 : 0;
+    for (int i = tid; i < n * half; i += kThreads) {
+        const int r = i / half;
+        cs[i] = turn(slots[r].position, __ldg(a.rope.freq + (i - r * half)), a.rope.amplitude);
+    }
+    __syncthreads();
+
+    const int units = c.head_dim / (2 * V), H = c.num_kv_heads;
+    const int lane = tid % kLanes, groups = kThreads / kLanes;
+    const int total = n * 2 * H, rounds = (total + groups - 1) / groups;
+    for (int it = 0; it < rounds; ++it) {
+        const int w = it * groups + tid / kLanes;                  // (row, K or V, head)
+        const int r = w / (2 * H), hv = w - r * 2 * H, is_v = hv >= H, h = hv - is_v * H;
+        const bool live = w < total && slots[w < total ? r : 0].live == 1;
+        float x[kUnits][2 * V];
+        float top = 0.f;
+        if (live) {
+            const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (row0 + r) * a.row_stride + h * a.head_stride;
+#pragma unroll
+            for (int q = 0; q < kUnits; ++q) {
+                const int u = lane + q * kLanes;
+                if (u >= units) continue;
+                int first, second;
+                unit_runs<V>(u, 2 * half, a.rope.interleaved, &first, &second);
+                load_n<T, V>(src + first, x[q]);
+                load_n<T, V>(src + second, x[q] + V);
+                if (!is_v) rotate_unit<V>(x[q], u, 2 * half, a.rope.interleaved, cs + r * half);
+#pragma unroll
+                for (int i = 0; i < 2 * V; ++i)
+                    if (isfinite(x[q][i])) top = fmaxf(top, fabsf(x[q][i]));
+            }
+        }
+        int e = 0;
+        if constexpr (sizeof(C) == 1) {
+#pragma unroll
+            for (int off = kLanes / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            e = e4m3_exponent(top);
+        }
+        if (!live) continue;
+        const RowSlot& slot = slots[r];
+        C* dst = static_cast<C*>(is_v ? c.v : c.k) + slot.at + h * c.head_stride;
+#pragma unroll
+        for (int q = 0; q < kUnits; ++q) {
+            const int u = lane + q * kLanes;
+            if (u >= units) continue;
+            int first, second;
+            unit_runs<V>(u, 2 * half, a.rope.interleaved, &first, &second);
+            if constexpr (sizeof(C) == 1) {
+                const float inv = __uint_as_float((uint32_t)(127 - e) << 23);     // 2^-e, e in [-126, 120]
+                store_e4m3<V>(reinterpret_cast<uint8_t*>(dst) + first, x[q], inv);
+                store_e4m3<V>(reinterpret_cast<uint8_t*>(dst) + second, x[q] + V, inv);
+            } else {
+                store_n<C, V>(dst + first, x[q]);
+                store_n<C, V>(dst + second, x[q] + V);
+            }
+        }
+        if constexpr (sizeof(C) == 1)
+            if (lane == 0) (is_v ? c.v_exp : c.k_exp)[slot.exp_at + (int64_t)h * c.page_size] = (uint8_t)(e + 127);
+    }
+}
+
+template <typename T, typename C> specdec_status_t launch_write(WriteArgs a, cudaStream_t stream)
+{
+    const specdec_kv_cache_t& c = a.cache;
+    const int rot = a.has_rope ? a.rope.rot_dim : 0;
+    const int64_t per = 16 / (int64_t)sizeof(T);
+    const bool wide = rot % 16 == 0 && aligned_to(a.k, 16) && aligned_to(a.v, 16) && a.row_stride % per == 0 &&
+                      a.head_stride % per == 0;
+    // rows for about four rounds of the CTA's groups
+    const int groups = wide ? kThreads / 8 : kThreads / 32;
+    int rpc = 4 * groups / (2 * c.num_kv_heads);
+    rpc = rpc < 1 ? 1 : rpc > kMaxRows ? kMaxRows : rpc;
+    a.rows_per_cta = rpc;
+    const unsigned grid = (unsigned)(((int64_t)a.rows + rpc - 1) / rpc);
+    const size_t smem = (size_t)rpc * (rot / 2) * sizeof(float2);
+    if (wide) specdec_kv_write_kernel<T, C, 8, 8, 1><<<grid, kThreads, smem, stream>>>(a);
+    else specdec_kv_write_kernel<T, C, 1, 32, 2><<<grid, kThreads, smem, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+}
+
+template <typename T> specdec_status_t launch_write_to(const WriteArgs& a, cudaStream_t stream)
+{
+    if (a.cache.dtype == SPECDEC_BF16) return launch_write<T, __nv_bfloat16>(a, stream);
+    if (a.cache.dtype == SPECDEC_F16) return launch_write<T, __half>(a, stream);
+    return launch_write<T, __nv_fp8_e4m3>(a, stream);
+}
+
+struct ReadArgs {
+    specdec_kv_cache_t cache;
+    Table table;
+    const int32_t* first;
+    const int64_t* cu_len;
+    int32_t B, rows_per_cta;
+    int64_t rows;
+    void *out_k, *out_v;
+    int64_t out_row, out_head;
+    uint32_t* status;
+};
+
+// Offsets and range of request b: 0 fine, else the status bit.
+__device__ __forceinline__ uint32_t read_fault(const ReadArgs& a, int b)
+{
+    const int64_t r0 = a.cu_len[b], r1 = a.cu_len[b + 1], end = a.cu_len[a.B];
+    if (a.cu_len[0] != 0 || r0 < 0 || r1 < r0 || r1 > end) return SPECDEC_ST_BAD_OFFSETS;
+    const int32_t f = a.first ? a.first[b] : 0;
+    if (f < 0 || (r1 > r0 && !fits(a.cache, a.table, f + (r1 - r0)))) return SPECDEC_ST_BAD_LENGTH;
+    return 0;
+}
+
+// Units of 16 elements; kWide: the outputs take 16-byte stores.
+template <typename C, typename T, bool kWide>
+__global__ void __launch_bounds__(kThreads) specdec_kv_read_kernel(const ReadArgs a)
+{
+    __shared__ RowSlot slots[kMaxRows];
+    const specdec_kv_cache_t& c = a.cache;
+    const int tid = threadIdx.x;
+    const int64_t row0 = (int64_t)blockIdx.x * a.rows_per_cta;
+    const int n = (int)min((int64_t)a.rows_per_cta, a.rows - row0);
+    if (a.status)
+        for (int64_t b = (int64_t)blockIdx.x * kThreads + tid; b < a.B; b += (int64_t)gridDim.x * kThreads) {
+            const uint32_t f = read_fault(a, (int)b);
+            if (f) atomicOr(a.status + b, f);
+        }
+    int b = owner_of<kThreads>(a.B, row0, [&](int i) { return (int64_t)__ldg((const long long*)a.cu_len + i); });
+    if (tid < n) {
+        const int64_t t = row0 + tid;
+        b = max(b, 0);
+        while (b < a.B && t >= a.cu_len[b + 1]) ++b;
+        RowSlot r = no_slot();
+        if (b < a.B && t >= a.cu_len[b] && read_fault(a, b) == 0)
+            r = slot_of(c, a.table, b, (a.first ? a.first[b] : 0) + (t - a.cu_len[b]), a.status);
+        slots[tid] = r;
+    }
+    __syncthreads();
+    const int units = c.head_dim / 16, H = c.num_kv_heads, per_row = 2 * H * units;
+    for (int i = tid; i < n * per_row; i += kThreads) {
+        const int r = i / per_row, w = i - r * per_row, hv = w / units, u = w - hv * units;
+        const int is_v = hv >= H, h = hv - is_v * H;
+        const RowSlot slot = slots[r];
+        T* out = static_cast<T*>(is_v ? a.out_v : a.out_k);
+        if (!slot.live || !out) continue;
+        float x[16];
+        if (slot.live > 0) {
+            load_n<C, 16>(static_cast<const C*>(is_v ? c.v : c.k) + slot.at + h * c.head_stride + u * 16, x);
+            if constexpr (sizeof(C) == 1) {
+                const float s = exp_value((is_v ? c.v_exp : c.k_exp)[slot.exp_at + (int64_t)h * c.page_size]);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] *= s;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = 0.f;               // a bad page reads as zeros
+        }
+        out += (row0 + r) * a.out_row + h * a.out_head + u * 16;
+        if constexpr (kWide) {
+            store_n<T, 16>(out, x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) out[e] = from_float<T>(x[e]);
+        }
+    }
+}
+
+template <typename C, typename T> specdec_status_t launch_read(ReadArgs a, cudaStream_t stream)
+{
+    const int64_t per = 16 / (int64_t)sizeof(T);
+    const bool wide = aligned_to(a.out_k, 16) && aligned_to(a.out_v, 16) && a.out_row % per == 0 && a.out_head % per == 0;
+    int rpc = 4 * kThreads / (2 * a.cache.num_kv_heads * (a.cache.head_dim / 16));
+    rpc = rpc < 1 ? 1 : rpc > kMaxRows ? kMaxRows : rpc;
+    a.rows_per_cta = rpc;
+    const int64_t grid = (a.rows + rpc - 1) / rpc;
+    if (grid > 0x7fffffff) return SPECDEC_ERR_UNSUPPORTED;
+    if (wide) specdec_kv_read_kernel<C, T, true><<<(unsigned)grid, kThreads, 0, stream>>>(a);
+    else specdec_kv_read_kernel<C, T, false><<<(unsigned)grid, kThreads, 0, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+}
+
+template <typename C> specdec_status_t launch_read_to(const ReadArgs& a, specdec_dtype_t out, cudaStream_t stream)
+{
+    if (out == SPECDEC_F32) return launch_read<C, float>(a, stream);
+    if (out == SPECDEC_BF16) return launch_read<C, __nv_bfloat16>(a, stream);
+    return launch_read<C, __half>(a, stream);
+}
+
+}  // namespace
+
+extern "C" specdec_status_t specdec_kv_write(const void* k, const void* v, specdec_dtype_t dtype, int32_t rows,
+                                             int64_t row_stride, int64_t head_stride, const specdec_rope_t* rope,
+                                             const int32_t* positions, const specdec_kv_cache_t* cache,
+                                             const int32_t* block_table, int32_t max_blocks, int64_t block_stride,
+                                             const int32_t* cached_len, const int32_t* cu_num_draft, int32_t B,
+                                             uint32_t* status, void* stream)
+{
+    if (!is_float_type(dtype)) return SPECDEC_ERR_UNSUPPORTED;
+    specdec_status_t rc = check_cache(cache);
+    if (rc != SPECDEC_OK) return rc;
+    if (rope && (rc = check_rope(rope, cache->head_dim)) != SPECDEC_OK) return rc;
+    if (rows < 0 || B < 0 || max_blocks < 0 || block_stride < 0 || row_stride < 0 || head_stride < 0)
+        return SPECDEC_ERR_INVALID_ARG;
+    if (rows == 0 || B == 0) return SPECDEC_OK;
+    if (!k || !v || !block_table || !cached_len || !cu_num_draft) return SPECDEC_ERR_INVALID_ARG;
+    const size_t es = elem_bytes(dtype);
+    if (!aligned_to(k, es) || !aligned_to(v, es) || !aligned_to(positions, 4) || !aligned_to(block_table, 4) ||
+        !aligned_to(cached_len, 4) || !aligned_to(cu_num_draft, 4) || !aligned_to(status, 4))
+        return SPECDEC_ERR_INVALID_ARG;
+    WriteArgs a = {k, v, row_stride, head_stride, rows, 0, rope != nullptr, rope ? *rope : specdec_rope_t{nullptr, 0, 0, 1.f},
+                   positions, *cache, {block_table, block_stride, max_blocks}, cached_len, cu_num_draft, B, status};
+    if (dtype == SPECDEC_F32) return launch_write_to<float>(a, (cudaStream_t)stream);
+    if (dtype == SPECDEC_BF16) return launch_write_to<__nv_bfloat16>(a, (cudaStream_t)stream);
+    return launch_write_to<__half>(a, (cudaStream_t)stream);
+}
+
+extern "C" specdec_status_t specdec_kv_read(const specdec_kv_cache_t* cache, const int32_t* block_table,
+                                            int32_t max_blocks, int64_t block_stride, const int32_t* first,
+                                            const int64_t* cu_len, int32_t B, int64_t rows, void* out_k, void* out_v,
+                                            specdec_dtype_t out_dtype, int64_t out_row_stride, int64_t out_head_stride,
+                                            uint32_t* status, void* stream)
+{
+    if (!is_float_type(out_dtype)) return SPECDEC_ERR_UNSUPPORTED;
+    const specdec_status_t rc = check_cache(cache);
+    if (rc != SPECDEC_OK) return rc;
+    if (rows < 0 || B < 0 || max_blocks < 0 || block_stride < 0 || out_row_stride < 0 || out_head_stride < 0)
+        return SPECDEC_ERR_INVALID_ARG;
+    if (rows == 0 || B == 0) return SPECDEC_OK;
+    if (!block_table || !cu_len || (!out_k && !out_v)) return SPECDEC_ERR_INVALID_ARG;
+    const size_t es = elem_bytes(out_dtype);
+    if (!aligned_to(out_k, es) || !aligned_to(out_v, es) || !aligned_to(block_table, 4) || !aligned_to(first, 4) ||
+        !aligned_to(cu_len, 8) || !aligned_to(status, 4))
+        return SPECDEC_ERR_INVALID_ARG;
+    const ReadArgs a = {*cache, {block_table, block_stride, max_blocks}, first, cu_len, B, 0, rows, out_k, out_v,
+                        out_row_stride, out_head_stride, status};
+    if (cache->dtype == SPECDEC_BF16) return launch_read_to<__nv_bfloat16>(a, out_dtype, (cudaStream_t)stream);
+    if (cache->dtype == SPECDEC_F16) return launch_read_to<__half>(a, out_dtype, (cudaStream_t)stream);
+    return launch_read_to<__nv_fp8_e4m3>(a, out_dtype, (cudaStream_t)stream);
+}

@@ -383,8 +383,8 @@ specdec_status_t specdec_rope(const void* x, void* out, specdec_dtype_t dtype, i
  * and slots may lie in either order). Token i of request b lives in page block_table[b][i / page_size]
  * at slot i % page_size.
  * dtype BF16, F16 or E4M3. An E4M3 cache has one power-of-two scale for each token and head in
- * k_exp and v_exp, [num_pages, num_kv_heads, page_size] contiguous bytes: the element stands for
- * e4m3 * 2^(byte - 127). Bytes the library writes are in [1, 254]. */
+ * k_exp and v_exp, [num_pages, num_kv_heads, page_size] contiguous bytes, 16-byte aligned: the element stands for
+ * e4m3 * 2^(byte - 127); 255 stands for NaN. Bytes the library writes are in [1, 254]. */
 typedef struct {
     void* k;
     void* v;

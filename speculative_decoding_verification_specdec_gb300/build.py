@@ -11,7 +11,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", f) for f in ("specdec_verify.cu", "specdec_ngram.cu", "specdec_bitmask.cu",
                                                   "specdec_rope.cu", "specdec_kvcache.cu", "specdec_attention.cu")]
-HEADERS = [os.path.join(PKG, "csrc", "specdec_rows.cuh"), os.path.join(ROOT, "include", "specdec.h")]
+HEADERS = [os.path.join(PKG, "csrc", f) for f in ("specdec_rows.cuh", "specdec_tensor.cuh")] + [os.path.join(ROOT, "include", "specdec.h")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libspecdec.so")
 

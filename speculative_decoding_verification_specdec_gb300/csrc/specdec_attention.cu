@@ -1,26 +1,54 @@
 /*
  * specdec_attention.cu -- attention of a verify step's rows over the paged key-value cache for
- * GB300 (sm_103a); C-ABI entry point in include/specdec.h.
+ * GB300 (sm_103a); C-ABI entry points in include/specdec.h.
  *
- * One CTA per (request row, query head): every warp takes each fourth token, a lane holds up to four
- * elements of the head, the score is a shuffle sum, and a running (m, l, O) keeps the softmax in
- * one pass over the tokens; the four warps' states are joined in shared memory.
+ * Mathematics. The (k_b + 1) * G query rows that share one key-value head of request b are the N
+ * columns of two products over a tile of 128 tokens (padded to N = 16, 32, 64 or 128):
+ *     S^T [128 tokens, N] = K Q^T          O^T [D, N] += V^T P^T,   P = exp2(c S - m)
+ * with tokens (and head elements) as the 128 rows of tcgen05.mma: the work grows with the rows there
+ * are, not with a row tile of 128, and the keys and values go from TMA's swizzled tiles into the
+ * products as they lie (V^T is V read with its rows contiguous). The softmax is one pass: a column keeps
+ * a reference m and the sum l of its weights; m moves only when a score exceeds it by more than 8
+ * (in log2), so that the common tile needs no maximum across lanes, only a vote, and O^T, which
+ * stays in tensor memory, is rarely rescaled. exp2(c S - m) <= 2^8 is exact to its rounding whatever m is.
+ *
+ * Work. Units of one tile of one (request, key-value head, row block) are numbered through the batch; CTA i
+ * of P takes the units [W i / P, W (i+1) / P): every CTA the same number of tiles whatever the lengths,
+ * without the host knowing them. A CTA that holds only part of an item writes (m, l, O) to its
+ * workspace slot, and specdec_paged_join_kernel joins the parts in the order of the CTAs.
+ *
+ * Warps: 4 per column group for the softmax (one lane quarter of tensor memory each), 4 that convert an
+ * e4m3 cache (keys to f16 in tensor memory, values to f16 tiles in shared memory; both exact), one
+ * that feeds TMA, one that issues the products, two that fetch Q.
+ *
+ * Bound by HBM: every visible key and value is read once per row block.
  */
+#include <cuda.h>
+
+#include <cfloat>
 #include <cmath>
+#include <cstddef>
+#include <type_traits>
 
 #include "specdec_rows.cuh"
+#include "specdec_tensor.cuh"
 
 namespace {
 
 using namespace specdec;
 
-constexpr int kThreads = 128;
+constexpr int kTile = 128;                               // tokens
+constexpr float kLazy = 8.f;                             // how far (log2) a score may pass the reference
+constexpr unsigned long long kWaitNs = 2000000000ull;    // a wait's default limit
+constexpr unsigned long long kDrainNs = 1000000000ull;   // more time for copies in flight before a CTA leaves
+constexpr int kSmemBytes = 227 * 1024;
+constexpr int kJoinRows = 4;
 
 struct Args {
     const void* q;
     void* out;
     float* lse;
-    int32_t rows, num_heads;
+    int32_t num_heads, group;
     int64_t q_row, q_head, out_row, out_head;
     specdec_kv_cache_t cache;
     const int32_t* block_table;
@@ -28,78 +56,986 @@ struct Args {
     int32_t max_blocks;
     const int32_t *cached, *cu;
     int32_t B, max_k, window;
-    float scale;
+    float scale_log2;                                    // scale * log2(e)
     uint32_t* status;
+    int4* split;                                         // [P]: the item that CTA i leaves to the next ones
+    float* parts;                                        // [2 P] slots of N (D + 2) floats
+    unsigned long long wait_ns;
 };
 
-template <typename T, typename C>
-__global__ void __launch_bounds__(kThreads) specdec_paged_attention_kernel(const Args a)
-{
-    __shared__ float sm[4], sl[4], so[4][128];
-    const specdec_kv_cache_t& c = a.cache;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = c.head_dim;
-    const int64_t t = blockIdx.x;
-    const int hq = blockIdx.y, h = hq / (a.num_heads / c.num_kv_heads);
-    if (a.status && hq == 0)
-        for (int64_t b = t * kThreads + tid; b < a.B; b += (int64_t)gridDim.x * kThreads)
-            if (!offsets_ok(a.cu, a.B, (int)b)) atomicOr(a.status + b, SPECDEC_ST_BAD_OFFSETS);
-    const int b = owner_of<kThreads>(a.B, t, [&](int i) { return (int64_t)__ldg(a.cu + i) + i; });
-    if (b < 0 || !offsets_ok(a.cu, a.B, b)) return;
-    const int64_t j = t - a.cu[b] - b, k = a.cu[b + 1] - a.cu[b];
-    if (j > k) return;
-    const int64_t cached = a.cached[b], last = cached + j;
-    uint32_t fault = 0;
-    if (k > a.max_k) fault = SPECDEC_ST_K_TOO_LARGE;
-    else if (cached < 0 || cached + k + 1 > (int64_t)a.max_blocks * c.page_size) fault = SPECDEC_ST_BAD_LENGTH;
-    if (fault && a.status && tid == 0) atomicOr(a.status + b, fault);
+// ---------------------------------------------------------------- the batch's units
 
-    float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-    const T* qp = static_cast<const T*>(a.q) + t * a.q_row + hq * a.q_head;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) q[e] = lane + 32 * e < D ? to_float<T>(qp[lane + 32 * e]) : 0.f;
-    const int64_t begin = fault ? 1 : (a.window > 0 ? max((int64_t)0, last - a.window + 1) : 0), end = fault ? 0 : last + 1;
-    for (int64_t i = begin + warp; i < end; i += 4) {
-        const int page = a.block_table[b * a.block_stride + i / c.page_size];
-        const bool good = page >= 0 && page < c.num_pages;
-        if (!good && a.status && lane == 0) atomicOr(a.status + b, SPECDEC_ST_BAD_PAGE);
-        const int slot = (int)(i % c.page_size);
-        const int64_t at = (good ? page : 0) * c.page_stride + h * c.head_stride + slot * c.slot_stride;
-        const int64_t ex = ((int64_t)(good ? page : 0) * c.num_kv_heads + h) * c.page_size + slot;
-        float ks = 1.f, vs = 1.f;
-        if constexpr (sizeof(C) == 1) { ks = exp_value(c.k_exp[ex]); vs = exp_value(c.v_exp[ex]); }
-        float s = 0.f, v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bool in = good && lane + 32 * e < D;
-            s += in ? q[e] * to_float<C>(static_cast<const C*>(c.k)[at + lane + 32 * e]) : 0.f;
-            v[e] = in ? to_float<C>(static_cast<const C*>(c.v)[at + lane + 32 * e]) * vs : 0.f;
+struct Request {
+    int64_t cached;
+    int32_t row0, rows, blocks;                          // first row, rows a key-value head, row blocks
+    int32_t first_tile, tiles;
+    uint32_t fault;
+    __device__ __forceinline__ int64_t units(int heads) const { return (int64_t)heads * blocks * tiles; }
+};
+
+template <int N> __device__ __forceinline__ Request request_of(const Args& a, int b)
+{
+    Request r = {0, 0, 0, 0, 0, 0, 0};
+    if (!offsets_ok(a.cu, a.B, b)) {
+        r.fault = SPECDEC_ST_BAD_OFFSETS;
+        return r;
+    }
+    const int32_t c0 = __ldg(a.cu + b), k = __ldg(a.cu + b + 1) - c0;
+    r.row0 = c0 + b;
+    r.cached = __ldg(a.cached + b);
+    if (k > a.max_k) {
+        r.fault = SPECDEC_ST_K_TOO_LARGE;
+    } else if (r.cached < 0 || r.cached + k + 1 > (int64_t)a.max_blocks * a.cache.page_size) {
+        r.fault = SPECDEC_ST_BAD_LENGTH;
+    } else {
+        r.rows = (k + 1) * a.group;
+        r.blocks = (r.rows + N - 1) / N;
+        r.first_tile = a.window > 0 && r.cached >= a.window ? (int32_t)((r.cached - a.window + 1) / kTile) : 0;
+        r.tiles = (int32_t)((r.cached + k + kTile) / kTile) - r.first_tile;
+    }
+    return r;
+}
+
+struct Item {
+    int b, h, block, t0, t1;                             // tiles [t0, t1) of the item, numbered in the request
+    bool begin, end;                                     // whether they hold its first and its last
+    int64_t first_unit, last_unit;                       // of the whole item
+};
+
+// Walks a CTA's units item by item; every role walks the same way.
+template <int N> struct Walker {
+    const Args& a;
+    int64_t u, u_end, base;
+    int b;
+    Request r;
+    __device__ __forceinline__ Walker(const Args& a_, int64_t begin, int64_t end, int b0, int64_t base0)
+        : a(a_), u(begin), u_end(end), base(base0), b(b0)
+    {
+        if (u < u_end) r = request_of<N>(a, b);
+    }
+    __device__ __forceinline__ bool next(Item& w)
+    {
+        if (u >= u_end) return false;
+        const int H = a.cache.num_kv_heads;
+        while (u >= base + r.units(H)) {
+            base += r.units(H);
+            r = request_of<N>(a, ++b);
         }
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= ks * a.scale;
-        const float mn = fmaxf(m, s);
-        if (mn == -INFINITY && s == s) continue;                   // nothing seen yet (a NaN score stays)
-        const float f = expf(m - mn), p = expf(s - mn);
-        m = mn;
-        l = l * f + p;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = o[e] * f + p * v[e];
+        const int64_t local = u - base, item = local / r.tiles;
+        const int tile = (int)(local - item * r.tiles);
+        const int n = (int)min((int64_t)(r.tiles - tile), u_end - u);
+        w.b = b;
+        w.h = (int)(item / r.blocks);
+        w.block = (int)(item - (int64_t)w.h * r.blocks);
+        w.t0 = r.first_tile + tile;
+        w.t1 = w.t0 + n;
+        w.begin = tile == 0;
+        w.end = tile + n == r.tiles;
+        w.first_unit = base + item * r.tiles;
+        w.last_unit = w.first_unit + r.tiles - 1;
+        u += n;
+        return true;
     }
-    if (lane == 0) { sm[warp] = m; sl[warp] = l; }
+};
+
+// The first unit of CTA i. With fewer units than CTAs the first ones take one each, so that no CTA between two
+// parts of an item is without a part.
+__device__ __forceinline__ int64_t cta_begin(int64_t units, int i, int P)
+{
+    return units < P ? min(units, (int64_t)i) : units * i / P;
+}
+
+// ---------------------------------------------------------------- shapes
+
+template <typename T_, bool kFp8_, int N_, int DB_> struct Shape {
+    using T = T_;                                        // type of q and out
+    using M = std::conditional_t<kFp8_, __half, T_>;     // type of the products' operands
+    static constexpr bool kFp8 = kFp8_;
+    static constexpr bool kScaleQ = kFp8_ && std::is_same<T_, __nv_bfloat16>::value;
+    static constexpr int N = N_, DB = DB_, DP = 64 * DB_;
+    static constexpr int kGroups = N >= 64 ? 2 : 1, NC = N / kGroups;
+    static constexpr int kQ = N == 128 && DB == 2 ? 1 : 2;               // Q buffers
+    static constexpr int kSoftWarps = 4 * kGroups, kConvWarps = kFp8 ? 4 : 0;
+    static constexpr int kProducer = kSoftWarps + kConvWarps, kMma = kProducer + 1, kLoader = kProducer + 2;
+    static constexpr int kThreads = 32 * (kLoader + 2);
+    static constexpr int kSlotBytes = kTile * DP * (kFp8 ? 1 : 2);
+    static constexpr int kQBytes = N * DP * 2, kPBytes = N * kTile * 2, kV16Bytes = kFp8 ? kTile * DP * 2 : 0;
+    static constexpr int kMiscBytes = 8 * 1024;
+    static constexpr int kRoom = kSmemBytes - 1024 - kMiscBytes - kQ * kQBytes - kPBytes - 2 * kV16Bytes;
+    static constexpr int kSlots = kRoom / kSlotBytes > 12 ? 12 : kRoom / kSlotBytes;
+    static constexpr int kTmem = 3 * N + (kFp8 ? DP : 0);                // O, two S, two f16 key tiles
+    static constexpr int kTmemColumns = kTmem <= 64 ? 64 : kTmem <= 128 ? 128 : kTmem <= 256 ? 256 : 512;
+    static constexpr int kSlotFloats = N * (DP + 2);
+    static_assert(kSlots >= 3 && kTmem <= 512, "shape does not fit the SM");
+};
+
+template <typename S> struct Misc {
+    uint64_t full[S::kSlots], empty[S::kSlots];
+    uint64_t s_full[2], pv_done[2], p_full, o_free, q_full[2], q_empty[2], k16_full[2], v16_full[2];
+    int64_t begin, end, base, units;
+    int64_t warp_units[32];
+    int first_b;
+    int expired;
+    uint32_t tmem;
+    uint32_t poison[2][4];                               // tokens of a tile whose values are taken one by one
+    alignas(16) float red[4][S::N];                                  // a column's value in each warp of its group
+    alignas(16) float fac[S::N];
+    int red_e[4 * S::kGroups];
+    alignas(16) int32_t last[2][S::N];                               // last token that a column sees (-1: no column)
+    alignas(16) float qscale[2][S::kScaleQ ? S::N : 4];
+    alignas(16) uint8_t exps[S::kSlots][S::kFp8 ? kTile : 16];
+};
+
+// ---------------------------------------------------------------- the kernel
+
+template <typename S>
+__global__ void __launch_bounds__(S::kThreads, 1)
+specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
+{
+    using T = typename S::T;
+    using M = typename S::M;
+    constexpr int N = S::N, NC = S::NC, DP = S::DP;
+    extern __shared__ unsigned char raw[];
+    unsigned char* const ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    unsigned char* const v16 = ring + S::kSlots * S::kSlotBytes;
+    unsigned char* const qbuf = v16 + 2 * S::kV16Bytes;
+    unsigned char* const pbuf = qbuf + S::kQ * S::kQBytes;
+    Misc<S>& ms = *reinterpret_cast<Misc<S>*>(pbuf + S::kPBytes);
+    static_assert(sizeof(Misc<S>) <= S::kMiscBytes, "misc");
+    static_assert(offsetof(Misc<S>, last) % 16 == 0 && offsetof(Misc<S>, qscale) % 16 == 0 && offsetof(Misc<S>, exps) % 16 == 0 &&
+                  offsetof(Misc<S>, fac) % 16 == 0 && sizeof(Misc<S>) % 16 == 0, "8- and 16-byte accesses");
+    static_assert(S::kSlotBytes % 1024 == 0 && S::kQBytes % 1024 == 0 && S::kPBytes % 1024 == 0, "swizzled tiles");
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, P = gridDim.x;
+    const specdec_kv_cache_t& c = a.cache;
+    const int H = c.num_kv_heads;
+    volatile int* const expired = &ms.expired;
+    auto bar = [](uint64_t& b) { return smem_u32(&b); };
+    auto wait = [&](uint64_t& b, uint32_t parity) { return bar_wait(smem_u32(&b), parity & 1u, a.wait_ns, expired); };
+
+    // ---- set-up: barriers, tensor memory, the CTA's units
+    if (tid == 0) {
+        for (int s = 0; s < S::kSlots; ++s) {
+            bar_init(bar(ms.full[s]), 1);
+            bar_init(bar(ms.empty[s]), S::kFp8 ? 4 + S::kSoftWarps : 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(bar(ms.s_full[i]), 1);
+            bar_init(bar(ms.pv_done[i]), 1);
+            bar_init(bar(ms.q_full[i]), 2);
+            bar_init(bar(ms.q_empty[i]), 1 + S::kSoftWarps);
+            bar_init(bar(ms.k16_full[i]), 4);
+            bar_init(bar(ms.v16_full[i]), 4);
+        }
+        bar_init(bar(ms.p_full), S::kSoftWarps);
+        bar_init(bar(ms.o_free), S::kSoftWarps);
+        ms.expired = 0;
+        for (int i = 0; i < 8; ++i) ms.poison[i >> 2][i & 3] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == S::kMma) tmem_alloc(smem_u32(&ms.tmem), S::kTmemColumns);
+    {
+        // every thread sums the units of consecutive requests, a scan over the threads places them
+        const int per = (a.B + S::kThreads - 1) / S::kThreads, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+        int64_t mine = 0;
+        for (int b = b0; b < b1; ++b) mine += request_of<N>(a, b).units(H);
+        int64_t upto = mine;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) so[warp][lane + 32 * e] = o[e];
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += x;
+        }
+        if (lane == 31) ms.warp_units[warp] = upto;
+        __syncthreads();
+        int64_t before = upto - mine, units = 0;
+        for (int w = 0; w < S::kThreads / 32; ++w) {
+            if (w < warp) before += ms.warp_units[w];
+            units += ms.warp_units[w];
+        }
+        const int64_t begin = cta_begin(units, blockIdx.x, P);
+        if (mine > 0 && begin >= before && begin < before + mine) {
+            int b = b0;
+            int64_t base = before;
+            while (true) {
+                const int64_t n = request_of<N>(a, b).units(H);
+                if (begin < base + n) break;
+                base += n;
+                ++b;
+            }
+            ms.first_b = b;
+            ms.base = base;
+        }
+        if (tid == 0) {
+            ms.begin = begin;
+            ms.end = cta_begin(units, blockIdx.x + 1, P);
+            ms.units = units;
+        }
+    }
+    tmem_before();
     __syncthreads();
-    const float mm = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    float ll = 0.f, oo = 0.f;
+    tmem_after();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t tmem = ms.tmem;
+    const uint32_t t_o = tmem, t_s = tmem + N, t_k = tmem + 3 * N;
+    Walker<N> walk(a, ms.begin, ms.end, ms.first_b, ms.base);
+    Item w;
+    if (tid == 0) a.split[blockIdx.x] = make_int4(-1, 0, 0, 0);         // this thread may fill it in below
+
+    if (warp == S::kProducer) {
+        // ================================================================ keys and values into the ring
+        const int ps = c.page_size, rows = min(ps, kTile), pages = kTile / rows;
+        uint32_t n = 0;                                  // slots filled so far
+        while (walk.next(w)) {
+            const int64_t len = walk.r.cached + (walk.r.rows / a.group);
+            const int32_t* const table = a.block_table + w.b * a.block_stride;
+            auto page_of = [&](int t) -> int {           // this lane's page of tile t (-1: none)
+                const int64_t token = (int64_t)t * kTile + lane * rows;
+                return lane < pages && token < len ? __ldg(table + token / ps) : -1;
+            };
+            auto used_of = [&](int t) {
+                const int64_t left = len - (int64_t)t * kTile;
+                return (int)min((int64_t)pages, (left + rows - 1) / rows);
+            };
+            int page = page_of(w.t0);
+            for (int t = w.t0; t < w.t1; ++t) {
+                const int next_page = t + 1 < w.t1 ? page_of(t + 1) : 0;
+                const int used = used_of(t), slot0 = ps > kTile ? (int)((int64_t)t * kTile % ps) : 0;
+                const bool bad = lane < used && (page < 0 || page >= c.num_pages);
+                if (bad && a.status) atomicOr(a.status + w.b, SPECDEC_ST_BAD_PAGE);
+                const int from = bad ? c.num_pages : page;      // past the end: the copy reads zeros
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const float f = sm[w] == -INFINITY ? 0.f : expf(sm[w] - mm);
-        ll += sl[w] * f;
-        oo += so[w][tid] * f;
+                for (int v = 0; v < 2; ++v, ++n) {
+                    const uint32_t s = n % S::kSlots;
+                    if (n >= (uint32_t)S::kSlots) wait(ms.empty[s], n / S::kSlots - 1);
+                    if (*expired) continue;
+                    const uint32_t fb = bar(ms.full[s]), dst = smem_u32(ring) + s * S::kSlotBytes;
+                    if (lane < used && S::kFp8 && bad) {
+                        for (int i = 0; i < rows; ++i) ms.exps[s][lane * rows + i] = 127;
+                        fence_async();
+                    }
+                    const uint32_t fine = __popc(__ballot_sync(0xffffffffu, lane < used && !bad));
+                    if (lane == 0) bar_expect(fb, used * rows * DP * (S::kFp8 ? 1 : 2) + (S::kFp8 ? fine * rows : 0));
+                    __syncwarp();
+                    if (lane < used) {
+                        const CUtensorMap* map = v ? &vmap : &kmap;
+                        if constexpr (S::kFp8) {
+                            tma_load_4d(dst + lane * rows * DP, map, fb, 0, slot0, w.h, from);
+                            if (!bad)
+                                bulk_load(smem_u32(&ms.exps[s][lane * rows]),
+                                          (v ? c.v_exp : c.k_exp) + ((int64_t)page * H + w.h) * ps + slot0, rows, fb);
+                        } else {
+#pragma unroll
+                            for (int d = 0; d < S::DB; ++d)
+                                tma_load_4d(dst + d * (kTile * 128) + lane * rows * 128, map, fb, d * 64, slot0, w.h, from);
+                        }
+                    }
+                }
+                page = next_page;
+            }
+        }
+        // nothing may still be on its way into shared memory when the CTA leaves
+        __syncwarp();
+        if (*expired && lane == 0) {
+            const unsigned long long t0 = time_ns();
+            for (uint32_t i = n > (uint32_t)S::kSlots ? n - S::kSlots : 0; i < n; ++i)
+                while (!bar_test(bar(ms.full[i % S::kSlots]), (i / S::kSlots) & 1u) && time_ns() - t0 < kDrainNs) {}
+        }
+    } else if (warp == S::kMma) {
+        // ================================================================ products
+        if (lane == 0) {
+            constexpr int kBf16 = std::is_same<M, __nv_bfloat16>::value;
+            constexpr uint32_t ds = product(kBf16, 0, 128, N), dv = product(kBf16, 1, 128, N);
+            uint32_t n = 0;                              // tiles of the CTA
+            uint32_t q = 0;                              // items
+            const uint32_t ring0 = smem_u32(ring), p0 = smem_u32(pbuf), q0 = smem_u32(qbuf), v0 = smem_u32(v16);
+            // S of tile i (the CTA's numbering) with item number qi
+            auto scores = [&](uint32_t i, uint32_t qi, bool first, bool last) {
+                const uint32_t qb = qi % S::kQ;
+                bool ok = true;
+                if (first) ok = wait(ms.q_full[qb], qi / S::kQ);
+                const uint32_t slot = 2 * i % S::kSlots;
+                if constexpr (S::kFp8) ok = wait(ms.k16_full[i & 1], i >> 1) && ok;
+                else ok = wait(ms.full[slot], 2 * i / S::kSlots) && ok;
+                if (!ok) return;
+                tmem_after();
+                const uint32_t d = t_s + (i & 1) * N;
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    const uint64_t bq = operand(q0 + qb * S::kQBytes + k * 256, 128, DP * 16, kNoSwizzle);
+                    if constexpr (S::kFp8)
+                        mma_ts(d, t_k + (i & 1) * (DP / 2) + k * 8, bq, ds, k > 0);
+                    else
+                        mma_ss(d, operand(ring0 + slot * S::kSlotBytes + (k / 4) * (kTile * 128) + (k % 4) * 32, 0, 1024, kSwizzle128), bq, ds, k > 0);
+                }
+                mma_commit(bar(ms.s_full[i & 1]));
+                if constexpr (!S::kFp8) mma_commit(bar(ms.empty[slot]));
+                if (last) mma_commit(bar(ms.q_empty[qb]));
+            };
+            bool more = walk.next(w);
+            if (more) scores(0, 0, true, w.t1 - w.t0 == 1);
+            while (more) {
+                const int tiles = w.t1 - w.t0;
+                Item after;
+                bool follows = false;
+                auto start_next = [&]() {
+                    follows = walk.next(after);
+                    if (follows) scores(n + 1, q + 1, true, after.t1 - after.t0 == 1);
+                };
+                for (int t = 0; t < tiles; ++t, ++n) {
+                    // the next scores before this tile's values; with one Q buffer the next item's wait for its turn
+                    if (t + 1 < tiles) scores(n + 1, q, false, t + 2 == tiles);
+                    else if (S::kQ == 2) start_next();
+                    bool ok = wait(ms.p_full, n);
+                    const uint32_t slot = (2 * n + 1) % S::kSlots;
+                    if constexpr (S::kFp8) ok = wait(ms.v16_full[n & 1], n >> 1) && ok;
+                    else ok = wait(ms.full[slot], (2 * n + 1) / S::kSlots) && ok;
+                    if (t == 0 && q > 0) ok = wait(ms.o_free, q - 1) && ok;
+                    if (ok) {
+                        tmem_after();
+                        const uint32_t va = S::kFp8 ? v0 + (n & 1) * S::kV16Bytes : ring0 + slot * S::kSlotBytes;
+                        // one block of 64 elements (DB = 1): the rows 64 .. 127 read the block again and are not used
+                        constexpr uint32_t lead = S::DB == 2 ? kTile * 128 : 0;
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)
+                            mma_ss(t_o, operand(va + k * 2048, lead, 1024, kSwizzle128), operand(p0 + k * 256, 128, 2048, kNoSwizzle), dv, t > 0 || k > 0);
+                        mma_commit(bar(ms.pv_done[n & 1]));
+                        if constexpr (!S::kFp8) mma_commit(bar(ms.empty[slot]));
+                    }
+                    if (t + 1 == tiles && S::kQ == 1) start_next();
+                }
+                more = follows;
+                w = after;
+                ++q;
+            }
+        }
+        __syncwarp();
+    } else if (warp >= S::kLoader) {
+        // ================================================================ Q, its scales and its columns' last tokens
+        const int lt = tid - 32 * S::kLoader;            // 0 .. 63
+        uint32_t q = 0;
+        while (walk.next(w)) {
+            const uint32_t qb = q % S::kQ;
+            if (q >= (uint32_t)S::kQ) wait(ms.q_empty[qb], q / S::kQ - 1);
+            const int rows = walk.r.rows, row_first = w.block * N;
+            auto source = [&](int n) {
+                const int r = row_first + n, j = r / a.group, g = r - j * a.group;
+                return static_cast<const T*>(a.q) + (int64_t)(walk.r.row0 + j) * a.q_row + (int64_t)(w.h * a.group + g) * a.q_head;
+            };
+            for (int n = lt; n < N; n += 64) {
+                const bool real = row_first + n < rows;
+                ms.last[qb][n] = real ? (int32_t)(walk.r.cached + (row_first + n) / a.group) : -1;
+                if constexpr (S::kScaleQ) {
+                    // a power of two brings the row's largest element to [2^13, 2^14): bf16's eight bits fit f16's
+                    // eleven exactly, but for elements under 2^-28 of the largest
+                    float top = 0.f;
+                    if (real) {
+                        const T* src = source(n);
+                        for (int d = 0; d < c.head_dim; d += 8) {
+                            float x[8];
+                            load_n<T, 8>(src + d, x);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (isfinite(x[i])) top = fmaxf(top, fabsf(x[i]));
+                        }
+                    }
+                    int e = 14;
+                    if (top > 0.f) e = max((int)((__float_as_uint(top) >> 23) & 255u) - 126, -100);
+                    ms.qscale[qb][n] = __uint_as_float((uint32_t)(127 + e - 14) << 23);
+                }
+            }
+            barrier_sync(1 + S::kGroups, 64);
+            unsigned char* const dst = qbuf + qb * S::kQBytes;
+            for (int i = lt; i < N * (DP / 8); i += 64) {
+                const int n = (i & 7) + 8 * (i / (DP)), ch = (i >> 3) % (DP / 8);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (row_first + n < rows && ch * 8 < c.head_dim) {
+                    v = *reinterpret_cast<const uint4*>(source(n) + ch * 8);
+                    if constexpr (S::kScaleQ) {
+                        const float inv = __uint_as_float((254u << 23) - __float_as_uint(ms.qscale[qb][n]));
+                        const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&v);
+                        uint4 o;
+                        __half2* y = reinterpret_cast<__half2*>(&o);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 f = __bfloat1622float2(x[k]);
+                            y[k] = __floats2half2_rn(f.x * inv, f.y * inv);
+                        }
+                        v = o;
+                    }
+                }
+                *reinterpret_cast<uint4*>(dst + ((n >> 3) * (DP / 8) + ch) * 128 + (n & 7) * 16) = v;
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(ms.q_full[qb]));
+            barrier_sync(1 + S::kGroups, 64);            // qscale is read before the next item writes it
+            ++q;
+        }
+    } else if (S::kFp8 && warp >= S::kSoftWarps) {
+        // ================================================================ e4m3 -> f16 (exact)
+        const int row = tid - 32 * S::kSoftWarps;        // token of the tile, and lane of tensor memory
+        uint32_t n = 0;
+        const uint32_t quarter = (uint32_t)(row & ~31) << 16;
+        auto chunk = [&](const unsigned char* slot, int ch) {            // 16 codes of this token
+            const int at = DP == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3);
+            return *reinterpret_cast<const uint4*>(slot + row * DP + at * 16);
+        };
+        auto widen = [](uint32_t codes, uint32_t* out) { // four codes to two f16 pairs
+            asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+                : "=r"(out[0]), "=r"(out[1]) : "r"(codes));
+        };
+        while (walk.next(w)) {
+            for (int t = w.t0; t < w.t1; ++t, ++n) {
+                const uint32_t ks = 2 * n % S::kSlots, vs = (2 * n + 1) % S::kSlots;
+                // keys: a token's elements along its lane of tensor memory, two to a column
+                wait(ms.full[ks], 2 * n / S::kSlots);
+                if (n >= 2) wait(ms.s_full[n & 1], (n >> 1) - 1);        // S of tile n - 2 has read the buffer
+                tmem_after();
+#pragma unroll
+                for (int g = 0; g < DP / 32; ++g) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 x = chunk(ring + ks * S::kSlotBytes, 2 * g + h);
+                        widen(x.x, r + 8 * h);
+                        widen(x.y, r + 8 * h + 2);
+                        widen(x.z, r + 8 * h + 4);
+                        widen(x.w, r + 8 * h + 6);
+                    }
+                    tmem_st_32x16(t_k + quarter + (n & 1) * (DP / 2) + g * 16, r);
+                }
+                tmem_wait_st();
+                tmem_before();
+                __syncwarp();
+                if (lane == 0) {
+                    bar_arrive(bar(ms.k16_full[n & 1]));
+                    bar_arrive(bar(ms.empty[ks]));
+                }
+                // values: the same layout as a 16-bit tile of TMA's
+                wait(ms.full[vs], (2 * n + 1) / S::kSlots);
+                if (n >= 2) wait(ms.pv_done[n & 1], (n >> 1) - 1);
+                unsigned char* const dst = v16 + (n & 1) * S::kV16Bytes + row * 128;
+#pragma unroll
+                for (int ch = 0; ch < DP / 16; ++ch) {
+                    const uint4 x = chunk(ring + vs * S::kSlotBytes, ch);
+                    uint32_t r[8];
+                    widen(x.x, r);
+                    widen(x.y, r + 2);
+                    widen(x.z, r + 4);
+                    widen(x.w, r + 6);
+                    unsigned char* const d = dst + (ch / 4) * (kTile * 128);
+                    *reinterpret_cast<uint4*>(d + ((2 * (ch % 4)) ^ (row & 7)) * 16) = make_uint4(r[0], r[1], r[2], r[3]);
+                    *reinterpret_cast<uint4*>(d + ((2 * (ch % 4) + 1) ^ (row & 7)) * 16) = make_uint4(r[4], r[5], r[6], r[7]);
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) {
+                    bar_arrive(bar(ms.v16_full[n & 1]));
+                    bar_arrive(bar(ms.empty[vs]));
+                }
+            }
+        }
+    } else {
+        // ================================================================ softmax
+        const int grp = warp >> 2, wq = warp & 3, gt = tid & 127;        // column group, lane quarter, thread of the group
+        const int col0 = grp * NC, id = 1 + grp;
+        const int tq = lane >> 2, cq = 2 * (lane & 3);                   // token and column within an 8 x 8 matrix
+        const uint32_t quarter = (uint32_t)wq << 21;                     // lane 32 wq
+        uint32_t n = 0, q = 0;
+        while (walk.next(w)) {
+            const uint32_t qb = q % S::kQ;
+            wait(ms.q_full[qb], q / S::kQ);
+            const int rows = walk.r.rows, row_first = w.block * N;
+            const int row_last = min(row_first + N, rows) - 1;
+            const int64_t seen_all = walk.r.cached + row_first / a.group, seen_any = walk.r.cached + row_last / a.group;
+            const int64_t from_all = a.window > 0 ? seen_any - a.window + 1 : 0, from_any = a.window > 0 ? seen_all - a.window + 1 : 0;
+            float m[NC / 4], l[NC / 4];
+#pragma unroll
+            for (int i = 0; i < NC / 4; ++i) m[i] = -FLT_MAX, l[i] = 0.f;
+            int E = -100000;                                             // e4m3: exponent that the values' scales are taken by
+            for (int t = w.t0; t < w.t1; ++t, ++n) {
+                const int64_t token0 = (int64_t)t * kTile;
+                const bool masked = token0 + kTile - 1 > seen_all || token0 < from_all;
+                const uint32_t ks = 2 * n % S::kSlots, vs = (2 * n + 1) % S::kSlots;
+                float kscale[4];
+                int ve[4];
+                if constexpr (S::kFp8) {
+                    wait(ms.full[ks], 2 * n / S::kSlots);
+                    wait(ms.full[vs], (2 * n + 1) / S::kSlots);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = 32 * wq + 8 * i + tq;
+                        kscale[i] = exp_value(ms.exps[ks][tok]) * a.scale_log2;
+                        ve[i] = (int)ms.exps[vs][tok] - 127;
+                        // a token that no row sees may hold anything
+                        if (masked && (token0 + tok > seen_any || token0 + tok < from_any)) ve[i] = -100000;
+                    }
+                    __syncwarp();
+                    if (lane == 0) {                                     // the scales are read: the slots may go
+                        bar_arrive(bar(ms.empty[ks]));
+                        bar_arrive(bar(ms.empty[vs]));
+                    }
+                }
+                wait(ms.s_full[n & 1], n >> 1);
+                tmem_after();
+                const uint32_t s_at = t_s + (n & 1) * N + quarter + col0;
+                float x[2][NC / 8][4];
+                auto fetch = [&]() {
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                        for (int r = 0; r < NC / 8; r += 2)
+                            tmem_ld_16x16(s_at + ((uint32_t)hf << 20) + r * 8, x[hf][r], x[hf][r + 1]);
+                    tmem_wait_ld();
+                };
+                // score (log2) of element (hf, r, e), before the reference is taken off
+                auto each = [&](auto f) {
+#pragma unroll
+                    for (int r = 0; r < NC / 8; ++r) {
+                        float2 qs = make_float2(1.f, 1.f);
+                        if constexpr (S::kScaleQ) qs = *reinterpret_cast<const float2*>(&ms.qscale[qb][col0 + 8 * r + cq]);
+                        int2 last = make_int2(0, 0);
+                        if (masked) last = *reinterpret_cast<const int2*>(&ms.last[qb][col0 + 8 * r + cq]);
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int i = 2 * hf + (e >> 1);
+                                float scale = a.scale_log2;
+                                if constexpr (S::kFp8) scale = kscale[i];
+                                if constexpr (S::kScaleQ) scale *= (e & 1) ? qs.y : qs.x;
+                                bool seen = true;
+                                if (masked) {
+                                    const int64_t tok = token0 + 32 * wq + 8 * i + tq;
+                                    const int32_t lt = (e & 1) ? last.y : last.x;
+                                    seen = tok <= lt && (a.window == 0 || tok > (int64_t)lt - a.window);
+                                }
+                                f(x[hf][r][e], scale, seen, 2 * r + (e & 1));
+                            }
+                    }
+                };
+                fetch();
+                float over = -INFINITY;
+                each([&](float& z, float scale, bool seen, int ci) {
+                    z = seen ? fmaf(z, scale, -m[ci]) : -INFINITY;
+                    over = fmaxf(over, z);
+                });
+                bool move = over > kLazy;
+                if constexpr (S::kFp8) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) move = move || (ve[i] > E + 4 && ve[i] < 128);
+                }
+                if (barrier_or(id, 128, move)) {
+                    // the references move to the columns' maxima so far (and E to the values' largest exponent)
+                    fetch();
+                    float top[NC / 4];
+#pragma unroll
+                    for (int i = 0; i < NC / 4; ++i) top[i] = -INFINITY;
+                    each([&](float& z, float scale, bool seen, int ci) {
+                        z = seen ? z * scale : -INFINITY;
+                        top[ci] = fmaxf(top[ci], z);
+                    });
+#pragma unroll
+                    for (int i = 0; i < NC / 4; ++i) {
+#pragma unroll
+                        for (int off = 4; off <= 16; off <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], off));
+                    }
+                    if (tq == 0) {
+#pragma unroll
+                        for (int i = 0; i < NC / 4; ++i) ms.red[wq][col0 + 8 * (i >> 1) + cq + (i & 1)] = top[i];
+                    }
+                    int e_new = E;
+                    if constexpr (S::kFp8) {
+                        int et = -100000;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) et = ve[i] < 128 ? max(et, ve[i]) : et;
+                        et = __reduce_max_sync(0xffffffffu, et);
+                        if (lane == 0) ms.red_e[4 * grp + wq] = et;
+                    }
+                    barrier_sync(id, 128);
+                    float e_fac = 1.f;
+                    if constexpr (S::kFp8) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) e_new = max(e_new, max(ms.red_e[4 * grp + i], -126));
+                        e_fac = E - e_new < -126 ? 0.f : __uint_as_float((uint32_t)(127 + E - e_new) << 23);
+                        E = e_new;
+                    }
+#pragma unroll
+                    for (int i = 0; i < NC / 4; ++i) {
+                        const int col = col0 + 8 * (i >> 1) + cq + (i & 1);
+                        const float now = fmaxf(fmaxf(fmaxf(ms.red[0][col], ms.red[1][col]), fmaxf(ms.red[2][col], ms.red[3][col])), m[i]);
+                        const float f = exp2_fast(m[i] - now);
+                        l[i] *= f;
+                        m[i] = now;
+                        if (wq == 0 && tq == 0) ms.fac[col] = f * e_fac;
+                    }
+                    each([&](float& z, float, bool, int ci) { z -= m[ci]; });
+                    barrier_sync(id, 128);
+                    if (t > w.t0) {
+                        // O^T: this thread's lane is an element of the head, its columns the group's
+                        wait(ms.pv_done[(n - 1) & 1], (n - 1) >> 1);
+                        tmem_after();
+#pragma unroll
+                        for (int i = 0; i < NC; i += 16) {
+                            float o[16];
+                            uint32_t r[16];
+                            tmem_ld_32x16(t_o + quarter + col0 + i, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(o[k] * ms.fac[col0 + i + k]);
+                            tmem_st_32x16(t_o + quarter + col0 + i, r);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                // weights, their sums, and P^T as the second product takes it: 8 x 8 blocks of 128 bytes
+                if (n > 0 && t > w.t0) wait(ms.pv_done[(n - 1) & 1], (n - 1) >> 1);
+                float vw[4];
+                if constexpr (S::kFp8) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int de = ve[i] - E;
+                        vw[i] = ve[i] >= 128 ? __int_as_float(0x7fffffff) : de < -126 ? 0.f : __uint_as_float((uint32_t)(127 + de) << 23);
+                    }
+                }
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int r = 0; r < NC / 8; r += 2) {
+                        uint32_t packed[4];
+#pragma unroll
+                        for (int rr = 0; rr < 2; ++rr)
+#pragma unroll
+                            for (int s = 0; s < 2; ++s) {
+                                float p0 = exp2_fast(x[hf][r + rr][2 * s]), p1 = exp2_fast(x[hf][r + rr][2 * s + 1]);
+                                l[2 * (r + rr)] += p0;
+                                l[2 * (r + rr) + 1] += p1;
+                                if constexpr (S::kFp8) p0 *= vw[2 * hf + s], p1 *= vw[2 * hf + s];
+                                if constexpr (std::is_same<M, __half>::value) {
+                                    const __half2 h2 = __floats2half2_rn(p0, p1);
+                                    packed[2 * rr + s] = *reinterpret_cast<const uint32_t*>(&h2);
+                                } else {
+                                    const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+                                    packed[2 * rr + s] = *reinterpret_cast<const uint32_t*>(&h2);
+                                }
+                            }
+                        // matrices (r, tokens 0-7), (r, tokens 8-15), (r + 1, ..), (r + 1, ..) of this half
+                        const int mi = lane >> 3, col_group = col0 / 8 + r + (mi >> 1), token_group = 4 * wq + 2 * hf + (mi & 1);
+                        store_matrices_t(smem_u32(pbuf) + (col_group * 16 + token_group) * 128 + (lane & 7) * 16, packed[0], packed[1],
+                                         packed[2], packed[3]);
+                    }
+                bool poisoned = false;
+                uint32_t* const pz = ms.poison[n & 1];
+                if (masked) {
+                    // values of tokens that no row sees become zeros (a weight of zero times NaN is NaN); those that some
+                    // rows see and others do not, and that are not finite, become zeros here and are added by hand below
+                    unsigned char* vt;
+                    if constexpr (S::kFp8) {
+                        wait(ms.v16_full[n & 1], n >> 1);
+                        vt = v16 + (n & 1) * S::kV16Bytes;
+                    } else {
+                        wait(ms.full[vs], (2 * n + 1) / S::kSlots);
+                        vt = ring + vs * S::kSlotBytes;
+                    }
+                    if (grp == 0) {
+                        const int64_t tok = token0 + gt;
+                        const bool none = tok > seen_any || tok < from_any, some = tok > seen_all || tok < from_all;
+                        bool clear = none;
+                        if (!none && some) {
+                            for (int ch = 0; ch < DP / 8 && !clear; ++ch) {
+                                const uint4 v4 = *reinterpret_cast<const uint4*>(vt + (ch / 8) * (kTile * 128) + gt * 128 + (((ch % 8) ^ (gt & 7)) * 16));
+                                const M* e = reinterpret_cast<const M*>(&v4);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) clear = clear || !isfinite(to_float<M>(e[k]));
+                            }
+                            if (clear) atomicOr(&pz[wq], 1u << lane);
+                        }
+                        if (clear)
+                            for (int ch = 0; ch < DP / 8; ++ch)
+                                *reinterpret_cast<uint4*>(vt + (ch / 8) * (kTile * 128) + gt * 128 + ch % 8 * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    if (S::kGroups == 2) barrier_sync(7, 256); else barrier_sync(id, 128);
+                    poisoned = (pz[0] | pz[1] | pz[2] | pz[3]) != 0;
+                }
+                fence_async();
+                tmem_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(ms.p_full));
+                if (poisoned) {
+                    wait(ms.pv_done[n & 1], n >> 1);
+                    tmem_after();
+                    const int d = gt;                                    // this thread's element of the head
+                    for (int tk = 0; tk < kTile; ++tk) {
+                        if (!(pz[tk >> 5] >> (tk & 31) & 1u)) continue;
+                        const int64_t tok = token0 + tk;
+                        const int page = __ldg(a.block_table + w.b * a.block_stride + tok / c.page_size);
+                        float v = 0.f;
+                        if (d < c.head_dim && page >= 0 && page < c.num_pages) {
+                            const int64_t at = page * c.page_stride + w.h * c.head_stride + tok % c.page_size * c.slot_stride + d;
+                            if constexpr (S::kFp8) v = to_float<__nv_fp8_e4m3>(static_cast<const __nv_fp8_e4m3*>(c.v)[at]);
+                            else v = to_float<M>(static_cast<const M*>(c.v)[at]);
+                        }
+                        for (int i = 0; i < NC; i += 16) {
+                            float o[16];
+                            uint32_t r[16];
+                            tmem_ld_32x16(t_o + quarter + col0 + i, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const int col = col0 + i + k, lt = ms.last[qb][col];
+                                const bool seen = tok <= lt && (a.window == 0 || tok > (int64_t)lt - a.window);
+                                const float p = to_float<M>(*reinterpret_cast<const M*>(pbuf + ((col >> 3) * 16 + (tk >> 3)) * 128 + (col & 7) * 16 + (tk & 7) * 2));
+                                r[k] = __float_as_uint(seen && p != 0.f ? fmaf(p, v, o[k]) : o[k]);
+                            }
+                            tmem_st_32x16(t_o + quarter + col0 + i, r);
+                            tmem_wait_st();
+                        }
+                    }
+                    if (S::kGroups == 2) barrier_sync(7, 256); else barrier_sync(id, 128);
+                    if (tid < 4) pz[tid] = 0;
+                    if (S::kGroups == 2) barrier_sync(7, 256); else barrier_sync(id, 128);
+                    tmem_before();
+                }
+            }
+            // ---- the item's (part of) result
+            const uint32_t lastn = n - 1;
+#pragma unroll
+            for (int i = 0; i < NC / 4; ++i) {
+#pragma unroll
+                for (int off = 4; off <= 16; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+            }
+            if (tq == 0) {
+#pragma unroll
+                for (int i = 0; i < NC / 4; ++i) ms.red[wq][col0 + 8 * (i >> 1) + cq + (i & 1)] = l[i];
+            }
+            const bool whole = w.begin && w.end;
+            float* const part = a.parts + (int64_t)(2 * blockIdx.x + (w.begin ? 1 : 0)) * S::kSlotFloats;
+            barrier_sync(id, 128);
+            if (wq == 0 && tq == 0) {
+#pragma unroll
+                for (int i = 0; i < NC / 4; ++i) {
+                    const int col = col0 + 8 * (i >> 1) + cq + (i & 1);
+                    const float sum = ms.red[0][col] + ms.red[1][col] + ms.red[2][col] + ms.red[3][col];
+                    const bool any = !(sum == 0.f);                      // (a NaN sum is one)
+                    // the join's factors are fp32 too: 2^E goes into O here
+                    float f = any && whole ? 1.f / sum : 1.f;
+                    if (S::kFp8 && E >= -126) f *= __uint_as_float((uint32_t)(127 + E) << 23);
+                    if (!any) f = 0.f;
+                    ms.fac[col] = f;
+                    if (whole) {
+                        const int r = row_first + col;
+                        if (a.lse && r < rows) {
+                            const int j = r / a.group, g = r - j * a.group;
+                            a.lse[(int64_t)(walk.r.row0 + j) * a.num_heads + w.h * a.group + g] = any ? (m[i] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+                        }
+                    } else {
+                        part[N * DP + col] = m[i];
+                        part[N * DP + N + col] = sum;
+                    }
+                }
+            }
+            wait(ms.pv_done[lastn & 1], lastn >> 1);
+            tmem_after();
+            barrier_sync(id, 128);
+            const int d = gt;
+#pragma unroll 1
+            for (int i = 0; i < NC; i += 16) {
+                float o[16];
+                tmem_ld_32x16(t_o + quarter + col0 + i, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const int col = col0 + i + k, r = row_first + col;
+                    if (r >= rows || d >= c.head_dim) continue;
+                    const float f = ms.fac[col], y = f == 0.f ? 0.f : o[k] * f;
+                    if (whole) {
+                        const int j = r / a.group, g = r - j * a.group;
+                        static_cast<T*>(a.out)[(int64_t)(walk.r.row0 + j) * a.out_row + (int64_t)(w.h * a.group + g) * a.out_head + d] = from_float<T>(y);
+                    } else {
+                        part[col * DP + d] = y;
+                    }
+                }
+            }
+            if (tid == 0 && w.begin && !w.end) {
+                // the CTA of the item's last unit
+                int lastc = ms.units < P ? (int)w.last_unit : (int)(w.last_unit * P / ms.units);
+                while (cta_begin(ms.units, lastc + 1, P) <= w.last_unit) ++lastc;
+                while (cta_begin(ms.units, lastc, P) > w.last_unit) --lastc;
+                a.split[blockIdx.x] = make_int4(w.b, w.h, w.block, lastc);
+            }
+            if (*expired && tid == 0 && a.status) atomicOr(a.status + w.b, SPECDEC_ST_DEVICE_TIMEOUT);
+            tmem_before();
+            __syncwarp();
+            if (lane == 0) {
+                bar_arrive(bar(ms.o_free));
+                bar_arrive(bar(ms.q_empty[qb]));
+            }
+            barrier_sync(id, 128);                                       // red and fac are read
+            ++q;
+        }
+        // requests that the kernel does not take: their bits, and zeros in the rows that are known
+        for (int b = blockIdx.x; b < a.B; b += P) {
+            const Request r = request_of<N>(a, b);
+            if (!r.fault) continue;
+            if (tid == 0 && a.status) atomicOr(a.status + b, r.fault);
+            if (r.fault == SPECDEC_ST_BAD_OFFSETS) continue;
+            const int64_t k1 = (int64_t)a.cu[b + 1] - a.cu[b] + 1;
+            for (int64_t i = tid; i < k1 * a.num_heads; i += 128 * S::kGroups) {
+                const int64_t row = r.row0 + i / a.num_heads, hq = i % a.num_heads;
+                if (a.lse) a.lse[row * a.num_heads + hq] = -INFINITY;
+                T* out = static_cast<T*>(a.out) + row * a.out_row + hq * a.out_head;
+                for (int d = 0; d < c.head_dim; d += 8) *reinterpret_cast<uint4*>(out + d) = make_uint4(0, 0, 0, 0);
+            }
+        }
     }
-    T* out = static_cast<T*>(a.out) + t * a.out_row + hq * a.out_head;
-    if (tid < D) out[tid] = from_float<T>(ll > 0.f || ll != ll ? oo / ll : 0.f);
-    if (a.lse && tid == 0) a.lse[t * a.num_heads + hq] = mm + logf(ll);
+    tmem_before();
+    __syncthreads();
+    tmem_after();
+    if (warp == S::kMma) {
+        if (*expired) {                                  // products issued so far end by themselves: wait for them
+            if (lane == 0) {
+                bar_init(bar(ms.k16_full[0]), 1);
+                asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+                mma_commit(bar(ms.k16_full[0]));
+                const unsigned long long t0 = time_ns();
+                while (!bar_test(bar(ms.k16_full[0]), 0) && time_ns() - t0 < kDrainNs) {}
+            }
+            __syncwarp();
+        }
+        tmem_free(tmem, S::kTmemColumns);
+    }
+}
+
+// Joins the parts of the item that CTA blockIdx.x of the kernel above left to its successors: slot
+// 2 i + 1, then slot 2 j of each CTA j up to the last. One thread an element, kJoinRows rows a CTA.
+template <typename T, int N, int DP>
+__global__ void __launch_bounds__(DP) specdec_paged_join_kernel(const Args a)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 s = a.split[blockIdx.x];
+    if (s.x < 0) return;
+    constexpr int64_t kSlot = N * (DP + 2);
+    const Request r = request_of<N>(a, s.x);
+    const int d = threadIdx.x, i = blockIdx.x;
+    for (int k = 0; k < kJoinRows; ++k) {
+        const int col = blockIdx.y * kJoinRows + k, row = s.z * N + col;
+        if (row >= r.rows) return;
+        auto slot = [&](int j) { return a.parts + (2 * (int64_t)j + (j == i ? 1 : 0)) * kSlot; };
+        float m = -FLT_MAX;
+        for (int j = i; j <= s.w; ++j) m = fmaxf(m, slot(j)[N * DP + col]);
+        float l = 0.f, o = 0.f;
+        for (int j = i; j <= s.w; ++j) {
+            const float* p = slot(j);
+            const float f = exp2_fast(p[N * DP + col] - m);
+            l += p[N * DP + N + col] * f;
+            if (d < a.cache.head_dim) o += p[col * DP + d] * f;
+        }
+        const int j = row / a.group, g = row - j * a.group;
+        const int64_t t = r.row0 + j, hq = s.y * a.group + g;
+        const bool any = !(l == 0.f);
+        if (d < a.cache.head_dim) static_cast<T*>(a.out)[t * a.out_row + hq * a.out_head + d] = from_float<T>(any ? o / l : 0.f);
+        if (d == 0 && a.lse) a.lse[t * a.num_heads + hq] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+int sm_count()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0)
+        return n;
+    (void)cudaGetLastError();
+    return 152;
+}
+
+int row_tile(int32_t max_k, int32_t group)
+{
+    const int64_t rows = (int64_t)(max_k + 1) * group;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+}
+
+size_t split_bytes(int P) { return ((size_t)P * sizeof(int4) + 255) / 256 * 256; }
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+Encode encoder()
+{
+    static const Encode e = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            fn = nullptr;
+        }
+        return reinterpret_cast<Encode>(fn);
+    }();
+    return e;
+}
+
+// [pages, heads, slots, elements] in tiles of one page's slots (at most 128) and 128 bytes (64 for an e4m3 head of up to 64)
+bool tile_map(CUtensorMap* map, const specdec_kv_cache_t& c, void* base)
+{
+    const int es = (int)elem_bytes(c.dtype);
+    const cuuint64_t size[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.num_kv_heads, (cuuint64_t)c.num_pages};
+    auto bytes = [&](int64_t stride, int64_t n) { return (cuuint64_t)(n > 1 ? stride * es : 16); };
+    const cuuint64_t stride[3] = {bytes(c.slot_stride, c.page_size), bytes(c.head_stride, c.num_kv_heads), bytes(c.page_stride, c.num_pages)};
+    const int inner = es == 1 && c.head_dim <= 64 ? 64 : es == 1 ? 128 : 64;
+    const cuuint32_t box[4] = {(cuuint32_t)inner, (cuuint32_t)(c.page_size < kTile ? c.page_size : kTile), 1, 1}, step[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type = es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : c.dtype == SPECDEC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUtensorMapSwizzle swizzle = inner * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    return encoder()(map, type, 4, base, size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename S> specdec_status_t launch(const Args& a, cudaStream_t stream, int P)
+{
+    static_assert(sizeof(CUtensorMap) == 128, "tensor map");
+    CUtensorMap kmap, vmap;
+    if (!encoder()) return SPECDEC_ERR_CUDA;
+    if (!tile_map(&kmap, a.cache, a.cache.k) || !tile_map(&vmap, a.cache, a.cache.v)) return SPECDEC_ERR_INVALID_ARG;
+    constexpr int smem = 1024 + S::kSlots * S::kSlotBytes + 2 * S::kV16Bytes + S::kQ * S::kQBytes + S::kPBytes + S::kMiscBytes;
+    static_assert(smem <= kSmemBytes, "shared memory");
+    auto kernel = specdec_paged_attention_kernel<S>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return SPECDEC_ERR_CUDA;
+    }
+    kernel<<<P, S::kThreads, smem, stream>>>(a, kmap, vmap);
+    if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)P, S::N / kJoinRows);
+    cfg.blockDim = dim3(S::DP);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, specdec_paged_join_kernel<typename S::T, S::N, S::DP>, a) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return SPECDEC_ERR_CUDA;
+    }
+    return SPECDEC_OK;
+}
+
+template <typename T, bool kFp8, int DB> specdec_status_t launch_rows(const Args& a, int N, cudaStream_t s, int P)
+{
+    if (N == 16) return launch<Shape<T, kFp8, 16, DB>>(a, s, P);
+    if (N == 32) return launch<Shape<T, kFp8, 32, DB>>(a, s, P);
+    if (N == 64) return launch<Shape<T, kFp8, 64, DB>>(a, s, P);
+    return launch<Shape<T, kFp8, 128, DB>>(a, s, P);
+}
+
+template <typename T> specdec_status_t launch_type(const Args& a, int N, cudaStream_t s, int P)
+{
+    const bool fp8 = a.cache.dtype == SPECDEC_E4M3, one = a.cache.head_dim <= 64;
+    if (fp8) return one ? launch_rows<T, true, 1>(a, N, s, P) : launch_rows<T, true, 2>(a, N, s, P);
+    return one ? launch_rows<T, false, 1>(a, N, s, P) : launch_rows<T, false, 2>(a, N, s, P);
 }
 
 }  // namespace
@@ -108,7 +1044,8 @@ extern "C" size_t specdec_paged_attention_workspace_size(int32_t B, int32_t max_
                                                          int32_t num_kv_heads, int32_t head_dim)
 {
     if (B <= 0 || max_k < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0) return 0;
-    return 16;
+    const int P = sm_count(), group = (num_heads + num_kv_heads - 1) / num_kv_heads, DP = head_dim <= 64 ? 64 : 128;
+    return split_bytes(P) + (size_t)2 * P * row_tile(max_k, group) * (DP + 2) * sizeof(float);
 }
 
 extern "C" specdec_status_t specdec_paged_attention(
@@ -135,16 +1072,11 @@ extern "C" specdec_status_t specdec_paged_attention(
         !aligned_to(cached_len, 4) || !aligned_to(cu_num_draft, 4) || !aligned_to(lse, 4) || !aligned_to(status, 4) ||
         workspace_bytes < specdec_paged_attention_workspace_size(B, max_k, num_heads, cache->num_kv_heads, cache->head_dim))
         return SPECDEC_ERR_INVALID_ARG;
-    const Args a = {q, out, lse, rows, num_heads, q_row_stride, q_head_stride, out_row_stride, out_head_stride, *cache,
-                    block_table, block_stride, max_blocks, cached_len, cu_num_draft, B, max_k, window, scale, status};
-    const dim3 grid((unsigned)rows, (unsigned)num_heads);
-    const cudaStream_t s = (cudaStream_t)stream;
-    if (dtype == SPECDEC_BF16) {
-        if (cache->dtype == SPECDEC_BF16) specdec_paged_attention_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kThreads, 0, s>>>(a);
-        else specdec_paged_attention_kernel<__nv_bfloat16, __nv_fp8_e4m3><<<grid, kThreads, 0, s>>>(a);
-    } else {
-        if (cache->dtype == SPECDEC_F16) specdec_paged_attention_kernel<__half, __half><<<grid, kThreads, 0, s>>>(a);
-        else specdec_paged_attention_kernel<__half, __nv_fp8_e4m3><<<grid, kThreads, 0, s>>>(a);
-    }
-    return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+    const int P = sm_count(), group = num_heads / cache->num_kv_heads;
+    const Args a = {q, out, lse, num_heads, group, q_row_stride, q_head_stride, out_row_stride, out_head_stride, *cache,
+                    block_table, block_stride, max_blocks, cached_len, cu_num_draft, B, max_k, window, scale * 1.4426950408889634f,
+                    status, static_cast<int4*>(workspace), reinterpret_cast<float*>(static_cast<char*>(workspace) + split_bytes(P)),
+                    wait_limit_us < 0 ? kWaitNs : (unsigned long long)wait_limit_us * 1000ull};
+    const int N = row_tile(max_k, group);
+    return dtype == SPECDEC_BF16 ? launch_type<__nv_bfloat16>(a, N, (cudaStream_t)stream, P) : launch_type<__half>(a, N, (cudaStream_t)stream, P);
 }

@@ -45,6 +45,7 @@ inline specdec_status_t check_cache(const specdec_kv_cache_t* c)
     for (int64_t s : st)
         if (s < 0 || s > ((int64_t)1 << 38) || (s * es) % 16 != 0) return SPECDEC_ERR_INVALID_ARG;
     if (c->dtype == SPECDEC_E4M3 ? (!c->k_exp || !c->v_exp) : (c->k_exp || c->v_exp)) return SPECDEC_ERR_INVALID_ARG;
+    if (!aligned_to(c->k_exp, 16) || !aligned_to(c->v_exp, 16)) return SPECDEC_ERR_INVALID_ARG;
     return SPECDEC_OK;
 }
 

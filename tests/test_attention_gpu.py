@@ -47,7 +47,7 @@ class Step:
         self.out = torch.full_like(self.q, 7.0)
         self.lse = torch.full((self.T + 2, H), 7.0, device=cuda)
         self.status = torch.zeros(self.B, dtype=torch.int32, device=cuda)
-        self.ws = torch.full((_native.paged_attention_workspace_size(self.B, self.max_k, H, heads, dim),), 0xA5, dtype=torch.uint8, device=cuda)
+        self.ws = torch.full((_native.paged_attention_workspace_size(self.B, self.max_k, H, heads, dim),), 0xFF, dtype=torch.uint8, device=cuda)
         self.dtab, self.dcached, self.dcu = dev(self.tab, cuda), dev(np.array(cached, dtype=np.int32), cuda), dev(self.cu, cuda)
 
     def run(self, **kw):

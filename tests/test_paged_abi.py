@@ -51,7 +51,7 @@ def test_rope_refusals(lib):
 
 BAD_CACHES = [(dict(k=None), 1), (dict(v=None), 1), (dict(k=P + 8), 1), (dict(num_pages=0), 1), (dict(num_kv_heads=0), 1),
               (dict(page_stride=-2048), 1), (dict(slot_stride=68), 1), (dict(page_stride=2 ** 39), 1), (dict(k_exp=P), 1), (dict(dtype=3), 1),
-              (dict(dtype=3, k_exp=P), 1), (dict(dtype=0), 2), (dict(dtype=7), 2), (dict(page_size=8), 2), (dict(page_size=48), 2),
+              (dict(dtype=3, k_exp=P), 1), (dict(dtype=3, k_exp=P, v_exp=P + 8), 1), (dict(dtype=0), 2), (dict(dtype=7), 2), (dict(page_size=8), 2), (dict(page_size=48), 2),
               (dict(page_size=512), 2), (dict(head_dim=8), 2), (dict(head_dim=72), 2), (dict(head_dim=144), 2)]
 
 

@@ -17,9 +17,9 @@
  * without the host knowing them. A CTA that holds only part of an item writes (m, l, O) to its
  * workspace slot, and specdec_paged_join_kernel joins the parts in the order of the CTAs.
  *
- * Warps: 4 per column group for the softmax (one lane quarter of tensor memory each), 4 that convert an
- * e4m3 cache (keys to f16 in tensor memory, values to f16 tiles in shared memory; both exact), one
- * that feeds TMA, one that issues the products, two that fetch Q.
+ * Warps: 4 per column group for the softmax (one lane quarter of tensor memory each), 8 that convert an
+ * e4m3 cache (4 the keys to f16 in tensor memory, 4 the values to f16 tiles in shared memory; both
+ * exact), one that feeds TMA, one that issues the products, two that fetch Q.
  *
  * Bound by HBM: every visible key and value is read once per row block.
  */
@@ -85,7 +85,7 @@ template <int N> __device__ __forceinline__ Request request_of(const Args& a, in
     r.cached = __ldg(a.cached + b);
     if (k > a.max_k) {
         r.fault = SPECDEC_ST_K_TOO_LARGE;
-    } else if (r.cached < 0 || r.cached + k + 1 > (int64_t)a.max_blocks * a.cache.page_size) {
+    } else if (r.cached < 0 || r.cached + k + 1 > min((int64_t)a.max_blocks * a.cache.page_size, (int64_t)INT32_MAX - kTile)) {
         r.fault = SPECDEC_ST_BAD_LENGTH;
     } else {
         r.rows = (k + 1) * a.group;
@@ -96,13 +96,27 @@ template <int N> __device__ __forceinline__ Request request_of(const Args& a, in
     return r;
 }
 
-struct Item {
-    int b, h, block, t0, t1;                             // tiles [t0, t1) of the item, numbered in the request
-    bool begin, end;                                     // whether they hold its first and its last
-    int64_t first_unit, last_unit;                       // of the whole item
+// The first unit of CTA i. With fewer units than CTAs the first ones take one each, so that no CTA between two
+// parts of an item is without a part.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y)       // x, y >= 0; 32-bit division where it will do
+{
+    return (x | y) >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
+}
+__device__ __forceinline__ int64_t cta_begin(int64_t units, int i, int P)
+{
+    const int64_t each = quotient(units, P), rest = units - each * P;
+    return each * i + min((int64_t)i, rest);
+}
+
+// What a CTA does of one item: tiles [t0, t1), numbered in the request.
+struct Task {
+    int32_t b, h, block, t0, t1;                         // b < 0: no more
+    int32_t begin, end;                                  // whether they hold the item's first tile, and its last
+    int32_t row0, rows, cached;
+    int64_t last_unit;                                   // of the whole item
 };
 
-// Walks a CTA's units item by item; every role walks the same way.
+// Walks a CTA's units item by item.
 template <int N> struct Walker {
     const Args& a;
     int64_t u, u_end, base;
@@ -113,37 +127,33 @@ template <int N> struct Walker {
     {
         if (u < u_end) r = request_of<N>(a, b);
     }
-    __device__ __forceinline__ bool next(Item& w)
+    __device__ __forceinline__ bool next(Task& w)
     {
+        w.b = -1;
         if (u >= u_end) return false;
         const int H = a.cache.num_kv_heads;
         while (u >= base + r.units(H)) {
             base += r.units(H);
             r = request_of<N>(a, ++b);
         }
-        const int64_t local = u - base, item = local / r.tiles;
+        const int64_t local = u - base, item = quotient(local, r.tiles);
         const int tile = (int)(local - item * r.tiles);
         const int n = (int)min((int64_t)(r.tiles - tile), u_end - u);
         w.b = b;
-        w.h = (int)(item / r.blocks);
+        w.h = (int)quotient(item, r.blocks);
         w.block = (int)(item - (int64_t)w.h * r.blocks);
         w.t0 = r.first_tile + tile;
         w.t1 = w.t0 + n;
         w.begin = tile == 0;
         w.end = tile + n == r.tiles;
-        w.first_unit = base + item * r.tiles;
-        w.last_unit = w.first_unit + r.tiles - 1;
+        w.row0 = r.row0;
+        w.rows = r.rows;
+        w.cached = (int32_t)r.cached;
+        w.last_unit = base + item * r.tiles + r.tiles - 1;
         u += n;
         return true;
     }
 };
-
-// The first unit of CTA i. With fewer units than CTAs the first ones take one each, so that no CTA between two
-// parts of an item is without a part.
-__device__ __forceinline__ int64_t cta_begin(int64_t units, int i, int P)
-{
-    return units < P ? min(units, (int64_t)i) : units * i / P;
-}
 
 // ---------------------------------------------------------------- shapes
 
@@ -153,14 +163,16 @@ template <typename T_, bool kFp8_, int N_, int DB_> struct Shape {
     static constexpr bool kFp8 = kFp8_;
     static constexpr bool kScaleQ = kFp8_ && std::is_same<T_, __nv_bfloat16>::value;
     static constexpr int N = N_, DB = DB_, DP = 64 * DB_;
-    static constexpr int kGroups = N >= 64 ? 2 : 1, NC = N / kGroups;
+    static constexpr int kGroups = N >= 64 ? N / 32 : 1, NC = N / kGroups;
     static constexpr int kQ = N == 128 && DB == 2 ? 1 : 2;               // Q buffers
-    static constexpr int kSoftWarps = 4 * kGroups, kConvWarps = kFp8 ? 4 : 0;
-    static constexpr int kProducer = kSoftWarps + kConvWarps, kMma = kProducer + 1, kLoader = kProducer + 2;
-    static constexpr int kThreads = 32 * (kLoader + 2);
+    static constexpr int kSoftWarps = 4 * kGroups, kConvWarps = kFp8 ? 8 : 0;
+    static constexpr int kProducer = kSoftWarps + kConvWarps, kMma = kProducer + 1, kLoader = kProducer + 2,
+                         kScheduler = kProducer + 3;
+    static constexpr int kThreads = 32 * (kScheduler + 1);
+    static constexpr int kTasks = 4;                                     // tasks between the scheduler and the slowest role
     static constexpr int kSlotBytes = kTile * DP * (kFp8 ? 1 : 2);
     static constexpr int kQBytes = N * DP * 2, kPBytes = N * kTile * 2, kV16Bytes = kFp8 ? kTile * DP * 2 : 0;
-    static constexpr int kMiscBytes = 8 * 1024;
+    static constexpr int kMiscBytes = 12 * 1024;
     static constexpr int kRoom = kSmemBytes - 1024 - kMiscBytes - kQ * kQBytes - kPBytes - 2 * kV16Bytes;
     static constexpr int kSlots = kRoom / kSlotBytes > 12 ? 12 : kRoom / kSlotBytes;
     static constexpr int kTmem = 3 * N + (kFp8 ? DP : 0);                // O, two S, two f16 key tiles
@@ -172,6 +184,8 @@ template <typename T_, bool kFp8_, int N_, int DB_> struct Shape {
 template <typename S> struct Misc {
     uint64_t full[S::kSlots], empty[S::kSlots];
     uint64_t s_full[2], pv_done[2], p_full, o_free, q_full[2], q_empty[2], k16_full[2], v16_full[2];
+    uint64_t task_full[S::kTasks], task_free[S::kTasks];
+    Task task[S::kTasks];
     int64_t begin, end, base, units;
     int64_t warp_units[32];
     int first_b;
@@ -181,7 +195,10 @@ template <typename S> struct Misc {
     alignas(16) float red[4][S::N];                                  // a column's value in each warp of its group
     alignas(16) float fac[S::N];
     int red_e[4 * S::kGroups];
-    alignas(16) int32_t last[2][S::N];                               // last token that a column sees (-1: no column)
+    alignas(16) int32_t last[2][S::N];                   // last token that a column sees (-1: no column)
+    alignas(16) int2 place[2][S::N];                     // a column's row of q and out, and its query head (row -1: no column)
+    alignas(16) int64_t out_at[2][S::N];                 // and where it lies in out
+    uint32_t top[S::kScaleQ ? S::N : 1];                 // bits of the largest magnitude of a row of Q
     alignas(16) float qscale[2][S::kScaleQ ? S::N : 4];
     alignas(16) uint8_t exps[S::kSlots][S::kFp8 ? kTile : 16];
 };
@@ -222,10 +239,14 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         for (int i = 0; i < 2; ++i) {
             bar_init(bar(ms.s_full[i]), 1);
             bar_init(bar(ms.pv_done[i]), 1);
-            bar_init(bar(ms.q_full[i]), 2);
+            bar_init(bar(ms.q_full[i]), 1);
             bar_init(bar(ms.q_empty[i]), 1 + S::kSoftWarps);
             bar_init(bar(ms.k16_full[i]), 4);
             bar_init(bar(ms.v16_full[i]), 4);
+        }
+        for (int i = 0; i < S::kTasks; ++i) {
+            bar_init(bar(ms.task_full[i]), 1);
+            bar_init(bar(ms.task_free[i]), S::kScheduler);           // every other warp
         }
         bar_init(bar(ms.p_full), S::kSoftWarps);
         bar_init(bar(ms.o_free), S::kSoftWarps);
@@ -277,29 +298,51 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = ms.tmem;
     const uint32_t t_o = tmem, t_s = tmem + N, t_k = tmem + 3 * N;
-    Walker<N> walk(a, ms.begin, ms.end, ms.first_b, ms.base);
-    Item w;
+    // The next task, copied out of the scheduler's ring; false: none is left (or a wait has expired).
+    auto take = [&](uint32_t q, Task& w) {
+        const int s = q % S::kTasks;
+        const bool ok = __all_sync(0xffffffffu, wait(ms.task_full[s], q / S::kTasks));
+        if (ok) {
+            w = ms.task[s];
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(ms.task_free[s]));
+        }
+        return ok && w.b >= 0;
+    };
+    Task w;
     if (tid == 0) a.split[blockIdx.x] = make_int4(-1, 0, 0, 0);         // this thread may fill it in below
 
-    if (warp == S::kProducer) {
+    if (warp == S::kScheduler) {
+        // ================================================================ tasks
+        Walker<N> walk(a, ms.begin, ms.end, ms.first_b, ms.base);
+        for (uint32_t q = 0;; ++q) {
+            const bool more = walk.next(w);
+            const int s = q % S::kTasks;
+            if (q >= (uint32_t)S::kTasks && !__all_sync(0xffffffffu, wait(ms.task_free[s], q / S::kTasks - 1))) break;
+            if (lane == 0) {
+                ms.task[s] = w;
+                bar_arrive(bar(ms.task_full[s]));
+            }
+            if (!more) break;
+        }
+    } else if (warp == S::kProducer) {
         // ================================================================ keys and values into the ring
         const int ps = c.page_size, rows = min(ps, kTile), pages = kTile / rows;
         uint32_t n = 0;                                  // slots filled so far
-        while (walk.next(w)) {
-            const int64_t len = walk.r.cached + (walk.r.rows / a.group);
+        for (uint32_t q = 0; take(q, w); ++q) {
+            const int32_t len = w.cached + w.rows / a.group;
             const int32_t* const table = a.block_table + w.b * a.block_stride;
             auto page_of = [&](int t) -> int {           // this lane's page of tile t (-1: none)
-                const int64_t token = (int64_t)t * kTile + lane * rows;
+                const int32_t token = t * kTile + lane * rows;
                 return lane < pages && token < len ? __ldg(table + token / ps) : -1;
             };
             auto used_of = [&](int t) {
-                const int64_t left = len - (int64_t)t * kTile;
-                return (int)min((int64_t)pages, (left + rows - 1) / rows);
+                return min(pages, (len - t * kTile + rows - 1) / rows);
             };
             int page = page_of(w.t0);
             for (int t = w.t0; t < w.t1; ++t) {
                 const int next_page = t + 1 < w.t1 ? page_of(t + 1) : 0;
-                const int used = used_of(t), slot0 = ps > kTile ? (int)((int64_t)t * kTile % ps) : 0;
+                const int used = used_of(t), slot0 = ps > kTile ? t * kTile % ps : 0;
                 const bool bad = lane < used && (page < 0 || page >= c.num_pages);
                 if (bad && a.status) atomicOr(a.status + w.b, SPECDEC_ST_BAD_PAGE);
                 const int from = bad ? c.num_pages : page;      // past the end: the copy reads zeros
@@ -342,7 +385,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         }
     } else if (warp == S::kMma) {
         // ================================================================ products
-        if (lane == 0) {
+        {
             constexpr int kBf16 = std::is_same<M, __nv_bfloat16>::value;
             constexpr uint32_t ds = product(kBf16, 0, 128, N), dv = product(kBf16, 1, 128, N);
             uint32_t n = 0;                              // tiles of the CTA
@@ -356,7 +399,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 const uint32_t slot = 2 * i % S::kSlots;
                 if constexpr (S::kFp8) ok = wait(ms.k16_full[i & 1], i >> 1) && ok;
                 else ok = wait(ms.full[slot], 2 * i / S::kSlots) && ok;
-                if (!ok) return;
+                if (!ok || lane != 0) return;
                 tmem_after();
                 const uint32_t d = t_s + (i & 1) * N;
 #pragma unroll
@@ -371,14 +414,14 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 if constexpr (!S::kFp8) mma_commit(bar(ms.empty[slot]));
                 if (last) mma_commit(bar(ms.q_empty[qb]));
             };
-            bool more = walk.next(w);
+            bool more = take(0, w);
             if (more) scores(0, 0, true, w.t1 - w.t0 == 1);
             while (more) {
                 const int tiles = w.t1 - w.t0;
-                Item after;
+                Task after;
                 bool follows = false;
                 auto start_next = [&]() {
-                    follows = walk.next(after);
+                    follows = take(q + 1, after);
                     if (follows) scores(n + 1, q + 1, true, after.t1 - after.t0 == 1);
                 };
                 for (int t = 0; t < tiles; ++t, ++n) {
@@ -390,7 +433,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                     if constexpr (S::kFp8) ok = wait(ms.v16_full[n & 1], n >> 1) && ok;
                     else ok = wait(ms.full[slot], (2 * n + 1) / S::kSlots) && ok;
                     if (t == 0 && q > 0) ok = wait(ms.o_free, q - 1) && ok;
-                    if (ok) {
+                    if (ok && lane == 0) {
                         tmem_after();
                         const uint32_t va = S::kFp8 ? v0 + (n & 1) * S::kV16Bytes : ring0 + slot * S::kSlotBytes;
                         // one block of 64 elements (DB = 1): the rows 64 .. 127 read the block again and are not used
@@ -409,50 +452,60 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             }
         }
         __syncwarp();
-    } else if (warp >= S::kLoader) {
-        // ================================================================ Q, its scales and its columns' last tokens
-        const int lt = tid - 32 * S::kLoader;            // 0 .. 63
-        uint32_t q = 0;
-        while (walk.next(w)) {
+    } else if (warp == S::kLoader) {
+        // ================================================================ Q, its scales and its columns' places
+        for (uint32_t q = 0; take(q, w); ++q) {
             const uint32_t qb = q % S::kQ;
             if (q >= (uint32_t)S::kQ) wait(ms.q_empty[qb], q / S::kQ - 1);
-            const int rows = walk.r.rows, row_first = w.block * N;
-            auto source = [&](int n) {
-                const int r = row_first + n, j = r / a.group, g = r - j * a.group;
-                return static_cast<const T*>(a.q) + (int64_t)(walk.r.row0 + j) * a.q_row + (int64_t)(w.h * a.group + g) * a.q_head;
-            };
-            for (int n = lt; n < N; n += 64) {
-                const bool real = row_first + n < rows;
-                ms.last[qb][n] = real ? (int32_t)(walk.r.cached + (row_first + n) / a.group) : -1;
+            for (int n = lane; n < N; n += 32) {
+                const int r = w.block * N + n, j = r / a.group, g = r - j * a.group;
+                const bool real = r < w.rows;
+                const int2 at = real ? make_int2(w.row0 + j, w.h * a.group + g) : make_int2(-1, 0);
+                ms.place[qb][n] = at;
+                ms.out_at[qb][n] = real ? at.x * a.out_row + at.y * a.out_head : -1;
+                ms.last[qb][n] = real ? w.cached + j : -1;
+                if constexpr (S::kScaleQ) ms.top[n] = 0;
+            }
+            __syncwarp();
+            unsigned char* const dst = qbuf + qb * S::kQBytes;
+            // 16-byte chunks, whole rows a batch, all of a batch's loads in flight together
+            constexpr int kChunks = N * (DP / 8) / 32, kBatch = kChunks < 8 ? kChunks : 8;
+#pragma unroll 1
+            for (int base = 0; base < kChunks; base += kBatch) {
+                uint4 v[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int i = lane + 32 * (base + u), n = (i & 7) + 8 * (i / DP), ch = (i >> 3) % (DP / 8);
+                    const int2 at = ms.place[qb][n];
+                    v[u] = make_uint4(0, 0, 0, 0);
+                    if (at.x >= 0 && ch * 8 < c.head_dim)
+                        v[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + at.x * a.q_row + at.y * a.q_head + ch * 8);
+                }
                 if constexpr (S::kScaleQ) {
                     // a power of two brings the row's largest element to [2^13, 2^14): bf16's eight bits fit f16's
                     // eleven exactly, but for elements under 2^-28 of the largest
-                    float top = 0.f;
-                    if (real) {
-                        const T* src = source(n);
-                        for (int d = 0; d < c.head_dim; d += 8) {
-                            float x[8];
-                            load_n<T, 8>(src + d, x);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (isfinite(x[i])) top = fmaxf(top, fabsf(x[i]));
+                    for (int u = 0; u < kBatch; ++u) {
+                        const int i = lane + 32 * (base + u), n = (i & 7) + 8 * (i / DP);
+                        const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t lo = x[k] << 16 & 0x7fffffffu, hi = x[k] & 0x7fff0000u;
+                            top = max(top, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
                         }
+                        if (top) atomicMax(&ms.top[n], top);
                     }
-                    int e = 14;
-                    if (top > 0.f) e = max((int)((__float_as_uint(top) >> 23) & 255u) - 126, -100);
-                    ms.qscale[qb][n] = __uint_as_float((uint32_t)(127 + e - 14) << 23);
+                    __syncwarp();
                 }
-            }
-            barrier_sync(1 + S::kGroups, 64);
-            unsigned char* const dst = qbuf + qb * S::kQBytes;
-            for (int i = lt; i < N * (DP / 8); i += 64) {
-                const int n = (i & 7) + 8 * (i / (DP)), ch = (i >> 3) % (DP / 8);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (row_first + n < rows && ch * 8 < c.head_dim) {
-                    v = *reinterpret_cast<const uint4*>(source(n) + ch * 8);
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int i = lane + 32 * (base + u), n = (i & 7) + 8 * (i / DP), ch = (i >> 3) % (DP / 8);
                     if constexpr (S::kScaleQ) {
-                        const float inv = __uint_as_float((254u << 23) - __float_as_uint(ms.qscale[qb][n]));
-                        const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&v);
+                        const int e = ms.top[n] ? max((int)(ms.top[n] >> 23) - 126, -100) : 14;
+                        const float inv = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+                        if (ch == 0) ms.qscale[qb][n] = __uint_as_float((uint32_t)(127 + e - 14) << 23);
+                        const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&v[u]);
                         uint4 o;
                         __half2* y = reinterpret_cast<__half2*>(&o);
 #pragma unroll
@@ -460,79 +513,62 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                             const float2 f = __bfloat1622float2(x[k]);
                             y[k] = __floats2half2_rn(f.x * inv, f.y * inv);
                         }
-                        v = o;
+                        v[u] = o;
                     }
+                    *reinterpret_cast<uint4*>(dst + ((n >> 3) * (DP / 8) + ch) * 128 + (n & 7) * 16) = v[u];
                 }
-                *reinterpret_cast<uint4*>(dst + ((n >> 3) * (DP / 8) + ch) * 128 + (n & 7) * 16) = v;
             }
             fence_async();
             __syncwarp();
             if (lane == 0) bar_arrive(bar(ms.q_full[qb]));
-            barrier_sync(1 + S::kGroups, 64);            // qscale is read before the next item writes it
-            ++q;
         }
     } else if (S::kFp8 && warp >= S::kSoftWarps) {
-        // ================================================================ e4m3 -> f16 (exact)
-        const int row = tid - 32 * S::kSoftWarps;        // token of the tile, and lane of tensor memory
-        uint32_t n = 0;
+        // ================================================================ e4m3 -> f16 (exact): four warps for K, four for V
+        const int row = tid & 127;                       // token of the tile, and (K) lane of tensor memory
+        const bool is_v = warp >= S::kSoftWarps + 4;
         const uint32_t quarter = (uint32_t)(row & ~31) << 16;
-        auto chunk = [&](const unsigned char* slot, int ch) {            // 16 codes of this token
-            const int at = DP == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3);
-            return *reinterpret_cast<const uint4*>(slot + row * DP + at * 16);
-        };
-        auto widen = [](uint32_t codes, uint32_t* out) { // four codes to two f16 pairs
-            asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
-                : "=r"(out[0]), "=r"(out[1]) : "r"(codes));
-        };
-        while (walk.next(w)) {
+        uint32_t n = 0;
+        for (uint32_t q = 0; take(q, w); ++q) {
             for (int t = w.t0; t < w.t1; ++t, ++n) {
-                const uint32_t ks = 2 * n % S::kSlots, vs = (2 * n + 1) % S::kSlots;
-                // keys: a token's elements along its lane of tensor memory, two to a column
-                wait(ms.full[ks], 2 * n / S::kSlots);
-                if (n >= 2) wait(ms.s_full[n & 1], (n >> 1) - 1);        // S of tile n - 2 has read the buffer
-                tmem_after();
+                const uint32_t i = 2 * n + is_v, slot = i % S::kSlots;
+                wait(ms.full[slot], i / S::kSlots);
+                const unsigned char* const src = ring + slot * S::kSlotBytes + row * DP;
+                uint4 x[DP / 16];                        // 16 codes each
 #pragma unroll
-                for (int g = 0; g < DP / 32; ++g) {
-                    uint32_t r[16];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint4 x = chunk(ring + ks * S::kSlotBytes, 2 * g + h);
-                        widen(x.x, r + 8 * h);
-                        widen(x.y, r + 8 * h + 2);
-                        widen(x.z, r + 8 * h + 4);
-                        widen(x.w, r + 8 * h + 6);
-                    }
-                    tmem_st_32x16(t_k + quarter + (n & 1) * (DP / 2) + g * 16, r);
-                }
-                tmem_wait_st();
-                tmem_before();
+                for (int ch = 0; ch < DP / 16; ++ch)
+                    x[ch] = *reinterpret_cast<const uint4*>(src + (DP == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) * 16);
                 __syncwarp();
-                if (lane == 0) {
-                    bar_arrive(bar(ms.k16_full[n & 1]));
-                    bar_arrive(bar(ms.empty[ks]));
-                }
-                // values: the same layout as a 16-bit tile of TMA's
-                wait(ms.full[vs], (2 * n + 1) / S::kSlots);
-                if (n >= 2) wait(ms.pv_done[n & 1], (n >> 1) - 1);
-                unsigned char* const dst = v16 + (n & 1) * S::kV16Bytes + row * 128;
+                if (lane == 0) bar_arrive(bar(ms.empty[slot]));
+                uint32_t r[DP / 2];
 #pragma unroll
                 for (int ch = 0; ch < DP / 16; ++ch) {
-                    const uint4 x = chunk(ring + vs * S::kSlotBytes, ch);
-                    uint32_t r[8];
-                    widen(x.x, r);
-                    widen(x.y, r + 2);
-                    widen(x.z, r + 4);
-                    widen(x.w, r + 6);
-                    unsigned char* const d = dst + (ch / 4) * (kTile * 128);
-                    *reinterpret_cast<uint4*>(d + ((2 * (ch % 4)) ^ (row & 7)) * 16) = make_uint4(r[0], r[1], r[2], r[3]);
-                    *reinterpret_cast<uint4*>(d + ((2 * (ch % 4) + 1) ^ (row & 7)) * 16) = make_uint4(r[4], r[5], r[6], r[7]);
+                    const uint32_t codes[4] = {x[ch].x, x[ch].y, x[ch].z, x[ch].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+                            : "=r"(r[8 * ch + 2 * k]), "=r"(r[8 * ch + 2 * k + 1]) : "r"(codes[k]));
                 }
-                fence_async();
+                if (!is_v) {
+                    // a token's elements along its lane of tensor memory, two to a column
+                    if (n >= 2) wait(ms.s_full[n & 1], (n >> 1) - 1);    // S of tile n - 2 has read the buffer
+                    tmem_after();
+#pragma unroll
+                    for (int g = 0; g < DP / 32; ++g)
+                        tmem_st_32x16(t_k + quarter + (n & 1) * (DP / 2) + g * 16, *reinterpret_cast<const uint32_t(*)[16]>(r + 16 * g));
+                    tmem_wait_st();
+                    tmem_before();
+                } else {
+                    // the layout of a 16-bit tile of TMA's
+                    if (n >= 2) wait(ms.pv_done[n & 1], (n >> 1) - 1);
+                    unsigned char* const dst = v16 + (n & 1) * S::kV16Bytes + row * 128;
+#pragma unroll
+                    for (int ch = 0; ch < DP / 8; ++ch)
+                        *reinterpret_cast<uint4*>(dst + (ch / 8) * (kTile * 128) + ((ch % 8) ^ (row & 7)) * 16) =
+                            make_uint4(r[4 * ch], r[4 * ch + 1], r[4 * ch + 2], r[4 * ch + 3]);
+                    fence_async();
+                }
                 __syncwarp();
-                if (lane == 0) {
-                    bar_arrive(bar(ms.v16_full[n & 1]));
-                    bar_arrive(bar(ms.empty[vs]));
-                }
+                if (lane == 0) bar_arrive(is_v ? bar(ms.v16_full[n & 1]) : bar(ms.k16_full[n & 1]));
             }
         }
     } else {
@@ -541,24 +577,26 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         const int col0 = grp * NC, id = 1 + grp;
         const int tq = lane >> 2, cq = 2 * (lane & 3);                   // token and column within an 8 x 8 matrix
         const uint32_t quarter = (uint32_t)wq << 21;                     // lane 32 wq
-        uint32_t n = 0, q = 0;
-        while (walk.next(w)) {
+        uint32_t n = 0;
+        for (uint32_t q = 0;; ++q) {
+            // (all of the softmax's threads go on, or none)
+            if (barrier_or(7, 128 * S::kGroups, !take(q, w))) break;
             const uint32_t qb = q % S::kQ;
             wait(ms.q_full[qb], q / S::kQ);
-            const int rows = walk.r.rows, row_first = w.block * N;
-            const int row_last = min(row_first + N, rows) - 1;
-            const int64_t seen_all = walk.r.cached + row_first / a.group, seen_any = walk.r.cached + row_last / a.group;
-            const int64_t from_all = a.window > 0 ? seen_any - a.window + 1 : 0, from_any = a.window > 0 ? seen_all - a.window + 1 : 0;
+            const int row_first = w.block * N, row_last = min(row_first + N, w.rows) - 1;
+            const int32_t seen_all = w.cached + row_first / a.group, seen_any = w.cached + row_last / a.group;
+            const int32_t from_all = a.window > 0 ? seen_any - a.window + 1 : 0, from_any = a.window > 0 ? seen_all - a.window + 1 : 0;
             float m[NC / 4], l[NC / 4];
 #pragma unroll
             for (int i = 0; i < NC / 4; ++i) m[i] = -FLT_MAX, l[i] = 0.f;
             int E = -100000;                                             // e4m3: exponent that the values' scales are taken by
-            for (int t = w.t0; t < w.t1; ++t, ++n) {
-                const int64_t token0 = (int64_t)t * kTile;
-                const bool masked = token0 + kTile - 1 > seen_all || token0 < from_all;
-                const uint32_t ks = 2 * n % S::kSlots, vs = (2 * n + 1) % S::kSlots;
-                float kscale[4];
-                int ve[4];
+            // One tile; kMasked: it holds a token that some row does not see.
+            auto tile = [&](auto masked, const int t) {
+                constexpr bool kMasked = decltype(masked)::value;
+                const int32_t token0 = t * kTile;
+                [[maybe_unused]] const uint32_t ks = 2 * n % S::kSlots, vs = (2 * n + 1) % S::kSlots;
+                [[maybe_unused]] float kscale[4];
+                [[maybe_unused]] int ve[4];
                 if constexpr (S::kFp8) {
                     wait(ms.full[ks], 2 * n / S::kSlots);
                     wait(ms.full[vs], (2 * n + 1) / S::kSlots);
@@ -568,7 +606,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                         kscale[i] = exp_value(ms.exps[ks][tok]) * a.scale_log2;
                         ve[i] = (int)ms.exps[vs][tok] - 127;
                         // a token that no row sees may hold anything
-                        if (masked && (token0 + tok > seen_any || token0 + tok < from_any)) ve[i] = -100000;
+                        if (kMasked && (token0 + tok > seen_any || token0 + tok < from_any)) ve[i] = -100000;
                     }
                     __syncwarp();
                     if (lane == 0) {                                     // the scales are read: the slots may go
@@ -588,27 +626,31 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                             tmem_ld_16x16(s_at + ((uint32_t)hf << 20) + r * 8, x[hf][r], x[hf][r + 1]);
                     tmem_wait_ld();
                 };
-                // score (log2) of element (hf, r, e), before the reference is taken off
+                // f(score, its scale to log2 units, whether its row sees its token, its column's number)
                 auto each = [&](auto f) {
 #pragma unroll
                     for (int r = 0; r < NC / 8; ++r) {
                         float2 qs = make_float2(1.f, 1.f);
                         if constexpr (S::kScaleQ) qs = *reinterpret_cast<const float2*>(&ms.qscale[qb][col0 + 8 * r + cq]);
                         int2 last = make_int2(0, 0);
-                        if (masked) last = *reinterpret_cast<const int2*>(&ms.last[qb][col0 + 8 * r + cq]);
+                        if constexpr (kMasked) {
+                            // in the tile's own numbering of this thread's tokens
+                            last = *reinterpret_cast<const int2*>(&ms.last[qb][col0 + 8 * r + cq]);
+                            last.x -= token0 + 32 * wq + tq;
+                            last.y -= token0 + 32 * wq + tq;
+                        }
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const int i = 2 * hf + (e >> 1);
+                                [[maybe_unused]] const int i = 2 * hf + (e >> 1);
                                 float scale = a.scale_log2;
                                 if constexpr (S::kFp8) scale = kscale[i];
                                 if constexpr (S::kScaleQ) scale *= (e & 1) ? qs.y : qs.x;
                                 bool seen = true;
-                                if (masked) {
-                                    const int64_t tok = token0 + 32 * wq + 8 * i + tq;
+                                if constexpr (kMasked) {
                                     const int32_t lt = (e & 1) ? last.y : last.x;
-                                    seen = tok <= lt && (a.window == 0 || tok > (int64_t)lt - a.window);
+                                    seen = 8 * i <= lt && (a.window == 0 || 8 * i > lt - a.window);
                                 }
                                 f(x[hf][r][e], scale, seen, 2 * r + (e & 1));
                             }
@@ -644,7 +686,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
 #pragma unroll
                         for (int i = 0; i < NC / 4; ++i) ms.red[wq][col0 + 8 * (i >> 1) + cq + (i & 1)] = top[i];
                     }
-                    int e_new = E;
+                    [[maybe_unused]] int e_new = E;
                     if constexpr (S::kFp8) {
                         int et = -100000;
 #pragma unroll
@@ -669,13 +711,18 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                         m[i] = now;
                         if (wq == 0 && tq == 0) ms.fac[col] = f * e_fac;
                     }
-                    each([&](float& z, float, bool, int ci) { z -= m[ci]; });
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                        for (int r = 0; r < NC / 8; ++r)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[hf][r][e] -= m[2 * r + (e & 1)];
                     barrier_sync(id, 128);
                     if (t > w.t0) {
                         // O^T: this thread's lane is an element of the head, its columns the group's
                         wait(ms.pv_done[(n - 1) & 1], (n - 1) >> 1);
                         tmem_after();
-#pragma unroll
+#pragma unroll 1
                         for (int i = 0; i < NC; i += 16) {
                             float o[16];
                             uint32_t r[16];
@@ -689,8 +736,8 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                     }
                 }
                 // weights, their sums, and P^T as the second product takes it: 8 x 8 blocks of 128 bytes
-                if (n > 0 && t > w.t0) wait(ms.pv_done[(n - 1) & 1], (n - 1) >> 1);
-                float vw[4];
+                if (t > w.t0) wait(ms.pv_done[(n - 1) & 1], (n - 1) >> 1);
+                [[maybe_unused]] float vw[4];
                 if constexpr (S::kFp8) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -726,7 +773,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                     }
                 bool poisoned = false;
                 uint32_t* const pz = ms.poison[n & 1];
-                if (masked) {
+                if constexpr (kMasked) {
                     // values of tokens that no row sees become zeros (a weight of zero times NaN is NaN); those that some
                     // rows see and others do not, and that are not finite, become zeros here and are added by hand below
                     unsigned char* vt;
@@ -738,11 +785,12 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                         vt = ring + vs * S::kSlotBytes;
                     }
                     if (grp == 0) {
-                        const int64_t tok = token0 + gt;
+                        const int32_t tok = token0 + gt;
                         const bool none = tok > seen_any || tok < from_any, some = tok > seen_all || tok < from_all;
                         bool clear = none;
                         if (!none && some) {
-                            for (int ch = 0; ch < DP / 8 && !clear; ++ch) {
+#pragma unroll 2
+                            for (int ch = 0; ch < DP / 8; ++ch) {
                                 const uint4 v4 = *reinterpret_cast<const uint4*>(vt + (ch / 8) * (kTile * 128) + gt * 128 + (((ch % 8) ^ (gt & 7)) * 16));
                                 const M* e = reinterpret_cast<const M*>(&v4);
 #pragma unroll
@@ -750,52 +798,64 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                             }
                             if (clear) atomicOr(&pz[wq], 1u << lane);
                         }
-                        if (clear)
+                        if (clear) {
+#pragma unroll 4
                             for (int ch = 0; ch < DP / 8; ++ch)
-                                *reinterpret_cast<uint4*>(vt + (ch / 8) * (kTile * 128) + gt * 128 + ch % 8 * 16) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4*>(vt + (ch / 8) * (kTile * 128) + gt * 128 + ((ch % 8) ^ (gt & 7)) * 16) = make_uint4(0, 0, 0, 0);
+                        }
                     }
-                    if (S::kGroups == 2) barrier_sync(7, 256); else barrier_sync(id, 128);
+                    barrier_sync(7, 128 * S::kGroups);
                     poisoned = (pz[0] | pz[1] | pz[2] | pz[3]) != 0;
                 }
                 fence_async();
                 tmem_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(bar(ms.p_full));
-                if (poisoned) {
-                    wait(ms.pv_done[n & 1], n >> 1);
-                    tmem_after();
-                    const int d = gt;                                    // this thread's element of the head
-                    for (int tk = 0; tk < kTile; ++tk) {
-                        if (!(pz[tk >> 5] >> (tk & 31) & 1u)) continue;
-                        const int64_t tok = token0 + tk;
-                        const int page = __ldg(a.block_table + w.b * a.block_stride + tok / c.page_size);
-                        float v = 0.f;
-                        if (d < c.head_dim && page >= 0 && page < c.num_pages) {
-                            const int64_t at = page * c.page_stride + w.h * c.head_stride + tok % c.page_size * c.slot_stride + d;
-                            if constexpr (S::kFp8) v = to_float<__nv_fp8_e4m3>(static_cast<const __nv_fp8_e4m3*>(c.v)[at]);
-                            else v = to_float<M>(static_cast<const M*>(c.v)[at]);
-                        }
-                        for (int i = 0; i < NC; i += 16) {
-                            float o[16];
-                            uint32_t r[16];
-                            tmem_ld_32x16(t_o + quarter + col0 + i, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const int col = col0 + i + k, lt = ms.last[qb][col];
-                                const bool seen = tok <= lt && (a.window == 0 || tok > (int64_t)lt - a.window);
-                                const float p = to_float<M>(*reinterpret_cast<const M*>(pbuf + ((col >> 3) * 16 + (tk >> 3)) * 128 + (col & 7) * 16 + (tk & 7) * 2));
-                                r[k] = __float_as_uint(seen && p != 0.f ? fmaf(p, v, o[k]) : o[k]);
+                if constexpr (kMasked) {
+                    if (poisoned) {
+                        wait(ms.pv_done[n & 1], n >> 1);
+                        tmem_after();
+                        const int d = gt;                                // this thread's element of the head
+#pragma unroll 1
+                        for (int tk = 0; tk < kTile; ++tk) {
+                            if (!(pz[tk >> 5] >> (tk & 31) & 1u)) continue;
+                            const int32_t tok = token0 + tk;
+                            const int page = __ldg(a.block_table + w.b * a.block_stride + tok / c.page_size);
+                            float v = 0.f;
+                            if (d < c.head_dim && page >= 0 && page < c.num_pages) {
+                                const int64_t at = page * c.page_stride + w.h * c.head_stride + tok % c.page_size * c.slot_stride + d;
+                                if constexpr (S::kFp8) v = to_float<__nv_fp8_e4m3>(static_cast<const __nv_fp8_e4m3*>(c.v)[at]);
+                                else v = to_float<M>(static_cast<const M*>(c.v)[at]);
                             }
-                            tmem_st_32x16(t_o + quarter + col0 + i, r);
-                            tmem_wait_st();
+#pragma unroll 1
+                            for (int i = 0; i < NC; i += 16) {
+                                float o[16];
+                                uint32_t r[16];
+                                tmem_ld_32x16(t_o + quarter + col0 + i, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) {
+                                    const int col = col0 + i + k, lt = ms.last[qb][col];
+                                    const bool seen = tok <= lt && (a.window == 0 || tok > lt - a.window);
+                                    const float p = to_float<M>(*reinterpret_cast<const M*>(pbuf + ((col >> 3) * 16 + (tk >> 3)) * 128 + (col & 7) * 16 + (tk & 7) * 2));
+                                    r[k] = __float_as_uint(seen && p != 0.f ? fmaf(p, v, o[k]) : o[k]);
+                                }
+                                tmem_st_32x16(t_o + quarter + col0 + i, r);
+                                tmem_wait_st();
+                            }
                         }
+                        barrier_sync(7, 128 * S::kGroups);
+                        if (tid < 4) pz[tid] = 0;
+                        barrier_sync(7, 128 * S::kGroups);
+                        tmem_before();
                     }
-                    if (S::kGroups == 2) barrier_sync(7, 256); else barrier_sync(id, 128);
-                    if (tid < 4) pz[tid] = 0;
-                    if (S::kGroups == 2) barrier_sync(7, 256); else barrier_sync(id, 128);
-                    tmem_before();
                 }
+            };
+#pragma unroll 1
+            for (int t = w.t0; t < w.t1; ++t, ++n) {
+                const int32_t token0 = t * kTile;
+                if (token0 + kTile - 1 > seen_all || token0 < from_all) tile(std::true_type{}, t);
+                else tile(std::false_type{}, t);
             }
             // ---- the item's (part of) result
             const uint32_t lastn = n - 1;
@@ -823,11 +883,9 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                     if (!any) f = 0.f;
                     ms.fac[col] = f;
                     if (whole) {
-                        const int r = row_first + col;
-                        if (a.lse && r < rows) {
-                            const int j = r / a.group, g = r - j * a.group;
-                            a.lse[(int64_t)(walk.r.row0 + j) * a.num_heads + w.h * a.group + g] = any ? (m[i] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
-                        }
+                        const int2 at = ms.place[qb][col];
+                        if (a.lse && at.x >= 0)
+                            a.lse[(int64_t)at.x * a.num_heads + at.y] = any ? (m[i] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
                     } else {
                         part[N * DP + col] = m[i];
                         part[N * DP + N + col] = sum;
@@ -845,25 +903,21 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 tmem_wait_ld();
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                    const int col = col0 + i + k, r = row_first + col;
-                    if (r >= rows || d >= c.head_dim) continue;
+                    const int col = col0 + i + k;
+                    const int64_t at = ms.out_at[qb][col];
+                    if (at < 0 || d >= c.head_dim) continue;
                     const float f = ms.fac[col], y = f == 0.f ? 0.f : o[k] * f;
-                    if (whole) {
-                        const int j = r / a.group, g = r - j * a.group;
-                        static_cast<T*>(a.out)[(int64_t)(walk.r.row0 + j) * a.out_row + (int64_t)(w.h * a.group + g) * a.out_head + d] = from_float<T>(y);
-                    } else {
-                        part[col * DP + d] = y;
-                    }
+                    if (whole) static_cast<T*>(a.out)[at + d] = from_float<T>(y);
+                    else part[col * DP + d] = y;
                 }
             }
             if (tid == 0 && w.begin && !w.end) {
                 // the CTA of the item's last unit
-                int lastc = ms.units < P ? (int)w.last_unit : (int)(w.last_unit * P / ms.units);
+                int lastc = (int)min((int64_t)P - 1, quotient(w.last_unit, max((int64_t)1, quotient(ms.units, P))));
                 while (cta_begin(ms.units, lastc + 1, P) <= w.last_unit) ++lastc;
                 while (cta_begin(ms.units, lastc, P) > w.last_unit) --lastc;
                 a.split[blockIdx.x] = make_int4(w.b, w.h, w.block, lastc);
             }
-            if (*expired && tid == 0 && a.status) atomicOr(a.status + w.b, SPECDEC_ST_DEVICE_TIMEOUT);
             tmem_before();
             __syncwarp();
             if (lane == 0) {
@@ -871,7 +925,6 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 bar_arrive(bar(ms.q_empty[qb]));
             }
             barrier_sync(id, 128);                                       // red and fac are read
-            ++q;
         }
         // requests that the kernel does not take: their bits, and zeros in the rows that are known
         for (int b = blockIdx.x; b < a.B; b += P) {
@@ -891,6 +944,15 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
     tmem_before();
     __syncthreads();
     tmem_after();
+    if (*expired && tid == 0 && a.status && ms.begin < ms.end) {
+        // every request that the CTA has a unit of
+        int64_t base = ms.base;
+        for (int b = ms.first_b; b < a.B && base < ms.end; ++b) {
+            const int64_t n = request_of<N>(a, b).units(H);
+            if (n > 0) atomicOr(a.status + b, SPECDEC_ST_DEVICE_TIMEOUT);
+            base += n;
+        }
+    }
     if (warp == S::kMma) {
         if (*expired) {                                  // products issued so far end by themselves: wait for them
             if (lane == 0) {

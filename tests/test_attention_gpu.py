@@ -339,3 +339,20 @@ def test_lse_and_status_are_optional_and_join_two_halves(cuda):
     s.run(lse=None, status=None)
     torch.cuda.synchronize()
     assert (s.lse == 7).all()
+
+
+@pytest.mark.parametrize("cache_kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("k,group", [(0, 1), (8, 8)])
+def test_wait_expiry_is_reported_and_the_context_stays_usable(cuda, cache_kind, k, group):
+    """With every wait inside the kernel limited to 0 us, waits expire: the requests get DEVICE_TIMEOUT, the call
+    ends, rows behind the last request stay, and the same step is then exact with the default limit."""
+    import torch
+
+    s = Step(cuda, [k] * 6, [3000] * 6, 2, group, 128, "bf16", cache_kind, 16)
+    s.run(wait_limit_us=0)
+    torch.cuda.synchronize()
+    assert ((s.status & _native.ST_DEVICE_TIMEOUT) != 0).all()
+    assert (s.out[s.T:] == 7).all() and (s.lse[s.T:] == 7).all()
+    s.status.zero_()
+    s.run().check()
+    assert (s.status == 0).all()

@@ -275,74 +275,99 @@ def bitmask_scatter(compact, compact_rows: int, constrained, n: int, cu_num_draf
 
 
 # ------------------------------------------------------------------ rotary positions, paged cache, attention
+#
+# These calls sit in a decode loop, where a kernel takes a few microseconds: the checks below ask each tensor
+# for each property once.
 
-def _stream(stream):
-    import torch
+_torch = None
+_FLOATS: dict = {}
 
+
+def _lazy_torch():
+    """torch and the library's numbers of its types, looked up once."""
+    global _torch
+    if _torch is None:
+        import torch
+
+        _FLOATS.update({torch.float32: SPECDEC_F32, torch.bfloat16: SPECDEC_BF16, torch.float16: SPECDEC_F16})
+        _torch = torch
+    return _torch
+
+
+def _stream(stream, device: int) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _torch._C._cuda_getCurrentRawStream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
 def _dtype_of(t) -> int:
-    import torch
-
-    types = {torch.float32: SPECDEC_F32, torch.bfloat16: SPECDEC_BF16, torch.float16: SPECDEC_F16}
-    if t.dtype not in types:
+    n = _FLOATS.get(t.dtype)
+    if n is None:
         raise SpecdecError(SPECDEC_ERR_UNSUPPORTED, f"dtype {t.dtype}")
-    return types[t.dtype]
+    return n
 
 
-def _on_device(*tensors) -> None:
-    """Every (name, tensor) given is on the current CUDA device: the library launches there."""
-    import torch
-
-    for name, t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-
-
-def _ints(name, t, dtype: str, *shape) -> None:
-    """t is None or a contiguous tensor of `dtype` that holds at least `shape` (its first dimension may be longer)."""
+def _at(name: str, t, device: int):
+    """t's address (None: none); t must be on `device`, the current one, where the library launches."""
     if t is None:
-        return
-    if str(t.dtype) != f"torch.{dtype}" or t.dim() != len(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {len(shape)} dimension(s)")
-    if t.shape[0] < shape[0] or tuple(t.shape[1:]) != shape[1:]:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, {shape} is needed")
+        return None
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+    return t.data_ptr()
 
 
-def _status_ints(status, B: int) -> None:
-    if status is not None and (status.element_size() != 4 or status.dim() != 1 or not status.is_contiguous() or status.shape[0] < B):
+def _ints(name: str, t, dtype, rows: int, device: int):
+    """Address of an integer tensor of at least `rows` elements (None: none)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] < rows or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {rows} elements, got {t.dtype} {tuple(t.shape)}")
+    return _at(name, t, device)
+
+
+def _status(status, B: int, device: int):
+    if status is None:
+        return None
+    if status.element_size() != 4 or status.dim() != 1 or status.shape[0] < B or not status.is_contiguous():
         raise ValueError("status must be a contiguous 32-bit integer tensor of B elements")
+    return _at("status", status, device)
 
 
-def _heads(name, t, like=None) -> None:
-    """t is [rows, heads, head_dim] with the elements of a head contiguous."""
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+def _heads(name: str, t):
+    """(shape, strides) of t, [rows, heads, head_dim] with the elements of a head contiguous."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1):
         raise ValueError(f"{name} must be [rows, heads, head_dim] with the elements of a head contiguous")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
-        raise ValueError(f"{name} has shape {tuple(t.shape)} {t.dtype}, {tuple(like.shape)} {like.dtype} is needed")
+    return shape, stride
 
 
-def _table(block_table, B: int):
-    if str(block_table.dtype) != "torch.int32" or block_table.dim() != 2 or block_table.shape[0] < B:
-        raise ValueError("block_table must be int32 [B, max_blocks]")
-    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
-        raise ValueError("a request's row of block_table must be contiguous")
-    return block_table.shape[1], block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
+def _like(name: str, t, shape, dtype):
+    """Strides of t, which must have that shape and type."""
+    got, stride = _heads(name, t)
+    if got != shape or t.dtype is not dtype:
+        raise ValueError(f"{name} has shape {tuple(got)} {t.dtype}, {tuple(shape)} {dtype} is needed")
+    return stride
+
+
+def _table(block_table, B: int, device: int):
+    """(address, max_blocks, stride between the requests' rows)"""
+    shape, stride = block_table.shape, block_table.stride()
+    if block_table.dtype is not _torch.int32 or len(shape) != 2 or shape[0] < B or (shape[1] > 1 and stride[1] != 1):
+        raise ValueError("block_table must be int32 [B, max_blocks], a request's row contiguous")
+    return _at("block_table", block_table, device), shape[1], stride[0] if shape[0] > 1 else shape[1]
+
+
+def _cache_of(cache, device: int):
+    if cache.device != device:
+        raise ValueError(f"the cache is on cuda:{cache.device}, the current device is cuda:{device}")
+    return cache.struct()
 
 
 def rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
                      original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0):
     """specdec_rope_frequencies: (table, amplitude). The table is a CPU int64 tensor [rot_dim / 2] that holds
     the unsigned 64-bit units; copy it to the device once. scaling: None, "linear" or "by_parts"."""
-    import torch
-
+    torch = _lazy_torch()
     if scaling not in ROPE_SCALINGS:
         raise SpecdecError(SPECDEC_ERR_INVALID_ARG, f"rope scaling {scaling!r}")
     table = torch.zeros(max(int(rot_dim) // 2, 1), dtype=torch.int64)
@@ -354,28 +379,27 @@ def rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: Optional[str
     return table, amplitude.value
 
 
-def _rope_struct(freqs, rot_dim: int, interleaved: bool = False, amplitude: float = 1.0) -> RopeStruct:
-    _ints("freqs", freqs, "int64", int(rot_dim) // 2)
-    _on_device(("freqs", freqs))
-    return RopeStruct(_p(freqs), int(rot_dim), int(bool(interleaved)), float(amplitude))
+def _rope_struct(device: int, freqs, rot_dim: int, interleaved: bool = False, amplitude: float = 1.0) -> RopeStruct:
+    return RopeStruct(_ints("freqs", freqs, _torch.int64, rot_dim // 2, device), rot_dim, 1 if interleaved else 0, amplitude)
 
 
 def rope(x, out, freqs, rot_dim: int, interleaved: bool = False, amplitude: float = 1.0, inverse: bool = False,
          positions=None, cu_num_draft=None, cached_len=None, B: int = 0, stream=None) -> None:
     """Queue specdec_rope: x rotated into out (which may be x), both [rows, heads, head_dim] with any row and
     head strides. Positions are given for every row, or follow from cu_num_draft, cached_len and B."""
-    _heads("x", x)
-    _heads("out", out, x)
+    torch = _lazy_torch()
+    device = x.get_device()
+    shape, xs = _heads("x", x)
+    os_ = _like("out", out, shape, x.dtype)
+    i32 = torch.int32
     if positions is None and (cu_num_draft is None or cached_len is None):
         raise ValueError("rope needs positions, or cu_num_draft and cached_len")
-    _ints("positions", positions, "int32", x.shape[0])
-    _ints("cu_num_draft", cu_num_draft, "int32", int(B) + 1)
-    _ints("cached_len", cached_len, "int32", int(B))
-    _on_device(("x", x), ("out", out), ("positions", positions), ("cu_num_draft", cu_num_draft), ("cached_len", cached_len))
-    r = _rope_struct(freqs, rot_dim, interleaved, amplitude)
-    rc = load().specdec_rope(_p(x), _p(out), _dtype_of(x), x.shape[0], x.shape[1], x.shape[2], x.stride(0), x.stride(1),
-                             out.stride(0), out.stride(1), ctypes.byref(r), int(bool(inverse)), _p(positions),
-                             _p(cu_num_draft), _p(cached_len), int(B), _stream(stream))
+    current = torch._C._cuda_getDevice() if device >= 0 else -2
+    r = _rope_struct(current, freqs, rot_dim, interleaved, amplitude)
+    rc = load().specdec_rope(_at("x", x, current), _at("out", out, current), _dtype_of(x), shape[0], shape[1], shape[2], xs[0], xs[1],
+                             os_[0], os_[1], ctypes.byref(r), 1 if inverse else 0, _ints("positions", positions, i32, shape[0], current),
+                             _ints("cu_num_draft", cu_num_draft, i32, B + 1, current),
+                             _ints("cached_len", cached_len, i32, B, current), B, _stream(stream, current))
     if rc != SPECDEC_OK:
         raise SpecdecError(rc, "specdec_rope")
 
@@ -385,25 +409,22 @@ def kv_write(k, v, cache, block_table, cached_len, cu_num_draft, B: int, rope=No
     """Queue specdec_kv_write: the rows of k and v [rows, num_kv_heads, head_dim] (same strides) into `cache`
     (kvcache.PagedCache). rope: None, or the keyword arguments of a rotation of the keys: a dict of freqs,
     rot_dim and, optionally, interleaved and amplitude."""
-    _heads("k", k)
-    _heads("v", v, k)
-    if k.stride() != v.stride():
+    torch = _lazy_torch()
+    device = k.get_device()
+    shape, ks = _heads("k", k)
+    if _like("v", v, shape, k.dtype) != ks:
         raise ValueError("k and v must have the same strides")
-    if tuple(k.shape[1:]) != (cache.k.shape[1], cache.k.shape[3]):
-        raise ValueError(f"rows of {tuple(k.shape[1:])} do not go into a cache of {(cache.k.shape[1], cache.k.shape[3])}")
-    max_blocks, block_stride = _table(block_table, B)
-    _ints("positions", positions, "int32", k.shape[0])
-    _ints("cu_num_draft", cu_num_draft, "int32", int(B) + 1)
-    _ints("cached_len", cached_len, "int32", int(B))
-    _status_ints(status, B)
-    _on_device(("k", k), ("v", v), ("cache", cache.k), ("block_table", block_table), ("cached_len", cached_len),
-               ("cu_num_draft", cu_num_draft), ("positions", positions), ("status", status))
-    r = None if rope is None else _rope_struct(**rope)
-    c = cache.struct()
-    rc = load().specdec_kv_write(_p(k), _p(v), _dtype_of(k), k.shape[0], k.stride(0), k.stride(1),
-                                 None if r is None else ctypes.byref(r), _p(positions), ctypes.byref(c), _p(block_table),
-                                 max_blocks, block_stride, _p(cached_len), _p(cu_num_draft), int(B), _p(status),
-                                 _stream(stream))
+    if shape[1] != cache.num_kv_heads or shape[2] != cache.head_dim:
+        raise ValueError(f"rows of {tuple(shape[1:])} do not go into a cache of {(cache.num_kv_heads, cache.head_dim)}")
+    current = torch._C._cuda_getDevice() if device >= 0 else -2
+    i32 = torch.int32
+    table, max_blocks, block_stride = _table(block_table, B, current)
+    r = None if rope is None else ctypes.byref(_rope_struct(current, **rope))
+    rc = load().specdec_kv_write(_at("k", k, current), _at("v", v, current), _dtype_of(k), shape[0], ks[0], ks[1], r,
+                                 _ints("positions", positions, i32, shape[0], current), ctypes.byref(_cache_of(cache, current)),
+                                 table, max_blocks, block_stride, _ints("cached_len", cached_len, i32, B, current),
+                                 _ints("cu_num_draft", cu_num_draft, i32, B + 1, current), B, _status(status, B, current),
+                                 _stream(stream, current))
     if rc != SPECDEC_OK:
         raise SpecdecError(rc, "specdec_kv_write")
 
@@ -411,26 +432,22 @@ def kv_write(k, v, cache, block_table, cached_len, cu_num_draft, B: int, rope=No
 def kv_read(cache, block_table, cu_len, B: int, out_k, out_v, first=None, status=None, stream=None) -> None:
     """Queue specdec_kv_read: tokens first[b] .. of every request into rows cu_len[b] .. of out_k and out_v
     ([rows, num_kv_heads, head_dim], same strides; either may be None)."""
+    torch = _lazy_torch()
     out = out_k if out_k is not None else out_v
     if out is None:
         raise ValueError("kv_read needs out_k or out_v")
-    _heads("out_k", out)
-    if out_k is not None and out_v is not None:
-        _heads("out_v", out_v, out_k)
-        if out_k.stride() != out_v.stride():
-            raise ValueError("out_k and out_v must have the same strides")
-    if tuple(out.shape[1:]) != (cache.k.shape[1], cache.k.shape[3]):
-        raise ValueError(f"rows of {tuple(out.shape[1:])} do not hold a cache of {(cache.k.shape[1], cache.k.shape[3])}")
-    max_blocks, block_stride = _table(block_table, B)
-    _ints("cu_len", cu_len, "int64", int(B) + 1)
-    _ints("first", first, "int32", int(B))
-    _status_ints(status, B)
-    _on_device(("out_k", out_k), ("out_v", out_v), ("cache", cache.k), ("block_table", block_table), ("cu_len", cu_len),
-               ("first", first), ("status", status))
-    c = cache.struct()
-    rc = load().specdec_kv_read(ctypes.byref(c), _p(block_table), max_blocks, block_stride, _p(first), _p(cu_len), int(B),
-                                out.shape[0], _p(out_k), _p(out_v), _dtype_of(out), out.stride(0), out.stride(1),
-                                _p(status), _stream(stream))
+    device = out.get_device()
+    shape, strides = _heads("out_k", out)
+    if out_k is not None and out_v is not None and _like("out_v", out_v, shape, out.dtype) != strides:
+        raise ValueError("out_k and out_v must have the same strides")
+    if shape[1] != cache.num_kv_heads or shape[2] != cache.head_dim:
+        raise ValueError(f"rows of {tuple(shape[1:])} do not hold a cache of {(cache.num_kv_heads, cache.head_dim)}")
+    current = torch._C._cuda_getDevice() if device >= 0 else -2
+    table, max_blocks, block_stride = _table(block_table, B, current)
+    rc = load().specdec_kv_read(ctypes.byref(_cache_of(cache, current)), table, max_blocks, block_stride,
+                                _ints("first", first, torch.int32, B, current), _ints("cu_len", cu_len, torch.int64, B + 1, current), B,
+                                shape[0], _at("out_k", out_k, current), _at("out_v", out_v, current), _dtype_of(out), strides[0],
+                                strides[1], _status(status, B, current), _stream(stream, current))
     if rc != SPECDEC_OK:
         raise SpecdecError(rc, "specdec_kv_read")
 
@@ -444,25 +461,26 @@ def paged_attention(q, cache, block_table, cached_len, cu_num_draft, B: int, max
                     wait_limit_us: Optional[int] = None, stream=None) -> None:
     """Queue specdec_paged_attention: q and out [rows, num_heads, head_dim], cache a kvcache.PagedCache, workspace a
     CUDA tensor of at least paged_attention_workspace_size(...) bytes. scale: default head_dim ** -0.5."""
-    _heads("q", q)
-    _heads("out", out, q)
-    if q.shape[2] != cache.k.shape[3]:
-        raise ValueError(f"head_dim {q.shape[2]} against the cache's {cache.k.shape[3]}")
-    max_blocks, block_stride = _table(block_table, B)
-    _ints("cu_num_draft", cu_num_draft, "int32", int(B) + 1)
-    _ints("cached_len", cached_len, "int32", int(B))
-    _ints("lse", lse, "float32", q.shape[0], q.shape[1])
-    _status_ints(status, B)
+    torch = _lazy_torch()
+    device = q.get_device()
+    shape, qs = _heads("q", q)
+    os_ = _like("out", out, shape, q.dtype)
+    if shape[2] != cache.head_dim:
+        raise ValueError(f"head_dim {shape[2]} against the cache's {cache.head_dim}")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous float32 tensor of shape {tuple(shape[:2])}")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _on_device(("q", q), ("out", out), ("cache", cache.k), ("block_table", block_table), ("cached_len", cached_len),
-               ("cu_num_draft", cu_num_draft), ("lse", lse), ("status", status), ("workspace", workspace))
-    c = cache.struct()
-    rc = load().specdec_paged_attention(_p(q), _dtype_of(q), q.shape[0], q.shape[1], q.stride(0), q.stride(1),
-                                        ctypes.byref(c), _p(block_table), max_blocks, block_stride, _p(cached_len),
-                                        _p(cu_num_draft), int(B), int(max_k),
-                                        float(q.shape[2] ** -0.5 if scale is None else scale), int(window), _p(out),
-                                        out.stride(0), out.stride(1), _p(lse), _p(status), _p(workspace), _nbytes(workspace),
-                                        -1 if wait_limit_us is None else int(wait_limit_us), _stream(stream))
+    current = torch._C._cuda_getDevice() if device >= 0 else -2
+    i32 = torch.int32
+    table, max_blocks, block_stride = _table(block_table, B, current)
+    rc = load().specdec_paged_attention(_at("q", q, current), _dtype_of(q), shape[0], shape[1], qs[0], qs[1],
+                                        ctypes.byref(_cache_of(cache, current)), table, max_blocks, block_stride,
+                                        _ints("cached_len", cached_len, i32, B, current),
+                                        _ints("cu_num_draft", cu_num_draft, i32, B + 1, current), B, max_k,
+                                        shape[2] ** -0.5 if scale is None else scale, window, _at("out", out, current), os_[0], os_[1],
+                                        _at("lse", lse, current), _status(status, B, current), _at("workspace", workspace, current),
+                                        workspace.numel() * workspace.element_size(), -1 if wait_limit_us is None else wait_limit_us,
+                                        _stream(stream, current))
     if rc != SPECDEC_OK:
         raise SpecdecError(rc, "specdec_paged_attention")

@@ -3,7 +3,7 @@
  * GB300 (sm_103a); C-ABI entry points in include/specdec.h.
  *
  * Mathematics. The (k_b + 1) * G query rows that share one key-value head of request b are the N
- * columns of two products over a tile of 128 tokens (padded to N = 16, 32, 64 or 128):
+ * columns of two products over a tile of 128 tokens (padded to N = 16, 32, 64, 96 or 128):
  *     S^T [128 tokens, N] = K Q^T          O^T [D, N] += V^T P^T,   P = exp2(c S - m)
  * with tokens (and head elements) as the 128 rows of tcgen05.mma: the work grows with the rows there
  * are, not with a row tile of 128, and the keys and values go from TMA's swizzled tiles into the
@@ -17,14 +17,15 @@
  * without the host knowing them. A CTA that holds only part of an item writes (m, l, O) to its
  * workspace slot, and specdec_paged_join_kernel joins the parts in the order of the CTAs.
  *
- * Warps: 4 per column group for the softmax (one lane quarter of tensor memory each), 8 that convert an
- * e4m3 cache (4 the keys to f16 in tensor memory, 4 the values to f16 tiles in shared memory; both
- * exact), one that feeds TMA, one that issues the products, two that fetch Q.
+ * Warps: 4 per column group for the softmax (one lane quarter of tensor memory each), 4 or 8 that convert
+ * an e4m3 cache (keys to f16 in tensor memory, values to f16 tiles in shared memory; both exact), one that
+ * feeds TMA, one that issues the products, one to four that fetch Q, one that hands out the work.
  *
  * Bound by HBM: every visible key and value is read once per row block.
  */
 #include <cuda.h>
 
+#include <atomic>
 #include <cfloat>
 #include <cmath>
 #include <cstddef>
@@ -42,7 +43,6 @@ constexpr float kLazy = 8.f;                             // how far (log2) a sco
 constexpr unsigned long long kWaitNs = 2000000000ull;    // a wait's default limit
 constexpr unsigned long long kDrainNs = 1000000000ull;   // more time for copies in flight before a CTA leaves
 constexpr int kSmemBytes = 227 * 1024;
-constexpr int kJoinRows = 4;
 
 struct Args {
     const void* q;
@@ -155,6 +155,12 @@ template <int N> struct Walker {
     }
 };
 
+// ln of the sum of a column's weights: log2's approximation is off by 2^-22 at most
+__device__ __forceinline__ float lse_of(bool any, float ref, float sum)
+{
+    return any ? (ref + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
+}
+
 // ---------------------------------------------------------------- shapes
 
 template <typename T_, bool kFp8_, int N_, int DB_> struct Shape {
@@ -164,10 +170,11 @@ template <typename T_, bool kFp8_, int N_, int DB_> struct Shape {
     static constexpr bool kScaleQ = kFp8_ && std::is_same<T_, __nv_bfloat16>::value;
     static constexpr int N = N_, DB = DB_, DP = 64 * DB_;
     static constexpr int kGroups = N >= 64 ? N / 32 : 1, NC = N / kGroups;
-    static constexpr int kQ = N == 128 && DB == 2 ? 1 : 2;               // Q buffers
-    static constexpr int kSoftWarps = 4 * kGroups, kConvWarps = kFp8 ? 8 : 0;
+    static constexpr int kQ = N >= 96 && DB == 2 ? 1 : 2;                // Q buffers
+    static constexpr int kSoftWarps = 4 * kGroups, kConvWarps = !kFp8 ? 0 : N >= 64 ? 4 : 8;
+    static constexpr int kLoaders = N < 64 ? 1 : kFp8 ? 2 : 4;
     static constexpr int kProducer = kSoftWarps + kConvWarps, kMma = kProducer + 1, kLoader = kProducer + 2,
-                         kScheduler = kProducer + 3;
+                         kScheduler = kLoader + kLoaders;
     static constexpr int kThreads = 32 * (kScheduler + 1);
     static constexpr int kTasks = 4;                                     // tasks between the scheduler and the slowest role
     static constexpr int kSlotBytes = kTile * DP * (kFp8 ? 1 : 2);
@@ -183,7 +190,7 @@ template <typename T_, bool kFp8_, int N_, int DB_> struct Shape {
 
 template <typename S> struct Misc {
     uint64_t full[S::kSlots], empty[S::kSlots];
-    uint64_t s_full[2], pv_done[2], p_full, o_free, q_full[2], q_empty[2], k16_full[2], v16_full[2];
+    uint64_t s_full[2], pv_done[2], p_full, done[2], q_full[2], q_empty[2], k16_full[2], v16_full[2];
     uint64_t task_full[S::kTasks], task_free[S::kTasks];
     Task task[S::kTasks];
     int64_t begin, end, base, units;
@@ -194,6 +201,7 @@ template <typename S> struct Misc {
     uint32_t poison[2][4];                               // tokens of a tile whose values are taken one by one
     alignas(16) float red[4][S::N];                                  // a column's value in each warp of its group
     alignas(16) float fac[S::N];
+    float ref[S::N];
     int red_e[4 * S::kGroups];
     alignas(16) int32_t last[2][S::N];                   // last token that a column sees (-1: no column)
     alignas(16) int2 place[2][S::N];                     // a column's row of q and out, and its query head (row -1: no column)
@@ -239,8 +247,9 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         for (int i = 0; i < 2; ++i) {
             bar_init(bar(ms.s_full[i]), 1);
             bar_init(bar(ms.pv_done[i]), 1);
-            bar_init(bar(ms.q_full[i]), 1);
-            bar_init(bar(ms.q_empty[i]), 1 + S::kSoftWarps);
+            bar_init(bar(ms.done[i]), S::kSoftWarps);
+            bar_init(bar(ms.q_full[i]), S::kLoaders);
+            bar_init(bar(ms.q_empty[i]), 1);
             bar_init(bar(ms.k16_full[i]), 4);
             bar_init(bar(ms.v16_full[i]), 4);
         }
@@ -249,7 +258,6 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             bar_init(bar(ms.task_free[i]), S::kScheduler);           // every other warp
         }
         bar_init(bar(ms.p_full), S::kSoftWarps);
-        bar_init(bar(ms.o_free), S::kSoftWarps);
         ms.expired = 0;
         for (int i = 0; i < 8; ++i) ms.poison[i >> 2][i & 3] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -274,17 +282,9 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             units += ms.warp_units[w];
         }
         const int64_t begin = cta_begin(units, blockIdx.x, P);
-        if (mine > 0 && begin >= before && begin < before + mine) {
-            int b = b0;
-            int64_t base = before;
-            while (true) {
-                const int64_t n = request_of<N>(a, b).units(H);
-                if (begin < base + n) break;
-                base += n;
-                ++b;
-            }
-            ms.first_b = b;
-            ms.base = base;
+        if (mine > 0 && begin >= before && begin < before + mine) {      // the scheduler walks on from here
+            ms.first_b = b0;
+            ms.base = before;
         }
         if (tid == 0) {
             ms.begin = begin;
@@ -432,7 +432,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                     const uint32_t slot = (2 * n + 1) % S::kSlots;
                     if constexpr (S::kFp8) ok = wait(ms.v16_full[n & 1], n >> 1) && ok;
                     else ok = wait(ms.full[slot], (2 * n + 1) / S::kSlots) && ok;
-                    if (t == 0 && q > 0) ok = wait(ms.o_free, q - 1) && ok;
+                    if (t == 0 && q > 0) ok = wait(ms.done[(q - 1) & 1], (q - 1) >> 1) && ok;
                     if (ok && lane == 0) {
                         tmem_after();
                         const uint32_t va = S::kFp8 ? v0 + (n & 1) * S::kV16Bytes : ring0 + slot * S::kSlotBytes;
@@ -452,31 +452,39 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             }
         }
         __syncwarp();
-    } else if (warp == S::kLoader) {
+    } else if (warp >= S::kLoader) {
         // ================================================================ Q, its scales and its columns' places
+        const int lt = tid - 32 * S::kLoader;
+        constexpr int kLt = 32 * S::kLoaders;
+        auto together = [&]() {
+            if constexpr (S::kLoaders > 1) barrier_sync(8, kLt);
+            else __syncwarp();
+        };
         for (uint32_t q = 0; take(q, w); ++q) {
-            const uint32_t qb = q % S::kQ;
+            const uint32_t qb = q % S::kQ, tb = q & 1;
+            if (q >= 2) wait(ms.done[tb], (q >> 1) - 1);                 // the tables' last item is done with
             if (q >= (uint32_t)S::kQ) wait(ms.q_empty[qb], q / S::kQ - 1);
-            for (int n = lane; n < N; n += 32) {
+            for (int n = lt; n < N; n += kLt) {
                 const int r = w.block * N + n, j = r / a.group, g = r - j * a.group;
                 const bool real = r < w.rows;
                 const int2 at = real ? make_int2(w.row0 + j, w.h * a.group + g) : make_int2(-1, 0);
-                ms.place[qb][n] = at;
-                ms.out_at[qb][n] = real ? at.x * a.out_row + at.y * a.out_head : -1;
-                ms.last[qb][n] = real ? w.cached + j : -1;
+                ms.place[tb][n] = at;
+                ms.out_at[tb][n] = real ? at.x * a.out_row + at.y * a.out_head : -1;
+                ms.last[tb][n] = real ? w.cached + j : -1;
                 if constexpr (S::kScaleQ) ms.top[n] = 0;
             }
-            __syncwarp();
+            together();
             unsigned char* const dst = qbuf + qb * S::kQBytes;
             // 16-byte chunks, whole rows a batch, all of a batch's loads in flight together
-            constexpr int kChunks = N * (DP / 8) / 32, kBatch = kChunks < 8 ? kChunks : 8;
+            constexpr int kChunks = N * (DP / 8) / kLt, kBatch = kChunks % 8 == 0 ? 8 : kChunks % 6 == 0 ? 6 : kChunks;
+            static_assert(kChunks * kLt == N * (DP / 8) && kChunks % kBatch == 0 && kBatch <= 8 && kBatch * kLt % DP == 0, "batches");
 #pragma unroll 1
             for (int base = 0; base < kChunks; base += kBatch) {
                 uint4 v[kBatch];
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
-                    const int i = lane + 32 * (base + u), n = (i & 7) + 8 * (i / DP), ch = (i >> 3) % (DP / 8);
-                    const int2 at = ms.place[qb][n];
+                    const int i = lt + kLt * (base + u), n = (i & 7) + 8 * (i / DP), ch = (i >> 3) % (DP / 8);
+                    const int2 at = ms.place[tb][n];
                     v[u] = make_uint4(0, 0, 0, 0);
                     if (at.x >= 0 && ch * 8 < c.head_dim)
                         v[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + at.x * a.q_row + at.y * a.q_head + ch * 8);
@@ -486,7 +494,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                     // eleven exactly, but for elements under 2^-28 of the largest
 #pragma unroll
                     for (int u = 0; u < kBatch; ++u) {
-                        const int i = lane + 32 * (base + u), n = (i & 7) + 8 * (i / DP);
+                        const int i = lt + kLt * (base + u), n = (i & 7) + 8 * (i / DP);
                         const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
                         uint32_t top = 0;
 #pragma unroll
@@ -496,15 +504,15 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                         }
                         if (top) atomicMax(&ms.top[n], top);
                     }
-                    __syncwarp();
+                    together();
                 }
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
-                    const int i = lane + 32 * (base + u), n = (i & 7) + 8 * (i / DP), ch = (i >> 3) % (DP / 8);
+                    const int i = lt + kLt * (base + u), n = (i & 7) + 8 * (i / DP), ch = (i >> 3) % (DP / 8);
                     if constexpr (S::kScaleQ) {
                         const int e = ms.top[n] ? max((int)(ms.top[n] >> 23) - 126, -100) : 14;
                         const float inv = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-                        if (ch == 0) ms.qscale[qb][n] = __uint_as_float((uint32_t)(127 + e - 14) << 23);
+                        if (ch == 0) ms.qscale[tb][n] = __uint_as_float((uint32_t)(127 + e - 14) << 23);
                         const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&v[u]);
                         uint4 o;
                         __half2* y = reinterpret_cast<__half2*>(&o);
@@ -521,54 +529,72 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             fence_async();
             __syncwarp();
             if (lane == 0) bar_arrive(bar(ms.q_full[qb]));
+            if constexpr (S::kScaleQ) together();        // top is read before the next item clears it
         }
     } else if (S::kFp8 && warp >= S::kSoftWarps) {
         // ================================================================ e4m3 -> f16 (exact): four warps for K, four for V
         const int row = tid & 127;                       // token of the tile, and (K) lane of tensor memory
-        const bool is_v = warp >= S::kSoftWarps + 4;
         const uint32_t quarter = (uint32_t)(row & ~31) << 16;
         uint32_t n = 0;
-        for (uint32_t q = 0; take(q, w); ++q) {
-            for (int t = w.t0; t < w.t1; ++t, ++n) {
-                const uint32_t i = 2 * n + is_v, slot = i % S::kSlots;
-                wait(ms.full[slot], i / S::kSlots);
-                const unsigned char* const src = ring + slot * S::kSlotBytes + row * DP;
-                uint4 x[DP / 16];                        // 16 codes each
+        auto widen = [&](const int is_v) {
+            const uint32_t i = 2 * n + is_v, slot = i % S::kSlots;
+            wait(ms.full[slot], i / S::kSlots);
+            const unsigned char* const src = ring + slot * S::kSlotBytes + row * DP;
+            uint4 x[DP / 16];                            // 16 codes each
 #pragma unroll
-                for (int ch = 0; ch < DP / 16; ++ch)
-                    x[ch] = *reinterpret_cast<const uint4*>(src + (DP == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) * 16);
-                __syncwarp();
-                if (lane == 0) bar_arrive(bar(ms.empty[slot]));
-                uint32_t r[DP / 2];
+            for (int ch = 0; ch < DP / 16; ++ch)
+                x[ch] = *reinterpret_cast<const uint4*>(src + (DP == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) * 16);
+            auto half = [](const uint4& x4, uint32_t* r) {
+                const uint32_t codes[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+                        : "=r"(r[2 * k]), "=r"(r[2 * k + 1]) : "r"(codes[k]));
+            };
+            if (!is_v) {
+                // a token's elements along its lane of tensor memory, two to a column
+                if (n >= 2) wait(ms.s_full[n & 1], (n >> 1) - 1);        // S of tile n - 2 has read the buffer
+                tmem_after();
+#pragma unroll
+                for (int g = 0; g < DP / 32; ++g) {
+                    uint32_t r[16];
+                    half(x[2 * g], r);
+                    half(x[2 * g + 1], r + 8);
+                    tmem_st_32x16(t_k + quarter + (n & 1) * (DP / 2) + g * 16, r);
+                }
+                tmem_wait_st();
+                tmem_before();
+            } else {
+                // the layout of a 16-bit tile of TMA's
+                if (n >= 2) wait(ms.pv_done[n & 1], (n >> 1) - 1);
+                unsigned char* const dst = v16 + (n & 1) * S::kV16Bytes + row * 128;
 #pragma unroll
                 for (int ch = 0; ch < DP / 16; ++ch) {
-                    const uint32_t codes[4] = {x[ch].x, x[ch].y, x[ch].z, x[ch].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
-                            : "=r"(r[8 * ch + 2 * k]), "=r"(r[8 * ch + 2 * k + 1]) : "r"(codes[k]));
+                    uint32_t r[8];
+                    half(x[ch], r);
+                    unsigned char* const d = dst + (ch / 4) * (kTile * 128);
+                    *reinterpret_cast<uint4*>(d + ((2 * (ch % 4)) ^ (row & 7)) * 16) = make_uint4(r[0], r[1], r[2], r[3]);
+                    *reinterpret_cast<uint4*>(d + ((2 * (ch % 4) + 1) ^ (row & 7)) * 16) = make_uint4(r[4], r[5], r[6], r[7]);
                 }
-                if (!is_v) {
-                    // a token's elements along its lane of tensor memory, two to a column
-                    if (n >= 2) wait(ms.s_full[n & 1], (n >> 1) - 1);    // S of tile n - 2 has read the buffer
-                    tmem_after();
-#pragma unroll
-                    for (int g = 0; g < DP / 32; ++g)
-                        tmem_st_32x16(t_k + quarter + (n & 1) * (DP / 2) + g * 16, *reinterpret_cast<const uint32_t(*)[16]>(r + 16 * g));
-                    tmem_wait_st();
-                    tmem_before();
+                fence_async();
+            }
+            __syncwarp();
+            if (lane == 0) {
+                bar_arrive(is_v ? bar(ms.v16_full[n & 1]) : bar(ms.k16_full[n & 1]));
+                bar_arrive(bar(ms.empty[slot]));
+            }
+        };
+        for (uint32_t q = 0; take(q, w); ++q) {
+#pragma unroll 1
+            for (int t = w.t0; t < w.t1; ++t, ++n) {
+                if constexpr (S::kConvWarps == 4) {
+                    widen(0);
+                    widen(1);
+                } else if (warp < S::kSoftWarps + 4) {
+                    widen(0);
                 } else {
-                    // the layout of a 16-bit tile of TMA's
-                    if (n >= 2) wait(ms.pv_done[n & 1], (n >> 1) - 1);
-                    unsigned char* const dst = v16 + (n & 1) * S::kV16Bytes + row * 128;
-#pragma unroll
-                    for (int ch = 0; ch < DP / 8; ++ch)
-                        *reinterpret_cast<uint4*>(dst + (ch / 8) * (kTile * 128) + ((ch % 8) ^ (row & 7)) * 16) =
-                            make_uint4(r[4 * ch], r[4 * ch + 1], r[4 * ch + 2], r[4 * ch + 3]);
-                    fence_async();
+                    widen(1);
                 }
-                __syncwarp();
-                if (lane == 0) bar_arrive(is_v ? bar(ms.v16_full[n & 1]) : bar(ms.k16_full[n & 1]));
             }
         }
     } else {
@@ -581,8 +607,8 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         for (uint32_t q = 0;; ++q) {
             // (all of the softmax's threads go on, or none)
             if (barrier_or(7, 128 * S::kGroups, !take(q, w))) break;
-            const uint32_t qb = q % S::kQ;
-            wait(ms.q_full[qb], q / S::kQ);
+            const uint32_t tb = q & 1;
+            wait(ms.q_full[q % S::kQ], q / S::kQ);
             const int row_first = w.block * N, row_last = min(row_first + N, w.rows) - 1;
             const int32_t seen_all = w.cached + row_first / a.group, seen_any = w.cached + row_last / a.group;
             const int32_t from_all = a.window > 0 ? seen_any - a.window + 1 : 0, from_any = a.window > 0 ? seen_all - a.window + 1 : 0;
@@ -631,11 +657,11 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
 #pragma unroll
                     for (int r = 0; r < NC / 8; ++r) {
                         float2 qs = make_float2(1.f, 1.f);
-                        if constexpr (S::kScaleQ) qs = *reinterpret_cast<const float2*>(&ms.qscale[qb][col0 + 8 * r + cq]);
+                        if constexpr (S::kScaleQ) qs = *reinterpret_cast<const float2*>(&ms.qscale[tb][col0 + 8 * r + cq]);
                         int2 last = make_int2(0, 0);
                         if constexpr (kMasked) {
                             // in the tile's own numbering of this thread's tokens
-                            last = *reinterpret_cast<const int2*>(&ms.last[qb][col0 + 8 * r + cq]);
+                            last = *reinterpret_cast<const int2*>(&ms.last[tb][col0 + 8 * r + cq]);
                             last.x -= token0 + 32 * wq + tq;
                             last.y -= token0 + 32 * wq + tq;
                         }
@@ -835,7 +861,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int k = 0; k < 16; ++k) {
-                                    const int col = col0 + i + k, lt = ms.last[qb][col];
+                                    const int col = col0 + i + k, lt = ms.last[tb][col];
                                     const bool seen = tok <= lt && (a.window == 0 || tok > lt - a.window);
                                     const float p = to_float<M>(*reinterpret_cast<const M*>(pbuf + ((col >> 3) * 16 + (tk >> 3)) * 128 + (col & 7) * 16 + (tk & 7) * 2));
                                     r[k] = __float_as_uint(seen && p != 0.f ? fmaf(p, v, o[k]) : o[k]);
@@ -866,30 +892,28 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             }
             if (tq == 0) {
 #pragma unroll
-                for (int i = 0; i < NC / 4; ++i) ms.red[wq][col0 + 8 * (i >> 1) + cq + (i & 1)] = l[i];
+                for (int i = 0; i < NC / 4; ++i) {
+                    const int col = col0 + 8 * (i >> 1) + cq + (i & 1);
+                    ms.red[wq][col] = l[i];
+                    if (wq == 0) ms.ref[col] = m[i];
+                }
             }
             const bool whole = w.begin && w.end;
             float* const part = a.parts + (int64_t)(2 * blockIdx.x + (w.begin ? 1 : 0)) * S::kSlotFloats;
             barrier_sync(id, 128);
-            if (wq == 0 && tq == 0) {
-#pragma unroll
-                for (int i = 0; i < NC / 4; ++i) {
-                    const int col = col0 + 8 * (i >> 1) + cq + (i & 1);
-                    const float sum = ms.red[0][col] + ms.red[1][col] + ms.red[2][col] + ms.red[3][col];
-                    const bool any = !(sum == 0.f);                      // (a NaN sum is one)
-                    // the join's factors are fp32 too: 2^E goes into O here
-                    float f = any && whole ? 1.f / sum : 1.f;
-                    if (S::kFp8 && E >= -126) f *= __uint_as_float((uint32_t)(127 + E) << 23);
-                    if (!any) f = 0.f;
-                    ms.fac[col] = f;
-                    if (whole) {
-                        const int2 at = ms.place[qb][col];
-                        if (a.lse && at.x >= 0)
-                            a.lse[(int64_t)at.x * a.num_heads + at.y] = any ? (m[i] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
-                    } else {
-                        part[N * DP + col] = m[i];
-                        part[N * DP + N + col] = sum;
-                    }
+            if (gt < NC) {
+                const int col = col0 + gt;
+                const float sum = ms.red[0][col] + ms.red[1][col] + ms.red[2][col] + ms.red[3][col], ref = ms.ref[col];
+                const bool any = !(sum == 0.f);                          // (a NaN sum is one)
+                float f = any ? (whole ? __frcp_rn(sum) : 1.f) : 0.f;
+                if (S::kFp8 && E >= -126) f *= __uint_as_float((uint32_t)(127 + E) << 23);
+                ms.fac[col] = f;
+                if (whole) {
+                    const int2 at = ms.place[tb][col];
+                    if (a.lse && at.x >= 0) a.lse[(int64_t)at.x * a.num_heads + at.y] = lse_of(any, ref, sum);
+                } else {
+                    part[N * DP + col] = ref;
+                    part[N * DP + N + col] = sum;
                 }
             }
             wait(ms.pv_done[lastn & 1], lastn >> 1);
@@ -904,7 +928,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     const int col = col0 + i + k;
-                    const int64_t at = ms.out_at[qb][col];
+                    const int64_t at = ms.out_at[tb][col];
                     if (at < 0 || d >= c.head_dim) continue;
                     const float f = ms.fac[col], y = f == 0.f ? 0.f : o[k] * f;
                     if (whole) static_cast<T*>(a.out)[at + d] = from_float<T>(y);
@@ -920,10 +944,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             }
             tmem_before();
             __syncwarp();
-            if (lane == 0) {
-                bar_arrive(bar(ms.o_free));
-                bar_arrive(bar(ms.q_empty[qb]));
-            }
+            if (lane == 0) bar_arrive(bar(ms.done[q & 1]));
             barrier_sync(id, 128);                                       // red and fac are read
         }
         // requests that the kernel does not take: their bits, and zeros in the rows that are known
@@ -968,35 +989,51 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
     }
 }
 
-// Joins the parts of the item that CTA blockIdx.x of the kernel above left to its successors: slot
-// 2 i + 1, then slot 2 j of each CTA j up to the last. One thread an element, kJoinRows rows a CTA.
+// Joins the parts of the item that CTA blockIdx.x of the kernel above left to its successors: slot 2 i + 1, then
+// slot 2 j of each CTA j up to the last. A warp takes 32 elements of a row: its lanes hold the parts' factors, and
+// the parts' elements are summed in their order.
 template <typename T, int N, int DP>
-__global__ void __launch_bounds__(DP) specdec_paged_join_kernel(const Args a)
+__global__ void __launch_bounds__(128) specdec_paged_join_kernel(const Args a)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 s = a.split[blockIdx.x];
     if (s.x < 0) return;
     constexpr int64_t kSlot = N * (DP + 2);
+    constexpr int kWarps = DP / 32, kRows = 4 / kWarps;
     const Request r = request_of<N>(a, s.x);
-    const int d = threadIdx.x, i = blockIdx.x;
-    for (int k = 0; k < kJoinRows; ++k) {
-        const int col = blockIdx.y * kJoinRows + k, row = s.z * N + col;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = (warp % kWarps) * 32 + lane, i = blockIdx.x, n = s.w - i + 1;
+    const float* const head = a.parts + (2 * (int64_t)i + 1) * kSlot;
+    const float* const tail = a.parts + 2 * (int64_t)i * kSlot;
+    auto part = [&](int j) { return j == 0 ? head : tail + 2 * j * kSlot; };
+    for (int col = blockIdx.y * kRows + warp / kWarps; col < N; col += gridDim.y * kRows) {
+        const int row = s.z * N + col;
         if (row >= r.rows) return;
-        auto slot = [&](int j) { return a.parts + (2 * (int64_t)j + (j == i ? 1 : 0)) * kSlot; };
         float m = -FLT_MAX;
-        for (int j = i; j <= s.w; ++j) m = fmaxf(m, slot(j)[N * DP + col]);
+        for (int j = lane; j < n; j += 32) m = fmaxf(m, part(j)[N * DP + col]);
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
         float l = 0.f, o = 0.f;
-        for (int j = i; j <= s.w; ++j) {
-            const float* p = slot(j);
-            const float f = exp2_fast(p[N * DP + col] - m);
-            l += p[N * DP + N + col] * f;
-            if (d < a.cache.head_dim) o += p[col * DP + d] * f;
+        for (int j0 = 0; j0 < n; j0 += 32) {
+            float f = 0.f;
+            if (j0 + lane < n) {
+                const float* p = part(j0 + lane) + N * DP + col;
+                f = exp2_fast(p[0] - m);
+                l += p[N] * f;
+            }
+            const int up = min(32, n - j0);
+#pragma unroll 8
+            for (int j = 0; j < up; ++j) {
+                const float fj = __shfl_sync(0xffffffffu, f, j);
+                o = fmaf(part(j0 + j)[col * DP + d], fj, o);
+            }
         }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
         const int j = row / a.group, g = row - j * a.group;
         const int64_t t = r.row0 + j, hq = s.y * a.group + g;
         const bool any = !(l == 0.f);
-        if (d < a.cache.head_dim) static_cast<T*>(a.out)[t * a.out_row + hq * a.out_head + d] = from_float<T>(any ? o / l : 0.f);
-        if (d == 0 && a.lse) a.lse[t * a.num_heads + hq] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        if (d < a.cache.head_dim) static_cast<T*>(a.out)[t * a.out_row + hq * a.out_head + d] = from_float<T>(any ? o * __frcp_rn(l) : 0.f);
+        if (d == 0 && a.lse) a.lse[t * a.num_heads + hq] = lse_of(any, m, l);
     }
 }
 
@@ -1014,7 +1051,7 @@ int sm_count()
 int row_tile(int32_t max_k, int32_t group)
 {
     const int64_t rows = (int64_t)(max_k + 1) * group;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 96 ? 96 : 128;
 }
 
 size_t split_bytes(int P) { return ((size_t)P * sizeof(int4) + 255) / 256 * 256; }
@@ -1063,15 +1100,27 @@ template <typename S> specdec_status_t launch(const Args& a, cudaStream_t stream
     constexpr int smem = 1024 + S::kSlots * S::kSlotBytes + 2 * S::kV16Bytes + S::kQ * S::kQBytes + S::kPBytes + S::kMiscBytes;
     static_assert(smem <= kSmemBytes, "shared memory");
     auto kernel = specdec_paged_attention_kernel<S>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    // the kernel's shared memory is allowed at its first launch (and again where a context has been reset since)
+    static std::atomic<uint64_t> allowed{0};             // devices, by bit
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
         (void)cudaGetLastError();
         return SPECDEC_ERR_CUDA;
     }
-    kernel<<<P, S::kThreads, smem, stream>>>(a, kmap, vmap);
-    if (cudaGetLastError() != cudaSuccess) return SPECDEC_ERR_CUDA;
+    const uint64_t bit = 1ull << (dev & 63);
+    for (int attempt = allowed.load() & bit ? 0 : 1;; ++attempt) {
+        if (attempt > 0 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return SPECDEC_ERR_CUDA;
+        }
+        kernel<<<P, S::kThreads, smem, stream>>>(a, kmap, vmap);
+        if (cudaGetLastError() == cudaSuccess) break;
+        if (attempt > 0) return SPECDEC_ERR_CUDA;
+    }
+    allowed |= bit;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)P, S::N / kJoinRows);
-    cfg.blockDim = dim3(S::DP);
+    cfg.gridDim = dim3((unsigned)P, 16);
+    cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1090,6 +1139,7 @@ template <typename T, bool kFp8, int DB> specdec_status_t launch_rows(const Args
     if (N == 16) return launch<Shape<T, kFp8, 16, DB>>(a, s, P);
     if (N == 32) return launch<Shape<T, kFp8, 32, DB>>(a, s, P);
     if (N == 64) return launch<Shape<T, kFp8, 64, DB>>(a, s, P);
+    if (N == 96) return launch<Shape<T, kFp8, 96, DB>>(a, s, P);
     return launch<Shape<T, kFp8, 128, DB>>(a, s, P);
 }
 

@@ -10,7 +10,7 @@ from . import _native
 PAGE_SIZES = (16, 32, 64, 128, 256)
 
 
-@dataclasses.dataclass
+@dataclasses.dataclass(frozen=True, eq=False)
 class PagedCache:
     """k, v: [num_pages, num_kv_heads, page_size, head_dim] CUDA tensors with the same strides and the
     elements of a head contiguous (a cache laid out slot by slot is passed as a permuted view):
@@ -33,8 +33,8 @@ class PagedCache:
             raise ValueError("k and v must be [num_pages, num_kv_heads, page_size, head_dim] of the same strides")
         if self.k.stride(3) != 1:
             raise ValueError("the elements of a head must be contiguous")
-        self.dtype = types[self.k.dtype]
-        quantised = self.dtype == _native.SPECDEC_E4M3
+        dtype = types[self.k.dtype]
+        quantised = dtype == _native.SPECDEC_E4M3
         for name, e in (("k_exp", self.k_exp), ("v_exp", self.v_exp)):
             if (e is not None) != quantised:
                 raise ValueError(f"{name} goes with an e4m3 cache")
@@ -44,19 +44,17 @@ class PagedCache:
             if t is not None and t.device != self.k.device:
                 raise ValueError("the cache's tensors must be on one device")
 
-    @property
-    def num_pages(self) -> int:
-        return self.k.shape[0]
-
-    @property
-    def page_size(self) -> int:
-        return self.k.shape[2]
+        n, heads, page, dim = self.k.shape
+        stride = self.k.stride()
+        struct = _native.KVCacheStruct(*(None if t is None else t.data_ptr() for t in (self.k, self.v, self.k_exp, self.v_exp)),
+                                       dtype, n, page, heads, dim, stride[0], stride[1], stride[2])
+        # the description is made once: the fields are frozen (the tensors' contents are not)
+        for name, value in (("dtype", dtype), ("num_pages", n), ("num_kv_heads", heads), ("page_size", page), ("head_dim", dim),
+                            ("device", self.k.get_device()), ("_struct", struct)):
+            object.__setattr__(self, name, value)
 
     def struct(self):
-        n, h, p, d = self.k.shape
-        s = self.k.stride()
-        return _native.KVCacheStruct(_native._p(self.k), _native._p(self.v), _native._p(self.k_exp), _native._p(self.v_exp),
-                                     self.dtype, n, p, h, d, s[0], s[1], s[2])
+        return self._struct
 
 
 def alloc(num_pages: int, num_kv_heads: int, page_size: int, head_dim: int, dtype, device="cuda") -> PagedCache:

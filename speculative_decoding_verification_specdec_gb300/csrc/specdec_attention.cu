@@ -19,7 +19,7 @@
  *
  * Warps: 4 per column group for the softmax (one lane quarter of tensor memory each), 4 or 8 that convert
  * an e4m3 cache (keys to f16 in tensor memory, values to f16 tiles in shared memory; both exact), one that
- * feeds TMA, one that issues the products, one to four that fetch Q, one that hands out the work.
+ * feeds TMA, one that issues the products, one that hands out the work and fetches Q.
  *
  * Bound by HBM: every visible key and value is read once per row block.
  */
@@ -169,28 +169,28 @@ template <typename T_, bool kFp8_, int N_, int DB_> struct Shape {
     static constexpr bool kFp8 = kFp8_;
     static constexpr bool kScaleQ = kFp8_ && std::is_same<T_, __nv_bfloat16>::value;
     static constexpr int N = N_, DB = DB_, DP = 64 * DB_;
-    static constexpr int kGroups = N >= 64 ? N / 32 : 1, NC = N / kGroups;
+    // softmax warps: kCol groups of NC columns, and for few columns two sets of them that take the tiles in turn
+    static constexpr int kCol = N >= 64 ? N / 32 : 1, NC = N / kCol, kPar = N <= 32 ? 2 : 1, kGroups = kPar * kCol;
     static constexpr int kQ = N >= 96 && DB == 2 ? 1 : 2;                // Q buffers
     static constexpr int kSoftWarps = 4 * kGroups, kConvWarps = !kFp8 ? 0 : N >= 64 ? 4 : 8;
-    static constexpr int kLoaders = N < 64 ? 1 : kFp8 ? 2 : 4;
-    static constexpr int kProducer = kSoftWarps + kConvWarps, kMma = kProducer + 1, kLoader = kProducer + 2,
-                         kScheduler = kLoader + kLoaders;
-    static constexpr int kThreads = 32 * (kScheduler + 1);
-    static constexpr int kTasks = 4;                                     // tasks between the scheduler and the slowest role
+    static constexpr int kProducer = kSoftWarps + kConvWarps, kMma = kProducer + 2, kLoader = kProducer + 3;
+    static constexpr int kThreads = 32 * (kLoader + 1);
+    static constexpr int kTasks = 4;                                     // tasks between the loader and the slowest role
     static constexpr int kSlotBytes = kTile * DP * (kFp8 ? 1 : 2);
     static constexpr int kQBytes = N * DP * 2, kPBytes = N * kTile * 2, kV16Bytes = kFp8 ? kTile * DP * 2 : 0;
     static constexpr int kMiscBytes = 12 * 1024;
-    static constexpr int kRoom = kSmemBytes - 1024 - kMiscBytes - kQ * kQBytes - kPBytes - 2 * kV16Bytes;
+    static constexpr int kRoom = kSmemBytes - 1024 - kMiscBytes - kQ * kQBytes - kPar * kPBytes - 2 * kV16Bytes;
     static constexpr int kSlots = kRoom / kSlotBytes > 12 ? 12 : kRoom / kSlotBytes;
-    static constexpr int kTmem = 3 * N + (kFp8 ? DP : 0);                // O, two S, two f16 key tiles
+    static constexpr int kKSlots = kSlots / 2, kVSlots = kSlots - kKSlots;
+    static constexpr int kTmem = (kPar + 2) * N + (kFp8 ? DP : 0);       // O, two S, two f16 key tiles
     static constexpr int kTmemColumns = kTmem <= 64 ? 64 : kTmem <= 128 ? 128 : kTmem <= 256 ? 256 : 512;
     static constexpr int kSlotFloats = N * (DP + 2);
-    static_assert(kSlots >= 3 && kTmem <= 512, "shape does not fit the SM");
+    static_assert(kKSlots >= 2 && kTmem <= 512, "shape does not fit the SM");
 };
 
 template <typename S> struct Misc {
     uint64_t full[S::kSlots], empty[S::kSlots];
-    uint64_t s_full[2], pv_done[2], p_full, done[2], q_full[2], q_empty[2], k16_full[2], v16_full[2];
+    uint64_t s_full[2], pv_done[2], p_full[2], done[2], q_full[2], q_empty[2], k16_full[2], v16_full[2];
     uint64_t task_full[S::kTasks], task_free[S::kTasks];
     Task task[S::kTasks];
     int64_t begin, end, base, units;
@@ -199,10 +199,10 @@ template <typename S> struct Misc {
     int expired;
     uint32_t tmem;
     uint32_t poison[2][4];                               // tokens of a tile whose values are taken one by one
-    alignas(16) float red[4][S::N];                                  // a column's value in each warp of its group
-    alignas(16) float fac[S::N];
-    float ref[S::N];
-    int red_e[4 * S::kGroups];
+    alignas(16) float red[S::kPar][4][S::N];                                  // a column's value in each warp of its group
+    alignas(16) float fac[S::kPar][S::N];
+    float ref[S::kPar][S::N];
+    int red_e[4 * S::kGroups], ref_e[S::kPar];
     alignas(16) int32_t last[2][S::N];                   // last token that a column sees (-1: no column)
     alignas(16) int2 place[2][S::N];                     // a column's row of q and out, and its query head (row -1: no column)
     alignas(16) int64_t out_at[2][S::N];                 // and where it lies in out
@@ -225,7 +225,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
     unsigned char* const v16 = ring + S::kSlots * S::kSlotBytes;
     unsigned char* const qbuf = v16 + 2 * S::kV16Bytes;
     unsigned char* const pbuf = qbuf + S::kQ * S::kQBytes;
-    Misc<S>& ms = *reinterpret_cast<Misc<S>*>(pbuf + S::kPBytes);
+    Misc<S>& ms = *reinterpret_cast<Misc<S>*>(pbuf + S::kPar * S::kPBytes);
     static_assert(sizeof(Misc<S>) <= S::kMiscBytes, "misc");
     static_assert(offsetof(Misc<S>, last) % 16 == 0 && offsetof(Misc<S>, qscale) % 16 == 0 && offsetof(Misc<S>, exps) % 16 == 0 &&
                   offsetof(Misc<S>, fac) % 16 == 0 && sizeof(Misc<S>) % 16 == 0, "8- and 16-byte accesses");
@@ -242,22 +242,22 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
     if (tid == 0) {
         for (int s = 0; s < S::kSlots; ++s) {
             bar_init(bar(ms.full[s]), 1);
-            bar_init(bar(ms.empty[s]), S::kFp8 ? 4 + S::kSoftWarps : 1);
+            bar_init(bar(ms.empty[s]), S::kFp8 ? 4 + 4 * S::kCol : 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(bar(ms.s_full[i]), 1);
             bar_init(bar(ms.pv_done[i]), 1);
+            bar_init(bar(ms.p_full[i]), 4 * S::kCol);
             bar_init(bar(ms.done[i]), S::kSoftWarps);
-            bar_init(bar(ms.q_full[i]), S::kLoaders);
+            bar_init(bar(ms.q_full[i]), 1);
             bar_init(bar(ms.q_empty[i]), 1);
             bar_init(bar(ms.k16_full[i]), 4);
             bar_init(bar(ms.v16_full[i]), 4);
         }
         for (int i = 0; i < S::kTasks; ++i) {
             bar_init(bar(ms.task_full[i]), 1);
-            bar_init(bar(ms.task_free[i]), S::kScheduler);           // every other warp
+            bar_init(bar(ms.task_free[i]), S::kThreads / 32);
         }
-        bar_init(bar(ms.p_full), S::kSoftWarps);
         ms.expired = 0;
         for (int i = 0; i < 8; ++i) ms.poison[i >> 2][i & 3] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -297,7 +297,10 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
     tmem_after();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = ms.tmem;
-    const uint32_t t_o = tmem, t_s = tmem + N, t_k = tmem + 3 * N;
+    const uint32_t t_o = tmem, t_s = tmem + S::kPar * N, t_k = t_s + 2 * N;
+    // ring slot of a tile's keys, and of its values
+    auto k_slot = [](uint32_t n) { return n % S::kKSlots; };
+    auto v_slot = [](uint32_t n) { return S::kKSlots + n % S::kVSlots; };
     // The next task, copied out of the scheduler's ring; false: none is left (or a wait has expired).
     auto take = [&](uint32_t q, Task& w) {
         const int s = q % S::kTasks;
@@ -312,23 +315,14 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
     Task w;
     if (tid == 0) a.split[blockIdx.x] = make_int4(-1, 0, 0, 0);         // this thread may fill it in below
 
-    if (warp == S::kScheduler) {
-        // ================================================================ tasks
-        Walker<N> walk(a, ms.begin, ms.end, ms.first_b, ms.base);
-        for (uint32_t q = 0;; ++q) {
-            const bool more = walk.next(w);
-            const int s = q % S::kTasks;
-            if (q >= (uint32_t)S::kTasks && !__all_sync(0xffffffffu, wait(ms.task_free[s], q / S::kTasks - 1))) break;
-            if (lane == 0) {
-                ms.task[s] = w;
-                bar_arrive(bar(ms.task_full[s]));
-            }
-            if (!more) break;
-        }
-    } else if (warp == S::kProducer) {
-        // ================================================================ keys and values into the ring
+    if (warp == S::kProducer || warp == S::kProducer + 1) {
+        // ================================================================ keys (one warp) and values (the other) into the ring
+        // (a page of 16 slots takes a copy of 2 KB; at about 90 cycles a copy one warp would hold up both streams)
+        const bool is_v = warp != S::kProducer;
         const int ps = c.page_size, rows = min(ps, kTile), pages = kTile / rows;
-        uint32_t n = 0;                                  // slots filled so far
+        const CUtensorMap* const map = is_v ? &vmap : &kmap;
+        const uint32_t slots = is_v ? S::kVSlots : S::kKSlots;
+        uint32_t n = 0;                                  // tiles so far
         for (uint32_t q = 0; take(q, w); ++q) {
             const int32_t len = w.cached + w.rows / a.group;
             const int32_t* const table = a.block_table + w.b * a.block_stride;
@@ -336,52 +330,56 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 const int32_t token = t * kTile + lane * rows;
                 return lane < pages && token < len ? __ldg(table + token / ps) : -1;
             };
-            auto used_of = [&](int t) {
-                return min(pages, (len - t * kTile + rows - 1) / rows);
+            auto first_slot = [&](int t) { return ps > kTile ? t * kTile % ps : 0; };
+            // e4m3: 16 of the tile's scales to each of eight lanes (scale 1 where there is no page)
+            auto scales_of = [&](int page, int t) {
+                uint4 x = make_uint4(0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f);
+                const int pg = __shfl_sync(0xffffffffu, page, (lane * 16 / rows) & 31);
+                if (lane < 8 && pg >= 0 && pg < c.num_pages)
+                    x = __ldg(reinterpret_cast<const uint4*>((is_v ? c.v_exp : c.k_exp) + ((int64_t)pg * H + w.h) * ps + first_slot(t) + lane * 16 % rows));
+                return x;
             };
             int page = page_of(w.t0);
-            for (int t = w.t0; t < w.t1; ++t) {
-                const int next_page = t + 1 < w.t1 ? page_of(t + 1) : 0;
-                const int used = used_of(t), slot0 = ps > kTile ? t * kTile % ps : 0;
+            [[maybe_unused]] uint4 scales;
+            if constexpr (S::kFp8) scales = scales_of(page, w.t0);
+#pragma unroll 1
+            for (int t = w.t0; t < w.t1; ++t, ++n) {
+                const int next_page = t + 1 < w.t1 ? page_of(t + 1) : -1;
+                const int used = min(pages, (len - t * kTile + rows - 1) / rows), slot0 = first_slot(t);
                 const bool bad = lane < used && (page < 0 || page >= c.num_pages);
                 if (bad && a.status) atomicOr(a.status + w.b, SPECDEC_ST_BAD_PAGE);
                 const int from = bad ? c.num_pages : page;      // past the end: the copy reads zeros
-#pragma unroll
-                for (int v = 0; v < 2; ++v, ++n) {
-                    const uint32_t s = n % S::kSlots;
-                    if (n >= (uint32_t)S::kSlots) wait(ms.empty[s], n / S::kSlots - 1);
-                    if (*expired) continue;
+                const uint32_t s = is_v ? v_slot(n) : k_slot(n);
+                if (n >= slots) wait(ms.empty[s], n / slots - 1);
+                if (!__any_sync(0xffffffffu, *expired)) {
                     const uint32_t fb = bar(ms.full[s]), dst = smem_u32(ring) + s * S::kSlotBytes;
-                    if (lane < used && S::kFp8 && bad) {
-                        for (int i = 0; i < rows; ++i) ms.exps[s][lane * rows + i] = 127;
-                        fence_async();
-                    }
-                    const uint32_t fine = __popc(__ballot_sync(0xffffffffu, lane < used && !bad));
-                    if (lane == 0) bar_expect(fb, used * rows * DP * (S::kFp8 ? 1 : 2) + (S::kFp8 ? fine * rows : 0));
+                    if constexpr (S::kFp8)
+                        if (lane < 8) *reinterpret_cast<uint4*>(&ms.exps[s][lane * 16]) = scales;
+                    __syncwarp();
+                    if (lane == 0) bar_expect(fb, used * rows * DP * (S::kFp8 ? 1 : 2));
                     __syncwarp();
                     if (lane < used) {
-                        const CUtensorMap* map = v ? &vmap : &kmap;
                         if constexpr (S::kFp8) {
                             tma_load_4d(dst + lane * rows * DP, map, fb, 0, slot0, w.h, from);
-                            if (!bad)
-                                bulk_load(smem_u32(&ms.exps[s][lane * rows]),
-                                          (v ? c.v_exp : c.k_exp) + ((int64_t)page * H + w.h) * ps + slot0, rows, fb);
                         } else {
 #pragma unroll
                             for (int d = 0; d < S::DB; ++d)
                                 tma_load_4d(dst + d * (kTile * 128) + lane * rows * 128, map, fb, d * 64, slot0, w.h, from);
                         }
                     }
+                    __syncwarp();
                 }
                 page = next_page;
+                if constexpr (S::kFp8)
+                    if (t + 1 < w.t1) scales = scales_of(page, t + 1);
             }
         }
         // nothing may still be on its way into shared memory when the CTA leaves
         __syncwarp();
         if (*expired && lane == 0) {
             const unsigned long long t0 = time_ns();
-            for (uint32_t i = n > (uint32_t)S::kSlots ? n - S::kSlots : 0; i < n; ++i)
-                while (!bar_test(bar(ms.full[i % S::kSlots]), (i / S::kSlots) & 1u) && time_ns() - t0 < kDrainNs) {}
+            for (uint32_t i = n > slots ? n - slots : 0; i < n; ++i)
+                while (!bar_test(bar(ms.full[is_v ? v_slot(i) : k_slot(i)]), (i / slots) & 1u) && time_ns() - t0 < kDrainNs) {}
         }
     } else if (warp == S::kMma) {
         // ================================================================ products
@@ -396,9 +394,9 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 const uint32_t qb = qi % S::kQ;
                 bool ok = true;
                 if (first) ok = wait(ms.q_full[qb], qi / S::kQ);
-                const uint32_t slot = 2 * i % S::kSlots;
+                const uint32_t slot = k_slot(i);
                 if constexpr (S::kFp8) ok = wait(ms.k16_full[i & 1], i >> 1) && ok;
-                else ok = wait(ms.full[slot], 2 * i / S::kSlots) && ok;
+                else ok = wait(ms.full[slot], i / S::kKSlots) && ok;
                 if (!ok || lane != 0) return;
                 tmem_after();
                 const uint32_t d = t_s + (i & 1) * N;
@@ -428,10 +426,10 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                     // the next scores before this tile's values; with one Q buffer the next item's wait for its turn
                     if (t + 1 < tiles) scores(n + 1, q, false, t + 2 == tiles);
                     else if (S::kQ == 2) start_next();
-                    bool ok = wait(ms.p_full, n);
-                    const uint32_t slot = (2 * n + 1) % S::kSlots;
+                    bool ok = wait(ms.p_full[n & 1], n >> 1);
+                    const uint32_t slot = v_slot(n), acc = t_o + n % S::kPar * N, pb = p0 + n % S::kPar * S::kPBytes;
                     if constexpr (S::kFp8) ok = wait(ms.v16_full[n & 1], n >> 1) && ok;
-                    else ok = wait(ms.full[slot], (2 * n + 1) / S::kSlots) && ok;
+                    else ok = wait(ms.full[slot], n / S::kVSlots) && ok;
                     if (t == 0 && q > 0) ok = wait(ms.done[(q - 1) & 1], (q - 1) >> 1) && ok;
                     if (ok && lane == 0) {
                         tmem_after();
@@ -440,7 +438,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                         constexpr uint32_t lead = S::DB == 2 ? kTile * 128 : 0;
 #pragma unroll
                         for (int k = 0; k < kTile / 16; ++k)
-                            mma_ss(t_o, operand(va + k * 2048, lead, 1024, kSwizzle128), operand(p0 + k * 256, 128, 2048, kNoSwizzle), dv, t > 0 || k > 0);
+                            mma_ss(acc, operand(va + k * 2048, lead, 1024, kSwizzle128), operand(pb + k * 256, 128, 2048, kNoSwizzle), dv, t >= S::kPar || k > 0);
                         mma_commit(bar(ms.pv_done[n & 1]));
                         if constexpr (!S::kFp8) mma_commit(bar(ms.empty[slot]));
                     }
@@ -452,19 +450,34 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             }
         }
         __syncwarp();
-    } else if (warp >= S::kLoader) {
-        // ================================================================ Q, its scales and its columns' places
-        const int lt = tid - 32 * S::kLoader;
-        constexpr int kLt = 32 * S::kLoaders;
-        auto together = [&]() {
-            if constexpr (S::kLoaders > 1) barrier_sync(8, kLt);
-            else __syncwarp();
+    } else if (warp == S::kLoader) {
+        // ================================================================ the tasks, a few ahead; Q, its scales and its columns' places
+        Walker<N> walk(a, ms.begin, ms.end, ms.first_b, ms.base);
+        uint32_t sent = 0;
+        bool more = true;
+        auto send = [&]() {
+            if (!more) return;
+            Task x;
+            more = walk.next(x);                         // (the last one says that no more come)
+            const int s = sent % S::kTasks;
+            if (sent >= (uint32_t)S::kTasks && !__all_sync(0xffffffffu, wait(ms.task_free[s], sent / S::kTasks - 1))) {
+                more = false;
+                return;
+            }
+            if (lane == 0) {
+                ms.task[s] = x;
+                bar_arrive(bar(ms.task_full[s]));
+            }
+            ++sent;
         };
+#pragma unroll 1
+        for (int i = 0; i < S::kTasks - 1; ++i) send();
+#pragma unroll 1
         for (uint32_t q = 0; take(q, w); ++q) {
             const uint32_t qb = q % S::kQ, tb = q & 1;
             if (q >= 2) wait(ms.done[tb], (q >> 1) - 1);                 // the tables' last item is done with
             if (q >= (uint32_t)S::kQ) wait(ms.q_empty[qb], q / S::kQ - 1);
-            for (int n = lt; n < N; n += kLt) {
+            for (int n = lane; n < N; n += 32) {
                 const int r = w.block * N + n, j = r / a.group, g = r - j * a.group;
                 const bool real = r < w.rows;
                 const int2 at = real ? make_int2(w.row0 + j, w.h * a.group + g) : make_int2(-1, 0);
@@ -473,28 +486,40 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 ms.last[tb][n] = real ? w.cached + j : -1;
                 if constexpr (S::kScaleQ) ms.top[n] = 0;
             }
-            together();
+            __syncwarp();
             unsigned char* const dst = qbuf + qb * S::kQBytes;
-            // 16-byte chunks, whole rows a batch, all of a batch's loads in flight together
-            constexpr int kChunks = N * (DP / 8) / kLt, kBatch = kChunks % 8 == 0 ? 8 : kChunks % 6 == 0 ? 6 : kChunks;
-            static_assert(kChunks * kLt == N * (DP / 8) && kChunks % kBatch == 0 && kBatch <= 8 && kBatch * kLt % DP == 0, "batches");
-#pragma unroll 1
-            for (int base = 0; base < kChunks; base += kBatch) {
-                uint4 v[kBatch];
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const int i = lt + kLt * (base + u), n = (i & 7) + 8 * (i / DP), ch = (i >> 3) % (DP / 8);
-                    const int2 at = ms.place[tb][n];
-                    v[u] = make_uint4(0, 0, 0, 0);
-                    if (at.x >= 0 && ch * 8 < c.head_dim)
-                        v[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + at.x * a.q_row + at.y * a.q_head + ch * 8);
+            constexpr int kChunks = N * (DP / 8) / 32;                   // of 16 bytes, a lane
+            // chunk i of this lane: its column, its place in the head, and where it comes from (nullptr: zeros)
+            auto column = [&](int i) { return (lane & 7) + 8 * ((lane + 32 * i) / DP); };
+            auto piece = [&](int i) { return ((lane + 32 * i) >> 3) % (DP / 8); };
+            auto source = [&](int i) -> const T* {
+                const int2 at = ms.place[tb][column(i)];
+                return at.x >= 0 && piece(i) * 8 < c.head_dim ? static_cast<const T*>(a.q) + at.x * a.q_row + at.y * a.q_head + piece(i) * 8 : nullptr;
+            };
+            auto target = [&](int i) { return dst + ((column(i) >> 3) * (DP / 8) + piece(i)) * 128 + (column(i) & 7) * 16; };
+            if constexpr (!S::kScaleQ) {
+#pragma unroll 4
+                for (int i = 0; i < kChunks; ++i) {
+                    const T* src = source(i);
+                    async_copy_16(smem_u32(target(i)), src ? src : static_cast<const T*>(a.q), src ? 16 : 0);
                 }
-                if constexpr (S::kScaleQ) {
+                async_copy_wait();
+            } else {
+                // whole rows a batch, all of a batch's loads in flight together
+                constexpr int kBatch = kChunks < 8 ? kChunks : 8;
+                static_assert(kChunks % kBatch == 0 && kBatch * 32 % DP == 0, "batches");
+#pragma unroll 1
+                for (int base = 0; base < kChunks; base += kBatch) {
+                    uint4 v[kBatch];
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) {
+                        const T* src = source(base + u);
+                        v[u] = src ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
+                    }
                     // a power of two brings the row's largest element to [2^13, 2^14): bf16's eight bits fit f16's
                     // eleven exactly, but for elements under 2^-28 of the largest
 #pragma unroll
                     for (int u = 0; u < kBatch; ++u) {
-                        const int i = lt + kLt * (base + u), n = (i & 7) + 8 * (i / DP);
                         const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
                         uint32_t top = 0;
 #pragma unroll
@@ -502,17 +527,15 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                             const uint32_t lo = x[k] << 16 & 0x7fffffffu, hi = x[k] & 0x7fff0000u;
                             top = max(top, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
                         }
-                        if (top) atomicMax(&ms.top[n], top);
+                        if (top) atomicMax(&ms.top[column(base + u)], top);
                     }
-                    together();
-                }
+                    __syncwarp();
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const int i = lt + kLt * (base + u), n = (i & 7) + 8 * (i / DP), ch = (i >> 3) % (DP / 8);
-                    if constexpr (S::kScaleQ) {
+                    for (int u = 0; u < kBatch; ++u) {
+                        const int n = column(base + u);
                         const int e = ms.top[n] ? max((int)(ms.top[n] >> 23) - 126, -100) : 14;
                         const float inv = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-                        if (ch == 0) ms.qscale[tb][n] = __uint_as_float((uint32_t)(127 + e - 14) << 23);
+                        if (piece(base + u) == 0) ms.qscale[tb][n] = __uint_as_float((uint32_t)(127 + e - 14) << 23);
                         const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&v[u]);
                         uint4 o;
                         __half2* y = reinterpret_cast<__half2*>(&o);
@@ -521,15 +544,14 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                             const float2 f = __bfloat1622float2(x[k]);
                             y[k] = __floats2half2_rn(f.x * inv, f.y * inv);
                         }
-                        v[u] = o;
+                        *reinterpret_cast<uint4*>(target(base + u)) = o;
                     }
-                    *reinterpret_cast<uint4*>(dst + ((n >> 3) * (DP / 8) + ch) * 128 + (n & 7) * 16) = v[u];
                 }
             }
             fence_async();
             __syncwarp();
             if (lane == 0) bar_arrive(bar(ms.q_full[qb]));
-            if constexpr (S::kScaleQ) together();        // top is read before the next item clears it
+            send();
         }
     } else if (S::kFp8 && warp >= S::kSoftWarps) {
         // ================================================================ e4m3 -> f16 (exact): four warps for K, four for V
@@ -537,8 +559,8 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         const uint32_t quarter = (uint32_t)(row & ~31) << 16;
         uint32_t n = 0;
         auto widen = [&](const int is_v) {
-            const uint32_t i = 2 * n + is_v, slot = i % S::kSlots;
-            wait(ms.full[slot], i / S::kSlots);
+            const uint32_t slot = is_v ? v_slot(n) : k_slot(n);
+            wait(ms.full[slot], n / (is_v ? S::kVSlots : S::kKSlots));
             const unsigned char* const src = ring + slot * S::kSlotBytes + row * DP;
             uint4 x[DP / 16];                            // 16 codes each
 #pragma unroll
@@ -551,17 +573,17 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                     asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
                         : "=r"(r[2 * k]), "=r"(r[2 * k + 1]) : "r"(codes[k]));
             };
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(ms.empty[slot]));
+            uint32_t r[DP / 32][16];                     // 32 codes each
+#pragma unroll
+            for (int ch = 0; ch < DP / 16; ++ch) half(x[ch], r[ch / 2] + 8 * (ch & 1));
             if (!is_v) {
                 // a token's elements along its lane of tensor memory, two to a column
                 if (n >= 2) wait(ms.s_full[n & 1], (n >> 1) - 1);        // S of tile n - 2 has read the buffer
                 tmem_after();
 #pragma unroll
-                for (int g = 0; g < DP / 32; ++g) {
-                    uint32_t r[16];
-                    half(x[2 * g], r);
-                    half(x[2 * g + 1], r + 8);
-                    tmem_st_32x16(t_k + quarter + (n & 1) * (DP / 2) + g * 16, r);
-                }
+                for (int g = 0; g < DP / 32; ++g) tmem_st_32x16(t_k + quarter + (n & 1) * (DP / 2) + g * 16, r[g]);
                 tmem_wait_st();
                 tmem_before();
             } else {
@@ -569,20 +591,14 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 if (n >= 2) wait(ms.pv_done[n & 1], (n >> 1) - 1);
                 unsigned char* const dst = v16 + (n & 1) * S::kV16Bytes + row * 128;
 #pragma unroll
-                for (int ch = 0; ch < DP / 16; ++ch) {
-                    uint32_t r[8];
-                    half(x[ch], r);
-                    unsigned char* const d = dst + (ch / 4) * (kTile * 128);
-                    *reinterpret_cast<uint4*>(d + ((2 * (ch % 4)) ^ (row & 7)) * 16) = make_uint4(r[0], r[1], r[2], r[3]);
-                    *reinterpret_cast<uint4*>(d + ((2 * (ch % 4) + 1) ^ (row & 7)) * 16) = make_uint4(r[4], r[5], r[6], r[7]);
+                for (int ch = 0; ch < DP / 8; ++ch) {
+                    const uint32_t* const y = r[ch / 4] + 4 * (ch & 3);
+                    *reinterpret_cast<uint4*>(dst + (ch / 8) * (kTile * 128) + ((ch % 8) ^ (row & 7)) * 16) = make_uint4(y[0], y[1], y[2], y[3]);
                 }
                 fence_async();
             }
             __syncwarp();
-            if (lane == 0) {
-                bar_arrive(is_v ? bar(ms.v16_full[n & 1]) : bar(ms.k16_full[n & 1]));
-                bar_arrive(bar(ms.empty[slot]));
-            }
+            if (lane == 0) bar_arrive(is_v ? bar(ms.v16_full[n & 1]) : bar(ms.k16_full[n & 1]));
         };
         for (uint32_t q = 0; take(q, w); ++q) {
 #pragma unroll 1
@@ -599,8 +615,10 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         }
     } else {
         // ================================================================ softmax
-        const int grp = warp >> 2, wq = warp & 3, gt = tid & 127;        // column group, lane quarter, thread of the group
-        const int col0 = grp * NC, id = 1 + grp;
+        const int wq = warp & 3, gt = tid & 127, grp = warp >> 2;        // lane quarter, thread of the group, group:
+        const int par = grp / S::kCol, cg = grp % S::kCol;               // which tiles, which columns
+        const int col0 = cg * NC, id = 1 + grp, id_par = 9 + par;        // barriers of the group, of the tile's groups
+        constexpr int kParThreads = 128 * S::kCol;
         const int tq = lane >> 2, cq = 2 * (lane & 3);                   // token and column within an 8 x 8 matrix
         const uint32_t quarter = (uint32_t)wq << 21;                     // lane 32 wq
         uint32_t n = 0;
@@ -620,12 +638,17 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             auto tile = [&](auto masked, const int t) {
                 constexpr bool kMasked = decltype(masked)::value;
                 const int32_t token0 = t * kTile;
-                [[maybe_unused]] const uint32_t ks = 2 * n % S::kSlots, vs = (2 * n + 1) % S::kSlots;
+                [[maybe_unused]] const uint32_t ks = k_slot(n), vs = v_slot(n);
+                const uint32_t acc = t_o + par * N + quarter + col0;
+                // the product before this one that reads P's buffer and adds to O
+                auto last_product = [&]() {
+                    if (t - S::kPar >= w.t0) wait(ms.pv_done[(n - S::kPar) & 1], (n - S::kPar) >> 1);
+                };
                 [[maybe_unused]] float kscale[4];
                 [[maybe_unused]] int ve[4];
                 if constexpr (S::kFp8) {
-                    wait(ms.full[ks], 2 * n / S::kSlots);
-                    wait(ms.full[vs], (2 * n + 1) / S::kSlots);
+                    wait(ms.full[ks], n / S::kKSlots);
+                    wait(ms.full[vs], n / S::kVSlots);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int tok = 32 * wq + 8 * i + tq;
@@ -710,7 +733,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                     }
                     if (tq == 0) {
 #pragma unroll
-                        for (int i = 0; i < NC / 4; ++i) ms.red[wq][col0 + 8 * (i >> 1) + cq + (i & 1)] = top[i];
+                        for (int i = 0; i < NC / 4; ++i) ms.red[par][wq][col0 + 8 * (i >> 1) + cq + (i & 1)] = top[i];
                     }
                     [[maybe_unused]] int e_new = E;
                     if constexpr (S::kFp8) {
@@ -731,11 +754,11 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
 #pragma unroll
                     for (int i = 0; i < NC / 4; ++i) {
                         const int col = col0 + 8 * (i >> 1) + cq + (i & 1);
-                        const float now = fmaxf(fmaxf(fmaxf(ms.red[0][col], ms.red[1][col]), fmaxf(ms.red[2][col], ms.red[3][col])), m[i]);
+                        const float now = fmaxf(fmaxf(fmaxf(ms.red[par][0][col], ms.red[par][1][col]), fmaxf(ms.red[par][2][col], ms.red[par][3][col])), m[i]);
                         const float f = exp2_fast(m[i] - now);
                         l[i] *= f;
                         m[i] = now;
-                        if (wq == 0 && tq == 0) ms.fac[col] = f * e_fac;
+                        if (wq == 0 && tq == 0) ms.fac[par][col] = f * e_fac;
                     }
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf)
@@ -744,25 +767,26 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
 #pragma unroll
                             for (int e = 0; e < 4; ++e) x[hf][r][e] -= m[2 * r + (e & 1)];
                     barrier_sync(id, 128);
-                    if (t > w.t0) {
+                    if (t - S::kPar >= w.t0) {
                         // O^T: this thread's lane is an element of the head, its columns the group's
-                        wait(ms.pv_done[(n - 1) & 1], (n - 1) >> 1);
+                        last_product();
                         tmem_after();
 #pragma unroll 1
                         for (int i = 0; i < NC; i += 16) {
                             float o[16];
                             uint32_t r[16];
-                            tmem_ld_32x16(t_o + quarter + col0 + i, o);
+                            tmem_ld_32x16(acc + i, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(o[k] * ms.fac[col0 + i + k]);
-                            tmem_st_32x16(t_o + quarter + col0 + i, r);
+                            for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(o[k] * ms.fac[par][col0 + i + k]);
+                            tmem_st_32x16(acc + i, r);
                         }
                         tmem_wait_st();
                     }
                 }
                 // weights, their sums, and P^T as the second product takes it: 8 x 8 blocks of 128 bytes
-                if (t > w.t0) wait(ms.pv_done[(n - 1) & 1], (n - 1) >> 1);
+                last_product();
+                unsigned char* const pt = pbuf + par * S::kPBytes;
                 [[maybe_unused]] float vw[4];
                 if constexpr (S::kFp8) {
 #pragma unroll
@@ -794,7 +818,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                             }
                         // matrices (r, tokens 0-7), (r, tokens 8-15), (r + 1, ..), (r + 1, ..) of this half
                         const int mi = lane >> 3, col_group = col0 / 8 + r + (mi >> 1), token_group = 4 * wq + 2 * hf + (mi & 1);
-                        store_matrices_t(smem_u32(pbuf) + (col_group * 16 + token_group) * 128 + (lane & 7) * 16, packed[0], packed[1],
+                        store_matrices_t(smem_u32(pt) + (col_group * 16 + token_group) * 128 + (lane & 7) * 16, packed[0], packed[1],
                                          packed[2], packed[3]);
                     }
                 bool poisoned = false;
@@ -807,10 +831,10 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                         wait(ms.v16_full[n & 1], n >> 1);
                         vt = v16 + (n & 1) * S::kV16Bytes;
                     } else {
-                        wait(ms.full[vs], (2 * n + 1) / S::kSlots);
+                        wait(ms.full[vs], n / S::kVSlots);
                         vt = ring + vs * S::kSlotBytes;
                     }
-                    if (grp == 0) {
+                    if (cg == 0) {
                         const int32_t tok = token0 + gt;
                         const bool none = tok > seen_any || tok < from_any, some = tok > seen_all || tok < from_all;
                         bool clear = none;
@@ -830,13 +854,13 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                                 *reinterpret_cast<uint4*>(vt + (ch / 8) * (kTile * 128) + gt * 128 + ((ch % 8) ^ (gt & 7)) * 16) = make_uint4(0, 0, 0, 0);
                         }
                     }
-                    barrier_sync(7, 128 * S::kGroups);
+                    barrier_sync(id_par, kParThreads);
                     poisoned = (pz[0] | pz[1] | pz[2] | pz[3]) != 0;
                 }
                 fence_async();
                 tmem_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(bar(ms.p_full));
+                if (lane == 0) bar_arrive(bar(ms.p_full[n & 1]));
                 if constexpr (kMasked) {
                     if (poisoned) {
                         wait(ms.pv_done[n & 1], n >> 1);
@@ -857,34 +881,35 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                             for (int i = 0; i < NC; i += 16) {
                                 float o[16];
                                 uint32_t r[16];
-                                tmem_ld_32x16(t_o + quarter + col0 + i, o);
+                                tmem_ld_32x16(acc + i, o);
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int k = 0; k < 16; ++k) {
                                     const int col = col0 + i + k, lt = ms.last[tb][col];
                                     const bool seen = tok <= lt && (a.window == 0 || tok > lt - a.window);
-                                    const float p = to_float<M>(*reinterpret_cast<const M*>(pbuf + ((col >> 3) * 16 + (tk >> 3)) * 128 + (col & 7) * 16 + (tk & 7) * 2));
+                                    const float p = to_float<M>(*reinterpret_cast<const M*>(pt + ((col >> 3) * 16 + (tk >> 3)) * 128 + (col & 7) * 16 + (tk & 7) * 2));
                                     r[k] = __float_as_uint(seen && p != 0.f ? fmaf(p, v, o[k]) : o[k]);
                                 }
-                                tmem_st_32x16(t_o + quarter + col0 + i, r);
+                                tmem_st_32x16(acc + i, r);
                                 tmem_wait_st();
                             }
                         }
-                        barrier_sync(7, 128 * S::kGroups);
-                        if (tid < 4) pz[tid] = 0;
-                        barrier_sync(7, 128 * S::kGroups);
+                        barrier_sync(id_par, kParThreads);
+                        if (cg == 0 && gt < 4) pz[gt] = 0;
+                        barrier_sync(id_par, kParThreads);
                         tmem_before();
                     }
                 }
             };
 #pragma unroll 1
             for (int t = w.t0; t < w.t1; ++t, ++n) {
+                if (S::kPar == 2 && (int)(n & 1) != par) continue;
                 const int32_t token0 = t * kTile;
                 if (token0 + kTile - 1 > seen_all || token0 < from_all) tile(std::true_type{}, t);
                 else tile(std::false_type{}, t);
             }
             // ---- the item's (part of) result
-            const uint32_t lastn = n - 1;
+            const uint32_t last_n = n - 1;
 #pragma unroll
             for (int i = 0; i < NC / 4; ++i) {
 #pragma unroll
@@ -894,43 +919,62 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
 #pragma unroll
                 for (int i = 0; i < NC / 4; ++i) {
                     const int col = col0 + 8 * (i >> 1) + cq + (i & 1);
-                    ms.red[wq][col] = l[i];
-                    if (wq == 0) ms.ref[col] = m[i];
+                    ms.red[par][wq][col] = l[i];
+                    if (wq == 0) ms.ref[par][col] = m[i];
                 }
             }
+            if (S::kFp8 && cg == 0 && gt == 0) ms.ref_e[par] = E;
             const bool whole = w.begin && w.end;
             float* const part = a.parts + (int64_t)(2 * blockIdx.x + (w.begin ? 1 : 0)) * S::kSlotFloats;
-            barrier_sync(id, 128);
-            if (gt < NC) {
-                const int col = col0 + gt;
-                const float sum = ms.red[0][col] + ms.red[1][col] + ms.red[2][col] + ms.red[3][col], ref = ms.ref[col];
+            barrier_sync(7, 128 * S::kGroups);
+            if (tid < N) {
+                // the column's sum, over both sets of tiles at one reference, and each set's factor for O
+                float ref = ms.ref[0][tid], sum = 0.f, f[S::kPar];
+                if constexpr (S::kPar == 2) ref = fmaxf(ref, ms.ref[1][tid]);
+#pragma unroll
+                for (int p = 0; p < S::kPar; ++p) {
+                    const float s = ms.red[p][0][tid] + ms.red[p][1][tid] + ms.red[p][2][tid] + ms.red[p][3][tid];
+                    f[p] = s == 0.f ? 0.f : S::kPar == 1 ? 1.f : exp2_fast(ms.ref[p][tid] - ref);
+                    sum += s == 0.f ? 0.f : s * f[p];
+                }
                 const bool any = !(sum == 0.f);                          // (a NaN sum is one)
-                float f = any ? (whole ? __frcp_rn(sum) : 1.f) : 0.f;
-                if (S::kFp8 && E >= -126) f *= __uint_as_float((uint32_t)(127 + E) << 23);
-                ms.fac[col] = f;
+#pragma unroll
+                for (int p = 0; p < S::kPar; ++p) {
+                    float y = f[p];
+                    if (S::kFp8 && ms.ref_e[p] >= -126) y *= __uint_as_float((uint32_t)(127 + ms.ref_e[p]) << 23);
+                    ms.fac[p][tid] = !any ? 0.f : whole ? y * __frcp_rn(sum) : y;
+                }
                 if (whole) {
-                    const int2 at = ms.place[tb][col];
+                    const int2 at = ms.place[tb][tid];
                     if (a.lse && at.x >= 0) a.lse[(int64_t)at.x * a.num_heads + at.y] = lse_of(any, ref, sum);
                 } else {
-                    part[N * DP + col] = ref;
-                    part[N * DP + N + col] = sum;
+                    part[N * DP + tid] = ref;
+                    part[N * DP + N + tid] = sum;
                 }
             }
-            wait(ms.pv_done[lastn & 1], lastn >> 1);
+            wait(ms.pv_done[last_n & 1], last_n >> 1);                   // (products end in order)
             tmem_after();
-            barrier_sync(id, 128);
+            barrier_sync(7, 128 * S::kGroups);
             const int d = gt;
+            constexpr int kEach = N / S::kGroups;                        // columns that a group writes
 #pragma unroll 1
-            for (int i = 0; i < NC; i += 16) {
-                float o[16];
-                tmem_ld_32x16(t_o + quarter + col0 + i, o);
+            for (int i = 0; i < kEach; i += 8) {
+                const int first = grp * kEach + i;
+                float o[S::kPar][8];
+#pragma unroll
+                for (int p = 0; p < S::kPar; ++p) tmem_ld_32x8(t_o + p * N + quarter + first, o[p]);
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const int col = col0 + i + k;
+                for (int k = 0; k < 8; ++k) {
+                    const int col = first + k;
                     const int64_t at = ms.out_at[tb][col];
                     if (at < 0 || d >= c.head_dim) continue;
-                    const float f = ms.fac[col], y = f == 0.f ? 0.f : o[k] * f;
+                    float y = 0.f;
+#pragma unroll
+                    for (int p = 0; p < S::kPar; ++p) {
+                        const float f = ms.fac[p][col];
+                        if (!(f == 0.f)) y += o[p][k] * f;               // (O is not set where its set had no tile)
+                    }
                     if (whole) static_cast<T*>(a.out)[at + d] = from_float<T>(y);
                     else part[col * DP + d] = y;
                 }
@@ -945,7 +989,6 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             tmem_before();
             __syncwarp();
             if (lane == 0) bar_arrive(bar(ms.done[q & 1]));
-            barrier_sync(id, 128);                                       // red and fac are read
         }
         // requests that the kernel does not take: their bits, and zeros in the rows that are known
         for (int b = blockIdx.x; b < a.B; b += P) {

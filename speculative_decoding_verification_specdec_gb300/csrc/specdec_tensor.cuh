@@ -91,11 +91,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
                  ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+// 16 bytes by this thread, of which `bytes` are read (the rest are zeros); then this thread's copies have landed.
+__device__ __forceinline__ void async_copy_16(uint32_t dst, const void* src, uint32_t bytes)
 {
-    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void async_copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Generic writes to shared memory become visible to the asynchronous proxy (tensor products, copies).
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -118,15 +119,7 @@ __device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::afte
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 16 lanes x 8 columns: thread t gets (lane t/4, columns 2(t%4), +1) and (lane t/4 + 8, the same).
-__device__ __forceinline__ void tmem_ld_16x8(uint32_t a, float (&x)[4])
-{
-    uint32_t r[4];
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(r[i]);
-}
-
+// 16 lanes x 16 columns: of each 8 columns thread t gets (lane t/4, columns 2(t%4), +1) and (lane t/4 + 8, the same).
 __device__ __forceinline__ void tmem_ld_16x16(uint32_t a, float (&x)[4], float (&y)[4])
 {
     uint32_t r[8];
@@ -136,7 +129,16 @@ __device__ __forceinline__ void tmem_ld_16x16(uint32_t a, float (&x)[4], float (
     for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(r[i]), y[i] = __uint_as_float(r[4 + i]);
 }
 
-// 32 lanes x 16 columns: thread t gets lane t.
+// 32 lanes x 8 (16) columns: thread t gets lane t.
+__device__ __forceinline__ void tmem_ld_32x8(uint32_t a, float (&x)[8])
+{
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(a));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r[i]);
+}
+
 __device__ __forceinline__ void tmem_ld_32x16(uint32_t a, float (&x)[16])
 {
     uint32_t r[16];

@@ -356,18 +356,21 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                     if constexpr (S::kFp8)
                         if (lane < 8) *reinterpret_cast<uint4*>(&ms.exps[s][lane * 16]) = scales;
                     __syncwarp();
-                    if (lane == 0) bar_expect(fb, used * rows * DP * (S::kFp8 ? 1 : 2));
-                    __syncwarp();
-                    if (lane < used) {
-                        if constexpr (S::kFp8) {
-                            tma_load_4d(dst + lane * rows * DP, map, fb, 0, slot0, w.h, from);
-                        } else {
+                    if (elected()) bar_expect(fb, used * rows * DP * (S::kFp8 ? 1 : 2));
+#pragma unroll 1
+                    for (int p = 0; p < used; ++p) {
+                        const int pg = __shfl_sync(0xffffffffu, from, p);
+                        if (elected()) {
+                            if constexpr (S::kFp8) {
+                                tma_load_4d(dst + p * rows * DP, map, fb, 0, slot0, w.h, pg);
+                            } else {
 #pragma unroll
-                            for (int d = 0; d < S::DB; ++d)
-                                tma_load_4d(dst + d * (kTile * 128) + lane * rows * 128, map, fb, d * 64, slot0, w.h, from);
+                                for (int d = 0; d < S::DB; ++d)
+                                    tma_load_4d(dst + d * (kTile * 128) + p * rows * 128, map, fb, d * 64, slot0, w.h, pg);
+                            }
                         }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
                 page = next_page;
                 if constexpr (S::kFp8)
@@ -397,16 +400,15 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 const uint32_t slot = k_slot(i);
                 if constexpr (S::kFp8) ok = wait(ms.k16_full[i & 1], i >> 1) && ok;
                 else ok = wait(ms.full[slot], i / S::kKSlots) && ok;
-                if (!ok || lane != 0) return;
+                if (!__all_sync(0xffffffffu, ok) || !elected()) return;
                 tmem_after();
-                const uint32_t d = t_s + (i & 1) * N;
+                const uint32_t d = t_s + (i & 1) * N, ka = t_k + (i & 1) * (DP / 2);
+                const uint64_t qo = operand(q0 + qb * S::kQBytes, 128, DP * 16, kNoSwizzle);
+                const uint64_t ko = operand(ring0 + slot * S::kSlotBytes, 0, 1024, kSwizzle128);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
-                    const uint64_t bq = operand(q0 + qb * S::kQBytes + k * 256, 128, DP * 16, kNoSwizzle);
-                    if constexpr (S::kFp8)
-                        mma_ts(d, t_k + (i & 1) * (DP / 2) + k * 8, bq, ds, k > 0);
-                    else
-                        mma_ss(d, operand(ring0 + slot * S::kSlotBytes + (k / 4) * (kTile * 128) + (k % 4) * 32, 0, 1024, kSwizzle128), bq, ds, k > 0);
+                    if constexpr (S::kFp8) mma_ts(d, ka + k * 8, qo + k * (256 >> 4), ds, k > 0);
+                    else mma_ss(d, ko + (k / 4) * (kTile * 128 >> 4) + (k % 4) * (32 >> 4), qo + k * (256 >> 4), ds, k > 0);
                 }
                 mma_commit(bar(ms.s_full[i & 1]));
                 if constexpr (!S::kFp8) mma_commit(bar(ms.empty[slot]));
@@ -431,14 +433,14 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                     if constexpr (S::kFp8) ok = wait(ms.v16_full[n & 1], n >> 1) && ok;
                     else ok = wait(ms.full[slot], n / S::kVSlots) && ok;
                     if (t == 0 && q > 0) ok = wait(ms.done[(q - 1) & 1], (q - 1) >> 1) && ok;
-                    if (ok && lane == 0) {
+                    if (__all_sync(0xffffffffu, ok) && elected()) {
                         tmem_after();
                         const uint32_t va = S::kFp8 ? v0 + (n & 1) * S::kV16Bytes : ring0 + slot * S::kSlotBytes;
                         // one block of 64 elements (DB = 1): the rows 64 .. 127 read the block again and are not used
                         constexpr uint32_t lead = S::DB == 2 ? kTile * 128 : 0;
+                        const uint64_t vo = operand(va, lead, 1024, kSwizzle128), po = operand(pb, 128, 2048, kNoSwizzle);
 #pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)
-                            mma_ss(acc, operand(va + k * 2048, lead, 1024, kSwizzle128), operand(pb + k * 256, 128, 2048, kNoSwizzle), dv, t >= S::kPar || k > 0);
+                        for (int k = 0; k < kTile / 16; ++k) mma_ss(acc, vo + k * (2048 >> 4), po + k * (256 >> 4), dv, t >= S::kPar || k > 0);
                         mma_commit(bar(ms.pv_done[n & 1]));
                         if constexpr (!S::kFp8) mma_commit(bar(ms.empty[slot]));
                     }

@@ -19,6 +19,15 @@ __device__ __forceinline__ unsigned long long time_ns()
     return t;
 }
 
+// One lane of a converged warp, always the same: what it alone executes keeps its operands in uniform registers
+// (a branch on the lane's number costs a move for each operand of each instruction).
+__device__ __forceinline__ bool elected()
+{
+    uint32_t one;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+    return one != 0;
+}
+
 // ---------------------------------------------------------------- mbarriers
 
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)

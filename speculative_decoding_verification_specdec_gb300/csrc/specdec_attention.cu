@@ -73,7 +73,7 @@ struct Request {
     __device__ __forceinline__ int64_t units(int heads) const { return (int64_t)heads * blocks * tiles; }
 };
 
-template <int N> __device__ __forceinline__ Request request_of(const Args& a, int b)
+template <int N> __device__ __noinline__ Request request_of(const Args& a, int b)
 {
     Request r = {0, 0, 0, 0, 0, 0, 0};
     if (!offsets_ok(a.cu, a.B, b)) {
@@ -98,7 +98,7 @@ template <int N> __device__ __forceinline__ Request request_of(const Args& a, in
 
 // The first unit of CTA i. With fewer units than CTAs the first ones take one each, so that no CTA between two
 // parts of an item is without a part.
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y)       // x, y >= 0; 32-bit division where it will do
+__device__ __noinline__ int64_t quotient(int64_t x, int64_t y)           // x, y >= 0; 32-bit division where it will do
 {
     return (x | y) >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
 }
@@ -132,6 +132,7 @@ template <int N> struct Walker {
         w.b = -1;
         if (u >= u_end) return false;
         const int H = a.cache.num_kv_heads;
+#pragma unroll 1
         while (u >= base + r.units(H)) {
             base += r.units(H);
             r = request_of<N>(a, ++b);
@@ -240,10 +241,12 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
 
     // ---- set-up: barriers, tensor memory, the CTA's units
     if (tid == 0) {
+#pragma unroll 1
         for (int s = 0; s < S::kSlots; ++s) {
             bar_init(bar(ms.full[s]), 1);
             bar_init(bar(ms.empty[s]), S::kFp8 ? 4 + 4 * S::kCol : 1);
         }
+#pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             bar_init(bar(ms.s_full[i]), 1);
             bar_init(bar(ms.pv_done[i]), 1);
@@ -267,6 +270,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         // every thread sums the units of consecutive requests, a scan over the threads places them
         const int per = (a.B + S::kThreads - 1) / S::kThreads, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
         int64_t mine = 0;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) mine += request_of<N>(a, b).units(H);
         int64_t upto = mine;
 #pragma unroll
@@ -277,6 +281,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         if (lane == 31) ms.warp_units[warp] = upto;
         __syncthreads();
         int64_t before = upto - mine, units = 0;
+#pragma unroll 1
         for (int w = 0; w < S::kThreads / 32; ++w) {
             if (w < warp) before += ms.warp_units[w];
             units += ms.warp_units[w];
@@ -322,65 +327,93 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         const int ps = c.page_size, rows = min(ps, kTile), pages = kTile / rows;
         const CUtensorMap* const map = is_v ? &vmap : &kmap;
         const uint32_t slots = is_v ? S::kVSlots : S::kKSlots;
-        uint32_t n = 0;                                  // tiles so far
-        for (uint32_t q = 0; take(q, w); ++q) {
-            const int32_t len = w.cached + w.rows / a.group;
-            const int32_t* const table = a.block_table + w.b * a.block_stride;
-            auto page_of = [&](int t) -> int {           // this lane's page of tile t (-1: none)
-                const int32_t token = t * kTile + lane * rows;
-                return lane < pages && token < len ? __ldg(table + token / ps) : -1;
-            };
-            auto first_slot = [&](int t) { return ps > kTile ? t * kTile % ps : 0; };
-            // e4m3: 16 of the tile's scales to each of eight lanes (scale 1 where there is no page)
-            auto scales_of = [&](int page, int t) {
-                uint4 x = make_uint4(0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f);
-                const int pg = __shfl_sync(0xffffffffu, page, (lane * 16 / rows) & 31);
-                if (lane < 8 && pg >= 0 && pg < c.num_pages)
-                    x = __ldg(reinterpret_cast<const uint4*>((is_v ? c.v_exp : c.k_exp) + ((int64_t)pg * H + w.h) * ps + first_slot(t) + lane * 16 % rows));
-                return x;
-            };
-            int page = page_of(w.t0);
-            [[maybe_unused]] uint4 scales;
-            if constexpr (S::kFp8) scales = scales_of(page, w.t0);
-#pragma unroll 1
-            for (int t = w.t0; t < w.t1; ++t, ++n) {
-                const int next_page = t + 1 < w.t1 ? page_of(t + 1) : -1;
-                const int used = min(pages, (len - t * kTile + rows - 1) / rows), slot0 = first_slot(t);
-                const bool bad = lane < used && (page < 0 || page >= c.num_pages);
-                if (bad && a.status) atomicOr(a.status + w.b, SPECDEC_ST_BAD_PAGE);
-                const int from = bad ? c.num_pages : page;      // past the end: the copy reads zeros
-                const uint32_t s = is_v ? v_slot(n) : k_slot(n);
-                if (n >= slots) wait(ms.empty[s], n / slots - 1);
-                if (!__any_sync(0xffffffffu, *expired)) {
-                    const uint32_t fb = bar(ms.full[s]), dst = smem_u32(ring) + s * S::kSlotBytes;
-                    if constexpr (S::kFp8)
-                        if (lane < 8) *reinterpret_cast<uint4*>(&ms.exps[s][lane * 16]) = scales;
-                    __syncwarp();
-                    if (elected()) bar_expect(fb, used * rows * DP * (S::kFp8 ? 1 : 2));
-#pragma unroll 1
-                    for (int p = 0; p < used; ++p) {
-                        const int pg = __shfl_sync(0xffffffffu, from, p);
-                        if (elected()) {
-                            if constexpr (S::kFp8) {
-                                tma_load_4d(dst + p * rows * DP, map, fb, 0, slot0, w.h, pg);
-                            } else {
-#pragma unroll
-                                for (int d = 0; d < S::DB; ++d)
-                                    tma_load_4d(dst + d * (kTile * 128) + p * rows * 128, map, fb, d * 64, slot0, w.h, pg);
-                            }
-                        }
-                        __syncwarp();
-                    }
+        // A tile on its way: the page ids are read three tiles before its copies are issued and an e4m3 tile's scales
+        // two (each a read from memory that the next step waits for), across the ends of tasks.
+        struct Ahead {
+            int page, used, h, slot0, b;                 // this lane's page id; pages (0: no more tiles), head, first slot
+        };
+        uint32_t q = 0, n = 0;                           // tasks so far, tiles issued
+        int t = 0, t_end = 0, len = 0;
+        bool more = true;
+        auto look = [&]() {
+            Ahead x = {-1, 0, 0, 0, 0};
+            if (t == t_end && more) {
+                more = take(q++, w);
+                if (more) {
+                    t = w.t0;
+                    t_end = w.t1;
+                    len = w.cached + w.rows / a.group;
                 }
-                page = next_page;
+            }
+            if (!more) return x;
+            const int32_t token = t * kTile + lane * rows;
+            x.used = min(pages, (len - t * kTile + rows - 1) / rows);
+            x.h = w.h;
+            x.b = w.b;
+            x.slot0 = ps > kTile ? t * kTile % ps : 0;
+            if (lane < x.used) x.page = __ldg(a.block_table + w.b * a.block_stride + token / ps);
+            ++t;
+            return x;
+        };
+        // 16 of the tile's scales to each of eight lanes (scale 1 where there is no page)
+        auto scales_of = [&](const Ahead& x) {
+            uint4 e = make_uint4(0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f);
+            if constexpr (S::kFp8) {
+                const int pg = __shfl_sync(0xffffffffu, x.page, (lane * 16 / rows) & 31);
+                if (lane < 8 && pg >= 0 && pg < c.num_pages)
+                    e = __ldg(reinterpret_cast<const uint4*>((is_v ? c.v_exp : c.k_exp) + ((int64_t)pg * H + x.h) * ps + x.slot0 + lane * 16 % rows));
+            }
+            return e;
+        };
+        Ahead x0, x1, x2 = {-1, 0, 0, 0, 0};
+        [[maybe_unused]] uint4 e0, e1;
+#pragma unroll 1
+        for (int k = 0;; ++k) {                          // (the first three rounds only look ahead)
+            const Ahead x3 = look();
+            [[maybe_unused]] const uint4 e2 = scales_of(x2);
+            if (k >= 3) {
+            if (x0.used == 0) break;
+            const bool bad = lane < x0.used && (x0.page < 0 || x0.page >= c.num_pages);
+            if (bad && a.status) atomicOr(a.status + x0.b, SPECDEC_ST_BAD_PAGE);
+            const int from = bad ? c.num_pages : x0.page;       // past the end: the copy reads zeros
+            const uint32_t s = is_v ? v_slot(n) : k_slot(n);
+            if (n >= slots) wait(ms.empty[s], n / slots - 1);
+            if (!__any_sync(0xffffffffu, *expired)) {
+                const uint32_t fb = bar(ms.full[s]), dst = smem_u32(ring) + s * S::kSlotBytes;
                 if constexpr (S::kFp8)
-                    if (t + 1 < w.t1) scales = scales_of(page, t + 1);
+                    if (lane < 8) *reinterpret_cast<uint4*>(&ms.exps[s][lane * 16]) = e0;
+                __syncwarp();
+                if (elected()) bar_expect(fb, x0.used * rows * DP * (S::kFp8 ? 1 : 2));
+#pragma unroll 1
+                for (int p = 0; p < x0.used; ++p) {
+                    const int pg = __shfl_sync(0xffffffffu, from, p);
+                    if (elected()) {
+                        if constexpr (S::kFp8) {
+                            tma_load_4d(dst + p * rows * DP, map, fb, 0, x0.slot0, x0.h, pg);
+                        } else {
+#pragma unroll
+                            for (int d = 0; d < S::DB; ++d)
+                                tma_load_4d(dst + d * (kTile * 128) + p * rows * 128, map, fb, d * 64, x0.slot0, x0.h, pg);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            ++n;
+            }
+            x0 = x1;
+            x1 = x2;
+            x2 = x3;
+            if constexpr (S::kFp8) {
+                e0 = e1;
+                e1 = e2;
             }
         }
         // nothing may still be on its way into shared memory when the CTA leaves
         __syncwarp();
         if (*expired && lane == 0) {
             const unsigned long long t0 = time_ns();
+#pragma unroll 1
             for (uint32_t i = n > slots ? n - slots : 0; i < n; ++i)
                 while (!bar_test(bar(ms.full[is_v ? v_slot(i) : k_slot(i)]), (i / slots) & 1u) && time_ns() - t0 < kDrainNs) {}
         }
@@ -389,66 +422,70 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         {
             constexpr int kBf16 = std::is_same<M, __nv_bfloat16>::value;
             constexpr uint32_t ds = product(kBf16, 0, 128, N), dv = product(kBf16, 1, 128, N);
-            uint32_t n = 0;                              // tiles of the CTA
-            uint32_t q = 0;                              // items
             const uint32_t ring0 = smem_u32(ring), p0 = smem_u32(pbuf), q0 = smem_u32(qbuf), v0 = smem_u32(v16);
-            // S of tile i (the CTA's numbering) with item number qi
-            auto scores = [&](uint32_t i, uint32_t qi, bool first, bool last) {
-                const uint32_t qb = qi % S::kQ;
-                bool ok = true;
-                if (first) ok = wait(ms.q_full[qb], qi / S::kQ);
-                const uint32_t slot = k_slot(i);
-                if constexpr (S::kFp8) ok = wait(ms.k16_full[i & 1], i >> 1) && ok;
-                else ok = wait(ms.full[slot], i / S::kKSlots) && ok;
-                if (!__all_sync(0xffffffffu, ok) || !elected()) return;
-                tmem_after();
-                const uint32_t d = t_s + (i & 1) * N, ka = t_k + (i & 1) * (DP / 2);
-                const uint64_t qo = operand(q0 + qb * S::kQBytes, 128, DP * 16, kNoSwizzle);
-                const uint64_t ko = operand(ring0 + slot * S::kSlotBytes, 0, 1024, kSwizzle128);
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
-                    if constexpr (S::kFp8) mma_ts(d, ka + k * 8, qo + k * (256 >> 4), ds, k > 0);
-                    else mma_ss(d, ko + (k / 4) * (kTile * 128 >> 4) + (k % 4) * (32 >> 4), qo + k * (256 >> 4), ds, k > 0);
-                }
-                mma_commit(bar(ms.s_full[i & 1]));
-                if constexpr (!S::kFp8) mma_commit(bar(ms.empty[slot]));
-                if (last) mma_commit(bar(ms.q_empty[qb]));
-            };
+            // The scores of tile n + 1, then the values' product of tile n (the CTA's numbering; t, t1: the later tile's
+            // in its task). With one Q buffer the scores of a new task come after the product.
+            uint32_t q = 0;                              // the later tile's task
+            int t = 0, since = 0;                        // since: tiles of the earlier one's task before it
+            uint32_t q_was = 0;
             bool more = take(0, w);
-            if (more) scores(0, 0, true, w.t1 - w.t0 == 1);
-            while (more) {
-                const int tiles = w.t1 - w.t0;
-                Task after;
-                bool follows = false;
-                auto start_next = [&]() {
-                    follows = take(q + 1, after);
-                    if (follows) scores(n + 1, q + 1, true, after.t1 - after.t0 == 1);
-                };
-                for (int t = 0; t < tiles; ++t, ++n) {
-                    // the next scores before this tile's values; with one Q buffer the next item's wait for its turn
-                    if (t + 1 < tiles) scores(n + 1, q, false, t + 2 == tiles);
-                    else if (S::kQ == 2) start_next();
-                    bool ok = wait(ms.p_full[n & 1], n >> 1);
-                    const uint32_t slot = v_slot(n), acc = t_o + n % S::kPar * N, pb = p0 + n % S::kPar * S::kPBytes;
-                    if constexpr (S::kFp8) ok = wait(ms.v16_full[n & 1], n >> 1) && ok;
-                    else ok = wait(ms.full[slot], n / S::kVSlots) && ok;
-                    if (t == 0 && q > 0) ok = wait(ms.done[(q - 1) & 1], (q - 1) >> 1) && ok;
-                    if (__all_sync(0xffffffffu, ok) && elected()) {
-                        tmem_after();
-                        const uint32_t va = S::kFp8 ? v0 + (n & 1) * S::kV16Bytes : ring0 + slot * S::kSlotBytes;
-                        // one block of 64 elements (DB = 1): the rows 64 .. 127 read the block again and are not used
-                        constexpr uint32_t lead = S::DB == 2 ? kTile * 128 : 0;
-                        const uint64_t vo = operand(va, lead, 1024, kSwizzle128), po = operand(pb, 128, 2048, kNoSwizzle);
+            t = w.t0;
+#pragma unroll 1
+            for (int64_t n = -1;; ++n) {
+                const bool late = S::kQ == 1 && n >= 0 && t == w.t0;
+                const uint32_t i = (uint32_t)(n + 1);
+#pragma unroll 1
+                for (int step = 0; step < 2; ++step) {
+                    if ((step == 0) != late) {
+                        if (!more) continue;
+                        const uint32_t qb = q % S::kQ, slot = k_slot(i);
+                        bool ok = true;
+                        if (t == w.t0) ok = wait(ms.q_full[qb], q / S::kQ);
+                        if constexpr (S::kFp8) ok = wait(ms.k16_full[i & 1], i >> 1) && ok;
+                        else ok = wait(ms.full[slot], i / S::kKSlots) && ok;
+                        if (__all_sync(0xffffffffu, ok) && elected()) {
+                            tmem_after();
+                            const uint32_t d = t_s + (i & 1) * N, ka = t_k + (i & 1) * (DP / 2);
+                            const uint64_t qo = operand(q0 + qb * S::kQBytes, 128, DP * 16, kNoSwizzle);
+                            const uint64_t ko = operand(ring0 + slot * S::kSlotBytes, 0, 1024, kSwizzle128);
 #pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k) mma_ss(acc, vo + k * (2048 >> 4), po + k * (256 >> 4), dv, t >= S::kPar || k > 0);
-                        mma_commit(bar(ms.pv_done[n & 1]));
-                        if constexpr (!S::kFp8) mma_commit(bar(ms.empty[slot]));
+                            for (int k = 0; k < DP / 16; ++k) {
+                                if constexpr (S::kFp8) mma_ts(d, ka + k * 8, qo + k * (256 >> 4), ds, k > 0);
+                                else mma_ss(d, ko + (k / 4) * (kTile * 128 >> 4) + (k % 4) * (32 >> 4), qo + k * (256 >> 4), ds, k > 0);
+                            }
+                            mma_commit(bar(ms.s_full[i & 1]));
+                            if constexpr (!S::kFp8) mma_commit(bar(ms.empty[slot]));
+                            if (t + 1 == w.t1) mma_commit(bar(ms.q_empty[qb]));
+                        }
+                        __syncwarp();
+                    } else {
+                        if (n < 0) continue;
+                        const uint32_t j = (uint32_t)n, slot = v_slot(j), acc = t_o + j % S::kPar * N, pb = p0 + j % S::kPar * S::kPBytes;
+                        bool ok = wait(ms.p_full[j & 1], j >> 1);
+                        if constexpr (S::kFp8) ok = wait(ms.v16_full[j & 1], j >> 1) && ok;
+                        else ok = wait(ms.full[slot], j / S::kVSlots) && ok;
+                        if (since == 0 && q_was > 0) ok = wait(ms.done[(q_was - 1) & 1], (q_was - 1) >> 1) && ok;
+                        if (__all_sync(0xffffffffu, ok) && elected()) {
+                            tmem_after();
+                            const uint32_t va = S::kFp8 ? v0 + (j & 1) * S::kV16Bytes : ring0 + slot * S::kSlotBytes;
+                            // one block of 64 elements (DB = 1): the rows 64 .. 127 read the block again and are not used
+                            constexpr uint32_t lead = S::DB == 2 ? kTile * 128 : 0;
+                            const uint64_t vo = operand(va, lead, 1024, kSwizzle128), po = operand(pb, 128, 2048, kNoSwizzle);
+#pragma unroll
+                            for (int k = 0; k < kTile / 16; ++k) mma_ss(acc, vo + k * (2048 >> 4), po + k * (256 >> 4), dv, since >= S::kPar || k > 0);
+                            mma_commit(bar(ms.pv_done[j & 1]));
+                            if constexpr (!S::kFp8) mma_commit(bar(ms.empty[slot]));
+                        }
+                        __syncwarp();
                     }
-                    if (t + 1 == tiles && S::kQ == 1) start_next();
                 }
-                more = follows;
-                w = after;
-                ++q;
+                if (!more) break;
+                since = t - w.t0;
+                q_was = q;
+                if (++t == w.t1) {
+                    more = take(++q, w);
+                    t = w.t0;
+                }
             }
         }
         __syncwarp();
@@ -473,12 +510,15 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             ++sent;
         };
 #pragma unroll 1
-        for (int i = 0; i < S::kTasks - 1; ++i) send();
-#pragma unroll 1
-        for (uint32_t q = 0; take(q, w); ++q) {
+        for (uint32_t i = 0;; ++i) {
+            send();
+            if (i + 1 < (uint32_t)S::kTasks - 1) continue;               // the first tasks before the first Q
+            const uint32_t q = i + 2 - S::kTasks;
+            if (!take(q, w)) break;
             const uint32_t qb = q % S::kQ, tb = q & 1;
             if (q >= 2) wait(ms.done[tb], (q >> 1) - 1);                 // the tables' last item is done with
             if (q >= (uint32_t)S::kQ) wait(ms.q_empty[qb], q / S::kQ - 1);
+#pragma unroll 1
             for (int n = lane; n < N; n += 32) {
                 const int r = w.block * N + n, j = r / a.group, g = r - j * a.group;
                 const bool real = r < w.rows;
@@ -553,7 +593,6 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             fence_async();
             __syncwarp();
             if (lane == 0) bar_arrive(bar(ms.q_full[qb]));
-            send();
         }
     } else if (S::kFp8 && warp >= S::kSoftWarps) {
         // ================================================================ e4m3 -> f16 (exact): four warps for K, four for V
@@ -993,16 +1032,19 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             if (lane == 0) bar_arrive(bar(ms.done[q & 1]));
         }
         // requests that the kernel does not take: their bits, and zeros in the rows that are known
+#pragma unroll 1
         for (int b = blockIdx.x; b < a.B; b += P) {
             const Request r = request_of<N>(a, b);
             if (!r.fault) continue;
             if (tid == 0 && a.status) atomicOr(a.status + b, r.fault);
             if (r.fault == SPECDEC_ST_BAD_OFFSETS) continue;
             const int64_t k1 = (int64_t)a.cu[b + 1] - a.cu[b] + 1;
+#pragma unroll 1
             for (int64_t i = tid; i < k1 * a.num_heads; i += 128 * S::kGroups) {
-                const int64_t row = r.row0 + i / a.num_heads, hq = i % a.num_heads;
+                const int64_t row = r.row0 + quotient(i, a.num_heads), hq = i - quotient(i, a.num_heads) * a.num_heads;
                 if (a.lse) a.lse[row * a.num_heads + hq] = -INFINITY;
                 T* out = static_cast<T*>(a.out) + row * a.out_row + hq * a.out_head;
+#pragma unroll 1
                 for (int d = 0; d < c.head_dim; d += 8) *reinterpret_cast<uint4*>(out + d) = make_uint4(0, 0, 0, 0);
             }
         }
@@ -1013,6 +1055,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
     if (*expired && tid == 0 && a.status && ms.begin < ms.end) {
         // every request that the CTA has a unit of
         int64_t base = ms.base;
+#pragma unroll 1
         for (int b = ms.first_b; b < a.B && base < ms.end; ++b) {
             const int64_t n = request_of<N>(a, b).units(H);
             if (n > 0) atomicOr(a.status + b, SPECDEC_ST_DEVICE_TIMEOUT);

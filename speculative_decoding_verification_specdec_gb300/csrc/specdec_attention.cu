@@ -12,9 +12,9 @@
  * (in log2), so that the common tile needs no maximum across lanes, only a vote, and O^T, which
  * stays in tensor memory, is rarely rescaled. exp2(c S - m) <= 2^8 is exact to its rounding whatever m is.
  *
- * Work. Units of one tile of one (request, key-value head, row block) are numbered through the batch; CTA i
- * of P takes the units [W i / P, W (i+1) / P): every CTA the same number of tiles whatever the lengths,
- * without the host knowing them. A CTA that holds only part of an item writes (m, l, O) to its
+ * Work. The tiles of every (request, key-value head, row block) are numbered through the batch, each such
+ * item preceded by kItem units for what it costs to start and end it; CTA i of P takes the i-th of P equal
+ * runs of units, whatever the lengths and without the host knowing them. A CTA that holds only part of an item writes (m, l, O) to its
  * workspace slot, and specdec_paged_join_kernel joins the parts in the order of the CTAs.
  *
  * Warps: 4 per column group for the softmax (one lane quarter of tensor memory each), 4 or 8 that convert
@@ -39,8 +39,9 @@ namespace {
 using namespace specdec;
 
 constexpr int kTile = 128;                               // tokens
+constexpr int kItem = 3;                                 // what starting and ending an item costs, in tiles
 constexpr float kLazy = 8.f;                             // how far (log2) a score may pass the reference
-constexpr unsigned long long kWaitNs = 2000000000ull;    // a wait's default limit
+constexpr uint32_t kWaitNs = 2000000000u;                // a wait's default limit
 constexpr unsigned long long kDrainNs = 1000000000ull;   // more time for copies in flight before a CTA leaves
 constexpr int kSmemBytes = 227 * 1024;
 
@@ -60,7 +61,7 @@ struct Args {
     uint32_t* status;
     int4* split;                                         // [P]: the item that CTA i leaves to the next ones
     float* parts;                                        // [2 P] slots of N (D + 2) floats
-    unsigned long long wait_ns;
+    uint32_t wait_ns;
 };
 
 // ---------------------------------------------------------------- the batch's units
@@ -70,7 +71,7 @@ struct Request {
     int32_t row0, rows, blocks;                          // first row, rows a key-value head, row blocks
     int32_t first_tile, tiles;
     uint32_t fault;
-    __device__ __forceinline__ int64_t units(int heads) const { return (int64_t)heads * blocks * tiles; }
+    __device__ __forceinline__ int64_t units(int heads) const { return tiles ? (int64_t)heads * blocks * (tiles + kItem) : 0; }
 };
 
 template <int N> __device__ __noinline__ Request request_of(const Args& a, int b)
@@ -129,6 +130,13 @@ template <int N> struct Walker {
     }
     __device__ __forceinline__ bool next(Task& w)
     {
+        do {
+            if (!step(w)) return false;
+        } while (w.t1 <= w.t0);
+        return true;
+    }
+    __device__ __forceinline__ bool step(Task& w)
+    {
         w.b = -1;
         if (u >= u_end) return false;
         const int H = a.cache.num_kv_heads;
@@ -137,24 +145,32 @@ template <int N> struct Walker {
             base += r.units(H);
             r = request_of<N>(a, ++b);
         }
-        const int64_t local = u - base, item = quotient(local, r.tiles);
-        const int tile = (int)(local - item * r.tiles);
-        const int n = (int)min((int64_t)(r.tiles - tile), u_end - u);
+        const int per = r.tiles + kItem;
+        const int64_t local = u - base, item = quotient(local, per);
+        const int at = (int)(local - item * per), tile = max(at - kItem, 0);
+        const int n = (int)min((int64_t)(per - at), u_end - u);
+        u += n;
         w.b = b;
         w.h = (int)quotient(item, r.blocks);
         w.block = (int)(item - (int64_t)w.h * r.blocks);
         w.t0 = r.first_tile + tile;
-        w.t1 = w.t0 + n;
+        w.t1 = r.first_tile + at + n - kItem;            // (t0 or less: none of the item's tiles are the CTA's)
         w.begin = tile == 0;
-        w.end = tile + n == r.tiles;
+        w.end = at + n == per;
         w.row0 = r.row0;
         w.rows = r.rows;
         w.cached = (int32_t)r.cached;
-        w.last_unit = base + item * r.tiles + r.tiles - 1;
-        u += n;
+        w.last_unit = base + item * per + per - 1;
         return true;
     }
 };
+
+// Whether either of two packed values has all bits of its exponent set: one more there carries into the sign's place.
+template <typename M> __device__ __forceinline__ uint32_t not_finite(uint32_t two)
+{
+    constexpr uint32_t kOne = std::is_same<M, __half>::value ? 0x04000400u : 0x00800080u;
+    return ((two & 0x7fff7fffu) + kOne) & 0x80008000u;
+}
 
 // ln of the sum of a column's weights: log2's approximation is off by 2^-22 at most
 __device__ __forceinline__ float lse_of(bool any, float ref, float sum)
@@ -176,10 +192,16 @@ template <typename T_, bool kFp8_, int N_, int DB_> struct Shape {
     static constexpr int kSoftWarps = 4 * kGroups, kConvWarps = !kFp8 ? 0 : N >= 64 ? 4 : 8;
     static constexpr int kProducer = kSoftWarps + kConvWarps, kMma = kProducer + 2, kLoader = kProducer + 3;
     static constexpr int kThreads = 32 * (kLoader + 1);
-    static constexpr int kTasks = 4;                                     // tasks between the loader and the slowest role
+    static constexpr int kAhead = kFp8 ? 4 : 2;                          // tiles that the copies look ahead
+    // Tasks between the loader and the slowest role. The copies of a tile are issued once the tile kAhead further is
+    // known, which may be as many tasks further, and the loader hands out a task only when the task kTasks before is
+    // taken and, before it, fetches the Q of one that waits for the item two before to end: which needs the copies
+    // of at most two items after that. kAhead + 4 tasks keep the two from waiting for one another.
+    static constexpr int kTasks = 8;
+    static_assert(kTasks >= kAhead + 4, "tasks ahead");
     static constexpr int kSlotBytes = kTile * DP * (kFp8 ? 1 : 2);
     static constexpr int kQBytes = N * DP * 2, kPBytes = N * kTile * 2, kV16Bytes = kFp8 ? kTile * DP * 2 : 0;
-    static constexpr int kMiscBytes = 12 * 1024;
+    static constexpr int kMiscBytes = 13 * 1024;
     static constexpr int kRoom = kSmemBytes - 1024 - kMiscBytes - kQ * kQBytes - kPar * kPBytes - 2 * kV16Bytes;
     static constexpr int kSlots = kRoom / kSlotBytes > 12 ? 12 : kRoom / kSlotBytes;
     static constexpr int kKSlots = kSlots / 2, kVSlots = kSlots - kKSlots;
@@ -327,8 +349,8 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         const int ps = c.page_size, rows = min(ps, kTile), pages = kTile / rows;
         const CUtensorMap* const map = is_v ? &vmap : &kmap;
         const uint32_t slots = is_v ? S::kVSlots : S::kKSlots;
-        // A tile on its way: the page ids are read three tiles before its copies are issued and an e4m3 tile's scales
-        // two (each a read from memory that the next step waits for), across the ends of tasks.
+        // A tile on its way. Its page ids are read two tiles before its copies are issued; an e4m3 tile's four tiles
+        // before, and its scales (which wait for the ids) two. Tasks follow one another without a break.
         struct Ahead {
             int page, used, h, slot0, b;                 // this lane's page id; pages (0: no more tiles), head, first slot
         };
@@ -365,49 +387,49 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             }
             return e;
         };
-        Ahead x0, x1, x2 = {-1, 0, 0, 0, 0};
-        [[maybe_unused]] uint4 e0, e1;
-#pragma unroll 1
-        for (int k = 0;; ++k) {                          // (the first three rounds only look ahead)
-            const Ahead x3 = look();
-            [[maybe_unused]] const uint4 e2 = scales_of(x2);
-            if (k >= 3) {
-            if (x0.used == 0) break;
-            const bool bad = lane < x0.used && (x0.page < 0 || x0.page >= c.num_pages);
-            if (bad && a.status) atomicOr(a.status + x0.b, SPECDEC_ST_BAD_PAGE);
-            const int from = bad ? c.num_pages : x0.page;       // past the end: the copy reads zeros
-            const uint32_t s = is_v ? v_slot(n) : k_slot(n);
-            if (n >= slots) wait(ms.empty[s], n / slots - 1);
-            if (!__any_sync(0xffffffffu, *expired)) {
-                const uint32_t fb = bar(ms.full[s]), dst = smem_u32(ring) + s * S::kSlotBytes;
-                if constexpr (S::kFp8)
-                    if (lane < 8) *reinterpret_cast<uint4*>(&ms.exps[s][lane * 16]) = e0;
-                __syncwarp();
-                if (elected()) bar_expect(fb, x0.used * rows * DP * (S::kFp8 ? 1 : 2));
-#pragma unroll 1
-                for (int p = 0; p < x0.used; ++p) {
-                    const int pg = __shfl_sync(0xffffffffu, from, p);
-                    if (elected()) {
-                        if constexpr (S::kFp8) {
-                            tma_load_4d(dst + p * rows * DP, map, fb, 0, x0.slot0, x0.h, pg);
-                        } else {
+        constexpr int kAhead = S::kAhead;
+        Ahead x[kAhead + 1];
+        [[maybe_unused]] uint4 e[3];
 #pragma unroll
-                            for (int d = 0; d < S::DB; ++d)
-                                tma_load_4d(dst + d * (kTile * 128) + p * rows * 128, map, fb, d * 64, x0.slot0, x0.h, pg);
-                        }
-                    }
+        for (int i = 0; i < kAhead; ++i) x[i] = {-1, 0, 0, 0, 0};
+#pragma unroll 1
+        for (int k = 0;; ++k) {                          // (the first rounds only look ahead)
+            const Ahead& x0 = x[0];
+            x[kAhead] = look();
+            if constexpr (S::kFp8) e[2] = scales_of(x[2]);
+            if (k >= kAhead) {
+                if (x0.used == 0) break;
+                const bool bad = lane < x0.used && (x0.page < 0 || x0.page >= c.num_pages);
+                if (bad && a.status) atomicOr(a.status + x0.b, SPECDEC_ST_BAD_PAGE);
+                const int from = bad ? c.num_pages : x0.page;       // past the end: the copy reads zeros
+                const uint32_t s = is_v ? v_slot(n) : k_slot(n);
+                if (n >= slots) wait(ms.empty[s], n / slots - 1);
+                if (!__any_sync(0xffffffffu, *expired)) {
+                    const uint32_t fb = bar(ms.full[s]), dst = smem_u32(ring) + s * S::kSlotBytes;
+                    if constexpr (S::kFp8)
+                        if (lane < 8) *reinterpret_cast<uint4*>(&ms.exps[s][lane * 16]) = e[0];
                     __syncwarp();
+                    if (elected()) bar_expect(fb, x0.used * rows * DP * (S::kFp8 ? 1 : 2));
+#pragma unroll 1
+                    for (int p = 0; p < x0.used; ++p) {
+                        const int pg = __shfl_sync(0xffffffffu, from, p);
+                        if (elected()) {
+                            if constexpr (S::kFp8) {
+                                tma_load_4d(dst + p * rows * DP, map, fb, 0, x0.slot0, x0.h, pg);
+                            } else {
+#pragma unroll
+                                for (int d = 0; d < S::DB; ++d)
+                                    tma_load_4d(dst + d * (kTile * 128) + p * rows * 128, map, fb, d * 64, x0.slot0, x0.h, pg);
+                            }
+                        }
+                        __syncwarp();
+                    }
                 }
+                ++n;
             }
-            ++n;
-            }
-            x0 = x1;
-            x1 = x2;
-            x2 = x3;
-            if constexpr (S::kFp8) {
-                e0 = e1;
-                e1 = e2;
-            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) x[i] = x[i + 1];
+            if constexpr (S::kFp8) e[0] = e[1], e[1] = e[2];
         }
         // nothing may still be on its way into shared memory when the CTA leaves
         __syncwarp();
@@ -883,9 +905,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
 #pragma unroll 2
                             for (int ch = 0; ch < DP / 8; ++ch) {
                                 const uint4 v4 = *reinterpret_cast<const uint4*>(vt + (ch / 8) * (kTile * 128) + gt * 128 + (((ch % 8) ^ (gt & 7)) * 16));
-                                const M* e = reinterpret_cast<const M*>(&v4);
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) clear = clear || !isfinite(to_float<M>(e[k]));
+                                clear = clear || (not_finite<M>(v4.x) | not_finite<M>(v4.y) | not_finite<M>(v4.z) | not_finite<M>(v4.w)) != 0;
                             }
                             if (clear) atomicOr(&pz[wq], 1u << lane);
                         }
@@ -1005,19 +1025,24 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
 #pragma unroll
                 for (int p = 0; p < S::kPar; ++p) tmem_ld_32x8(t_o + p * N + quarter + first, o[p]);
                 tmem_wait_ld();
+                // (every read before the first write, and no branch between them)
+                int64_t at[8];
+                float y[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int col = first + k;
-                    const int64_t at = ms.out_at[tb][col];
-                    if (at < 0 || d >= c.head_dim) continue;
-                    float y = 0.f;
+                    at[k] = ms.out_at[tb][first + k];
+                    y[k] = 0.f;
 #pragma unroll
                     for (int p = 0; p < S::kPar; ++p) {
-                        const float f = ms.fac[p][col];
-                        if (!(f == 0.f)) y += o[p][k] * f;               // (O is not set where its set had no tile)
+                        const float f = ms.fac[p][first + k];
+                        y[k] += f == 0.f ? 0.f : o[p][k] * f;            // (O is not set where its set had no tile)
                     }
-                    if (whole) static_cast<T*>(a.out)[at + d] = from_float<T>(y);
-                    else part[col * DP + d] = y;
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const bool mine = at[k] >= 0 && d < c.head_dim;
+                    if (whole && mine) static_cast<T*>(a.out)[at[k] + d] = from_float<T>(y[k]);
+                    if (!whole && mine) part[(first + k) * DP + d] = y[k];
                 }
             }
             if (tid == 0 && w.begin && !w.end) {
@@ -1276,7 +1301,7 @@ extern "C" specdec_status_t specdec_paged_attention(
     const Args a = {q, out, lse, num_heads, group, q_row_stride, q_head_stride, out_row_stride, out_head_stride, *cache,
                     block_table, block_stride, max_blocks, cached_len, cu_num_draft, B, max_k, window, scale * 1.4426950408889634f,
                     status, static_cast<int4*>(workspace), reinterpret_cast<float*>(static_cast<char*>(workspace) + split_bytes(P)),
-                    wait_limit_us < 0 ? kWaitNs : (unsigned long long)wait_limit_us * 1000ull};
+                    wait_limit_us < 0 ? kWaitNs : (uint32_t)wait_limit_us * 1000u};
     const int N = row_tile(max_k, group);
     return dtype == SPECDEC_BF16 ? launch_type<__nv_bfloat16>(a, N, (cudaStream_t)stream, P) : launch_type<__half>(a, N, (cudaStream_t)stream, P);
 }

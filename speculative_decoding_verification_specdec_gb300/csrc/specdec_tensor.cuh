@@ -63,25 +63,19 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
 
 // Waits for the phase of that parity, at most limit_ns; on expiry, and at once when another wait of
 // the CTA has expired, returns false with *expired set. Callers then go on without issuing work.
-// The polling is a call: inlined at some fifty places it made the attention's kernels 120 to 180 KB of
-// code, more than the instruction caches hold.
-__device__ __noinline__ bool bar_poll(uint32_t bar, uint32_t parity, unsigned long long limit_ns, volatile int* expired)
+// (Some forty places inline it: it is kept short.)
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t limit_ns, volatile int* expired)
 {
-    const bool poll = limit_ns < 1000000ull;             // try_wait may sleep for longer than so short a limit
+    if (limit_ns >= 1000000u ? bar_try(bar, parity) : bar_test(bar, parity)) return true;   // (try_wait may sleep)
     const unsigned long long t0 = time_ns();
     while (true) {
-        if (poll ? bar_test(bar, parity) : bar_try(bar, parity)) return true;
         if (*expired) return false;
         if (time_ns() - t0 >= limit_ns) {
             *expired = 1;
             return false;
         }
+        if (bar_try(bar, parity)) return true;
     }
-}
-
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns, volatile int* expired)
-{
-    return bar_test(bar, parity) || bar_poll(bar, parity, limit_ns, expired);
 }
 
 // The threads of one named barrier agree on whether any of them has p set.

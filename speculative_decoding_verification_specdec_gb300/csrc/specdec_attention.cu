@@ -182,14 +182,16 @@ __device__ __forceinline__ float lse_of(bool any, float ref, float sum)
 
 template <typename T_, bool kFp8_, int N_, int DB_> struct Shape {
     using T = T_;                                        // type of q and out
-    using M = std::conditional_t<kFp8_, __half, T_>;     // type of the products' operands
+    using M = std::conditional_t<kFp8_, __half, T_>;     // type of the second product's operands
     static constexpr bool kFp8 = kFp8_;
-    static constexpr bool kScaleQ = kFp8_ && std::is_same<T_, __nv_bfloat16>::value;
+    // e4m3 keys are multiplied by Q as e4m3 too, taken apart into pieces whose sum it is: four significant bits
+    // each (and the sign of the rest), so two for bf16's eight and three for f16's eleven
+    static constexpr int kPieces = std::is_same<T_, __nv_bfloat16>::value ? 2 : 3;
     static constexpr int N = N_, DB = DB_, DP = 64 * DB_;
     // softmax warps: kCol groups of NC columns, and for few columns two sets of them that take the tiles in turn
     static constexpr int kCol = N >= 64 ? N / 32 : 1, NC = N / kCol, kPar = N <= 32 ? 2 : 1, kGroups = kPar * kCol;
     static constexpr int kQ = N >= 96 && DB == 2 ? 1 : 2;                // Q buffers
-    static constexpr int kSoftWarps = 4 * kGroups, kConvWarps = !kFp8 ? 0 : N >= 64 ? 4 : 8;
+    static constexpr int kSoftWarps = 4 * kGroups, kConvWarps = kFp8 ? 4 : 0;
     static constexpr int kProducer = kSoftWarps + kConvWarps, kMma = kProducer + 2, kLoader = kProducer + 3;
     static constexpr int kThreads = 32 * (kLoader + 1);
     static constexpr int kAhead = kFp8 ? 4 : 2;                          // tiles that the copies look ahead
@@ -200,12 +202,12 @@ template <typename T_, bool kFp8_, int N_, int DB_> struct Shape {
     static constexpr int kTasks = 8;
     static_assert(kTasks >= kAhead + 4, "tasks ahead");
     static constexpr int kSlotBytes = kTile * DP * (kFp8 ? 1 : 2);
-    static constexpr int kQBytes = N * DP * 2, kPBytes = N * kTile * 2, kV16Bytes = kFp8 ? kTile * DP * 2 : 0;
+    static constexpr int kQBytes = N * DP * (kFp8 ? kPieces : 2), kPBytes = N * kTile * 2, kV16Bytes = kFp8 ? kTile * DP * 2 : 0;
     static constexpr int kMiscBytes = 13 * 1024;
     static constexpr int kRoom = kSmemBytes - 1024 - kMiscBytes - kQ * kQBytes - kPar * kPBytes - 2 * kV16Bytes;
     static constexpr int kSlots = kRoom / kSlotBytes > 12 ? 12 : kRoom / kSlotBytes;
     static constexpr int kKSlots = kSlots / 2, kVSlots = kSlots - kKSlots;
-    static constexpr int kTmem = (kPar + 2) * N + (kFp8 ? DP : 0);       // O, two S, two f16 key tiles
+    static constexpr int kTmem = (kPar + 2) * N;                         // O, two S
     static constexpr int kTmemColumns = kTmem <= 64 ? 64 : kTmem <= 128 ? 128 : kTmem <= 256 ? 256 : 512;
     static constexpr int kSlotFloats = N * (DP + 2);
     static_assert(kKSlots >= 2 && kTmem <= 512, "shape does not fit the SM");
@@ -213,7 +215,7 @@ template <typename T_, bool kFp8_, int N_, int DB_> struct Shape {
 
 template <typename S> struct Misc {
     uint64_t full[S::kSlots], empty[S::kSlots];
-    uint64_t s_full[2], pv_done[2], p_full[2], done[2], q_full[2], q_empty[2], k16_full[2], v16_full[2];
+    uint64_t s_full[2], pv_done[2], p_full[2], done[2], q_full[2], q_empty[2], v16_full[2], drained;
     uint64_t task_full[S::kTasks], task_free[S::kTasks];
     Task task[S::kTasks];
     int64_t begin, end, base, units;
@@ -229,8 +231,8 @@ template <typename S> struct Misc {
     alignas(16) int32_t last[2][S::N];                   // last token that a column sees (-1: no column)
     alignas(16) int2 place[2][S::N];                     // a column's row of q and out, and its query head (row -1: no column)
     alignas(16) int64_t out_at[2][S::N];                 // and where it lies in out
-    uint32_t top[S::kScaleQ ? S::N : 1];                 // bits of the largest magnitude of a row of Q
-    alignas(16) float qscale[2][S::kScaleQ ? S::N : 4];
+    uint32_t top[S::kFp8 ? S::N : 1];                 // bits of the largest magnitude of a row of Q
+    alignas(16) float qscale[2][S::kFp8 ? S::N : 4];
     alignas(16) uint8_t exps[S::kSlots][S::kFp8 ? kTile : 16];
 };
 
@@ -266,7 +268,8 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
 #pragma unroll 1
         for (int s = 0; s < S::kSlots; ++s) {
             bar_init(bar(ms.full[s]), 1);
-            bar_init(bar(ms.empty[s]), S::kFp8 ? 4 + 4 * S::kCol : 1);
+            // given back by the product that read it; of e4m3 also by the softmax (the scales), values by the converters
+            bar_init(bar(ms.empty[s]), !S::kFp8 ? 1 : s < S::kKSlots ? 1 + 4 * S::kCol : 4 + 4 * S::kCol);
         }
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
@@ -276,13 +279,13 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             bar_init(bar(ms.done[i]), S::kSoftWarps);
             bar_init(bar(ms.q_full[i]), 1);
             bar_init(bar(ms.q_empty[i]), 1);
-            bar_init(bar(ms.k16_full[i]), 4);
             bar_init(bar(ms.v16_full[i]), 4);
         }
         for (int i = 0; i < S::kTasks; ++i) {
             bar_init(bar(ms.task_full[i]), 1);
             bar_init(bar(ms.task_free[i]), S::kThreads / 32);
         }
+        bar_init(bar(ms.drained), 1);
         ms.expired = 0;
         for (int i = 0; i < 8; ++i) ms.poison[i >> 2][i & 3] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -324,7 +327,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
     tmem_after();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = ms.tmem;
-    const uint32_t t_o = tmem, t_s = tmem + S::kPar * N, t_k = t_s + 2 * N;
+    const uint32_t t_o = tmem, t_s = tmem + S::kPar * N;
     // ring slot of a tile's keys, and of its values
     auto k_slot = [](uint32_t n) { return n % S::kKSlots; };
     auto v_slot = [](uint32_t n) { return S::kKSlots + n % S::kVSlots; };
@@ -443,7 +446,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         // ================================================================ products
         {
             constexpr int kBf16 = std::is_same<M, __nv_bfloat16>::value;
-            constexpr uint32_t ds = product(kBf16, 0, 128, N), dv = product(kBf16, 1, 128, N);
+            constexpr uint32_t ds = product(S::kFp8 ? 0 : kBf16, 0, 128, N), dv = product(kBf16, 1, 128, N);
             const uint32_t ring0 = smem_u32(ring), p0 = smem_u32(pbuf), q0 = smem_u32(qbuf), v0 = smem_u32(v16);
             // The scores of tile n + 1, then the values' product of tile n (the CTA's numbering; t, t1: the later tile's
             // in its task). With one Q buffer the scores of a new task come after the product.
@@ -463,20 +466,28 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                         const uint32_t qb = q % S::kQ, slot = k_slot(i);
                         bool ok = true;
                         if (t == w.t0) ok = wait(ms.q_full[qb], q / S::kQ);
-                        if constexpr (S::kFp8) ok = wait(ms.k16_full[i & 1], i >> 1) && ok;
-                        else ok = wait(ms.full[slot], i / S::kKSlots) && ok;
+                        ok = wait(ms.full[slot], i / S::kKSlots) && ok;
                         if (__all_sync(0xffffffffu, ok) && elected()) {
                             tmem_after();
-                            const uint32_t d = t_s + (i & 1) * N, ka = t_k + (i & 1) * (DP / 2);
-                            const uint64_t qo = operand(q0 + qb * S::kQBytes, 128, DP * 16, kNoSwizzle);
-                            const uint64_t ko = operand(ring0 + slot * S::kSlotBytes, 0, 1024, kSwizzle128);
+                            const uint32_t d = t_s + (i & 1) * N;
+                            if constexpr (S::kFp8) {
+                                // 16 elements to 16 bytes of a row; the pieces of Q one after the other into the same sums
+                                const uint64_t qo = operand(q0 + qb * S::kQBytes, 128, DP * 8, kNoSwizzle);
+                                const uint64_t ko = operand(ring0 + slot * S::kSlotBytes, 0, DP * 8, DP == 128 ? kSwizzle128 : kSwizzle64);
 #pragma unroll
-                            for (int k = 0; k < DP / 16; ++k) {
-                                if constexpr (S::kFp8) mma_ts(d, ka + k * 8, qo + k * (256 >> 4), ds, k > 0);
-                                else mma_ss(d, ko + (k / 4) * (kTile * 128 >> 4) + (k % 4) * (32 >> 4), qo + k * (256 >> 4), ds, k > 0);
+                                for (int p = 0; p < S::kPieces; ++p)
+#pragma unroll
+                                    for (int k = 0; k < DP / 32; ++k)
+                                        mma_ss_e4m3(d, ko + k * (32 >> 4), qo + p * (N * DP >> 4) + k * (256 >> 4), ds, p > 0 || k > 0);
+                            } else {
+                                const uint64_t qo = operand(q0 + qb * S::kQBytes, 128, DP * 16, kNoSwizzle);
+                                const uint64_t ko = operand(ring0 + slot * S::kSlotBytes, 0, 1024, kSwizzle128);
+#pragma unroll
+                                for (int k = 0; k < DP / 16; ++k)
+                                    mma_ss(d, ko + (k / 4) * (kTile * 128 >> 4) + (k % 4) * (32 >> 4), qo + k * (256 >> 4), ds, k > 0);
                             }
                             mma_commit(bar(ms.s_full[i & 1]));
-                            if constexpr (!S::kFp8) mma_commit(bar(ms.empty[slot]));
+                            mma_commit(bar(ms.empty[slot]));
                             if (t + 1 == w.t1) mma_commit(bar(ms.q_empty[qb]));
                         }
                         __syncwarp();
@@ -548,7 +559,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 ms.place[tb][n] = at;
                 ms.out_at[tb][n] = real ? at.x * a.out_row + at.y * a.out_head : -1;
                 ms.last[tb][n] = real ? w.cached + j : -1;
-                if constexpr (S::kScaleQ) ms.top[n] = 0;
+                if constexpr (S::kFp8) ms.top[n] = 0;
             }
             __syncwarp();
             unsigned char* const dst = qbuf + qb * S::kQBytes;
@@ -561,7 +572,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 return at.x >= 0 && piece(i) * 8 < c.head_dim ? static_cast<const T*>(a.q) + at.x * a.q_row + at.y * a.q_head + piece(i) * 8 : nullptr;
             };
             auto target = [&](int i) { return dst + ((column(i) >> 3) * (DP / 8) + piece(i)) * 128 + (column(i) & 7) * 16; };
-            if constexpr (!S::kScaleQ) {
+            if constexpr (!S::kFp8) {
 #pragma unroll 4
                 for (int i = 0; i < kChunks; ++i) {
                     const T* src = source(i);
@@ -580,35 +591,47 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                         const T* src = source(base + u);
                         v[u] = src ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
                     }
-                    // a power of two brings the row's largest element to [2^13, 2^14): bf16's eight bits fit f16's
-                    // eleven exactly, but for elements under 2^-28 of the largest
+                    // A power of two brings the row's largest magnitude to [128, 256): a piece is the nearest e4m3 number to
+                    // what the pieces before it leave, in all exact to 2^-10, e4m3's half step at its smallest, so to
+                    // 2^-17 of the row's largest element at worst. What is not finite becomes NaN.
 #pragma unroll
                     for (int u = 0; u < kBatch; ++u) {
-                        const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-                        uint32_t top = 0;
+                        const T* y = reinterpret_cast<const T*>(&v[u]);
+                        float top = 0.f;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t lo = x[k] << 16 & 0x7fffffffu, hi = x[k] & 0x7fff0000u;
-                            top = max(top, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
+                        for (int k = 0; k < 8; ++k) {
+                            const float z = fabsf(to_float<T>(y[k]));
+                            top = fmaxf(top, z < INFINITY ? z : 0.f);
                         }
-                        if (top) atomicMax(&ms.top[column(base + u)], top);
+                        if (top > 0.f) atomicMax(&ms.top[column(base + u)], __float_as_uint(top));
                     }
                     __syncwarp();
 #pragma unroll
                     for (int u = 0; u < kBatch; ++u) {
-                        const int n = column(base + u);
-                        const int e = ms.top[n] ? max((int)(ms.top[n] >> 23) - 126, -100) : 14;
-                        const float inv = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-                        if (piece(base + u) == 0) ms.qscale[tb][n] = __uint_as_float((uint32_t)(127 + e - 14) << 23);
-                        const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&v[u]);
-                        uint4 o;
-                        __half2* y = reinterpret_cast<__half2*>(&o);
+                        const int n = column(base + u), at = piece(base + u);
+                        const int e = ms.top[n] ? max((int)(ms.top[n] >> 23) - 126, -100) : 8;
+                        const float inv = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+                        if (at == 0) ms.qscale[tb][n] = __uint_as_float((uint32_t)(127 + e - 8) << 23);
+                        const T* y = reinterpret_cast<const T*>(&v[u]);
+                        unsigned char* const d = dst + ((n >> 3) * (DP / 16) + (at >> 1)) * 128 + (n & 7) * 16 + (at & 1) * 8;
+                        float z[8];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 f = __bfloat1622float2(x[k]);
-                            y[k] = __floats2half2_rn(f.x * inv, f.y * inv);
+                        for (int k = 0; k < 8; ++k) z[k] = to_float<T>(y[k]) * inv;
+#pragma unroll
+                        for (int p = 0; p < S::kPieces; ++p) {
+                            uint32_t codes[2];
+#pragma unroll
+                            for (int k = 0; k < 8; k += 2) {
+                                const float a0 = fabsf(z[k]) < INFINITY ? z[k] : NAN, a1 = fabsf(z[k + 1]) < INFINITY ? z[k + 1] : NAN;
+                                const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(a0, a1), __NV_SATFINITE, __NV_E4M3);
+                                codes[k / 4] = k & 2 ? codes[k / 4] | two << 16 : two;
+                                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+                                const float2 back = __half22float2(__half2(h));
+                                z[k] -= back.x;
+                                z[k + 1] -= back.y;
+                            }
+                            *reinterpret_cast<uint2*>(d + p * N * DP) = make_uint2(codes[0], codes[1]);
                         }
-                        *reinterpret_cast<uint4*>(target(base + u)) = o;
                     }
                 }
             }
@@ -617,63 +640,39 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             if (lane == 0) bar_arrive(bar(ms.q_full[qb]));
         }
     } else if (S::kFp8 && warp >= S::kSoftWarps) {
-        // ================================================================ e4m3 -> f16 (exact): four warps for K, four for V
-        const int row = tid & 127;                       // token of the tile, and (K) lane of tensor memory
-        const uint32_t quarter = (uint32_t)(row & ~31) << 16;
+        // ================================================================ e4m3 values -> f16 (exact), a token a thread
+        const int row = tid & 127;
         uint32_t n = 0;
-        auto widen = [&](const int is_v) {
-            const uint32_t slot = is_v ? v_slot(n) : k_slot(n);
-            wait(ms.full[slot], n / (is_v ? S::kVSlots : S::kKSlots));
-            const unsigned char* const src = ring + slot * S::kSlotBytes + row * DP;
-            uint4 x[DP / 16];                            // 16 codes each
-#pragma unroll
-            for (int ch = 0; ch < DP / 16; ++ch)
-                x[ch] = *reinterpret_cast<const uint4*>(src + (DP == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) * 16);
-            auto half = [](const uint4& x4, uint32_t* r) {
-                const uint32_t codes[4] = {x4.x, x4.y, x4.z, x4.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
-                        : "=r"(r[2 * k]), "=r"(r[2 * k + 1]) : "r"(codes[k]));
-            };
-            __syncwarp();
-            if (lane == 0) bar_arrive(bar(ms.empty[slot]));
-            uint32_t r[DP / 32][16];                     // 32 codes each
-#pragma unroll
-            for (int ch = 0; ch < DP / 16; ++ch) half(x[ch], r[ch / 2] + 8 * (ch & 1));
-            if (!is_v) {
-                // a token's elements along its lane of tensor memory, two to a column
-                if (n >= 2) wait(ms.s_full[n & 1], (n >> 1) - 1);        // S of tile n - 2 has read the buffer
-                tmem_after();
-#pragma unroll
-                for (int g = 0; g < DP / 32; ++g) tmem_st_32x16(t_k + quarter + (n & 1) * (DP / 2) + g * 16, r[g]);
-                tmem_wait_st();
-                tmem_before();
-            } else {
-                // the layout of a 16-bit tile of TMA's
-                if (n >= 2) wait(ms.pv_done[n & 1], (n >> 1) - 1);
-                unsigned char* const dst = v16 + (n & 1) * S::kV16Bytes + row * 128;
-#pragma unroll
-                for (int ch = 0; ch < DP / 8; ++ch) {
-                    const uint32_t* const y = r[ch / 4] + 4 * (ch & 3);
-                    *reinterpret_cast<uint4*>(dst + (ch / 8) * (kTile * 128) + ((ch % 8) ^ (row & 7)) * 16) = make_uint4(y[0], y[1], y[2], y[3]);
-                }
-                fence_async();
-            }
-            __syncwarp();
-            if (lane == 0) bar_arrive(is_v ? bar(ms.v16_full[n & 1]) : bar(ms.k16_full[n & 1]));
-        };
         for (uint32_t q = 0; take(q, w); ++q) {
 #pragma unroll 1
             for (int t = w.t0; t < w.t1; ++t, ++n) {
-                if constexpr (S::kConvWarps == 4) {
-                    widen(0);
-                    widen(1);
-                } else if (warp < S::kSoftWarps + 4) {
-                    widen(0);
-                } else {
-                    widen(1);
+                const uint32_t slot = v_slot(n);
+                wait(ms.full[slot], n / S::kVSlots);
+                const unsigned char* const src = ring + slot * S::kSlotBytes + row * DP;
+                uint4 x[DP / 16];                        // 16 codes each
+#pragma unroll
+                for (int ch = 0; ch < DP / 16; ++ch)
+                    x[ch] = *reinterpret_cast<const uint4*>(src + (DP == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) * 16);
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(ms.empty[slot]));
+                if (n >= 2) wait(ms.pv_done[n & 1], (n >> 1) - 1);       // the product of tile n - 2 has read the buffer
+                // the layout of a 16-bit tile of TMA's
+                unsigned char* const dst = v16 + (n & 1) * S::kV16Bytes + row * 128;
+#pragma unroll
+                for (int ch = 0; ch < DP / 16; ++ch) {
+                    const uint32_t codes[4] = {x[ch].x, x[ch].y, x[ch].z, x[ch].w};
+                    uint32_t r[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+                            : "=r"(r[2 * k]), "=r"(r[2 * k + 1]) : "r"(codes[k]));
+                    unsigned char* const d = dst + (ch / 4) * (kTile * 128);
+                    *reinterpret_cast<uint4*>(d + ((2 * (ch % 4)) ^ (row & 7)) * 16) = make_uint4(r[0], r[1], r[2], r[3]);
+                    *reinterpret_cast<uint4*>(d + ((2 * (ch % 4) + 1) ^ (row & 7)) * 16) = make_uint4(r[4], r[5], r[6], r[7]);
                 }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(ms.v16_full[n & 1]));
             }
         }
     } else {
@@ -743,7 +742,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
 #pragma unroll
                     for (int r = 0; r < NC / 8; ++r) {
                         float2 qs = make_float2(1.f, 1.f);
-                        if constexpr (S::kScaleQ) qs = *reinterpret_cast<const float2*>(&ms.qscale[tb][col0 + 8 * r + cq]);
+                        if constexpr (S::kFp8) qs = *reinterpret_cast<const float2*>(&ms.qscale[tb][col0 + 8 * r + cq]);
                         int2 last = make_int2(0, 0);
                         if constexpr (kMasked) {
                             // in the tile's own numbering of this thread's tokens
@@ -758,7 +757,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                                 [[maybe_unused]] const int i = 2 * hf + (e >> 1);
                                 float scale = a.scale_log2;
                                 if constexpr (S::kFp8) scale = kscale[i];
-                                if constexpr (S::kScaleQ) scale *= (e & 1) ? qs.y : qs.x;
+                                if constexpr (S::kFp8) scale *= (e & 1) ? qs.y : qs.x;
                                 bool seen = true;
                                 if constexpr (kMasked) {
                                     const int32_t lt = (e & 1) ? last.y : last.x;
@@ -1089,12 +1088,10 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
     }
     if (warp == S::kMma) {
         if (*expired) {                                  // products issued so far end by themselves: wait for them
-            if (lane == 0) {
-                bar_init(bar(ms.k16_full[0]), 1);
-                asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-                mma_commit(bar(ms.k16_full[0]));
+            if (elected()) {
+                mma_commit(bar(ms.drained));
                 const unsigned long long t0 = time_ns();
-                while (!bar_test(bar(ms.k16_full[0]), 0) && time_ns() - t0 < kDrainNs) {}
+                while (!bar_test(bar(ms.drained), 0) && time_ns() - t0 < kDrainNs) {}
             }
             __syncwarp();
         }

@@ -170,14 +170,14 @@ __device__ __forceinline__ void tmem_st_32x16(uint32_t a, const uint32_t (&r)[16
 // ---------------------------------------------------------------- tcgen05 products
 
 // Shared-memory operand: start address, leading and stride byte offsets (16-byte units) and swizzle.
-constexpr uint64_t kNoSwizzle = 0, kSwizzle128 = 2;
+constexpr uint64_t kNoSwizzle = 0, kSwizzle128 = 2, kSwizzle64 = 4;
 __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride, uint64_t swizzle)
 {
     return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)((lead >> 4) & 0x3fff) << 16 | (uint64_t)((stride >> 4) & 0x3fff) << 32 |
            (uint64_t)1 << 46 | swizzle << 61;
 }
 
-// fp32 accumulator, both operands f16 (0) or both bf16 (1); mn_major_a: A's rows are contiguous.
+// fp32 accumulator, both operands f16 (or e4m3: 0) or both bf16 (1); mn_major_a: A's rows are contiguous.
 __host__ __device__ constexpr uint32_t product(int bf16, int mn_major_a, int m, int n)
 {
     return 1u << 4 | (uint32_t)bf16 << 7 | (uint32_t)bf16 << 10 | (uint32_t)mn_major_a << 15 | (uint32_t)(n >> 3) << 17 |
@@ -190,10 +190,11 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
                  ::"r"(d), "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add) : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add)
+// The same with e4m3 operands, 32 elements deep where the above is 16 (the format bits of e4m3 are zeros).
+__device__ __forceinline__ void mma_ss_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add)
 {
-    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
-                 ::"r"(d), "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add) : "memory");
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }"
+                 ::"r"(d), "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add) : "memory");
 }
 
 // The barrier gets one arrival when the products issued so far by this thread are done.

@@ -17,6 +17,7 @@ using namespace specdec;
 
 constexpr int kThreads = 256;
 constexpr int kMaxRows = 32;
+constexpr int kReadBatch = 4;             // units of 16 elements a thread has in flight
 
 struct Table {
     const int32_t* block_table;
@@ -36,6 +37,7 @@ struct WriteArgs {
     const int32_t *cached, *cu;
     int32_t B;
     uint32_t* status;
+    float per_row;                        // 1 / heads of a row (keys and values)
 };
 
 struct RowSlot {
@@ -105,11 +107,12 @@ template <int N> __device__ __forceinline__ void store_e4m3(uint8_t* p, const fl
 }
 
 // A head is held by a group of kLanes lanes, kUnits units of 2V elements a lane, so that its largest
-// magnitude is a shuffle reduction and its elements are read once.
+// magnitude is a shuffle reduction and its elements are read once. A group takes kHeads heads at a time, the first
+// of them read before the rows' places are known.
 // V = 8: 16-byte runs, groups of 8 lanes (head_dim <= 128); V = 1 takes any even rot_dim and any
 // alignment of the inputs with a warp a head.
-template <typename T, typename C, int V, int kLanes, int kUnits>
-__global__ void __launch_bounds__(kThreads) specdec_kv_write_kernel(const WriteArgs a)
+template <typename T, typename C, int V, int kLanes, int kUnits, int kHeads>
+__global__ void __launch_bounds__(kThreads, 4) specdec_kv_write_kernel(const WriteArgs a)
 {
     extern __shared__ float2 cs[];                                 // [rows_per_cta][rot_dim / 2]
     __shared__ RowSlot slots[kMaxRows];
@@ -117,6 +120,31 @@ __global__ void __launch_bounds__(kThreads) specdec_kv_write_kernel(const WriteA
     const int tid = threadIdx.x;
     const int64_t row0 = (int64_t)blockIdx.x * a.rows_per_cta;
     const int n = (int)min((int64_t)a.rows_per_cta, a.rows - row0);
+    const int half = a.has_rope ? a.rope.rot_dim / 2 : 0;
+    const int units = c.head_dim / (2 * V), H = c.num_kv_heads, total = n * 2 * H;
+    const int lane = tid % kLanes, group = tid / kLanes;
+    constexpr int kGroups = kThreads / kLanes;
+
+    Raw<T, V> raw[kHeads][kUnits][2];
+    auto fetch = [&](int base) {
+#pragma unroll
+        for (int s = 0; s < kHeads; ++s) {
+            const int w = base + s * kGroups;                      // (row, K or V, head)
+            if (w >= total) continue;
+            const int r = over(w, a.per_row), hv = w - r * 2 * H, is_v = hv >= H, h = hv - is_v * H;
+            const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (row0 + r) * a.row_stride + h * a.head_stride;
+#pragma unroll
+            for (int q = 0; q < kUnits; ++q) {
+                const int u = lane + q * kLanes;
+                if (u >= units) continue;
+                int first, second;
+                unit_runs<V>(u, 2 * half, a.rope.interleaved, &first, &second);
+                raw[s][q][0].load(src + first);
+                raw[s][q][1].load(src + second);
+            }
+        }
+    };
+    fetch(group);
 
     if (a.status)
         for (int64_t b = (int64_t)blockIdx.x * kThreads + tid; b < a.B; b += (int64_t)gridDim.x * kThreads) {
@@ -124,7 +152,6 @@ __global__ void __launch_bounds__(kThreads) specdec_kv_write_kernel(const WriteA
             else if (a.cached[b] < 0 || !fits(c, a.table, (int64_t)a.cached[b] + a.cu[b + 1] - a.cu[b] + 1))
                 atomicOr(a.status + b, SPECDEC_ST_BAD_LENGTH);
         }
-
     int b = owner_of<kThreads>(a.B, row0, [&](int i) { return (int64_t)__ldg(a.cu + i) + i; });
     if (tid < n) {
         const int64_t t = row0 + tid;
@@ -142,64 +169,67 @@ __global__ void __launch_bounds__(kThreads) specdec_kv_write_kernel(const WriteA
         slots[tid] = r;
     }
     __syncthreads();
-    const int half = a.has_rope ? a.rope.rot_dim / 2 : 0;
     for (int i = tid; i < n * half; i += kThreads) {
         const int r = i / half;
         cs[i] = turn(slots[r].position, __ldg(a.rope.freq + (i - r * half)), a.rope.amplitude);
     }
     __syncthreads();
 
-    const int units = c.head_dim / (2 * V), H = c.num_kv_heads;
-    const int lane = tid % kLanes, groups = kThreads / kLanes;
-    const int total = n * 2 * H, rounds = (total + groups - 1) / groups;
-    for (int it = 0; it < rounds; ++it) {
-        const int w = it * groups + tid / kLanes;                  // (row, K or V, head)
-        const int r = w / (2 * H), hv = w - r * 2 * H, is_v = hv >= H, h = hv - is_v * H;
-        const bool live = w < total && slots[w < total ? r : 0].live == 1;
-        float x[kUnits][2 * V];
-        float top = 0.f;
-        if (live) {
-            const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (row0 + r) * a.row_stride + h * a.head_stride;
+    // (whole warps go round together: the reduction needs their lanes)
+    for (int round = 0; round < total; round += kHeads * kGroups) {
+        if (round > 0) fetch(round + group);
+#pragma unroll
+        for (int s = 0; s < kHeads; ++s) {
+            const int w = round + group + s * kGroups;
+            const int r = over(min(w, total - 1), a.per_row), hv = w - r * 2 * H, is_v = hv >= H, h = hv - is_v * H;
+            const bool live = w < total && slots[r].live == 1;
+            float x[kUnits][2 * V];
+            float top = 0.f;
+            if (live) {
+#pragma unroll
+                for (int q = 0; q < kUnits; ++q) {
+                    const int u = lane + q * kLanes;
+                    if (u >= units) continue;
+                    raw[s][q][0].to(x[q]);
+                    raw[s][q][1].to(x[q] + V);
+                    if (!is_v) rotate_unit<V>(x[q], u, 2 * half, a.rope.interleaved, cs + r * half);
+#pragma unroll
+                    for (int i = 0; i < 2 * V; ++i) {
+                        const float m = fabsf(x[q][i]);
+                        top = fmaxf(top, m < INFINITY ? m : 0.f);
+                    }
+                }
+            }
+            int e = 0;
+            if constexpr (sizeof(C) == 1) {
+#pragma unroll
+                for (int off = kLanes / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                e = e4m3_exponent(top);
+            }
+            if (!live) continue;
+            const RowSlot& slot = slots[r];
+            C* dst = static_cast<C*>(is_v ? c.v : c.k) + slot.at + h * c.head_stride;
 #pragma unroll
             for (int q = 0; q < kUnits; ++q) {
                 const int u = lane + q * kLanes;
                 if (u >= units) continue;
                 int first, second;
                 unit_runs<V>(u, 2 * half, a.rope.interleaved, &first, &second);
-                load_n<T, V>(src + first, x[q]);
-                load_n<T, V>(src + second, x[q] + V);
-                if (!is_v) rotate_unit<V>(x[q], u, 2 * half, a.rope.interleaved, cs + r * half);
-#pragma unroll
-                for (int i = 0; i < 2 * V; ++i)
-                    if (isfinite(x[q][i])) top = fmaxf(top, fabsf(x[q][i]));
+                if constexpr (sizeof(C) == 1) {
+                    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);     // 2^-e, e in [-126, 120]
+                    store_e4m3<V>(reinterpret_cast<uint8_t*>(dst) + first, x[q], inv);
+                    store_e4m3<V>(reinterpret_cast<uint8_t*>(dst) + second, x[q] + V, inv);
+                } else {
+                    Raw<C, V> y;
+                    y.from(x[q]);
+                    y.store(dst + first);
+                    y.from(x[q] + V);
+                    y.store(dst + second);
+                }
             }
+            if constexpr (sizeof(C) == 1)
+                if (lane == 0) (is_v ? c.v_exp : c.k_exp)[slot.exp_at + (int64_t)h * c.page_size] = (uint8_t)(e + 127);
         }
-        int e = 0;
-        if constexpr (sizeof(C) == 1) {
-#pragma unroll
-            for (int off = kLanes / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            e = e4m3_exponent(top);
-        }
-        if (!live) continue;
-        const RowSlot& slot = slots[r];
-        C* dst = static_cast<C*>(is_v ? c.v : c.k) + slot.at + h * c.head_stride;
-#pragma unroll
-        for (int q = 0; q < kUnits; ++q) {
-            const int u = lane + q * kLanes;
-            if (u >= units) continue;
-            int first, second;
-            unit_runs<V>(u, 2 * half, a.rope.interleaved, &first, &second);
-            if constexpr (sizeof(C) == 1) {
-                const float inv = __uint_as_float((uint32_t)(127 - e) << 23);     // 2^-e, e in [-126, 120]
-                store_e4m3<V>(reinterpret_cast<uint8_t*>(dst) + first, x[q], inv);
-                store_e4m3<V>(reinterpret_cast<uint8_t*>(dst) + second, x[q] + V, inv);
-            } else {
-                store_n<C, V>(dst + first, x[q]);
-                store_n<C, V>(dst + second, x[q] + V);
-            }
-        }
-        if constexpr (sizeof(C) == 1)
-            if (lane == 0) (is_v ? c.v_exp : c.k_exp)[slot.exp_at + (int64_t)h * c.page_size] = (uint8_t)(e + 127);
     }
 }
 
@@ -210,15 +240,19 @@ template <typename T, typename C> specdec_status_t launch_write(WriteArgs a, cud
     const int64_t per = 16 / (int64_t)sizeof(T);
     const bool wide = rot % 16 == 0 && aligned_to(a.k, 16) && aligned_to(a.v, 16) && a.row_stride % per == 0 &&
                       a.head_stride % per == 0;
-    // rows for about four rounds of the CTA's groups
-    const int groups = wide ? kThreads / 8 : kThreads / 32;
-    int rpc = 4 * groups / (2 * c.num_kv_heads);
-    rpc = rpc < 1 ? 1 : rpc > kMaxRows ? kMaxRows : rpc;
-    a.rows_per_cta = rpc;
+    // rows of one wave of CTAs (four on each of 152 SMs), up to a batch of heads a group; never fewer than fill a CTA
+    const int groups = wide ? kThreads / 8 : kThreads / 32, heads = 2 * c.num_kv_heads, batch = (wide ? 4 : 2) * groups;
+    if (heads >= 1 << 18) return SPECDEC_ERR_UNSUPPORTED;          // over() is exact below that
+    const int64_t wave = ((int64_t)a.rows + 607) / 608, most = (batch + heads - 1) / heads, fill = (groups + heads - 1) / heads;
+    int64_t rpc = wave < most ? wave : most;
+    rpc = rpc > fill ? rpc : fill;
+    rpc = rpc > kMaxRows ? kMaxRows : rpc;
+    a.rows_per_cta = (int)rpc;
+    a.per_row = 1.f / (float)heads;
     const unsigned grid = (unsigned)(((int64_t)a.rows + rpc - 1) / rpc);
     const size_t smem = (size_t)rpc * (rot / 2) * sizeof(float2);
-    if (wide) specdec_kv_write_kernel<T, C, 8, 8, 1><<<grid, kThreads, smem, stream>>>(a);
-    else specdec_kv_write_kernel<T, C, 1, 32, 2><<<grid, kThreads, smem, stream>>>(a);
+    if (wide) specdec_kv_write_kernel<T, C, 8, 8, 1, sizeof(T) == 4 ? 2 : 4><<<grid, kThreads, smem, stream>>>(a);
+    else specdec_kv_write_kernel<T, C, 1, 32, 2, 2><<<grid, kThreads, smem, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 
@@ -239,6 +273,7 @@ struct ReadArgs {
     void *out_k, *out_v;
     int64_t out_row, out_head;
     uint32_t* status;
+    float per_row, per_head;              // 1 / units of a row (keys and values), of a head
 };
 
 // Offsets and range of request b: 0 fine, else the status bit.
@@ -253,7 +288,7 @@ __device__ __forceinline__ uint32_t read_fault(const ReadArgs& a, int b)
 
 // Units of 16 elements; kWide: the outputs take 16-byte stores.
 template <typename C, typename T, bool kWide>
-__global__ void __launch_bounds__(kThreads) specdec_kv_read_kernel(const ReadArgs a)
+__global__ void __launch_bounds__(kThreads, 4) specdec_kv_read_kernel(const ReadArgs a)
 {
     __shared__ RowSlot slots[kMaxRows];
     const specdec_kv_cache_t& c = a.cache;
@@ -276,31 +311,48 @@ __global__ void __launch_bounds__(kThreads) specdec_kv_read_kernel(const ReadArg
         slots[tid] = r;
     }
     __syncthreads();
-    const int units = c.head_dim / 16, H = c.num_kv_heads, per_row = 2 * H * units;
-    for (int i = tid; i < n * per_row; i += kThreads) {
-        const int r = i / per_row, w = i - r * per_row, hv = w / units, u = w - hv * units;
-        const int is_v = hv >= H, h = hv - is_v * H;
-        const RowSlot slot = slots[r];
-        T* out = static_cast<T*>(is_v ? a.out_v : a.out_k);
-        if (!slot.live || !out) continue;
-        float x[16];
-        if (slot.live > 0) {
-            load_n<C, 16>(static_cast<const C*>(is_v ? c.v : c.k) + slot.at + h * c.head_stride + u * 16, x);
-            if constexpr (sizeof(C) == 1) {
-                const float s = exp_value((is_v ? c.v_exp : c.k_exp)[slot.exp_at + (int64_t)h * c.page_size]);
+    const int units = c.head_dim / 16, H = c.num_kv_heads, row_units = 2 * H * units, total = n * row_units;
+    for (int base = tid; base < total; base += kReadBatch * kThreads) {
+        Raw<C, 16> raw[kReadBatch];
+        float scale[kReadBatch];
+        T* out[kReadBatch];                                        // nullptr: nothing to write
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] *= s;
+        for (int q = 0; q < kReadBatch; ++q) {
+            const int i = base + q * kThreads;
+            out[q] = nullptr;
+            scale[q] = 1.f;
+            if (i >= total) continue;
+            const int r = over(i, a.per_row), w = i - r * row_units, hv = over(w, a.per_head), u = w - hv * units;
+            const int is_v = hv >= H, h = hv - is_v * H;
+            const RowSlot& slot = slots[r];
+            T* const to = static_cast<T*>(is_v ? a.out_v : a.out_k);
+            if (!slot.live || !to) continue;
+            out[q] = to + (row0 + r) * a.out_row + h * a.out_head + u * 16;
+            if (slot.live > 0) {
+                raw[q].load(static_cast<const C*>(is_v ? c.v : c.k) + slot.at + h * c.head_stride + u * 16);
+                if constexpr (sizeof(C) == 1) scale[q] = exp_value((is_v ? c.v_exp : c.k_exp)[slot.exp_at + (int64_t)h * c.page_size]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) raw[q].e[e] = C();    // a bad page reads as zeros
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = 0.f;               // a bad page reads as zeros
         }
-        out += (row0 + r) * a.out_row + h * a.out_head + u * 16;
-        if constexpr (kWide) {
-            store_n<T, 16>(out, x);
-        } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) out[e] = from_float<T>(x[e]);
+        for (int q = 0; q < kReadBatch; ++q) {
+            if (!out[q]) continue;
+            float x[16];
+            raw[q].to(x);
+            if constexpr (sizeof(C) == 1) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] *= scale[q];
+            }
+            if constexpr (kWide) {
+                Raw<T, 16> y;
+                y.from(x);
+                y.store(out[q]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) out[q][e] = from_float<T>(x[e]);
+            }
         }
     }
 }
@@ -309,9 +361,18 @@ template <typename C, typename T> specdec_status_t launch_read(ReadArgs a, cudaS
 {
     const int64_t per = 16 / (int64_t)sizeof(T);
     const bool wide = aligned_to(a.out_k, 16) && aligned_to(a.out_v, 16) && a.out_row % per == 0 && a.out_head % per == 0;
-    int rpc = 4 * kThreads / (2 * a.cache.num_kv_heads * (a.cache.head_dim / 16));
-    rpc = rpc < 1 ? 1 : rpc > kMaxRows ? kMaxRows : rpc;
-    a.rows_per_cta = rpc;
+    const int units = a.cache.head_dim / 16;
+    const int64_t row_units = (int64_t)2 * a.cache.num_kv_heads * units;
+    if (row_units >= 1 << 21) return SPECDEC_ERR_UNSUPPORTED;      // over() is exact below that
+    // as the write's: one wave's rows, up to two batches of units a thread, never fewer than fill a CTA
+    const int64_t wave = (a.rows + 607) / 608, most = (2 * kReadBatch * kThreads + row_units - 1) / row_units,
+                  fill = (kThreads + row_units - 1) / row_units;
+    int64_t rpc = wave < most ? wave : most;
+    rpc = rpc > fill ? rpc : fill;
+    while (rpc > 1 && (rpc > kMaxRows || rpc * row_units >= 1 << 21)) --rpc;
+    a.rows_per_cta = (int)rpc;
+    a.per_row = 1.f / (float)row_units;
+    a.per_head = 1.f / (float)units;
     const int64_t grid = (a.rows + rpc - 1) / rpc;
     if (grid > 0x7fffffff) return SPECDEC_ERR_UNSUPPORTED;
     if (wide) specdec_kv_read_kernel<C, T, true><<<(unsigned)grid, kThreads, 0, stream>>>(a);
@@ -348,7 +409,7 @@ extern "C" specdec_status_t specdec_kv_write(const void* k, const void* v, specd
         !aligned_to(cached_len, 4) || !aligned_to(cu_num_draft, 4) || !aligned_to(status, 4))
         return SPECDEC_ERR_INVALID_ARG;
     WriteArgs a = {k, v, row_stride, head_stride, rows, 0, rope != nullptr, rope ? *rope : specdec_rope_t{nullptr, 0, 0, 1.f},
-                   positions, *cache, {block_table, block_stride, max_blocks}, cached_len, cu_num_draft, B, status};
+                   positions, *cache, {block_table, block_stride, max_blocks}, cached_len, cu_num_draft, B, status, 0.f};
     if (dtype == SPECDEC_F32) return launch_write_to<float>(a, (cudaStream_t)stream);
     if (dtype == SPECDEC_BF16) return launch_write_to<__nv_bfloat16>(a, (cudaStream_t)stream);
     return launch_write_to<__half>(a, (cudaStream_t)stream);
@@ -372,7 +433,7 @@ extern "C" specdec_status_t specdec_kv_read(const specdec_kv_cache_t* cache, con
         !aligned_to(cu_len, 8) || !aligned_to(status, 4))
         return SPECDEC_ERR_INVALID_ARG;
     const ReadArgs a = {*cache, {block_table, block_stride, max_blocks}, first, cu_len, B, 0, rows, out_k, out_v,
-                        out_row_stride, out_head_stride, status};
+                        out_row_stride, out_head_stride, status, 0.f, 0.f};
     if (cache->dtype == SPECDEC_BF16) return launch_read_to<__nv_bfloat16>(a, out_dtype, (cudaStream_t)stream);
     if (cache->dtype == SPECDEC_F16) return launch_read_to<__half>(a, out_dtype, (cudaStream_t)stream);
     return launch_read_to<__nv_fp8_e4m3>(a, out_dtype, (cudaStream_t)stream);

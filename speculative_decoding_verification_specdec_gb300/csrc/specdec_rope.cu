@@ -15,8 +15,8 @@ namespace {
 using namespace specdec;
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 4;                 // units a thread has in flight
 constexpr int kMaxRows = 16;              // rows a CTA takes at most
-constexpr int kUnitsPerCta = 1024;        // units it aims at: four a thread
 
 struct RopeArgs {
     const void* x;
@@ -26,10 +26,13 @@ struct RopeArgs {
     specdec_rope_t rope;
     const int32_t *positions, *cu, *cached;
     int32_t B;
+    float per_row, per_head;              // 1 / units of a row, of a head
 };
 
+// The first batch is read before the rows' positions are known: their chain of reads and the angles
+// then cost nothing on top of it.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) specdec_rope_kernel(const RopeArgs a)
+__global__ void __launch_bounds__(kThreads, 4) specdec_rope_kernel(const RopeArgs a)
 {
     extern __shared__ float2 cs[];                                 // [rows_per_cta][rot_dim / 2]
     __shared__ int64_t pos[kMaxRows];
@@ -37,6 +40,28 @@ __global__ void __launch_bounds__(kThreads) specdec_rope_kernel(const RopeArgs a
     const int tid = threadIdx.x, half = a.rope.rot_dim / 2;
     const int64_t row0 = (int64_t)blockIdx.x * a.rows_per_cta;
     const int n = (int)min((int64_t)a.rows_per_cta, a.rows - row0);
+    const int row_units = a.heads * a.units, total = n * row_units;
+    Raw<T, V> v[kBatch][2];
+    auto place = [&](int i, int* r, int* h, int* u, int* first, int* second) {
+        *r = over(i, a.per_row);
+        const int w = i - *r * row_units;
+        *h = over(w, a.per_head);
+        *u = w - *h * a.units;
+        unit_runs<V>(*u, a.rope.rot_dim, a.rope.interleaved, first, second);
+    };
+    auto fetch = [&](int base) {
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int i = base + q * kThreads;
+            if (i >= total) continue;
+            int r, h, u, first, second;
+            place(i, &r, &h, &u, &first, &second);
+            const T* x = static_cast<const T*>(a.x) + (row0 + r) * a.x_row + h * a.x_head;
+            v[q][0].load(x + first);
+            v[q][1].load(x + second);
+        }
+    };
+    fetch(tid);
     int b = 0;
     if (!a.positions) b = owner_of<kThreads>(a.B, row0, [&](int i) { return (int64_t)__ldg(a.cu + i) + i; });
     if (tid < n) {
@@ -61,20 +86,26 @@ __global__ void __launch_bounds__(kThreads) specdec_rope_kernel(const RopeArgs a
         cs[i] = t;
     }
     __syncthreads();
-    const int per_row = a.heads * a.units;
-    for (int i = tid; i < n * per_row; i += kThreads) {
-        const int r = i / per_row, w = i - r * per_row, h = w / a.units, u = w - h * a.units;
-        if (!live[r]) continue;
-        int first, second;
-        unit_runs<V>(u, a.rope.rot_dim, a.rope.interleaved, &first, &second);
-        const T* x = static_cast<const T*>(a.x) + (row0 + r) * a.x_row + h * a.x_head;
-        T* out = static_cast<T*>(a.out) + (row0 + r) * a.out_row + h * a.out_head;
-        float v[2 * V];
-        load_n<T, V>(x + first, v);
-        load_n<T, V>(x + second, v + V);
-        rotate_unit<V>(v, u, a.rope.rot_dim, a.rope.interleaved, cs + r * half);
-        store_n<T, V>(out + first, v);
-        store_n<T, V>(out + second, v + V);
+    for (int base = tid; base < total; base += kBatch * kThreads) {
+        if (base != tid) fetch(base);
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int i = base + q * kThreads;
+            if (i >= total) continue;
+            int r, h, u, first, second;
+            place(i, &r, &h, &u, &first, &second);
+            if (!live[r]) continue;
+            float x[2 * V];
+            v[q][0].to(x);
+            v[q][1].to(x + V);
+            rotate_unit<V>(x, u, a.rope.rot_dim, a.rope.interleaved, cs + r * half);
+            T* out = static_cast<T*>(a.out) + (row0 + r) * a.out_row + h * a.out_head;
+            Raw<T, V> y;
+            y.from(x);
+            y.store(out + first);
+            y.from(x + V);
+            y.store(out + second);
+        }
     }
 }
 
@@ -89,8 +120,17 @@ specdec_status_t launch_rope(RopeArgs a, cudaStream_t stream)
     for (int64_t s : st) wide = wide && s % kV == 0;
     const int V = wide ? kV : 1;
     a.units = a.head_dim / (2 * V);
-    const int64_t per_row = (int64_t)a.heads * a.units;
-    a.rows_per_cta = (int)(per_row >= kUnitsPerCta ? 1 : (kUnitsPerCta / per_row < kMaxRows ? kUnitsPerCta / per_row : kMaxRows));
+    const int64_t row_units = (int64_t)a.heads * a.units;
+    if (row_units >= 1 << 21) return SPECDEC_ERR_UNSUPPORTED;      // over() is exact below that
+    // rows of one wave of CTAs (four on each of 152 SMs), up to a batch of units a thread; never fewer than fill a CTA
+    const int64_t wave = ((int64_t)a.rows + 607) / 608, batch = (kBatch * kThreads + row_units - 1) / row_units,
+                  fill = (kThreads + row_units - 1) / row_units;
+    int64_t rpc = wave < batch ? wave : batch;
+    rpc = rpc > fill ? rpc : fill;
+    while (rpc > 1 && (rpc > kMaxRows || rpc * row_units >= 1 << 21)) --rpc;
+    a.rows_per_cta = (int)rpc;
+    a.per_row = 1.f / (float)row_units;
+    a.per_head = 1.f / (float)a.units;
     const unsigned grid = (unsigned)(((int64_t)a.rows + a.rows_per_cta - 1) / a.rows_per_cta);
     const size_t smem = (size_t)a.rows_per_cta * (a.rope.rot_dim / 2) * sizeof(float2);
     if (wide) specdec_rope_kernel<T, kV><<<grid, kThreads, smem, stream>>>(a);
@@ -148,7 +188,7 @@ extern "C" specdec_status_t specdec_rope(const void* x, void* out, specdec_dtype
         !aligned_to(cached_len, 4))
         return SPECDEC_ERR_INVALID_ARG;
     RopeArgs a = {x, out, rows, heads, head_dim, 0, 0, inverse != 0, x_row_stride, x_head_stride, out_row_stride,
-                  out_head_stride, *rope, positions, cu_num_draft, cached_len, B};
+                  out_head_stride, *rope, positions, cu_num_draft, cached_len, B, 0.f, 0.f};
     if (dtype == SPECDEC_F32) return launch_rope<float>(a, (cudaStream_t)stream);
     if (dtype == SPECDEC_BF16) return launch_rope<__nv_bfloat16>(a, (cudaStream_t)stream);
     return launch_rope<__half>(a, (cudaStream_t)stream);

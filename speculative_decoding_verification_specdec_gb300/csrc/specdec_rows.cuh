@@ -96,39 +96,54 @@ template <> __device__ __forceinline__ float from_float<float>(float x) { return
 template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 template <> __device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
 
-// N consecutive elements <-> fp32 registers, in 16-byte accesses where N elements fill them (the
-// caller knows the address to be aligned then).
-template <typename T, int N> __device__ __forceinline__ void load_n(const T* p, float* x)
-{
-    constexpr int kBytes = N * (int)sizeof(T);
-    if constexpr (kBytes % 16 == 0) {
-        uint4 raw[kBytes / 16];
+// N consecutive elements as they lie: read and written in 16-byte accesses where N elements fill them, in 8-byte ones
+// where they fill those (the caller knows the address to be aligned then), else one by one; the halves of a
+// load and its use may so be far apart.
+template <typename T, int N> struct Raw {
+    static constexpr int kBytes = N * (int)sizeof(T);
+    static constexpr bool kWide = kBytes % 8 == 0 && N > 1;
+    alignas(16) T e[N];
+    __device__ __forceinline__ void load(const T* p)
+    {
+        if constexpr (kBytes % 16 == 0 && kWide) {
 #pragma unroll
-        for (int i = 0; i < kBytes / 16; ++i) raw[i] = reinterpret_cast<const uint4*>(p)[i];
-        const T* e = reinterpret_cast<const T*>(raw);
+            for (int i = 0; i < kBytes / 16; ++i) reinterpret_cast<uint4*>(e)[i] = reinterpret_cast<const uint4*>(p)[i];
+        } else if constexpr (kWide) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 8; ++i) reinterpret_cast<uint2*>(e)[i] = reinterpret_cast<const uint2*>(p)[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) e[i] = p[i];
+        }
+    }
+    __device__ __forceinline__ void store(T* p) const
+    {
+        if constexpr (kBytes % 16 == 0 && kWide) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 16; ++i) reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(e)[i];
+        } else if constexpr (kWide) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 8; ++i) reinterpret_cast<uint2*>(p)[i] = reinterpret_cast<const uint2*>(e)[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) p[i] = e[i];
+        }
+    }
+    __device__ __forceinline__ void to(float* x) const
+    {
 #pragma unroll
         for (int i = 0; i < N; ++i) x[i] = to_float<T>(e[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = to_float<T>(p[i]);
     }
-}
-
-template <typename T, int N> __device__ __forceinline__ void store_n(T* p, const float* x)
-{
-    constexpr int kBytes = N * (int)sizeof(T);
-    if constexpr (kBytes % 16 == 0) {
-        uint4 raw[kBytes / 16];
-        T* e = reinterpret_cast<T*>(raw);
+    __device__ __forceinline__ void from(const float* x)
+    {
 #pragma unroll
         for (int i = 0; i < N; ++i) e[i] = from_float<T>(x[i]);
-#pragma unroll
-        for (int i = 0; i < kBytes / 16; ++i) reinterpret_cast<uint4*>(p)[i] = raw[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) p[i] = from_float<T>(x[i]);
     }
-}
+};
+
+// floor(x / y) by the reciprocal 1.f / y: exact for 0 <= x < 2^21 (x + 1/2 is at least 1/2 away from a multiple of y,
+// relative to x more than the two roundings of 2^-24)
+__device__ __forceinline__ int over(int x, float reciprocal) { return __float2int_rd(((float)x + 0.5f) * reciprocal); }
 
 // A head is taken in units of 2V elements: the two runs of V that rotate together (half layout), 2V
 // consecutive ones (interleaved layout, and the elements behind rot_dim). Needs rot_dim and

@@ -37,7 +37,6 @@ struct WriteArgs {
     const int32_t *cached, *cu;
     int32_t B;
     uint32_t* status;
-    float per_row;                        // 1 / heads of a row (keys and values)
 };
 
 struct RowSlot {
@@ -81,38 +80,28 @@ __device__ __forceinline__ int e4m3_exponent(float top)
     return max(m <= 0.875f ? x - 9 : x - 8, -126);
 }
 
+// N finite (or NaN) values times a power of two, to nearest e4m3, of which the largest is at most 448.
 template <int N> __device__ __forceinline__ void store_e4m3(uint8_t* p, const float* x, float inverse_scale)
 {
-    uint8_t q[N];
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const float a = isfinite(x[i]) ? x[i] * inverse_scale : NAN;
-        const float b = i + 1 < N ? (isfinite(x[i + 1]) ? x[i + 1] * inverse_scale : NAN) : 0.f;
-        const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-        q[i] = (uint8_t)(two & 0xff);
-        if (i + 1 < N) q[i + 1] = (uint8_t)(two >> 8);
-    }
-    if constexpr (N % 8 == 0) {
-#pragma unroll
-        for (int i = 0; i < N; i += 8) {
-            uint2 w;
-            w.x = q[i] | q[i + 1] << 8 | q[i + 2] << 16 | (uint32_t)q[i + 3] << 24;
-            w.y = q[i + 4] | q[i + 5] << 8 | q[i + 6] << 16 | (uint32_t)q[i + 7] << 24;
-            *reinterpret_cast<uint2*>(p + i) = w;
-        }
+    if constexpr (N == 1) {
+        *p = (uint8_t)__nv_cvt_float_to_fp8(x[0] * inverse_scale, __NV_SATFINITE, __NV_E4M3);
     } else {
+        static_assert(N == 8, "an 8-byte store");
+        uint32_t two[4];
 #pragma unroll
-        for (int i = 0; i < N; ++i) p[i] = q[i];
+        for (int i = 0; i < 4; ++i)
+            two[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inverse_scale, x[2 * i + 1] * inverse_scale), __NV_SATFINITE, __NV_E4M3);
+        *reinterpret_cast<uint2*>(p) = make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
     }
 }
 
 // A head is held by a group of kLanes lanes, kUnits units of 2V elements a lane, so that its largest
-// magnitude is a shuffle reduction and its elements are read once. A group takes kHeads heads at a time, the first
-// of them read before the rows' places are known.
+// magnitude is a shuffle reduction and its elements are read once. The group's first head is read before the rows'
+// places are known.
 // V = 8: 16-byte runs, groups of 8 lanes (head_dim <= 128); V = 1 takes any even rot_dim and any
 // alignment of the inputs with a warp a head.
-template <typename T, typename C, int V, int kLanes, int kUnits, int kHeads>
-__global__ void __launch_bounds__(kThreads, 4) specdec_kv_write_kernel(const WriteArgs a)
+template <typename T, typename C, int V, int kLanes, int kUnits>
+__global__ void __launch_bounds__(kThreads, 6) specdec_kv_write_kernel(const WriteArgs a)
 {
     extern __shared__ float2 cs[];                                 // [rows_per_cta][rot_dim / 2]
     __shared__ RowSlot slots[kMaxRows];
@@ -125,26 +114,26 @@ __global__ void __launch_bounds__(kThreads, 4) specdec_kv_write_kernel(const Wri
     const int lane = tid % kLanes, group = tid / kLanes;
     constexpr int kGroups = kThreads / kLanes;
 
-    Raw<T, V> raw[kHeads][kUnits][2];
-    auto fetch = [&](int base) {
-#pragma unroll
-        for (int s = 0; s < kHeads; ++s) {
-            const int w = base + s * kGroups;                      // (row, K or V, head)
-            if (w >= total) continue;
-            const int r = over(w, a.per_row), hv = w - r * 2 * H, is_v = hv >= H, h = hv - is_v * H;
-            const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (row0 + r) * a.row_stride + h * a.head_stride;
+    Raw<T, V> raw[kUnits][2];
+    const Place step(kGroups, 2 * H, 1);
+    Place ahead(group, 2 * H, 1), at = ahead;                      // row, and head of K (below H) or V, next to read, to write
+    auto fetch = [&](bool in) {
+        if (in) {
+            const int is_v = ahead.h >= H, h = ahead.h - is_v * H;
+            const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (row0 + ahead.r) * a.row_stride + h * a.head_stride;
 #pragma unroll
             for (int q = 0; q < kUnits; ++q) {
                 const int u = lane + q * kLanes;
                 if (u >= units) continue;
                 int first, second;
                 unit_runs<V>(u, 2 * half, a.rope.interleaved, &first, &second);
-                raw[s][q][0].load(src + first);
-                raw[s][q][1].load(src + second);
+                raw[q][0].load(src + first);
+                raw[q][1].load(src + second);
             }
         }
+        ahead.move(step, 2 * H, 1);
     };
-    fetch(group);
+    fetch(group < total);
 
     if (a.status)
         for (int64_t b = (int64_t)blockIdx.x * kThreads + tid; b < a.B; b += (int64_t)gridDim.x * kThreads) {
@@ -176,60 +165,68 @@ __global__ void __launch_bounds__(kThreads, 4) specdec_kv_write_kernel(const Wri
     __syncthreads();
 
     // (whole warps go round together: the reduction needs their lanes)
-    for (int round = 0; round < total; round += kHeads * kGroups) {
-        if (round > 0) fetch(round + group);
-#pragma unroll
-        for (int s = 0; s < kHeads; ++s) {
-            const int w = round + group + s * kGroups;
-            const int r = over(min(w, total - 1), a.per_row), hv = w - r * 2 * H, is_v = hv >= H, h = hv - is_v * H;
-            const bool live = w < total && slots[r].live == 1;
-            float x[kUnits][2 * V];
-            float top = 0.f;
-            if (live) {
-#pragma unroll
-                for (int q = 0; q < kUnits; ++q) {
-                    const int u = lane + q * kLanes;
-                    if (u >= units) continue;
-                    raw[s][q][0].to(x[q]);
-                    raw[s][q][1].to(x[q] + V);
-                    if (!is_v) rotate_unit<V>(x[q], u, 2 * half, a.rope.interleaved, cs + r * half);
-#pragma unroll
-                    for (int i = 0; i < 2 * V; ++i) {
-                        const float m = fabsf(x[q][i]);
-                        top = fmaxf(top, m < INFINITY ? m : 0.f);
-                    }
-                }
-            }
-            int e = 0;
-            if constexpr (sizeof(C) == 1) {
-#pragma unroll
-                for (int off = kLanes / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                e = e4m3_exponent(top);
-            }
-            if (!live) continue;
-            const RowSlot& slot = slots[r];
-            C* dst = static_cast<C*>(is_v ? c.v : c.k) + slot.at + h * c.head_stride;
+    for (int round = 0; round < total; round += kGroups, at.move(step, 2 * H, 1)) {
+        const bool in = round + group < total;
+        if (round > 0) fetch(in);
+        const int r = in ? at.r : 0, is_v = at.h >= H, h = at.h - is_v * H;
+        const bool live = in && slots[r].live == 1;
+        float x[kUnits][2 * V];
+        float top = 0.f;
+        if (live) {
 #pragma unroll
             for (int q = 0; q < kUnits; ++q) {
                 const int u = lane + q * kLanes;
                 if (u >= units) continue;
-                int first, second;
-                unit_runs<V>(u, 2 * half, a.rope.interleaved, &first, &second);
-                if constexpr (sizeof(C) == 1) {
-                    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);     // 2^-e, e in [-126, 120]
-                    store_e4m3<V>(reinterpret_cast<uint8_t*>(dst) + first, x[q], inv);
-                    store_e4m3<V>(reinterpret_cast<uint8_t*>(dst) + second, x[q] + V, inv);
-                } else {
-                    Raw<C, V> y;
-                    y.from(x[q]);
-                    y.store(dst + first);
-                    y.from(x[q] + V);
-                    y.store(dst + second);
+                raw[q][0].to(x[q]);
+                raw[q][1].to(x[q] + V);
+                if (!is_v) rotate_unit<V>(x[q], u, 2 * half, a.rope.interleaved, cs + r * half);
+#pragma unroll
+                for (int i = 0; i < 2 * V; ++i) top = fmaxf(top, fabsf(x[q][i]));      // (fmaxf passes over NaN)
+            }
+        }
+        int e = 0;
+        if constexpr (sizeof(C) == 1) {
+            if (__any_sync(0xffffffffu, top == INFINITY)) {
+                // infinities become NaN and leave the scale to the others
+                top = 0.f;
+                if (live) {
+#pragma unroll
+                    for (int q = 0; q < kUnits; ++q)
+                        if (lane + q * kLanes < units)
+#pragma unroll
+                            for (int i = 0; i < 2 * V; ++i) {
+                                if (fabsf(x[q][i]) == INFINITY) x[q][i] = NAN;
+                                top = fmaxf(top, fabsf(x[q][i]));
+                            }
                 }
             }
-            if constexpr (sizeof(C) == 1)
-                if (lane == 0) (is_v ? c.v_exp : c.k_exp)[slot.exp_at + (int64_t)h * c.page_size] = (uint8_t)(e + 127);
+#pragma unroll
+            for (int off = kLanes / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            e = e4m3_exponent(top);
         }
+        if (!live) continue;
+        const RowSlot& slot = slots[r];
+        C* dst = static_cast<C*>(is_v ? c.v : c.k) + slot.at + h * c.head_stride;
+#pragma unroll
+        for (int q = 0; q < kUnits; ++q) {
+            const int u = lane + q * kLanes;
+            if (u >= units) continue;
+            int first, second;
+            unit_runs<V>(u, 2 * half, a.rope.interleaved, &first, &second);
+            if constexpr (sizeof(C) == 1) {
+                const float inv = __uint_as_float((uint32_t)(127 - e) << 23);     // 2^-e, e in [-126, 120]
+                store_e4m3<V>(reinterpret_cast<uint8_t*>(dst) + first, x[q], inv);
+                store_e4m3<V>(reinterpret_cast<uint8_t*>(dst) + second, x[q] + V, inv);
+            } else {
+                Raw<C, V> y;
+                y.from(x[q]);
+                y.store(dst + first);
+                y.from(x[q] + V);
+                y.store(dst + second);
+            }
+        }
+        if constexpr (sizeof(C) == 1)
+            if (lane == 0) (is_v ? c.v_exp : c.k_exp)[slot.exp_at + (int64_t)h * c.page_size] = (uint8_t)(e + 127);
     }
 }
 
@@ -240,19 +237,18 @@ template <typename T, typename C> specdec_status_t launch_write(WriteArgs a, cud
     const int64_t per = 16 / (int64_t)sizeof(T);
     const bool wide = rot % 16 == 0 && aligned_to(a.k, 16) && aligned_to(a.v, 16) && a.row_stride % per == 0 &&
                       a.head_stride % per == 0;
-    // rows of one wave of CTAs (four on each of 152 SMs), up to a batch of heads a group; never fewer than fill a CTA
-    const int groups = wide ? kThreads / 8 : kThreads / 32, heads = 2 * c.num_kv_heads, batch = (wide ? 4 : 2) * groups;
-    if (heads >= 1 << 18) return SPECDEC_ERR_UNSUPPORTED;          // over() is exact below that
+    // rows of one wave of CTAs (four on each of 152 SMs), up to eight heads a group; never fewer than fill a CTA
+    const int groups = wide ? kThreads / 8 : kThreads / 32, heads = 2 * c.num_kv_heads, batch = 8 * groups;
+    if (heads >= 1 << 24) return SPECDEC_ERR_UNSUPPORTED;          // (32-bit places within a CTA's rows)
     const int64_t wave = ((int64_t)a.rows + 607) / 608, most = (batch + heads - 1) / heads, fill = (groups + heads - 1) / heads;
     int64_t rpc = wave < most ? wave : most;
     rpc = rpc > fill ? rpc : fill;
     rpc = rpc > kMaxRows ? kMaxRows : rpc;
     a.rows_per_cta = (int)rpc;
-    a.per_row = 1.f / (float)heads;
     const unsigned grid = (unsigned)(((int64_t)a.rows + rpc - 1) / rpc);
     const size_t smem = (size_t)rpc * (rot / 2) * sizeof(float2);
-    if (wide) specdec_kv_write_kernel<T, C, 8, 8, 1, sizeof(T) == 4 ? 2 : 4><<<grid, kThreads, smem, stream>>>(a);
-    else specdec_kv_write_kernel<T, C, 1, 32, 2, 2><<<grid, kThreads, smem, stream>>>(a);
+    if (wide) specdec_kv_write_kernel<T, C, 8, 8, 1><<<grid, kThreads, smem, stream>>>(a);
+    else specdec_kv_write_kernel<T, C, 1, 32, 2><<<grid, kThreads, smem, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 
@@ -273,7 +269,6 @@ struct ReadArgs {
     void *out_k, *out_v;
     int64_t out_row, out_head;
     uint32_t* status;
-    float per_row, per_head;              // 1 / units of a row (keys and values), of a head
 };
 
 // Offsets and range of request b: 0 fine, else the status bit.
@@ -312,18 +307,18 @@ __global__ void __launch_bounds__(kThreads, 4) specdec_kv_read_kernel(const Read
     }
     __syncthreads();
     const int units = c.head_dim / 16, H = c.num_kv_heads, row_units = 2 * H * units, total = n * row_units;
+    const Place step(kThreads, 2 * H, units);
+    Place at(tid, 2 * H, units);
     for (int base = tid; base < total; base += kReadBatch * kThreads) {
         Raw<C, 16> raw[kReadBatch];
         float scale[kReadBatch];
         T* out[kReadBatch];                                        // nullptr: nothing to write
 #pragma unroll
-        for (int q = 0; q < kReadBatch; ++q) {
-            const int i = base + q * kThreads;
+        for (int q = 0; q < kReadBatch; ++q, at.move(step, 2 * H, units)) {
             out[q] = nullptr;
             scale[q] = 1.f;
-            if (i >= total) continue;
-            const int r = over(i, a.per_row), w = i - r * row_units, hv = over(w, a.per_head), u = w - hv * units;
-            const int is_v = hv >= H, h = hv - is_v * H;
+            if (base + q * kThreads >= total) continue;
+            const int r = at.r, u = at.u, is_v = at.h >= H, h = at.h - is_v * H;
             const RowSlot& slot = slots[r];
             T* const to = static_cast<T*>(is_v ? a.out_v : a.out_k);
             if (!slot.live || !to) continue;
@@ -363,16 +358,14 @@ template <typename C, typename T> specdec_status_t launch_read(ReadArgs a, cudaS
     const bool wide = aligned_to(a.out_k, 16) && aligned_to(a.out_v, 16) && a.out_row % per == 0 && a.out_head % per == 0;
     const int units = a.cache.head_dim / 16;
     const int64_t row_units = (int64_t)2 * a.cache.num_kv_heads * units;
-    if (row_units >= 1 << 21) return SPECDEC_ERR_UNSUPPORTED;      // over() is exact below that
-    // as the write's: one wave's rows, up to two batches of units a thread, never fewer than fill a CTA
-    const int64_t wave = (a.rows + 607) / 608, most = (2 * kReadBatch * kThreads + row_units - 1) / row_units,
+    if (row_units >= 1 << 24) return SPECDEC_ERR_UNSUPPORTED;      // (32-bit places within a CTA's rows)
+    // as the write's: one wave's rows, up to 16 units a thread, never fewer than fill a CTA
+    const int64_t wave = (a.rows + 607) / 608, most = (16 * kThreads + row_units - 1) / row_units,
                   fill = (kThreads + row_units - 1) / row_units;
     int64_t rpc = wave < most ? wave : most;
     rpc = rpc > fill ? rpc : fill;
-    while (rpc > 1 && (rpc > kMaxRows || rpc * row_units >= 1 << 21)) --rpc;
+    rpc = rpc > kMaxRows ? kMaxRows : rpc;
     a.rows_per_cta = (int)rpc;
-    a.per_row = 1.f / (float)row_units;
-    a.per_head = 1.f / (float)units;
     const int64_t grid = (a.rows + rpc - 1) / rpc;
     if (grid > 0x7fffffff) return SPECDEC_ERR_UNSUPPORTED;
     if (wide) specdec_kv_read_kernel<C, T, true><<<(unsigned)grid, kThreads, 0, stream>>>(a);
@@ -409,7 +402,7 @@ extern "C" specdec_status_t specdec_kv_write(const void* k, const void* v, specd
         !aligned_to(cached_len, 4) || !aligned_to(cu_num_draft, 4) || !aligned_to(status, 4))
         return SPECDEC_ERR_INVALID_ARG;
     WriteArgs a = {k, v, row_stride, head_stride, rows, 0, rope != nullptr, rope ? *rope : specdec_rope_t{nullptr, 0, 0, 1.f},
-                   positions, *cache, {block_table, block_stride, max_blocks}, cached_len, cu_num_draft, B, status, 0.f};
+                   positions, *cache, {block_table, block_stride, max_blocks}, cached_len, cu_num_draft, B, status};
     if (dtype == SPECDEC_F32) return launch_write_to<float>(a, (cudaStream_t)stream);
     if (dtype == SPECDEC_BF16) return launch_write_to<__nv_bfloat16>(a, (cudaStream_t)stream);
     return launch_write_to<__half>(a, (cudaStream_t)stream);
@@ -433,7 +426,7 @@ extern "C" specdec_status_t specdec_kv_read(const specdec_kv_cache_t* cache, con
         !aligned_to(cu_len, 8) || !aligned_to(status, 4))
         return SPECDEC_ERR_INVALID_ARG;
     const ReadArgs a = {*cache, {block_table, block_stride, max_blocks}, first, cu_len, B, 0, rows, out_k, out_v,
-                        out_row_stride, out_head_stride, status, 0.f, 0.f};
+                        out_row_stride, out_head_stride, status};
     if (cache->dtype == SPECDEC_BF16) return launch_read_to<__nv_bfloat16>(a, out_dtype, (cudaStream_t)stream);
     if (cache->dtype == SPECDEC_F16) return launch_read_to<__half>(a, out_dtype, (cudaStream_t)stream);
     return launch_read_to<__nv_fp8_e4m3>(a, out_dtype, (cudaStream_t)stream);

@@ -26,13 +26,12 @@ struct RopeArgs {
     specdec_rope_t rope;
     const int32_t *positions, *cu, *cached;
     int32_t B;
-    float per_row, per_head;              // 1 / units of a row, of a head
 };
 
 // The first batch is read before the rows' positions are known: their chain of reads and the angles
 // then cost nothing on top of it.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, 4) specdec_rope_kernel(const RopeArgs a)
+__global__ void __launch_bounds__(kThreads, 3) specdec_rope_kernel(const RopeArgs a)
 {
     extern __shared__ float2 cs[];                                 // [rows_per_cta][rot_dim / 2]
     __shared__ int64_t pos[kMaxRows];
@@ -42,21 +41,15 @@ __global__ void __launch_bounds__(kThreads, 4) specdec_rope_kernel(const RopeArg
     const int n = (int)min((int64_t)a.rows_per_cta, a.rows - row0);
     const int row_units = a.heads * a.units, total = n * row_units;
     Raw<T, V> v[kBatch][2];
-    auto place = [&](int i, int* r, int* h, int* u, int* first, int* second) {
-        *r = over(i, a.per_row);
-        const int w = i - *r * row_units;
-        *h = over(w, a.per_head);
-        *u = w - *h * a.units;
-        unit_runs<V>(*u, a.rope.rot_dim, a.rope.interleaved, first, second);
-    };
+    const Place step(kThreads, a.heads, a.units);
+    Place ahead(tid, a.heads, a.units), at = ahead;                // of the next unit to read, to write
     auto fetch = [&](int base) {
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-            const int i = base + q * kThreads;
-            if (i >= total) continue;
-            int r, h, u, first, second;
-            place(i, &r, &h, &u, &first, &second);
-            const T* x = static_cast<const T*>(a.x) + (row0 + r) * a.x_row + h * a.x_head;
+        for (int q = 0; q < kBatch; ++q, ahead.move(step, a.heads, a.units)) {
+            if (base + q * kThreads >= total) continue;
+            int first, second;
+            unit_runs<V>(ahead.u, a.rope.rot_dim, a.rope.interleaved, &first, &second);
+            const T* x = static_cast<const T*>(a.x) + (row0 + ahead.r) * a.x_row + ahead.h * a.x_head;
             v[q][0].load(x + first);
             v[q][1].load(x + second);
         }
@@ -89,17 +82,15 @@ __global__ void __launch_bounds__(kThreads, 4) specdec_rope_kernel(const RopeArg
     for (int base = tid; base < total; base += kBatch * kThreads) {
         if (base != tid) fetch(base);
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-            const int i = base + q * kThreads;
-            if (i >= total) continue;
-            int r, h, u, first, second;
-            place(i, &r, &h, &u, &first, &second);
-            if (!live[r]) continue;
+        for (int q = 0; q < kBatch; ++q, at.move(step, a.heads, a.units)) {
+            if (base + q * kThreads >= total || !live[at.r]) continue;
+            int first, second;
+            unit_runs<V>(at.u, a.rope.rot_dim, a.rope.interleaved, &first, &second);
             float x[2 * V];
             v[q][0].to(x);
             v[q][1].to(x + V);
-            rotate_unit<V>(x, u, a.rope.rot_dim, a.rope.interleaved, cs + r * half);
-            T* out = static_cast<T*>(a.out) + (row0 + r) * a.out_row + h * a.out_head;
+            rotate_unit<V>(x, at.u, a.rope.rot_dim, a.rope.interleaved, cs + at.r * half);
+            T* out = static_cast<T*>(a.out) + (row0 + at.r) * a.out_row + at.h * a.out_head;
             Raw<T, V> y;
             y.from(x);
             y.store(out + first);
@@ -121,16 +112,14 @@ specdec_status_t launch_rope(RopeArgs a, cudaStream_t stream)
     const int V = wide ? kV : 1;
     a.units = a.head_dim / (2 * V);
     const int64_t row_units = (int64_t)a.heads * a.units;
-    if (row_units >= 1 << 21) return SPECDEC_ERR_UNSUPPORTED;      // over() is exact below that
+    if (row_units >= 1 << 24) return SPECDEC_ERR_UNSUPPORTED;      // (32-bit places within a CTA's rows)
     // rows of one wave of CTAs (four on each of 152 SMs), up to a batch of units a thread; never fewer than fill a CTA
     const int64_t wave = ((int64_t)a.rows + 607) / 608, batch = (kBatch * kThreads + row_units - 1) / row_units,
                   fill = (kThreads + row_units - 1) / row_units;
     int64_t rpc = wave < batch ? wave : batch;
     rpc = rpc > fill ? rpc : fill;
-    while (rpc > 1 && (rpc > kMaxRows || rpc * row_units >= 1 << 21)) --rpc;
+    rpc = rpc > kMaxRows ? kMaxRows : rpc;
     a.rows_per_cta = (int)rpc;
-    a.per_row = 1.f / (float)row_units;
-    a.per_head = 1.f / (float)a.units;
     const unsigned grid = (unsigned)(((int64_t)a.rows + a.rows_per_cta - 1) / a.rows_per_cta);
     const size_t smem = (size_t)a.rows_per_cta * (a.rope.rot_dim / 2) * sizeof(float2);
     if (wide) specdec_rope_kernel<T, kV><<<grid, kThreads, smem, stream>>>(a);
@@ -188,7 +177,7 @@ extern "C" specdec_status_t specdec_rope(const void* x, void* out, specdec_dtype
         !aligned_to(cached_len, 4))
         return SPECDEC_ERR_INVALID_ARG;
     RopeArgs a = {x, out, rows, heads, head_dim, 0, 0, inverse != 0, x_row_stride, x_head_stride, out_row_stride,
-                  out_head_stride, *rope, positions, cu_num_draft, cached_len, B, 0.f, 0.f};
+                  out_head_stride, *rope, positions, cu_num_draft, cached_len, B};
     if (dtype == SPECDEC_F32) return launch_rope<float>(a, (cudaStream_t)stream);
     if (dtype == SPECDEC_BF16) return launch_rope<__nv_bfloat16>(a, (cudaStream_t)stream);
     return launch_rope<__half>(a, (cudaStream_t)stream);

@@ -141,9 +141,25 @@ template <typename T, int N> struct Raw {
     }
 };
 
-// floor(x / y) by the reciprocal 1.f / y: exact for 0 <= x < 2^21 (x + 1/2 is at least 1/2 away from a multiple of y,
-// relative to x more than the two roundings of 2^-24)
-__device__ __forceinline__ int over(int x, float reciprocal) { return __float2int_rd(((float)x + 0.5f) * reciprocal); }
+// A place in rows of heads of units that moves on by a fixed number of units, without divisions on the way.
+struct Place {
+    int r, h, u;
+    __device__ __forceinline__ Place(int i, int heads, int units)
+    {
+        const int w = i / units;
+        u = i - w * units;
+        r = w / heads;
+        h = w - r * heads;
+    }
+    __device__ __forceinline__ void move(const Place& by, int heads, int units)
+    {
+        u += by.u;
+        h += by.h;
+        r += by.r;
+        if (u >= units) u -= units, ++h;
+        if (h >= heads) h -= heads, ++r;
+    }
+};
 
 // A head is taken in units of 2V elements: the two runs of V that rotate together (half layout), 2V
 // consecutive ones (interleaved layout, and the elements behind rot_dim). Needs rot_dim and

@@ -44,6 +44,13 @@ constexpr float kLazy = 8.f;                             // how far (log2) a sco
 constexpr uint32_t kWaitNs = 2000000000u;                // a wait's default limit
 constexpr unsigned long long kDrainNs = 1000000000ull;   // more time for copies in flight before a CTA leaves
 constexpr int kSmemBytes = 227 * 1024;
+constexpr int kJoinThreads = 512;                        // of the join: four rows of 128 elements, or eight of 64
+
+// An item that a CTA begins and others go on with: its first row, rows and first column's row, head, and the last CTA
+// (below 0: none).
+struct Split {
+    int32_t row0, rows, first, head, last;
+};
 
 struct Args {
     const void* q;
@@ -59,7 +66,7 @@ struct Args {
     int32_t B, max_k, window;
     float scale_log2;                                    // scale * log2(e)
     uint32_t* status;
-    int4* split;                                         // [P]: the item that CTA i leaves to the next ones
+    Split* split;                                        // [P]: the item that CTA i leaves to the next ones
     float* parts;                                        // [2 P] slots of N (D + 2) floats
     uint32_t wait_ns;
 };
@@ -291,6 +298,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == S::kMma) tmem_alloc(smem_u32(&ms.tmem), S::kTmemColumns);
+    after_predecessor();
     {
         // every thread sums the units of consecutive requests, a scan over the threads places them
         const int per = (a.B + S::kThreads - 1) / S::kThreads, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
@@ -325,7 +333,6 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
     tmem_before();
     __syncthreads();
     tmem_after();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = ms.tmem;
     const uint32_t t_o = tmem, t_s = tmem + S::kPar * N;
     // ring slot of a tile's keys, and of its values
@@ -343,7 +350,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         return ok && w.b >= 0;
     };
     Task w;
-    if (tid == 0) a.split[blockIdx.x] = make_int4(-1, 0, 0, 0);         // this thread may fill it in below
+    if (tid == 0) a.split[blockIdx.x].last = -1;         // this thread may fill it in below
 
     if (warp == S::kProducer || warp == S::kProducer + 1) {
         // ================================================================ keys (one warp) and values (the other) into the ring
@@ -1049,7 +1056,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 int lastc = (int)min((int64_t)P - 1, quotient(w.last_unit, max((int64_t)1, quotient(ms.units, P))));
                 while (cta_begin(ms.units, lastc + 1, P) <= w.last_unit) ++lastc;
                 while (cta_begin(ms.units, lastc, P) > w.last_unit) --lastc;
-                a.split[blockIdx.x] = make_int4(w.b, w.h, w.block, lastc);
+                a.split[blockIdx.x] = {w.row0, w.rows, w.block * N, w.h, lastc};
             }
             tmem_before();
             __syncwarp();
@@ -1103,26 +1110,28 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
 // slot 2 j of each CTA j up to the last. A warp takes 32 elements of a row: its lanes hold the parts' factors, and
 // the parts' elements are summed in their order.
 template <typename T, int N, int DP>
-__global__ void __launch_bounds__(128) specdec_paged_join_kernel(const Args a)
+__global__ void __launch_bounds__(kJoinThreads) specdec_paged_join_kernel(const Args a)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 s = a.split[blockIdx.x];
-    if (s.x < 0) return;
+    after_predecessor();
+    const Split s = a.split[blockIdx.x];
+    if (s.last < 0) return;
     constexpr int64_t kSlot = N * (DP + 2);
-    constexpr int kWarps = DP / 32, kRows = 4 / kWarps;
-    const Request r = request_of<N>(a, s.x);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = (warp % kWarps) * 32 + lane, i = blockIdx.x, n = s.w - i + 1;
+    constexpr int kWarps = DP / 32, kRows = kJoinThreads / DP;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = (warp % kWarps) * 32 + lane, i = blockIdx.x, n = s.last - i + 1;
     const float* const head = a.parts + (2 * (int64_t)i + 1) * kSlot;
     const float* const tail = a.parts + 2 * (int64_t)i * kSlot;
     auto part = [&](int j) { return j == 0 ? head : tail + 2 * j * kSlot; };
+#pragma unroll 1
     for (int col = blockIdx.y * kRows + warp / kWarps; col < N; col += gridDim.y * kRows) {
-        const int row = s.z * N + col;
-        if (row >= r.rows) return;
+        const int row = s.first + col;
+        if (row >= s.rows) return;
         float m = -FLT_MAX;
+#pragma unroll 1
         for (int j = lane; j < n; j += 32) m = fmaxf(m, part(j)[N * DP + col]);
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
         float l = 0.f, o = 0.f;
+#pragma unroll 1
         for (int j0 = 0; j0 < n; j0 += 32) {
             float f = 0.f;
             if (j0 + lane < n) {
@@ -1131,16 +1140,22 @@ __global__ void __launch_bounds__(128) specdec_paged_join_kernel(const Args a)
                 l += p[N] * f;
             }
             const int up = min(32, n - j0);
-#pragma unroll 8
-            for (int j = 0; j < up; ++j) {
-                const float fj = __shfl_sync(0xffffffffu, f, j);
-                o = fmaf(part(j0 + j)[col * DP + d], fj, o);
+#pragma unroll 1
+            for (int j = 0; j < up; j += 8) {                            // eight parts' elements in flight
+                float x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = j + k < up ? part(j0 + j + k)[col * DP + d] : 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float fk = __shfl_sync(0xffffffffu, f, j + k);
+                    o = j + k < up ? fmaf(x[k], fk, o) : o;
+                }
             }
         }
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
         const int j = row / a.group, g = row - j * a.group;
-        const int64_t t = r.row0 + j, hq = s.y * a.group + g;
+        const int64_t t = s.row0 + j, hq = s.head * a.group + g;
         const bool any = !(l == 0.f);
         if (d < a.cache.head_dim) static_cast<T*>(a.out)[t * a.out_row + hq * a.out_head + d] = from_float<T>(any ? o * __frcp_rn(l) : 0.f);
         if (d == 0 && a.lse) a.lse[t * a.num_heads + hq] = lse_of(any, m, l);
@@ -1164,7 +1179,7 @@ int row_tile(int32_t max_k, int32_t group)
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 96 ? 96 : 128;
 }
 
-size_t split_bytes(int P) { return ((size_t)P * sizeof(int4) + 255) / 256 * 256; }
+size_t split_bytes(int P) { return ((size_t)P * sizeof(Split) + 255) / 256 * 256; }
 
 using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -1223,24 +1238,12 @@ template <typename S> specdec_status_t launch(const Args& a, cudaStream_t stream
             (void)cudaGetLastError();
             return SPECDEC_ERR_CUDA;
         }
-        kernel<<<P, S::kThreads, smem, stream>>>(a, kmap, vmap);
-        if (cudaGetLastError() == cudaSuccess) break;
+        if (launch_dependent(kernel, P, S::kThreads, smem, stream, a, kmap, vmap) == cudaSuccess) break;
         if (attempt > 0) return SPECDEC_ERR_CUDA;
     }
     allowed |= bit;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)P, 16);
-    cfg.blockDim = dim3(128);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, specdec_paged_join_kernel<typename S::T, S::N, S::DP>, a) != cudaSuccess) {
-        (void)cudaGetLastError();
+    if (launch_dependent(specdec_paged_join_kernel<typename S::T, S::N, S::DP>, dim3((unsigned)P, 4), kJoinThreads, 0, stream, a) != cudaSuccess)
         return SPECDEC_ERR_CUDA;
-    }
     return SPECDEC_OK;
 }
 
@@ -1297,7 +1300,7 @@ extern "C" specdec_status_t specdec_paged_attention(
     const int P = sm_count(), group = num_heads / cache->num_kv_heads;
     const Args a = {q, out, lse, num_heads, group, q_row_stride, q_head_stride, out_row_stride, out_head_stride, *cache,
                     block_table, block_stride, max_blocks, cached_len, cu_num_draft, B, max_k, window, scale * 1.4426950408889634f,
-                    status, static_cast<int4*>(workspace), reinterpret_cast<float*>(static_cast<char*>(workspace) + split_bytes(P)),
+                    status, static_cast<Split*>(workspace), reinterpret_cast<float*>(static_cast<char*>(workspace) + split_bytes(P)),
                     wait_limit_us < 0 ? kWaitNs : (uint32_t)wait_limit_us * 1000u};
     const int N = row_tile(max_k, group);
     return dtype == SPECDEC_BF16 ? launch_type<__nv_bfloat16>(a, N, (cudaStream_t)stream, P) : launch_type<__half>(a, N, (cudaStream_t)stream, P);

@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kThreads, 6) specdec_kv_write_kernel(const Wri
 {
     extern __shared__ float2 cs[];                                 // [rows_per_cta][rot_dim / 2]
     __shared__ RowSlot slots[kMaxRows];
+    after_predecessor();
     const specdec_kv_cache_t& c = a.cache;
     const int tid = threadIdx.x;
     const int64_t row0 = (int64_t)blockIdx.x * a.rows_per_cta;
@@ -247,9 +248,9 @@ template <typename T, typename C> specdec_status_t launch_write(WriteArgs a, cud
     a.rows_per_cta = (int)rpc;
     const unsigned grid = (unsigned)(((int64_t)a.rows + rpc - 1) / rpc);
     const size_t smem = (size_t)rpc * (rot / 2) * sizeof(float2);
-    if (wide) specdec_kv_write_kernel<T, C, 8, 8, 1><<<grid, kThreads, smem, stream>>>(a);
-    else specdec_kv_write_kernel<T, C, 1, 32, 2><<<grid, kThreads, smem, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+    const cudaError_t e = wide ? launch_dependent(specdec_kv_write_kernel<T, C, 8, 8, 1>, grid, kThreads, smem, stream, a)
+                               : launch_dependent(specdec_kv_write_kernel<T, C, 1, 32, 2>, grid, kThreads, smem, stream, a);
+    return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 
 template <typename T> specdec_status_t launch_write_to(const WriteArgs& a, cudaStream_t stream)
@@ -286,6 +287,7 @@ template <typename C, typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads, 4) specdec_kv_read_kernel(const ReadArgs a)
 {
     __shared__ RowSlot slots[kMaxRows];
+    after_predecessor();
     const specdec_kv_cache_t& c = a.cache;
     const int tid = threadIdx.x;
     const int64_t row0 = (int64_t)blockIdx.x * a.rows_per_cta;
@@ -368,9 +370,9 @@ template <typename C, typename T> specdec_status_t launch_read(ReadArgs a, cudaS
     a.rows_per_cta = (int)rpc;
     const int64_t grid = (a.rows + rpc - 1) / rpc;
     if (grid > 0x7fffffff) return SPECDEC_ERR_UNSUPPORTED;
-    if (wide) specdec_kv_read_kernel<C, T, true><<<(unsigned)grid, kThreads, 0, stream>>>(a);
-    else specdec_kv_read_kernel<C, T, false><<<(unsigned)grid, kThreads, 0, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+    const cudaError_t e = wide ? launch_dependent(specdec_kv_read_kernel<C, T, true>, (unsigned)grid, kThreads, 0, stream, a)
+                               : launch_dependent(specdec_kv_read_kernel<C, T, false>, (unsigned)grid, kThreads, 0, stream, a);
+    return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 
 template <typename C> specdec_status_t launch_read_to(const ReadArgs& a, specdec_dtype_t out, cudaStream_t stream)

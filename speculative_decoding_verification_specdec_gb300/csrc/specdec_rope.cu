@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(kThreads, 3) specdec_rope_kernel(const RopeArg
     extern __shared__ float2 cs[];                                 // [rows_per_cta][rot_dim / 2]
     __shared__ int64_t pos[kMaxRows];
     __shared__ int live[kMaxRows];
+    after_predecessor();
     const int tid = threadIdx.x, half = a.rope.rot_dim / 2;
     const int64_t row0 = (int64_t)blockIdx.x * a.rows_per_cta;
     const int n = (int)min((int64_t)a.rows_per_cta, a.rows - row0);
@@ -122,9 +123,9 @@ specdec_status_t launch_rope(RopeArgs a, cudaStream_t stream)
     a.rows_per_cta = (int)rpc;
     const unsigned grid = (unsigned)(((int64_t)a.rows + a.rows_per_cta - 1) / a.rows_per_cta);
     const size_t smem = (size_t)a.rows_per_cta * (a.rope.rot_dim / 2) * sizeof(float2);
-    if (wide) specdec_rope_kernel<T, kV><<<grid, kThreads, smem, stream>>>(a);
-    else specdec_rope_kernel<T, 1><<<grid, kThreads, smem, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
+    const cudaError_t e = wide ? launch_dependent(specdec_rope_kernel<T, kV>, grid, kThreads, smem, stream, a)
+                               : launch_dependent(specdec_rope_kernel<T, 1>, grid, kThreads, smem, stream, a);
+    return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 
 }  // namespace

@@ -11,6 +11,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "specdec.h"
 
 namespace specdec {
@@ -47,6 +49,33 @@ inline specdec_status_t check_cache(const specdec_kv_cache_t* c)
     if (c->dtype == SPECDEC_E4M3 ? (!c->k_exp || !c->v_exp) : (c->k_exp || c->v_exp)) return SPECDEC_ERR_INVALID_ARG;
     if (!aligned_to(c->k_exp, 16) || !aligned_to(c->v_exp, 16)) return SPECDEC_ERR_INVALID_ARG;
     return SPECDEC_OK;
+}
+
+// These kernels are launched as programmatic dependents of what the stream holds before them: a launch is set up while
+// its predecessor still runs, and waits for its end (and its writes) here, before anything else is read or written.
+// The next launch may be set up from here on.
+__device__ __forceinline__ void after_predecessor()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A&&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return e;
 }
 
 // Whether request b's rows are known: offsets as SPECDEC_ST_BAD_OFFSETS describes them.

@@ -238,7 +238,6 @@ template <typename S> struct Misc {
     alignas(16) int32_t last[2][S::N];                   // last token that a column sees (-1: no column)
     alignas(16) int2 place[2][S::N];                     // a column's row of q and out, and its query head (row -1: no column)
     alignas(16) int64_t out_at[2][S::N];                 // and where it lies in out
-    uint32_t top[S::kFp8 ? S::N : 1];                 // bits of the largest magnitude of a row of Q
     alignas(16) float qscale[2][S::kFp8 ? S::N : 4];
     alignas(16) uint8_t exps[S::kSlots][S::kFp8 ? kTile : 16];
 };
@@ -566,7 +565,6 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 ms.place[tb][n] = at;
                 ms.out_at[tb][n] = real ? at.x * a.out_row + at.y * a.out_head : -1;
                 ms.last[tb][n] = real ? w.cached + j : -1;
-                if constexpr (S::kFp8) ms.top[n] = 0;
             }
             __syncwarp();
             unsigned char* const dst = qbuf + qb * S::kQBytes;
@@ -587,59 +585,71 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 }
                 async_copy_wait();
             } else {
-                // whole rows a batch, all of a batch's loads in flight together
-                constexpr int kBatch = kChunks < 8 ? kChunks : 8;
-                static_assert(kChunks % kBatch == 0 && kBatch * 32 % DP == 0, "batches");
-#pragma unroll 1
-                for (int base = 0; base < kChunks; base += kBatch) {
-                    uint4 v[kBatch];
+                // Eight rows at a time: lanes of the same number modulo 8 hold a row, kRow chunks each; the next eight
+                // rows are on their way while these are taken apart.
+                // A power of two brings the row's largest magnitude to [128, 256): a piece is the nearest e4m3 number to
+                // what the pieces before it leave, in all exact to 2^-10, e4m3's half step at its smallest, so to
+                // 2^-17 of the row's largest element at worst. What is not finite becomes NaN.
+                constexpr int kRow = DP / 32;
+                auto read = [&](int base, uint4 (&v)[kRow]) {
 #pragma unroll
-                    for (int u = 0; u < kBatch; ++u) {
+                    for (int u = 0; u < kRow; ++u) {
                         const T* src = source(base + u);
                         v[u] = src ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
                     }
-                    // A power of two brings the row's largest magnitude to [128, 256): a piece is the nearest e4m3 number to
-                    // what the pieces before it leave, in all exact to 2^-10, e4m3's half step at its smallest, so to
-                    // 2^-17 of the row's largest element at worst. What is not finite becomes NaN.
+                };
+                uint4 now[kRow], next[kRow];
+                read(0, now);
+#pragma unroll 1
+                for (int base = 0; base < kChunks; base += kRow) {
+                    if (base + kRow < kChunks) read(base + kRow, next);
+                    float z[kRow][8], top = 0.f;
 #pragma unroll
-                    for (int u = 0; u < kBatch; ++u) {
-                        const T* y = reinterpret_cast<const T*>(&v[u]);
-                        float top = 0.f;
+                    for (int u = 0; u < kRow; ++u) {
+                        const T* y = reinterpret_cast<const T*>(&now[u]);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            const float z = fabsf(to_float<T>(y[k]));
-                            top = fmaxf(top, z < INFINITY ? z : 0.f);
+                            z[u][k] = to_float<T>(y[k]);
+                            top = fmaxf(top, fabsf(z[u][k]));            // (fmaxf passes over NaN)
                         }
-                        if (top > 0.f) atomicMax(&ms.top[column(base + u)], __float_as_uint(top));
                     }
-                    __syncwarp();
+                    if (__any_sync(0xffffffffu, top == INFINITY)) {
+                        top = 0.f;
 #pragma unroll
-                    for (int u = 0; u < kBatch; ++u) {
-                        const int n = column(base + u), at = piece(base + u);
-                        const int e = ms.top[n] ? max((int)(ms.top[n] >> 23) - 126, -100) : 8;
-                        const float inv = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
-                        if (at == 0) ms.qscale[tb][n] = __uint_as_float((uint32_t)(127 + e - 8) << 23);
-                        const T* y = reinterpret_cast<const T*>(&v[u]);
+                        for (int u = 0; u < kRow; ++u)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                if (fabsf(z[u][k]) == INFINITY) z[u][k] = NAN;
+                                top = fmaxf(top, fabsf(z[u][k]));
+                            }
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    const int n = column(base);
+                    const int e = top > 0.f ? max((int)(__float_as_uint(top) >> 23) - 126, -100) : 8;
+                    const float inv = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+                    if (lane < 8) ms.qscale[tb][n] = __uint_as_float((uint32_t)(127 + e - 8) << 23);
+#pragma unroll
+                    for (int u = 0; u < kRow; ++u) {
+                        const int at = piece(base + u);
                         unsigned char* const d = dst + ((n >> 3) * (DP / 16) + (at >> 1)) * 128 + (n & 7) * 16 + (at & 1) * 8;
-                        float z[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) z[k] = to_float<T>(y[k]) * inv;
 #pragma unroll
                         for (int p = 0; p < S::kPieces; ++p) {
-                            uint32_t codes[2];
+                            uint32_t two[4];
 #pragma unroll
-                            for (int k = 0; k < 8; k += 2) {
-                                const float a0 = fabsf(z[k]) < INFINITY ? z[k] : NAN, a1 = fabsf(z[k + 1]) < INFINITY ? z[k + 1] : NAN;
-                                const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(a0, a1), __NV_SATFINITE, __NV_E4M3);
-                                codes[k / 4] = k & 2 ? codes[k / 4] | two << 16 : two;
-                                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-                                const float2 back = __half22float2(__half2(h));
-                                z[k] -= back.x;
-                                z[k + 1] -= back.y;
+                            for (int k = 0; k < 4; ++k) {
+                                const float scale = p == 0 ? inv : 1.f;
+                                const float2 x = make_float2(z[u][2 * k] * scale, z[u][2 * k + 1] * scale);
+                                two[k] = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+                                const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two[k], __NV_E4M3)));
+                                z[u][2 * k] = x.x - back.x;
+                                z[u][2 * k + 1] = x.y - back.y;
                             }
-                            *reinterpret_cast<uint2*>(d + p * N * DP) = make_uint2(codes[0], codes[1]);
+                            *reinterpret_cast<uint2*>(d + p * N * DP) = make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
                         }
                     }
+#pragma unroll
+                    for (int u = 0; u < kRow; ++u) now[u] = next[u];
                 }
             }
             fence_async();

@@ -322,7 +322,8 @@ specdec_status_t specdec_bitmask_scatter(const int32_t* compact, int64_t compact
  * so that one array can collect a step's calls. All pointers are device pointers on the current
  * device unless said otherwise; nothing is allocated; every call is asynchronous on `stream`
  * and may be captured into a graph (lengths, offsets and block tables are read on the device, so a
- * replay uses their values at that time).
+ * replay uses their values at that time). The kernels are launched as programmatic dependents: set up
+ * while the work before them in the stream still runs, they wait for its end before they read or write.
  * ------------------------------------------------------------------------------------------ */
 
 /* A rotary embedding. freq[i] (device) is how far the i-th pair turns per position, in units of
@@ -465,13 +466,19 @@ specdec_status_t specdec_kv_read(const specdec_kv_cache_t* cache, const int32_t*
  *   wait_limit_us -1: 2 s; 0..2000000: the limit of every wait inside the kernel, after which the
  *                requests concerned get SPECDEC_ST_DEVICE_TIMEOUT and undefined outputs; nothing
  *                hangs or traps.
- * A row's result depends on its own request alone, and equal calls give equal bits. Scores, maxima,
- * sums and the output are accumulated in fp32; the weights exp(s - m) are rounded to the cache's
- * 16-bit type (F16 for E4M3) before their product with V. Keys and values that a row does not see
- * do not reach it, whatever they hold (infinities, NaN, pages never written). A row that sees no
- * finite score gets zeros and lse = -inf.
- * status: K_TOO_LARGE, BAD_OFFSETS (rows unknown: not written), BAD_LENGTH (both: zeros,
- * lse -inf in its rows), BAD_PAGE (its tokens read as zeros), DEVICE_TIMEOUT.
+ * Equal calls give equal bits; where the batch's work is cut among the SMs (which depends on all of its
+ * lengths) a request's result may differ in its last bits. Scores, maxima, sums and the output are
+ * accumulated in fp32. The weights exp(s - m) are rounded to the cache's 16-bit type before their product
+ * with V; over an E4M3 cache to F16, times their token's scale relative to the largest scale so far, so
+ * a weight whose product falls 2^24 below that is lost. There Q is taken as a sum of two (BF16) or three
+ * (F16) e4m3 numbers an element, exact but for elements under 2^-9 (BF16) or 2^-6 (F16) of the row's
+ * largest, which are off by at most 2^-17 of it; an infinity in Q counts as NaN there.
+ * Keys and values that a row does not see do not reach it, whatever they hold (infinities, NaN, pages
+ * never written; with a window, block_table entries of pages that lie wholly before it are not read).
+ * A row that sees no finite score gets zeros and lse = -inf.
+ * status: K_TOO_LARGE, BAD_OFFSETS (also where cu names a row at or behind `rows`; rows unknown: not
+ * written), BAD_LENGTH (both others: zeros, lse -inf in its rows; also 2^31 - 128 tokens or more),
+ * BAD_PAGE (its tokens read as zeros), DEVICE_TIMEOUT.
  * Errors: INVALID_ARG for a NULL required pointer, a bad size or stride, num_heads not a multiple of
  * num_kv_heads, a workspace too small or misaligned; UNSUPPORTED for types, page_size or head_dim
  * outside those above; CUDA.

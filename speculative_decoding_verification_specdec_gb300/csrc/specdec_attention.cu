@@ -56,7 +56,7 @@ struct Args {
     const void* q;
     void* out;
     float* lse;
-    int32_t num_heads, group;
+    int32_t rows, num_heads, group;
     int64_t q_row, q_head, out_row, out_head;
     specdec_kv_cache_t cache;
     const int32_t* block_table;
@@ -84,11 +84,11 @@ struct Request {
 template <int N> __device__ __noinline__ Request request_of(const Args& a, int b)
 {
     Request r = {0, 0, 0, 0, 0, 0, 0};
-    if (!offsets_ok(a.cu, a.B, b)) {
+    const int32_t c0 = __ldg(a.cu + b), k = __ldg(a.cu + b + 1) - c0;
+    if (!offsets_ok(a.cu, a.B, b) || (int64_t)c0 + b + k + 1 > a.rows) {
         r.fault = SPECDEC_ST_BAD_OFFSETS;
         return r;
     }
-    const int32_t c0 = __ldg(a.cu + b), k = __ldg(a.cu + b + 1) - c0;
     r.row0 = c0 + b;
     r.cached = __ldg(a.cached + b);
     if (k > a.max_k) {
@@ -210,13 +210,14 @@ template <typename T_, bool kFp8_, int N_, int DB_> struct Shape {
     static_assert(kTasks >= kAhead + 4, "tasks ahead");
     static constexpr int kSlotBytes = kTile * DP * (kFp8 ? 1 : 2);
     static constexpr int kQBytes = N * DP * (kFp8 ? kPieces : 2), kPBytes = N * kTile * 2, kV16Bytes = kFp8 ? kTile * DP * 2 : 0;
-    static constexpr int kMiscBytes = 13 * 1024;
+    static constexpr int kMiscBytes = (kFp8 ? 16 : 13) * 1024;
     static constexpr int kRoom = kSmemBytes - 1024 - kMiscBytes - kQ * kQBytes - kPar * kPBytes - 2 * kV16Bytes;
     static constexpr int kSlots = kRoom / kSlotBytes > 12 ? 12 : kRoom / kSlotBytes;
     static constexpr int kKSlots = kSlots / 2, kVSlots = kSlots - kKSlots;
     static constexpr int kTmem = (kPar + 2) * N;                         // O, two S
     static constexpr int kTmemColumns = kTmem <= 64 ? 64 : kTmem <= 128 ? 128 : kTmem <= 256 ? 256 : 512;
     static constexpr int kSlotFloats = N * (DP + 2);
+    static_assert(kKSlots + kAhead <= 12 && kVSlots + kAhead <= 12, "a tile's scales stay in their ring of 16 until it is done with");
     static_assert(kKSlots >= 2 && kTmem <= 512, "shape does not fit the SM");
 };
 
@@ -239,7 +240,8 @@ template <typename S> struct Misc {
     alignas(16) int2 place[2][S::N];                     // a column's row of q and out, and its query head (row -1: no column)
     alignas(16) int64_t out_at[2][S::N];                 // and where it lies in out
     alignas(16) float qscale[2][S::kFp8 ? S::N : 4];
-    alignas(16) uint8_t exps[S::kSlots][S::kFp8 ? kTile : 16];
+    alignas(16) int32_t pages[2][8][8];                  // of keys and of values: page ids of the tiles looked ahead to
+    alignas(16) uint8_t scales[2][S::kFp8 ? 16 : 1][kTile];              // and exponents of their e4m3 tokens
 };
 
 // ---------------------------------------------------------------- the kernel
@@ -258,7 +260,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
     unsigned char* const pbuf = qbuf + S::kQ * S::kQBytes;
     Misc<S>& ms = *reinterpret_cast<Misc<S>*>(pbuf + S::kPar * S::kPBytes);
     static_assert(sizeof(Misc<S>) <= S::kMiscBytes, "misc");
-    static_assert(offsetof(Misc<S>, last) % 16 == 0 && offsetof(Misc<S>, qscale) % 16 == 0 && offsetof(Misc<S>, exps) % 16 == 0 &&
+    static_assert(offsetof(Misc<S>, last) % 16 == 0 && offsetof(Misc<S>, qscale) % 16 == 0 && offsetof(Misc<S>, scales) % 16 == 0 &&
                   offsetof(Misc<S>, fac) % 16 == 0 && sizeof(Misc<S>) % 16 == 0, "8- and 16-byte accesses");
     static_assert(S::kSlotBytes % 1024 == 0 && S::kQBytes % 1024 == 0 && S::kPBytes % 1024 == 0, "swizzled tiles");
 
@@ -355,72 +357,78 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         // ================================================================ keys (one warp) and values (the other) into the ring
         // (a page of 16 slots takes a copy of 2 KB; at about 90 cycles a copy one warp would hold up both streams)
         const bool is_v = warp != S::kProducer;
-        const int ps = c.page_size, rows = min(ps, kTile), pages = kTile / rows;
+        const int ps = c.page_size, bits = __ffs(ps) - 1, row_bits = min(bits, 7), rows = 1 << row_bits, pages = kTile >> row_bits;
         const CUtensorMap* const map = is_v ? &vmap : &kmap;
         const uint32_t slots = is_v ? S::kVSlots : S::kKSlots;
-        // A tile on its way. Its page ids are read two tiles before its copies are issued; an e4m3 tile's four tiles
-        // before, and its scales (which wait for the ids) two. Tasks follow one another without a break.
+        // A tile on its way. Its page ids are on their way to shared memory while the two tiles before it are issued, an
+        // e4m3 tile's scales (which need the ids) too, so its ids four tiles: a read that had to land in a register
+        // would hold up each turn of the loop. Tasks follow one another without a break.
         struct Ahead {
-            int page, used, h, slot0, b;                 // this lane's page id; pages (0: no more tiles), head, first slot
-        };
-        uint32_t q = 0, n = 0;                           // tasks so far, tiles issued
-        int t = 0, t_end = 0, len = 0;
-        bool more = true;
-        auto look = [&]() {
-            Ahead x = {-1, 0, 0, 0, 0};
-            if (t == t_end && more) {
-                more = take(q++, w);
-                if (more) {
-                    t = w.t0;
-                    t_end = w.t1;
-                    len = w.cached + w.rows / a.group;
-                }
-            }
-            if (!more) return x;
-            const int32_t token = t * kTile + lane * rows;
-            x.used = min(pages, (len - t * kTile + rows - 1) / rows);
-            x.h = w.h;
-            x.b = w.b;
-            x.slot0 = ps > kTile ? t * kTile % ps : 0;
-            if (lane < x.used) x.page = __ldg(a.block_table + w.b * a.block_stride + token / ps);
-            ++t;
-            return x;
-        };
-        // 16 of the tile's scales to each of eight lanes (scale 1 where there is no page)
-        auto scales_of = [&](const Ahead& x) {
-            uint4 e = make_uint4(0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f);
-            if constexpr (S::kFp8) {
-                const int pg = __shfl_sync(0xffffffffu, x.page, (lane * 16 / rows) & 31);
-                if (lane < 8 && pg >= 0 && pg < c.num_pages)
-                    e = __ldg(reinterpret_cast<const uint4*>((is_v ? c.v_exp : c.k_exp) + ((int64_t)pg * H + x.h) * ps + x.slot0 + lane * 16 % rows));
-            }
-            return e;
+            int first, used, h, slot0, b;                // its pages first .. used - 1 (used 0: no more tiles), head, ...
         };
         constexpr int kAhead = S::kAhead;
+        uint32_t q = 0, n = 0, issued = 0;               // tasks so far, tiles, those whose copies were issued
+        int t = 0, t_end = 0, len = 0;
+        bool more = true;
         Ahead x[kAhead + 1];
-        [[maybe_unused]] uint4 e[3];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) x[i] = {-1, 0, 0, 0, 0};
+        for (int i = 0; i < kAhead; ++i) x[i] = {0, 0, 0, 0, 0};
 #pragma unroll 1
-        for (int k = 0;; ++k) {                          // (the first rounds only look ahead)
-            const Ahead& x0 = x[0];
-            x[kAhead] = look();
-            if constexpr (S::kFp8) e[2] = scales_of(x[2]);
+        for (int k = 0;; ++k) {                          // looks at tile k, issues tile k - kAhead
+            async_copy_wait_but_one();                   // what was under way two turns ago has landed
+            __syncwarp();
+            Ahead& ahead = x[kAhead];
+            ahead = {0, 0, 0, 0, 0};
+            if (t == t_end && more) {
+                more = take(q++, w);
+                t = w.t0;
+                t_end = w.t1;
+                len = w.cached + w.rows / a.group;
+            }
+            if (more) {
+                const int32_t token0 = t * kTile;
+                ahead.used = min(pages, (len - token0 + rows - 1) >> row_bits);
+                ahead.first = a.window > 0 ? max(w.cached - a.window + 1 - token0, 0) >> row_bits : 0;   // (no row sees those before)
+                ahead.h = w.h;
+                ahead.b = w.b;
+                ahead.slot0 = token0 & (ps - 1) & ~(rows - 1);
+                if (lane < 8) {
+                    int32_t* const to = &ms.pages[is_v][k & 7][lane];
+                    if (lane >= ahead.first && lane < ahead.used)
+                        async_copy_4(smem_u32(to), a.block_table + w.b * a.block_stride + ((token0 + (lane << row_bits)) >> bits));
+                    else
+                        *to = -1;
+                }
+                ++t;
+            }
+            if constexpr (S::kFp8) {
+                const Ahead& y = x[2];                   // tile k - 2: 16 of its scales a lane (1 where there is no page)
+                if (y.used > 0 && lane < 8) {
+                    const int pg = ms.pages[is_v][(k - 2) & 7][(lane << 4) >> row_bits];
+                    uint8_t* const to = &ms.scales[is_v][(k - 2) & 15][lane * 16];
+                    if (pg >= 0 && pg < c.num_pages)
+                        async_copy_16(smem_u32(to), (is_v ? c.v_exp : c.k_exp) + ((((int64_t)pg * H + y.h) << bits) + y.slot0 + ((lane << 4) & (rows - 1))), 16);
+                    else
+                        *reinterpret_cast<uint4*>(to) = make_uint4(0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f);
+                }
+            }
+            async_copy_commit();
             if (k >= kAhead) {
+                const Ahead& x0 = x[0];
                 if (x0.used == 0) break;
-                const bool bad = lane < x0.used && (x0.page < 0 || x0.page >= c.num_pages);
+                const int page = lane < 8 ? ms.pages[is_v][n & 7][lane] : -1;
+                const bool bad = lane >= x0.first && lane < x0.used && (page < 0 || page >= c.num_pages);
                 if (bad && a.status) atomicOr(a.status + x0.b, SPECDEC_ST_BAD_PAGE);
-                const int from = bad ? c.num_pages : x0.page;       // past the end: the copy reads zeros
+                const int from = bad ? c.num_pages : page;       // past the end: the copy reads zeros
                 const uint32_t s = is_v ? v_slot(n) : k_slot(n);
                 if (n >= slots) wait(ms.empty[s], n / slots - 1);
                 if (!__any_sync(0xffffffffu, *expired)) {
+                    issued = n + 1;
                     const uint32_t fb = bar(ms.full[s]), dst = smem_u32(ring) + s * S::kSlotBytes;
-                    if constexpr (S::kFp8)
-                        if (lane < 8) *reinterpret_cast<uint4*>(&ms.exps[s][lane * 16]) = e[0];
                     __syncwarp();
-                    if (elected()) bar_expect(fb, x0.used * rows * DP * (S::kFp8 ? 1 : 2));
+                    if (elected()) bar_expect(fb, (x0.used - x0.first) * rows * DP * (S::kFp8 ? 1 : 2));
 #pragma unroll 1
-                    for (int p = 0; p < x0.used; ++p) {
+                    for (int p = x0.first; p < x0.used; ++p) {
                         const int pg = __shfl_sync(0xffffffffu, from, p);
                         if (elected()) {
                             if constexpr (S::kFp8) {
@@ -438,14 +446,14 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             }
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) x[i] = x[i + 1];
-            if constexpr (S::kFp8) e[0] = e[1], e[1] = e[2];
         }
+        async_copy_wait();
         // nothing may still be on its way into shared memory when the CTA leaves
         __syncwarp();
         if (*expired && lane == 0) {
             const unsigned long long t0 = time_ns();
 #pragma unroll 1
-            for (uint32_t i = n > slots ? n - slots : 0; i < n; ++i)
+            for (uint32_t i = issued > slots ? issued - slots : 0; i < issued; ++i)
                 while (!bar_test(bar(ms.full[is_v ? v_slot(i) : k_slot(i)]), (i / slots) & 1u) && time_ns() - t0 < kDrainNs) {}
         }
     } else if (warp == S::kMma) {
@@ -731,8 +739,8 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int tok = 32 * wq + 8 * i + tq;
-                        kscale[i] = exp_value(ms.exps[ks][tok]) * a.scale_log2;
-                        ve[i] = (int)ms.exps[vs][tok] - 127;
+                        kscale[i] = exp_value(ms.scales[0][n & 15][tok]) * a.scale_log2;
+                        ve[i] = (int)ms.scales[1][n & 15][tok] - 127;
                         // a token that no row sees may hold anything
                         if (kMasked && (token0 + tok > seen_any || token0 + tok < from_any)) ve[i] = -100000;
                     }
@@ -886,7 +894,12 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                                 float p0 = exp2_fast(x[hf][r + rr][2 * s]), p1 = exp2_fast(x[hf][r + rr][2 * s + 1]);
                                 l[2 * (r + rr)] += p0;
                                 l[2 * (r + rr) + 1] += p1;
-                                if constexpr (S::kFp8) p0 *= vw[2 * hf + s], p1 *= vw[2 * hf + s];
+                                if constexpr (S::kFp8) {
+                                    const float v = vw[2 * hf + s];
+                                    // (a scale that is no number stays out of the rows that do not see its token)
+                                    p0 = kMasked && p0 == 0.f ? 0.f : p0 * v;
+                                    p1 = kMasked && p1 == 0.f ? 0.f : p1 * v;
+                                }
                                 if constexpr (std::is_same<M, __half>::value) {
                                     const __half2 h2 = __floats2half2_rn(p0, p1);
                                     packed[2 * rr + s] = *reinterpret_cast<const uint32_t*>(&h2);
@@ -1308,7 +1321,7 @@ extern "C" specdec_status_t specdec_paged_attention(
         workspace_bytes < specdec_paged_attention_workspace_size(B, max_k, num_heads, cache->num_kv_heads, cache->head_dim))
         return SPECDEC_ERR_INVALID_ARG;
     const int P = sm_count(), group = num_heads / cache->num_kv_heads;
-    const Args a = {q, out, lse, num_heads, group, q_row_stride, q_head_stride, out_row_stride, out_head_stride, *cache,
+    const Args a = {q, out, lse, rows, num_heads, group, q_row_stride, q_head_stride, out_row_stride, out_head_stride, *cache,
                     block_table, block_stride, max_blocks, cached_len, cu_num_draft, B, max_k, window, scale * 1.4426950408889634f,
                     status, static_cast<Split*>(workspace), reinterpret_cast<float*>(static_cast<char*>(workspace) + split_bytes(P)),
                     wait_limit_us < 0 ? kWaitNs : (uint32_t)wait_limit_us * 1000u};

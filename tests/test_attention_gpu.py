@@ -356,3 +356,59 @@ def test_wait_expiry_is_reported_and_the_context_stays_usable(cuda, cache_kind, 
     s.status.zero_()
     s.run().check()
     assert (s.status == 0).all()
+
+
+@pytest.mark.parametrize("cache_kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [16, 64])
+def test_pages_before_the_window_may_be_gone(cuda, cache_kind, page):
+    """Block-table entries of pages that lie wholly before every row's window are not read."""
+    import torch
+
+    s = Step(cuda, [3, 0], [1000, 517], 2, 4, 64, "bf16", cache_kind, page)
+    want = s.run(window=150).check(window=150).out.clone()
+    for b in range(2):
+        s.dtab[b, : (s.cached[b] - 150 + 1) // page] = -1
+    s.out.fill_(7.0)
+    s.run(window=150)
+    assert torch.equal(s.out, want) and (s.status == 0).all()
+
+
+def test_rows_behind_the_capacity_are_refused(cuda):
+    """Offsets that name more rows than q and out have: the request is reported and nothing of it is read or written."""
+    import torch
+
+    s = Step(cuda, [1, 2], [40, 70], 1, 2, 64)
+    s.q, s.out, s.lse = s.q[:4], s.out[:4], s.lse[:4]                 # request 1 would end at row 5
+    s.T, s.B = 4, 2
+    s.run()
+    torch.cuda.synchronize()
+    assert s.status.tolist() == [0, _native.ST_BAD_OFFSETS]
+    assert (s.out[2:] == 7).all() and (s.lse[2:] == 7).all() and not (s.out[:2] == 7).any()
+
+
+def test_a_scale_that_is_no_number_stays_in_the_rows_that_see_it(cuda):
+    """Exponent byte 255 on the last draft's key and value: NaN in the last row alone."""
+    import torch
+
+    s = Step(cuda, [4], [200], 2, 4, 64, "bf16", "e4m3", 16)
+    want = s.run().check().out.clone()
+    p, sl = s.tab[0, 204 // 16], 204 % 16
+    for e in (s.cache.v_exp, s.cache.k_exp):
+        keep = e[p, :, sl].clone()
+        e[p, :, sl] = 255
+        s.run()
+        torch.cuda.synchronize()
+        assert torch.equal(s.out[:4], want[:4]) and torch.isnan(s.out[4].float()).all()
+        e[p, :, sl] = keep
+
+
+def test_no_rows_and_no_requests(cuda):
+    """Empty calls launch nothing and leave everything as it was."""
+    import torch
+
+    s = Step(cuda, [0], [10], 1, 1, 32)
+    args = (s.cache, s.dtab, s.dcached, s.dcu)
+    _native.paged_attention(s.q, *args, 0, 0, s.out, s.ws)
+    _native.paged_attention(s.q[:0], *args, 1, 0, s.out[:0], s.ws)
+    torch.cuda.synchronize()
+    assert (s.out == 7).all()

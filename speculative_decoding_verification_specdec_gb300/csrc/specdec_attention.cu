@@ -199,8 +199,13 @@ template <typename T_, bool kFp8_, int N_, int DB_> struct Shape {
     static constexpr int kCol = N >= 64 ? N / 32 : 1, NC = N / kCol, kPar = N <= 32 ? 2 : 1, kGroups = kPar * kCol;
     static constexpr int kQ = N >= 96 && DB == 2 ? 1 : 2;                // Q buffers
     static constexpr int kSoftWarps = 4 * kGroups, kConvWarps = kFp8 ? 4 : 0;
-    static constexpr int kProducer = kSoftWarps + kConvWarps, kMma = kProducer + 2, kLoader = kProducer + 3;
-    static constexpr int kThreads = 32 * (kLoader + 1);
+    // With many columns, and over e4m3 from 32, the warp that issues the scores also fetches Q: one warp less leaves
+    // the softmax's threads registers that are worth more than Q fetched ahead (bf16, 96 columns, 64 requests of up to
+    // 32000 tokens: 739 against 795 us; e4m3, 32 columns, 128 requests of up to 8000: 314 against 349).
+    static constexpr bool kOneWarp = N >= 96 || (kFp8_ && N >= 32);
+    static constexpr int kProducer = kSoftWarps + kConvWarps, kScores = kProducer + 2, kValues = kProducer + 3,
+                         kLoader = kOneWarp ? kScores : kProducer + 4, kWarps = kProducer + (kOneWarp ? 4 : 5);
+    static constexpr int kThreads = 32 * kWarps;
     static constexpr int kAhead = kFp8 ? 4 : 2;                          // tiles that the copies look ahead
     // Tasks between the loader and the slowest role. The copies of a tile are issued once the tile kAhead further is
     // known, which may be as many tasks further, and the loader hands out a task only when the task kTasks before is
@@ -241,7 +246,7 @@ template <typename S> struct Misc {
     alignas(16) int64_t out_at[2][S::N];                 // and where it lies in out
     alignas(16) float qscale[2][S::kFp8 ? S::N : 4];
     alignas(16) int32_t pages[2][8][8];                  // of keys and of values: page ids of the tiles looked ahead to
-    alignas(16) uint8_t scales[2][S::kFp8 ? 16 : 1][kTile];              // and exponents of their e4m3 tokens
+    alignas(16) uint8_t scales[2][S::kFp8 ? 16 : 1][kTile];              // and exponents of their e4m3 keys and values
 };
 
 // ---------------------------------------------------------------- the kernel
@@ -260,7 +265,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
     unsigned char* const pbuf = qbuf + S::kQ * S::kQBytes;
     Misc<S>& ms = *reinterpret_cast<Misc<S>*>(pbuf + S::kPar * S::kPBytes);
     static_assert(sizeof(Misc<S>) <= S::kMiscBytes, "misc");
-    static_assert(offsetof(Misc<S>, last) % 16 == 0 && offsetof(Misc<S>, qscale) % 16 == 0 && offsetof(Misc<S>, scales) % 16 == 0 &&
+    static_assert(offsetof(Misc<S>, last) % 16 == 0 && offsetof(Misc<S>, qscale) % 16 == 0 && offsetof(Misc<S>, scales) % 16 == 0 && offsetof(Misc<S>, pages) % 16 == 0 &&
                   offsetof(Misc<S>, fac) % 16 == 0 && sizeof(Misc<S>) % 16 == 0, "8- and 16-byte accesses");
     static_assert(S::kSlotBytes % 1024 == 0 && S::kQBytes % 1024 == 0 && S::kPBytes % 1024 == 0, "swizzled tiles");
 
@@ -293,12 +298,12 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             bar_init(bar(ms.task_full[i]), 1);
             bar_init(bar(ms.task_free[i]), S::kThreads / 32);
         }
-        bar_init(bar(ms.drained), 1);
+        bar_init(bar(ms.drained), 2);
         ms.expired = 0;
         for (int i = 0; i < 8; ++i) ms.poison[i >> 2][i & 3] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == S::kMma) tmem_alloc(smem_u32(&ms.tmem), S::kTmemColumns);
+    if (warp == S::kScores) tmem_alloc(smem_u32(&ms.tmem), S::kTmemColumns);
     after_predecessor();
     {
         // every thread sums the units of consecutive requests, a scan over the threads places them
@@ -353,191 +358,9 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
     Task w;
     if (tid == 0) a.split[blockIdx.x].last = -1;         // this thread may fill it in below
 
-    if (warp == S::kProducer || warp == S::kProducer + 1) {
-        // ================================================================ keys (one warp) and values (the other) into the ring
-        // (a page of 16 slots takes a copy of 2 KB; at about 90 cycles a copy one warp would hold up both streams)
-        const bool is_v = warp != S::kProducer;
-        const int ps = c.page_size, bits = __ffs(ps) - 1, row_bits = min(bits, 7), rows = 1 << row_bits, pages = kTile >> row_bits;
-        const CUtensorMap* const map = is_v ? &vmap : &kmap;
-        const uint32_t slots = is_v ? S::kVSlots : S::kKSlots;
-        // A tile on its way. Its page ids are on their way to shared memory while the two tiles before it are issued, an
-        // e4m3 tile's scales (which need the ids) too, so its ids four tiles: a read that had to land in a register
-        // would hold up each turn of the loop. Tasks follow one another without a break.
-        struct Ahead {
-            int first, used, h, slot0, b;                // its pages first .. used - 1 (used 0: no more tiles), head, ...
-        };
-        constexpr int kAhead = S::kAhead;
-        uint32_t q = 0, n = 0, issued = 0;               // tasks so far, tiles, those whose copies were issued
-        int t = 0, t_end = 0, len = 0;
-        bool more = true;
-        Ahead x[kAhead + 1];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) x[i] = {0, 0, 0, 0, 0};
-#pragma unroll 1
-        for (int k = 0;; ++k) {                          // looks at tile k, issues tile k - kAhead
-            async_copy_wait_but_one();                   // what was under way two turns ago has landed
-            __syncwarp();
-            Ahead& ahead = x[kAhead];
-            ahead = {0, 0, 0, 0, 0};
-            if (t == t_end && more) {
-                more = take(q++, w);
-                t = w.t0;
-                t_end = w.t1;
-                len = w.cached + w.rows / a.group;
-            }
-            if (more) {
-                const int32_t token0 = t * kTile;
-                ahead.used = min(pages, (len - token0 + rows - 1) >> row_bits);
-                ahead.first = a.window > 0 ? max(w.cached - a.window + 1 - token0, 0) >> row_bits : 0;   // (no row sees those before)
-                ahead.h = w.h;
-                ahead.b = w.b;
-                ahead.slot0 = token0 & (ps - 1) & ~(rows - 1);
-                if (lane < 8) {
-                    int32_t* const to = &ms.pages[is_v][k & 7][lane];
-                    if (lane >= ahead.first && lane < ahead.used)
-                        async_copy_4(smem_u32(to), a.block_table + w.b * a.block_stride + ((token0 + (lane << row_bits)) >> bits));
-                    else
-                        *to = -1;
-                }
-                ++t;
-            }
-            if constexpr (S::kFp8) {
-                const Ahead& y = x[2];                   // tile k - 2: 16 of its scales a lane (1 where there is no page)
-                if (y.used > 0 && lane < 8) {
-                    const int pg = ms.pages[is_v][(k - 2) & 7][(lane << 4) >> row_bits];
-                    uint8_t* const to = &ms.scales[is_v][(k - 2) & 15][lane * 16];
-                    if (pg >= 0 && pg < c.num_pages)
-                        async_copy_16(smem_u32(to), (is_v ? c.v_exp : c.k_exp) + ((((int64_t)pg * H + y.h) << bits) + y.slot0 + ((lane << 4) & (rows - 1))), 16);
-                    else
-                        *reinterpret_cast<uint4*>(to) = make_uint4(0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f);
-                }
-            }
-            async_copy_commit();
-            if (k >= kAhead) {
-                const Ahead& x0 = x[0];
-                if (x0.used == 0) break;
-                const int page = lane < 8 ? ms.pages[is_v][n & 7][lane] : -1;
-                const bool bad = lane >= x0.first && lane < x0.used && (page < 0 || page >= c.num_pages);
-                if (bad && a.status) atomicOr(a.status + x0.b, SPECDEC_ST_BAD_PAGE);
-                const int from = bad ? c.num_pages : page;       // past the end: the copy reads zeros
-                const uint32_t s = is_v ? v_slot(n) : k_slot(n);
-                if (n >= slots) wait(ms.empty[s], n / slots - 1);
-                if (!__any_sync(0xffffffffu, *expired)) {
-                    issued = n + 1;
-                    const uint32_t fb = bar(ms.full[s]), dst = smem_u32(ring) + s * S::kSlotBytes;
-                    __syncwarp();
-                    if (elected()) bar_expect(fb, (x0.used - x0.first) * rows * DP * (S::kFp8 ? 1 : 2));
-#pragma unroll 1
-                    for (int p = x0.first; p < x0.used; ++p) {
-                        const int pg = __shfl_sync(0xffffffffu, from, p);
-                        if (elected()) {
-                            if constexpr (S::kFp8) {
-                                tma_load_4d(dst + p * rows * DP, map, fb, 0, x0.slot0, x0.h, pg);
-                            } else {
-#pragma unroll
-                                for (int d = 0; d < S::DB; ++d)
-                                    tma_load_4d(dst + d * (kTile * 128) + p * rows * 128, map, fb, d * 64, x0.slot0, x0.h, pg);
-                            }
-                        }
-                        __syncwarp();
-                    }
-                }
-                ++n;
-            }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) x[i] = x[i + 1];
-        }
-        async_copy_wait();
-        // nothing may still be on its way into shared memory when the CTA leaves
-        __syncwarp();
-        if (*expired && lane == 0) {
-            const unsigned long long t0 = time_ns();
-#pragma unroll 1
-            for (uint32_t i = issued > slots ? issued - slots : 0; i < issued; ++i)
-                while (!bar_test(bar(ms.full[is_v ? v_slot(i) : k_slot(i)]), (i / slots) & 1u) && time_ns() - t0 < kDrainNs) {}
-        }
-    } else if (warp == S::kMma) {
-        // ================================================================ products
-        {
-            constexpr int kBf16 = std::is_same<M, __nv_bfloat16>::value;
-            constexpr uint32_t ds = product(S::kFp8 ? 0 : kBf16, 0, 128, N), dv = product(kBf16, 1, 128, N);
-            const uint32_t ring0 = smem_u32(ring), p0 = smem_u32(pbuf), q0 = smem_u32(qbuf), v0 = smem_u32(v16);
-            // The scores of tile n + 1, then the values' product of tile n (the CTA's numbering; t, t1: the later tile's
-            // in its task). With one Q buffer the scores of a new task come after the product.
-            uint32_t q = 0;                              // the later tile's task
-            int t = 0, since = 0;                        // since: tiles of the earlier one's task before it
-            uint32_t q_was = 0;
-            bool more = take(0, w);
-            t = w.t0;
-#pragma unroll 1
-            for (int64_t n = -1;; ++n) {
-                const bool late = S::kQ == 1 && n >= 0 && t == w.t0;
-                const uint32_t i = (uint32_t)(n + 1);
-#pragma unroll 1
-                for (int step = 0; step < 2; ++step) {
-                    if ((step == 0) != late) {
-                        if (!more) continue;
-                        const uint32_t qb = q % S::kQ, slot = k_slot(i);
-                        bool ok = true;
-                        if (t == w.t0) ok = wait(ms.q_full[qb], q / S::kQ);
-                        ok = wait(ms.full[slot], i / S::kKSlots) && ok;
-                        if (__all_sync(0xffffffffu, ok) && elected()) {
-                            tmem_after();
-                            const uint32_t d = t_s + (i & 1) * N;
-                            if constexpr (S::kFp8) {
-                                // 16 elements to 16 bytes of a row; the pieces of Q one after the other into the same sums
-                                const uint64_t qo = operand(q0 + qb * S::kQBytes, 128, DP * 8, kNoSwizzle);
-                                const uint64_t ko = operand(ring0 + slot * S::kSlotBytes, 0, DP * 8, DP == 128 ? kSwizzle128 : kSwizzle64);
-#pragma unroll
-                                for (int p = 0; p < S::kPieces; ++p)
-#pragma unroll
-                                    for (int k = 0; k < DP / 32; ++k)
-                                        mma_ss_e4m3(d, ko + k * (32 >> 4), qo + p * (N * DP >> 4) + k * (256 >> 4), ds, p > 0 || k > 0);
-                            } else {
-                                const uint64_t qo = operand(q0 + qb * S::kQBytes, 128, DP * 16, kNoSwizzle);
-                                const uint64_t ko = operand(ring0 + slot * S::kSlotBytes, 0, 1024, kSwizzle128);
-#pragma unroll
-                                for (int k = 0; k < DP / 16; ++k)
-                                    mma_ss(d, ko + (k / 4) * (kTile * 128 >> 4) + (k % 4) * (32 >> 4), qo + k * (256 >> 4), ds, k > 0);
-                            }
-                            mma_commit(bar(ms.s_full[i & 1]));
-                            mma_commit(bar(ms.empty[slot]));
-                            if (t + 1 == w.t1) mma_commit(bar(ms.q_empty[qb]));
-                        }
-                        __syncwarp();
-                    } else {
-                        if (n < 0) continue;
-                        const uint32_t j = (uint32_t)n, slot = v_slot(j), acc = t_o + j % S::kPar * N, pb = p0 + j % S::kPar * S::kPBytes;
-                        bool ok = wait(ms.p_full[j & 1], j >> 1);
-                        if constexpr (S::kFp8) ok = wait(ms.v16_full[j & 1], j >> 1) && ok;
-                        else ok = wait(ms.full[slot], j / S::kVSlots) && ok;
-                        if (since == 0 && q_was > 0) ok = wait(ms.done[(q_was - 1) & 1], (q_was - 1) >> 1) && ok;
-                        if (__all_sync(0xffffffffu, ok) && elected()) {
-                            tmem_after();
-                            const uint32_t va = S::kFp8 ? v0 + (j & 1) * S::kV16Bytes : ring0 + slot * S::kSlotBytes;
-                            // one block of 64 elements (DB = 1): the rows 64 .. 127 read the block again and are not used
-                            constexpr uint32_t lead = S::DB == 2 ? kTile * 128 : 0;
-                            const uint64_t vo = operand(va, lead, 1024, kSwizzle128), po = operand(pb, 128, 2048, kNoSwizzle);
-#pragma unroll
-                            for (int k = 0; k < kTile / 16; ++k) mma_ss(acc, vo + k * (2048 >> 4), po + k * (256 >> 4), dv, since >= S::kPar || k > 0);
-                            mma_commit(bar(ms.pv_done[j & 1]));
-                            if constexpr (!S::kFp8) mma_commit(bar(ms.empty[slot]));
-                        }
-                        __syncwarp();
-                    }
-                }
-                if (!more) break;
-                since = t - w.t0;
-                q_was = q;
-                if (++t == w.t1) {
-                    more = take(++q, w);
-                    t = w.t0;
-                }
-            }
-        }
-        __syncwarp();
-    } else if (warp == S::kLoader) {
-        // ================================================================ the tasks, a few ahead; Q, its scales and its columns' places
+    // ================================================================ the tasks, a few ahead; Q, its scales and its columns' places
+    // (of the loader's warp, or the scores'; then(q) once Q is there)
+    [[maybe_unused]] auto load_items = [&](auto then) {
         Walker<N> walk(a, ms.begin, ms.end, ms.first_b, ms.base);
         uint32_t sent = 0;
         bool more = true;
@@ -663,7 +486,187 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             fence_async();
             __syncwarp();
             if (lane == 0) bar_arrive(bar(ms.q_full[qb]));
+            then(q);
         }
+    };
+
+    if (warp == S::kProducer || warp == S::kProducer + 1) {
+        // ================================================================ keys (one warp) and values (the other) into the ring
+        // (a page of 16 slots takes a copy of 2 KB; at about 90 cycles a copy one warp would hold up both streams)
+        const bool is_v = warp != S::kProducer;
+        const int ps = c.page_size, bits = __ffs(ps) - 1, row_bits = min(bits, 7), rows = 1 << row_bits, pages = kTile >> row_bits;
+        const CUtensorMap* const map = is_v ? &vmap : &kmap;
+        const uint32_t slots = is_v ? S::kVSlots : S::kKSlots;
+        // A tile on its way. Its page ids are on their way to shared memory while the two tiles before it are issued, an
+        // e4m3 tile's scales (which need the ids) too, so its ids four tiles: a read that had to land in a register
+        // would hold up each turn of the loop. Tasks follow one another without a break.
+        struct Ahead {
+            int first, used, h, slot0, b;                // its pages first .. used - 1 (used 0: no more tiles), head, ...
+        };
+        constexpr int kAhead = S::kAhead;
+        uint32_t q = 0, n = 0, issued = 0;               // tasks so far, tiles, those whose copies were issued
+        int t = 0, t_end = 0, len = 0;
+        bool more = true;
+        Ahead x[kAhead + 1];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) x[i] = {0, 0, 0, 0, 0};
+#pragma unroll 1
+        for (int k = 0;; ++k) {                          // looks at tile k, issues tile k - kAhead
+            async_copy_wait_but_one();                   // what was under way two turns ago has landed
+            __syncwarp();
+            Ahead& ahead = x[kAhead];
+            ahead = {0, 0, 0, 0, 0};
+            if (t == t_end && more) {
+                more = take(q++, w);
+                t = w.t0;
+                t_end = w.t1;
+                len = w.cached + w.rows / a.group;
+            }
+            if (more) {
+                const int32_t token0 = t * kTile;
+                ahead.used = min(pages, (len - token0 + rows - 1) >> row_bits);
+                ahead.first = a.window > 0 ? max(w.cached - a.window + 1 - token0, 0) >> row_bits : 0;   // (no row sees those before)
+                ahead.h = w.h;
+                ahead.b = w.b;
+                ahead.slot0 = token0 & (ps - 1) & ~(rows - 1);
+                if (lane < 8) {
+                    int32_t* const to = &ms.pages[is_v][k & 7][lane];
+                    if (lane >= ahead.first && lane < ahead.used)
+                        async_copy_4(smem_u32(to), a.block_table + w.b * a.block_stride + ((token0 + (lane << row_bits)) >> bits));
+                    else
+                        *to = -1;
+                }
+                ++t;
+            }
+            if constexpr (S::kFp8) {
+                const Ahead& y = x[2];                   // tile k - 2: 16 of its scales a lane (1 where there is no page)
+                if (y.used > 0 && lane < 8) {
+                    const int pg = ms.pages[is_v][(k - 2) & 7][(lane << 4) >> row_bits];
+                    uint8_t* const to = &ms.scales[is_v][(k - 2) & 15][lane * 16];
+                    if (pg >= 0 && pg < c.num_pages)
+                        async_copy_16(smem_u32(to), (is_v ? c.v_exp : c.k_exp) + ((((int64_t)pg * H + y.h) << bits) + y.slot0 + ((lane << 4) & (rows - 1))), 16);
+                    else
+                        *reinterpret_cast<uint4*>(to) = make_uint4(0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f);
+                }
+            }
+            async_copy_commit();
+            if (k >= kAhead) {
+                const Ahead& x0 = x[0];
+                if (x0.used == 0) break;
+                const int page = lane < 8 ? ms.pages[is_v][n & 7][lane] : -1;
+                const bool bad = lane >= x0.first && lane < x0.used && (page < 0 || page >= c.num_pages);
+                if (bad && a.status) atomicOr(a.status + x0.b, SPECDEC_ST_BAD_PAGE);
+                const int from = bad ? c.num_pages : page;       // past the end: the copy reads zeros
+                const uint32_t s = is_v ? v_slot(n) : k_slot(n);
+                if (n >= slots) wait(ms.empty[s], n / slots - 1);
+                if (!__any_sync(0xffffffffu, *expired)) {
+                    issued = n + 1;
+                    const uint32_t fb = bar(ms.full[s]), dst = smem_u32(ring) + s * S::kSlotBytes;
+                    __syncwarp();
+                    if (elected()) bar_expect(fb, (x0.used - x0.first) * rows * DP * (S::kFp8 ? 1 : 2));
+#pragma unroll 1
+                    for (int p = x0.first; p < x0.used; ++p) {
+                        const int pg = __shfl_sync(0xffffffffu, from, p);
+                        if (elected()) {
+                            if constexpr (S::kFp8) {
+                                tma_load_4d(dst + p * rows * DP, map, fb, 0, x0.slot0, x0.h, pg);
+                            } else {
+#pragma unroll
+                                for (int d = 0; d < S::DB; ++d)
+                                    tma_load_4d(dst + d * (kTile * 128) + p * rows * 128, map, fb, d * 64, x0.slot0, x0.h, pg);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+                ++n;
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) x[i] = x[i + 1];
+        }
+        async_copy_wait();
+        // nothing may still be on its way into shared memory when the CTA leaves
+        __syncwarp();
+        if (*expired && lane == 0) {
+            const unsigned long long t0 = time_ns();
+#pragma unroll 1
+            for (uint32_t i = issued > slots ? issued - slots : 0; i < issued; ++i)
+                while (!bar_test(bar(ms.full[is_v ? v_slot(i) : k_slot(i)]), (i / slots) & 1u) && time_ns() - t0 < kDrainNs) {}
+        }
+    } else if (warp == S::kScores) {
+        // ================================================================ S^T = K Q^T
+        // (the two products are issued by a warp each: what a warp does between its products, some hundred instructions
+        // that wait for one another, is longer than the products of few columns)
+        constexpr uint32_t ds = product(std::is_same<M, __nv_bfloat16>::value, 0, 128, N);
+        const uint32_t ring0 = smem_u32(ring), q0 = smem_u32(qbuf);
+        uint32_t n = 0;                                  // tiles of the CTA
+        auto item = [&](uint32_t q, bool have_q) {
+            const uint32_t qb = q % S::kQ;
+            const uint64_t qo = operand(q0 + qb * S::kQBytes, 128, DP * (S::kFp8 ? 8 : 16), kNoSwizzle);
+#pragma unroll 1
+            for (int t = w.t0; t < w.t1; ++t, ++n) {
+                const uint32_t slot = k_slot(n);
+                bool ok = wait(ms.full[slot], n / S::kKSlots) && have_q;
+                if (n >= 2) ok = wait(ms.p_full[n & 1], (n >> 1) - 1) && ok;             // the scores of tile n - 2 are read
+                if (__all_sync(0xffffffffu, ok) && elected()) {
+                    tmem_after();
+                    const uint32_t d = t_s + (n & 1) * N;
+                    if constexpr (S::kFp8) {
+                        // 16 elements to 16 bytes of a row; the pieces of Q one after the other into the same sums
+                        const uint64_t ko = operand(ring0 + slot * S::kSlotBytes, 0, DP * 8, DP == 128 ? kSwizzle128 : kSwizzle64);
+#pragma unroll
+                        for (int p = 0; p < S::kPieces; ++p)
+#pragma unroll
+                            for (int k = 0; k < DP / 32; ++k)
+                                mma_ss_e4m3(d, ko + k * (32 >> 4), qo + p * (N * DP >> 4) + k * (256 >> 4), ds, p > 0 || k > 0);
+                    } else {
+                        const uint64_t ko = operand(ring0 + slot * S::kSlotBytes, 0, 1024, kSwizzle128);
+#pragma unroll
+                        for (int k = 0; k < DP / 16; ++k)
+                            mma_ss(d, ko + (k / 4) * (kTile * 128 >> 4) + (k % 4) * (32 >> 4), qo + k * (256 >> 4), ds, k > 0);
+                    }
+                    mma_commit(bar(ms.s_full[n & 1]));
+                    mma_commit(bar(ms.empty[slot]));
+                    if (t + 1 == w.t1) mma_commit(bar(ms.q_empty[qb]));
+                }
+                __syncwarp();
+            }
+        };
+        if constexpr (S::kOneWarp) {
+            load_items([&](uint32_t q) { item(q, true); });
+        } else {
+            for (uint32_t q = 0; take(q, w); ++q) item(q, wait(ms.q_full[q % S::kQ], q / S::kQ));
+        }
+    } else if (warp == S::kValues) {
+        // ================================================================ O^T += V^T P^T
+        constexpr uint32_t dv = product(std::is_same<M, __nv_bfloat16>::value, 1, 128, N);
+        const uint32_t ring0 = smem_u32(ring), p0 = smem_u32(pbuf), v0 = smem_u32(v16);
+        // one block of 64 elements (DB = 1): the rows 64 .. 127 read the block again and are not used
+        constexpr uint32_t lead = S::DB == 2 ? kTile * 128 : 0;
+        uint32_t n = 0;
+        for (uint32_t q = 0; take(q, w); ++q) {
+            const bool o_free = q == 0 || wait(ms.done[(q - 1) & 1], (q - 1) >> 1);
+#pragma unroll 1
+            for (int t = w.t0; t < w.t1; ++t, ++n) {
+                const uint32_t slot = v_slot(n);
+                bool ok = S::kFp8 ? wait(ms.v16_full[n & 1], n >> 1) : wait(ms.full[slot], n / S::kVSlots);
+                ok = wait(ms.p_full[n & 1], n >> 1) && ok && o_free;
+                if (__all_sync(0xffffffffu, ok) && elected()) {
+                    tmem_after();
+                    const uint32_t acc = t_o + n % S::kPar * N;
+                    const uint64_t vo = operand(S::kFp8 ? v0 + (n & 1) * S::kV16Bytes : ring0 + slot * S::kSlotBytes, lead, 1024, kSwizzle128);
+                    const uint64_t po = operand(p0 + n % S::kPar * S::kPBytes, 128, 2048, kNoSwizzle);
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_ss(acc, vo + k * (2048 >> 4), po + k * (256 >> 4), dv, t - w.t0 >= S::kPar || k > 0);
+                    mma_commit(bar(ms.pv_done[n & 1]));
+                    if constexpr (!S::kFp8) mma_commit(bar(ms.empty[slot]));
+                }
+                __syncwarp();
+            }
+        }
+    } else if (!S::kOneWarp && warp == S::kLoader) {
+        load_items([](uint32_t) {});
     } else if (S::kFp8 && warp >= S::kSoftWarps) {
         // ================================================================ e4m3 values -> f16 (exact), a token a thread
         const int row = tid & 127;
@@ -1116,13 +1119,15 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             base += n;
         }
     }
-    if (warp == S::kMma) {
-        if (*expired) {                                  // products issued so far end by themselves: wait for them
-            if (elected()) {
-                mma_commit(bar(ms.drained));
-                const unsigned long long t0 = time_ns();
-                while (!bar_test(bar(ms.drained), 0) && time_ns() - t0 < kDrainNs) {}
-            }
+    if (*expired && (warp == S::kScores || warp == S::kValues)) {
+        // products issued so far end by themselves: wait for them
+        if (elected()) mma_commit(bar(ms.drained));
+        __syncwarp();
+    }
+    if (warp == S::kScores) {
+        if (*expired) {
+            const unsigned long long t0 = time_ns();
+            while (!bar_test(bar(ms.drained), 0) && time_ns() - t0 < kDrainNs) {}
             __syncwarp();
         }
         tmem_free(tmem, S::kTmemColumns);

@@ -8,10 +8,17 @@ from ._native import (  # noqa: F401
     SPECDEC_F32,
     SPECDEC_KMAX,
     SpecdecError,
+    kv_read,
+    kv_write,
     launch_config,
     load,
+    paged_attention,
+    paged_attention_workspace_size,
+    rope,
+    rope_frequencies,
     specdec_verify,
     specdec_wait,
     status_string,
 )
+from .kvcache import PagedCache  # noqa: F401
 from .metrics import acceptance_rates, mean_acceptance_length  # noqa: F401

@@ -7,7 +7,10 @@
  * max |x| in (224, 448] 2^e. Scaling by a power of two is exact, so the only rounding is the one to
  * e4m3's three mantissa bits (relative error at most 2^-4), and the scale takes one byte.
  *
- * Both kernels only move data: bound by HBM.
+ * Both kernels only move data: bound by HBM. Measured on one GB300, calls through the binding: a prompt
+ * into a bf16 cache 40.7 us where the copy rate would take 32.2 (79 %); prefixes out of an e4m3 cache 124.2 us for
+ * 109.6 (88 %; 139 before four units a thread were in flight). A step's rows into an e4m3 cache take 4 us on
+ * the GPU and 14.7 through the binding: small calls are bound by the host.
  */
 #include "specdec_rows.cuh"
 

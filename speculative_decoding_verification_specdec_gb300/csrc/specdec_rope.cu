@@ -5,6 +5,11 @@
  * pair's frequency. All heads of a row share the angles, so a CTA takes whole rows: its threads first
  * put the rows' cosines and sines into shared memory (rot_dim / 2 pairs a row, one sincospif each),
  * then rotate the heads in 32-byte units. Bound by HBM: every element is read and written once.
+ *
+ * A thread has four units in flight and reads the first of them before the rows' places are known; few rows
+ * are spread over one wave of CTAs. Measured on one GB300, calls through the binding: a prompt whose floor at the
+ * copy rate is 29.8 us takes 41.1 (72 %, 4.9 TB/s). Those choices took 1280 query rows from 10.2 to
+ * 8.2 us; called without the binding they take 4 to 6, so the host bounds small calls.
  */
 #include <cmath>
 

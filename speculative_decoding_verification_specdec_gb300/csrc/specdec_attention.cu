@@ -227,6 +227,10 @@ template <typename T_, bool kFp8_, int N_, int DB_> struct Shape {
     static constexpr int kRoom = kSmemBytes - 1024 - kMiscBytes - kQ * kQBytes - kPar * kPBytes - 2 * kV16Bytes;
     static constexpr int kSlots = kRoom / kSlotBytes > 12 ? 12 : kRoom / kSlotBytes;
     static constexpr int kKSlots = kSlots / 2, kVSlots = kSlots - kKSlots;
+    // where things lie behind the 1024-byte boundary that the ring starts at (up to 1023 bytes behind the base)
+    static constexpr int kV16At = kSlots * kSlotBytes, kQAt = kV16At + 2 * kV16Bytes, kPAt = kQAt + kQ * kQBytes,
+                         kMiscAt = kPAt + kPar * kPBytes, kSmem = 1024 + kMiscAt + kMiscBytes;
+    static_assert(kSmem <= kSmemBytes, "shared memory");
     static constexpr int kTmem = (kPar + 2) * N;                         // O, two S
     static constexpr int kTmemColumns = kTmem <= 64 ? 64 : kTmem <= 128 ? 128 : kTmem <= 256 ? 256 : 512;
     static constexpr int kSlotFloats = N * (DP + 2);
@@ -268,10 +272,10 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
     constexpr int N = S::N, NC = S::NC, DP = S::DP;
     extern __shared__ unsigned char raw[];
     unsigned char* const ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    unsigned char* const v16 = ring + S::kSlots * S::kSlotBytes;
-    unsigned char* const qbuf = v16 + 2 * S::kV16Bytes;
-    unsigned char* const pbuf = qbuf + S::kQ * S::kQBytes;
-    Misc<S>& ms = *reinterpret_cast<Misc<S>*>(pbuf + S::kPar * S::kPBytes);
+    unsigned char* const v16 = ring + S::kV16At;
+    unsigned char* const qbuf = ring + S::kQAt;
+    unsigned char* const pbuf = ring + S::kPAt;
+    Misc<S>& ms = *reinterpret_cast<Misc<S>*>(ring + S::kMiscAt);
     static_assert(sizeof(Misc<S>) <= S::kMiscBytes, "misc");
     static_assert(offsetof(Misc<S>, last) % 16 == 0 && offsetof(Misc<S>, qscale) % 16 == 0 && offsetof(Misc<S>, scales) % 16 == 0 &&
                   offsetof(Misc<S>, pages) % 16 == 0 && offsetof(Misc<S>, fac) % 16 == 0, "8- and 16-byte accesses");
@@ -1258,8 +1262,8 @@ template <typename S> specdec_status_t launch(const Args& a, cudaStream_t stream
     CUtensorMap kmap, vmap;
     if (!encoder()) return SPECDEC_ERR_CUDA;
     if (!tile_map(&kmap, a.cache, a.cache.k) || !tile_map(&vmap, a.cache, a.cache.v)) return SPECDEC_ERR_INVALID_ARG;
-    constexpr int smem = 1024 + S::kSlots * S::kSlotBytes + 2 * S::kV16Bytes + S::kQ * S::kQBytes + S::kPBytes + S::kMiscBytes;
-    static_assert(smem <= kSmemBytes, "shared memory");
+    constexpr int smem = S::kSmem;
+    static_assert(1023 + S::kMiscAt + (int)sizeof(Misc<S>) <= smem, "shared memory, wherever its base lies");
     auto kernel = specdec_paged_attention_kernel<S>;
     // the kernel's shared memory is allowed at its first launch (and again where a context has been reset since)
     static std::atomic<uint64_t> allowed{0};             // devices, by bit

@@ -352,7 +352,8 @@ typedef enum { SPECDEC_ROPE_PLAIN = 0, SPECDEC_ROPE_LINEAR = 1, SPECDEC_ROPE_BY_
  * PLAIN and LINEAR give amplitude 1. amplitude may be NULL. factor is ignored by PLAIN;
  * original_len, beta_fast and beta_slow matter to BY_PARTS alone.
  * Errors: INVALID_ARG for rot_dim odd, < 2 or > 256, freq NULL, theta < 1 or not finite, factor
- * not in (0, inf), an unknown scaling, original_len < 1 or beta_fast <= beta_slow where they matter.
+ * not in (0, inf) or so small that a frequency is infinite, an unknown scaling, original_len < 1 or
+ * beta_fast <= beta_slow where they matter.
  */
 specdec_status_t specdec_rope_frequencies(int32_t rot_dim, double theta, specdec_rope_scaling_t scaling,
                                           double factor, int64_t original_len, double beta_fast,

@@ -156,6 +156,7 @@ extern "C" specdec_status_t specdec_rope_frequencies(int32_t rot_dim, double the
             w = w < 0.0 ? 0.0 : w > 1.0 ? 1.0 : w;
             f *= w + (1.0 - w) / factor;
         }
+        if (!std::isfinite(f)) return SPECDEC_ERR_INVALID_ARG;     // (a factor whose reciprocal is none)
         const double turns = std::fmod(f / kTwoPi, 1.0);
         freq[i] = (uint64_t)std::ldexp(turns, 64);                 // turns < 1: fits; 53 bits, exact
     }

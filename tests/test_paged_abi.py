@@ -170,3 +170,11 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(lib):
             call()
     with pytest.raises(E.SpecdecError):
         _native.rope_frequencies(32, scaling="by parts")
+
+
+@pytest.mark.parametrize("scaling", ["linear", "by_parts"])
+def test_frequencies_that_are_no_number_are_refused(scaling):
+    # a factor whose reciprocal is beyond the largest double: infinite frequencies
+    with pytest.raises(_native.SpecdecError):
+        _native.rope_frequencies(32, scaling=scaling, factor=5e-324, original_len=1)
+    _native.rope_frequencies(32, scaling=scaling, factor=1e-300, original_len=1)

@@ -89,6 +89,13 @@ struct Request {
     __device__ __forceinline__ int64_t units(int heads) const { return tiles ? (int64_t)heads * blocks * (tiles + kItem) : 0; }
 };
 
+// Tokens that a request may have: its row of block_table, and what keeps token numbers and their tiles within 32 bits.
+__host__ __device__ __forceinline__ int64_t most_tokens(int32_t max_blocks, int32_t page_size)
+{
+    const int64_t held = (int64_t)max_blocks * page_size, most = (int64_t)INT32_MAX - kTile;
+    return held < most ? held : most;
+}
+
 template <int N> __device__ __noinline__ Request request_of(const Args& a, int b)
 {
     Request r = {0, 0, 0, 0, 0, 0, 0};
@@ -101,7 +108,7 @@ template <int N> __device__ __noinline__ Request request_of(const Args& a, int b
     r.cached = __ldg(a.cached + b);
     if (k > a.max_k) {
         r.fault = SPECDEC_ST_K_TOO_LARGE;
-    } else if (r.cached < 0 || r.cached + k + 1 > min((int64_t)a.max_blocks * a.cache.page_size, (int64_t)INT32_MAX - kTile)) {
+    } else if (r.cached < 0 || r.cached + k + 1 > most_tokens(a.max_blocks, a.cache.page_size)) {
         r.fault = SPECDEC_ST_BAD_LENGTH;
     } else {
         r.rows = (k + 1) * a.group;
@@ -801,7 +808,8 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                                 bool seen = true;
                                 if constexpr (kMasked) {
                                     const int32_t lt = (e & 1) ? last.y : last.x;
-                                    seen = 8 * i <= lt && (a.window == 0 || 8 * i > lt - a.window);
+                                    // (a difference that wraps, under a window next to 2^31, has lt < 0 and so no say)
+                                    seen = 8 * i <= lt && (a.window == 0 || 8 * i > (int32_t)((uint32_t)lt - (uint32_t)a.window));
                                 }
                                 f(x[hf][r][e], scale, seen, 2 * r + (e & 1));
                             }
@@ -1219,6 +1227,14 @@ int row_tile(int32_t max_k, int32_t group)
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 96 ? 96 : 128;
 }
 
+// A window that no request can be longer than hides nothing: it is none (0). One that is left is below most_tokens, and
+// a tile's first token lies at most SPECDEC_KMAX behind `cached`, so that cached - window + 1 - token0, the copies' smallest
+// difference, is at least -32 - (2^31 - 130) + 1 and does not wrap.
+int32_t window_of(int32_t window, int32_t max_blocks, int32_t page_size)
+{
+    return window >= most_tokens(max_blocks, page_size) ? 0 : window;
+}
+
 size_t split_bytes(int P) { return ((size_t)P * sizeof(Split) + 255) / 256 * 256; }
 
 using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -1339,7 +1355,8 @@ extern "C" specdec_status_t specdec_paged_attention(
         return SPECDEC_ERR_INVALID_ARG;
     const int P = sm_count(), group = num_heads / cache->num_kv_heads;
     const Args a = {q, out, lse, rows, num_heads, group, q_row_stride, q_head_stride, out_row_stride, out_head_stride, *cache,
-                    block_table, block_stride, max_blocks, cached_len, cu_num_draft, B, max_k, window, scale * 1.4426950408889634f,
+                    block_table, block_stride, max_blocks, cached_len, cu_num_draft, B, max_k,
+                    window_of(window, max_blocks, cache->page_size), scale * 1.4426950408889634f,
                     status, static_cast<Split*>(workspace), reinterpret_cast<float*>(static_cast<char*>(workspace) + split_bytes(P)),
                     wait_limit_us < 0 ? kWaitNs : (uint32_t)wait_limit_us * 1000u};
     const int N = row_tile(max_k, group);

@@ -412,3 +412,39 @@ def test_no_rows_and_no_requests(cuda):
     _native.paged_attention(s.q[:0], *args, 1, 0, s.out[:0], s.ws)
     torch.cuda.synchronize()
     assert (s.out == 7).all()
+
+
+@pytest.mark.parametrize("cache_kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("k,group", [(3, 4), (32, 1)])
+def test_windows_that_hide_nothing(cuda, cache_kind, k, group):
+    """A window as long as the longest request, as its row of the table, and up to the largest number equals no window,
+    bit for bit; lengths whose last tile begins behind `cached`."""
+    import torch
+
+    # 50 pages of 16 a request: more than the 701 + k tokens of the longest
+    s = Step(cuda, [k, k, k, 0], [125, 127, 700, 0], 2, group, 64, "bf16", cache_kind, 16, width=50)
+    want = s.run().check().out.clone(), s.lse.clone()
+    capacity = s.dtab.shape[1] * s.page
+    for window in (700 + k + 1, capacity - 1, capacity, capacity + 1, 2 ** 31 - 200, 2 ** 31 - 130, 2 ** 31 - 129, 2 ** 31 - 2, 2 ** 31 - 1):
+        s.out.fill_(7.0)
+        s.lse.fill_(7.0)
+        s.run(window=window)
+        assert torch.equal(s.out, want[0]) and torch.equal(s.lse, want[1]), window
+    assert (s.status == 0).all()
+
+
+def test_a_wide_table_and_a_window_next_to_the_largest(cuda):
+    """Rows of block_table that could hold 2^31 tokens, of which only the first pages are there: windows just under what 32-bit differences bear, in a tile that begins behind `cached`."""
+    import torch
+
+    s = Step(cuda, [3, 32], [125, 1000], 1, 2, 64, "bf16", "bf16", 256)
+    want = s.run().check().out.clone()
+    wide = torch.full((2, 2 ** 23), -1, dtype=torch.int32, device=cuda)         # 2^31 tokens a request
+    wide[:, : s.dtab.shape[1]] = s.dtab
+    s.dtab = wide
+    for window in (2 ** 31 - 131, 2 ** 31 - 130, 2 ** 31 - 129, 2 ** 31 - 1):
+        s.out.fill_(7.0)
+        s.run(window=window)
+        assert torch.equal(s.out, want), window
+    s.run(window=60).check(window=60)
+    assert (s.status == 0).all()

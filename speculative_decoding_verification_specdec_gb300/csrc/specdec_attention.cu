@@ -310,7 +310,10 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             bar_init(bar(ms.p_full[i]), 4 * S::kCol);
             bar_init(bar(ms.done[i]), S::kSoftWarps);
             bar_init(bar(ms.q_full[i]), 1);
-            bar_init(bar(ms.q_empty[i]), 1);
+            // given back by the scores' last product; a single buffer also by the softmax's warps, once they have seen it
+            // full: else the loader could fill it twice before a late one looks, whose phase then never comes. (Of two
+            // buffers the next filling waits for the item to be done.)
+            bar_init(bar(ms.q_empty[i]), S::kQ == 1 ? 1 + S::kSoftWarps : 1);
             bar_init(bar(ms.v16_full[i]), 4);
         }
         for (int i = 0; i < S::kTasks; ++i) {
@@ -736,6 +739,10 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             if (barrier_or(7, 128 * S::kGroups, !take(q, w))) break;
             const uint32_t tb = q & 1;
             wait(ms.q_full[q % S::kQ], q / S::kQ);
+            if constexpr (S::kQ == 1) {
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(ms.q_empty[0]));
+            }
             const int row_first = w.block * N, row_last = min(row_first + N, w.rows) - 1;
             const int32_t seen_all = w.cached + row_first / a.group, seen_any = w.cached + row_last / a.group;
             const int32_t from_all = a.window > 0 ? seen_any - a.window + 1 : 0, from_any = a.window > 0 ? seen_all - a.window + 1 : 0;

@@ -448,3 +448,21 @@ def test_a_wide_table_and_a_window_next_to_the_largest(cuda):
         assert torch.equal(s.out, want), window
     s.run(window=60).check(window=60)
     assert (s.status == 0).all()
+
+
+@pytest.mark.parametrize("kind,cache_kind", TYPES)
+@pytest.mark.parametrize("k,group,dim", [(8, 8, 128), (8, 8, 80), (7, 16, 128), (32, 16, 128)])
+def test_short_items_with_one_buffer_for_q(cuda, kind, cache_kind, k, group, dim):
+    """Items of one or two tiles at 72 and 128 rows a key head (and several row blocks) of heads over 64: their scores wait
+    for nothing but Q, which there has a single buffer that is filled again as soon as all its readers have passed."""
+    import torch
+
+    rng = np.random.default_rng([k, group, dim])
+    B, cached = 90, rng.integers(0, 200, size=90)
+    cached[:3] = 0, 127, 128
+    s = Step(cuda, [k] * B, cached, 3, group, dim, kind, cache_kind, 16)
+    want = s.run().check().out.clone()
+    for _ in range(20):
+        s.run()
+    torch.cuda.synchronize()
+    assert (s.status == 0).all() and torch.equal(s.out, want)

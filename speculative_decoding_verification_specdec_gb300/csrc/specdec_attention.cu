@@ -259,7 +259,7 @@ template <typename S> struct Misc {
     alignas(16) float red[S::kPar][4][S::N];             // a column's value in each warp of its group
     alignas(16) float fac[S::kPar][S::N];
     float ref[S::kPar][S::N];
-    int red_e[4 * S::kGroups], ref_e[S::kPar];
+    int red_e[4 * S::kGroups], ref_e[S::kGroups];        // (the values' exponent is a group's own, as its votes are)
     alignas(16) int32_t last[2][S::N];                   // last token that a column sees (-1: no column)
     alignas(16) int2 place[2][S::N];                     // a column's row of q and out, and its query head (row -1: no column)
     alignas(16) int64_t out_at[2][S::N];                 // and where it lies in out
@@ -1043,7 +1043,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                     if (wq == 0) ms.ref[par][col] = m[i];
                 }
             }
-            if (S::kFp8 && cg == 0 && gt == 0) ms.ref_e[par] = E;
+            if (S::kFp8 && gt == 0) ms.ref_e[grp] = E;
             const bool whole = w.begin && w.end;
             float* const part = a.parts + (int64_t)(2 * blockIdx.x + (w.begin ? 1 : 0)) * S::kSlotFloats;
             barrier_sync(7, 128 * S::kGroups);
@@ -1061,7 +1061,10 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
 #pragma unroll
                 for (int p = 0; p < S::kPar; ++p) {
                     float y = f[p];
-                    if (S::kFp8 && ms.ref_e[p] >= -126) y *= __uint_as_float((uint32_t)(127 + ms.ref_e[p]) << 23);
+                    if constexpr (S::kFp8) {
+                        const int e = ms.ref_e[p * S::kCol + tid / NC];
+                        if (e >= -126) y *= __uint_as_float((uint32_t)(127 + e) << 23);
+                    }
                     ms.fac[p][tid] = !any ? 0.f : whole ? y * __frcp_rn(sum) : y;
                 }
                 if (whole) {

@@ -466,3 +466,32 @@ def test_short_items_with_one_buffer_for_q(cuda, kind, cache_kind, k, group, dim
         s.run()
     torch.cuda.synchronize()
     assert (s.status == 0).all() and torch.equal(s.out, want)
+
+
+@pytest.mark.parametrize("kind,dim", [("bf16", 128), ("f16", 64)])
+@pytest.mark.parametrize("k,group,block", [(3, 16, 0), (3, 16, 1), (8, 8, 1), (8, 8, 2), (7, 16, 0), (7, 16, 3)])
+@pytest.mark.parametrize("B,heads,cached", [(160, 1, 500), (1, 8, 9000)])
+def test_value_scales_that_rise_where_some_columns_scores_do(cuda, kind, dim, k, group, block, B, heads, cached):
+    """64, 96 and 128 rows a key head over an e4m3 cache, whose columns are dealt with 32 at a time: in every second tile the
+    values' scales are 2 to 2^4 times those of the tile before, and the scores of one block of 32 columns alone are
+    higher by 12 in log2, so that this block moves its reference and the others do not. Many items a CTA, and items cut
+    among the CTAs with some tiles each."""
+    import torch
+
+    s = Step(cuda, [k] * B, [cached] * B, heads, group, dim, kind, "e4m3", 16)
+    rng = np.random.default_rng([k, group, block, B])
+    n = cached + k + 1
+    odd = (np.arange(n) // 128) % 2 == 1
+    lift = 12.0 * np.log(2.0) * dim ** 0.5 / 32.0            # times the block's 32 in Q, and scale: 12 in log2
+    keys = torch.from_numpy(rng.standard_normal((n, heads, dim)).astype(np.float32))
+    keys[..., 0] = torch.from_numpy(np.where(odd, lift, 0.0).astype(np.float32))[:, None]
+    s.cache.k_exp.fill_(127)
+    s.cache.v_exp.fill_(118)
+    for b in range(B):
+        page = torch.from_numpy(s.tab[b, np.arange(n) // s.page].astype(np.int64)).to(cuda)
+        slot = torch.arange(n, device=cuda) % s.page
+        s.cache.k.view(torch.uint8)[page, :, slot] = keys.to(torch.float8_e4m3fn).view(torch.uint8).to(cuda)
+        s.cache.v_exp[page, :, slot] = dev(np.where(odd, 118 + rng.integers(1, 5), 118).astype(np.uint8), cuda)[:, None].expand(-1, heads)
+    rows = (torch.arange((k + 1) * group) // 32 == block).view(1, k + 1, 1, group)
+    s.q[: s.T, :, 0] = torch.where(rows, 32.0, 0.0).expand(B, -1, heads, -1).reshape(s.T, -1).to(s.q.dtype).to(cuda)
+    s.run().check()

@@ -158,7 +158,7 @@ extern "C" specdec_status_t specdec_rope_frequencies(int32_t rot_dim, double the
         }
         if (!std::isfinite(f)) return SPECDEC_ERR_INVALID_ARG;     // (a factor whose reciprocal is none)
         const double turns = std::fmod(f / kTwoPi, 1.0);
-        freq[i] = (uint64_t)std::ldexp(turns, 64);                 // turns < 1: fits; 53 bits, exact
+        freq[i] = (uint64_t)std::ldexp(turns, 64);                 // turns < 1: fits; what is under 2^-64 turn is dropped
     }
     if (amplitude)
         *amplitude = scaling == SPECDEC_ROPE_BY_PARTS && factor > 1.0 ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;

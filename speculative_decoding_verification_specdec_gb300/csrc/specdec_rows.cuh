@@ -100,15 +100,15 @@ __device__ __forceinline__ int owner_of(int32_t B, int64_t t, Start start)
 }
 
 // cos and sin of position * freq (units of 2^-64 turn): the product wraps modulo one turn, the
-// nearest quarter is taken off in integers, and the rest, at most an eighth of a turn, goes to fp32
-// with a relative error of 2^-24.
+// nearest quarter is taken off in integers, and all of the rest, at most an eighth of a turn, goes to fp32
+// once, with a relative error of 2^-24 however small it is.
 __device__ __forceinline__ float2 turn(int64_t position, uint64_t freq, float amplitude)
 {
     const uint64_t phase = (uint64_t)position * freq;
     const uint32_t quarter = (uint32_t)((phase + (1ull << 61)) >> 62);
-    const int32_t rest = (int32_t)((int64_t)(phase - ((uint64_t)quarter << 62)) >> 30);   // units of 2^-34 turn
+    const int64_t rest = (int64_t)(phase - ((uint64_t)quarter << 62));
     float s, c;
-    sincospif((float)rest * 0x1p-33f, &s, &c);
+    sincospif(__ll2float_rn(rest) * 0x1p-63f, &s, &c);
     const float cq = (quarter & 1u) ? s : c, sq = (quarter & 1u) ? c : s;
     return make_float2(((quarter + 1u) & 2u) ? -cq * amplitude : cq * amplitude,
                        (quarter & 2u) ? -sq * amplitude : sq * amplitude);

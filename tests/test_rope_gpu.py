@@ -176,3 +176,26 @@ def test_another_stream_and_capture(cuda):
     g.replay()
     torch.cuda.synchronize()
     check(P.host(out), P.host(x), np.arange(6), ref.frequencies(32)[0], "f32", False, 1.0)
+
+
+@pytest.mark.parametrize("kw", [dict(theta=1e6), dict(theta=1e7), dict(theta=1e7, scaling="linear", factor=1e5)])
+@pytest.mark.parametrize("rot", [128, 256])
+def test_small_angles_keep_their_sine(cuda, kw, rot):
+    """Pairs (1, 0) become (c, s). The angle's rest goes to fp32 once (2^-24 of itself), the sine is off by a unit in the last
+    place (2^-23), its products and sum by 2^-24 each, all relative to the sine, which so keeps its digits however slow
+    the pair, up to the table's own 2^-64 turn a position. Angles under an eighth of a turn."""
+    import torch
+
+    pos = np.array([1, 2, 3, 100, 12345, -1, -77], dtype=np.int32)
+    x = torch.zeros((len(pos), 1, rot), device=cuda)
+    x[..., : rot // 2] = 1.0
+    table, amp = _native.rope_frequencies(rot, **kw)
+    out = torch.empty_like(x)
+    _native.rope(x, out, table.to(cuda), rot, positions=torch.from_numpy(pos).to(cuda), amplitude=amp)
+    f, _ = ref.frequencies(rot, **kw)
+    angle = pos[:, None] * f[None, :]
+    small = np.abs(angle) < np.pi / 4
+    assert small.sum() > len(pos) * rot // 8 and np.abs(angle[small]).min() < 2e-6
+    off = np.abs(P.host(out)[:, 0, rot // 2:] / np.sin(angle) - 1)
+    tol = 5 * 2.0 ** -24 + np.broadcast_to(2.0 ** -64 * 2 * np.pi / f, angle.shape)
+    assert np.all((off <= tol)[small]), (off / tol)[small].max()

@@ -137,7 +137,8 @@ __global__ void __launch_bounds__(kThreads, 6) specdec_kv_write_kernel(const Wri
         }
         ahead.move(step, 2 * H, 1);
     };
-    fetch(group < total);
+    const int there = rows_there(a.cu, a.B, row0, n) * 2 * H;
+    fetch(group < there);
 
     if (a.status)
         for (int64_t b = (int64_t)blockIdx.x * kThreads + tid; b < a.B; b += (int64_t)gridDim.x * kThreads) {
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 6) specdec_kv_write_kernel(const Wri
     // (whole warps go round together: the reduction needs their lanes)
     for (int round = 0; round < total; round += kGroups, at.move(step, 2 * H, 1)) {
         const bool in = round + group < total;
-        if (round > 0) fetch(in);
+        if (round > 0) fetch(round + group < there);
         const int r = in ? at.r : 0, is_v = at.h >= H, h = at.h - is_v * H;
         const bool live = in && slots[r].live == 1;
         float x[kUnits][2 * V];

@@ -33,8 +33,8 @@ struct RopeArgs {
     int32_t B;
 };
 
-// The first batch is read before the rows' positions are known: their chain of reads and the angles
-// then cost nothing on top of it.
+// The first batch is read before the rows' positions are known (only that the requests have so many rows): their
+// chain of reads and the angles then cost nothing on top of it.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads, 3) specdec_rope_kernel(const RopeArgs a)
 {
@@ -46,13 +46,14 @@ __global__ void __launch_bounds__(kThreads, 3) specdec_rope_kernel(const RopeArg
     const int64_t row0 = (int64_t)blockIdx.x * a.rows_per_cta;
     const int n = (int)min((int64_t)a.rows_per_cta, a.rows - row0);
     const int row_units = a.heads * a.units, total = n * row_units;
+    const int there = a.positions ? total : rows_there(a.cu, a.B, row0, n) * row_units;
     Raw<T, V> v[kBatch][2];
     const Place step(kThreads, a.heads, a.units);
     Place ahead(tid, a.heads, a.units), at = ahead;                // of the next unit to read, to write
     auto fetch = [&](int base) {
 #pragma unroll
         for (int q = 0; q < kBatch; ++q, ahead.move(step, a.heads, a.units)) {
-            if (base + q * kThreads >= total) continue;
+            if (base + q * kThreads >= there) continue;
             int first, second;
             unit_runs<V>(ahead.u, a.rope.rot_dim, a.rope.interleaved, &first, &second);
             const T* x = static_cast<const T*>(a.x) + (row0 + ahead.r) * a.x_row + ahead.h * a.x_head;

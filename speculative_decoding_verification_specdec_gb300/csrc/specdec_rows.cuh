@@ -85,6 +85,12 @@ __device__ __forceinline__ bool offsets_ok(const int32_t* cu, int32_t B, int b)
     return __ldg(cu) == 0 && a0 >= 0 && a1 >= a0 && a1 <= __ldg(cu + B);
 }
 
+// Of n rows from row0 on, how many the requests have (as far as the offsets' total says): those behind are not read.
+__device__ __forceinline__ int rows_there(const int32_t* cu, int32_t B, int64_t row0, int n)
+{
+    return (int)max((int64_t)0, min((int64_t)n, (int64_t)__ldg(cu + B) + B - row0));
+}
+
 // The request that owns row t, by counting the requests that start at or before it (every thread
 // of the CTA calls it; one round of independent loads per 256 requests, where a search would
 // wait out a chain of them). The caller checks that the request really holds the row.

@@ -262,3 +262,14 @@ def test_long_cache_offsets_pass_32_bits(cuda):
     ex = ref.e4m3_exponent(xs)[..., None].astype(np.float64)
     assert np.array_equal(P.host(out), ref.E4M3[ref.e4m3_code(xs * 2.0 ** -ex)] * 2.0 ** ex)
     assert (k.view(torch.uint8)[0] == 0).all()
+
+
+@pytest.mark.parametrize("inputs", ["odd", "packed"])
+@pytest.mark.parametrize("cache_kind", ["bf16", "e4m3"])
+def test_a_capacity_far_beyond_the_rows(cuda, cache_kind, inputs):
+    """Inputs of 9000 rows of which the requests have 12: CTAs that hold some of them, and none, leave the rest."""
+    rope = dict(freqs=_native.rope_frequencies(32)[0].to(cuda), rot_dim=32)
+    cache, k, v, tab, status, cu = write(cuda, [4, 0, 5], [7, 0, 100], 3, 48, "bf16", cache_kind, 16, rope=rope, extra_rows=8988, inputs=inputs)
+    pos = [[7, 0, 100][b] + j for b, j in ref.owners(cu, 3)]
+    check_written(cache, ref.rope(k, pos, ref.frequencies(32)[0]), v, tab, cu, [7, 0, 100], cache_kind, 16, slack=8 * 2.0 ** -24)
+    assert (status == 0).all()

@@ -199,3 +199,19 @@ def test_small_angles_keep_their_sine(cuda, kw, rot):
     off = np.abs(P.host(out)[:, 0, rot // 2:] / np.sin(angle) - 1)
     tol = 5 * 2.0 ** -24 + np.broadcast_to(2.0 ** -64 * 2 * np.pi / f, angle.shape)
     assert np.all((off <= tol)[small]), (off / tol)[small].max()
+
+
+@pytest.mark.parametrize("dim", [32, 34])
+def test_a_capacity_far_beyond_the_rows(cuda, dim):
+    """Buffers of 9000 rows of which the requests have 12: CTAs that hold some of them, and none, leave the rest."""
+    import torch
+
+    cu, cached = np.array([0, 4, 4, 9], dtype=np.int32), np.array([7, 0, 100], dtype=np.int32)
+    x = torch.full((9000, 3, dim), float("nan"), device=cuda)
+    x[:12] = torch.randn((12, 3, dim), generator=torch.Generator().manual_seed(dim)).to(cuda)
+    out = torch.full_like(x, 7.0)
+    table = _native.rope_frequencies(dim)[0].to(cuda)
+    _native.rope(x, out, table, dim, cu_num_draft=torch.from_numpy(cu).to(cuda), cached_len=torch.from_numpy(cached).to(cuda), B=3)
+    pos = np.array([cached[b] + j for b, j in ref.owners(cu, 3)])
+    check(P.host(out)[:12], P.host(x)[:12], pos, ref.frequencies(dim)[0], "f32", False, 1.0)
+    assert (out[12:] == 7).all()

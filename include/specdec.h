@@ -316,7 +316,9 @@ specdec_status_t specdec_bitmask_scatter(const int32_t* compact, int64_t compact
  * cached_len[b] + out_num_accepted[b] + 1; the cache entries of rejected drafts lie behind it and
  * are written over. A prompt is a request whose k_b + 1 rows are its tokens (the cache write and
  * the rotation take any k_b; the attention takes k_b <= max_k <= SPECDEC_KMAX). A request with
- * cached_len[b] < 0 is skipped. Rows at and behind cu[B] + B are neither read nor written.
+ * cached_len[b] < 0 is skipped (the attention fills its rows with zeros). Rows at and behind cu[B] + B are
+ * neither read nor written. A request whose offsets name a row at or behind the `rows` of a call is malformed
+ * (BAD_OFFSETS): nothing of it is written.
  *
  * status[b], where a call takes it (NULL: not reported), has bits OR-ed in and is never cleared,
  * so that one array can collect a step's calls. All pointers are device pointers on the current
@@ -440,7 +442,7 @@ specdec_status_t specdec_kv_write(const void* k, const void* v, specdec_dtype_t 
  *   first        [B] int32 or NULL (0).
  *   out_k, out_v [rows, num_kv_heads, head_dim], F32, BF16 or F16; either may be NULL.
  * status: BAD_LENGTH (first[b] < 0, or a token past max_blocks pages: none of its rows are written),
- * BAD_PAGE (zeros), BAD_OFFSETS. Errors as specdec_kv_write's.
+ * BAD_PAGE (zeros), BAD_OFFSETS (also for rows at or behind `rows`). Errors as specdec_kv_write's.
  */
 specdec_status_t specdec_kv_read(const specdec_kv_cache_t* cache, const int32_t* block_table,
                                  int32_t max_blocks, int64_t block_stride, const int32_t* first,
@@ -477,8 +479,7 @@ specdec_status_t specdec_kv_read(const specdec_kv_cache_t* cache, const int32_t*
  * Keys and values that a row does not see do not reach it, whatever they hold (infinities, NaN, pages
  * never written; with a window, block_table entries of pages that lie wholly before it are not read).
  * A row that sees no finite score gets zeros and lse = -inf.
- * status: K_TOO_LARGE, BAD_OFFSETS (also where cu names a row at or behind `rows`; rows unknown: not
- * written), BAD_LENGTH (both others: zeros, lse -inf in its rows; also 2^31 - 128 tokens or more),
+ * status: K_TOO_LARGE, BAD_OFFSETS (rows unknown: not written), BAD_LENGTH (both others: zeros, lse -inf in its rows; also 2^31 - 128 tokens or more),
  * BAD_PAGE (its tokens read as zeros), DEVICE_TIMEOUT.
  * Errors: INVALID_ARG for a NULL required pointer, a bad size or stride, num_heads not a multiple of
  * num_kv_heads, a workspace too small or misaligned; UNSUPPORTED for types, page_size or head_dim

@@ -100,7 +100,7 @@ template <int N> __device__ __noinline__ Request request_of(const Args& a, int b
 {
     Request r = {0, 0, 0, 0, 0, 0, 0};
     const int32_t c0 = __ldg(a.cu + b), k = __ldg(a.cu + b + 1) - c0;
-    if (!offsets_ok(a.cu, a.B, b) || (int64_t)c0 + b + k + 1 > a.rows) {
+    if (!rows_ok(a.cu, a.B, b, a.rows)) {
         r.fault = SPECDEC_ST_BAD_OFFSETS;
         return r;
     }

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 6) specdec_kv_write_kernel(const Wri
 
     if (a.status)
         for (int64_t b = (int64_t)blockIdx.x * kThreads + tid; b < a.B; b += (int64_t)gridDim.x * kThreads) {
-            if (!offsets_ok(a.cu, a.B, (int)b)) atomicOr(a.status + b, SPECDEC_ST_BAD_OFFSETS);
+            if (!rows_ok(a.cu, a.B, (int)b, a.rows)) atomicOr(a.status + b, SPECDEC_ST_BAD_OFFSETS);
             else if (a.cached[b] < 0 || !fits(c, a.table, (int64_t)a.cached[b] + a.cu[b + 1] - a.cu[b] + 1))
                 atomicOr(a.status + b, SPECDEC_ST_BAD_LENGTH);
         }
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 6) specdec_kv_write_kernel(const Wri
         b = max(b, 0);
         while (b < a.B && t > (int64_t)__ldg(a.cu + b + 1) + b) ++b;
         RowSlot r = no_slot();
-        if (b < a.B && offsets_ok(a.cu, a.B, b)) {
+        if (b < a.B && rows_ok(a.cu, a.B, b, a.rows)) {
             const int64_t j = t - __ldg(a.cu + b) - b, k = (int64_t)__ldg(a.cu + b + 1) - __ldg(a.cu + b);
             const int64_t cached = __ldg(a.cached + b);
             if (j >= 0 && cached >= 0 && fits(c, a.table, cached + k + 1)) {
@@ -280,7 +280,7 @@ struct ReadArgs {
 __device__ __forceinline__ uint32_t read_fault(const ReadArgs& a, int b)
 {
     const int64_t r0 = a.cu_len[b], r1 = a.cu_len[b + 1], end = a.cu_len[a.B];
-    if (a.cu_len[0] != 0 || r0 < 0 || r1 < r0 || r1 > end) return SPECDEC_ST_BAD_OFFSETS;
+    if (a.cu_len[0] != 0 || r0 < 0 || r1 < r0 || r1 > end || r1 > a.rows) return SPECDEC_ST_BAD_OFFSETS;
     const int32_t f = a.first ? a.first[b] : 0;
     if (f < 0 || (r1 > r0 && !fits(a.cache, a.table, f + (r1 - r0)))) return SPECDEC_ST_BAD_LENGTH;
     return 0;

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads, 3) specdec_rope_kernel(const RopeArg
             while (b < a.B && t > (int64_t)__ldg(a.cu + b + 1) + b) ++b;
             const int64_t j = b < a.B ? t - __ldg(a.cu + b) - b : -1;
             const int32_t c = b < a.B ? __ldg(a.cached + b) : -1;
-            live[tid] = j >= 0 && c >= 0 && offsets_ok(a.cu, a.B, b);
+            live[tid] = j >= 0 && c >= 0 && rows_ok(a.cu, a.B, b, a.rows);
             pos[tid] = (int64_t)c + j;
         }
     }

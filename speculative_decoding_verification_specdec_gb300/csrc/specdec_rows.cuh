@@ -85,6 +85,12 @@ __device__ __forceinline__ bool offsets_ok(const int32_t* cu, int32_t B, int b)
     return __ldg(cu) == 0 && a0 >= 0 && a1 >= a0 && a1 <= __ldg(cu + B);
 }
 
+// And whether there are as many rows as they name.
+__device__ __forceinline__ bool rows_ok(const int32_t* cu, int32_t B, int b, int64_t rows)
+{
+    return offsets_ok(cu, B, b) && (int64_t)__ldg(cu + b + 1) + b < rows;
+}
+
 // Of n rows from row0 on, how many the requests have (as far as the offsets' total says): those behind are not read.
 __device__ __forceinline__ int rows_there(const int32_t* cu, int32_t B, int64_t row0, int n)
 {

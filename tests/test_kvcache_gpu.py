@@ -273,3 +273,24 @@ def test_a_capacity_far_beyond_the_rows(cuda, cache_kind, inputs):
     pos = [[7, 0, 100][b] + j for b, j in ref.owners(cu, 3)]
     check_written(cache, ref.rope(k, pos, ref.frequencies(32)[0]), v, tab, cu, [7, 0, 100], cache_kind, 16, slack=8 * 2.0 ** -24)
     assert (status == 0).all()
+
+
+@pytest.mark.parametrize("cache_kind", ["bf16", "e4m3"])
+def test_rows_behind_the_capacity_are_refused(cuda, cache_kind):
+    """Offsets that name more rows than k and v, or the outputs, have: the request is reported and nothing of it is written."""
+    import torch
+
+    cache = kvcache.alloc(4, 2, 16, 32, P.torch_type(cache_kind), cuda)
+    tab = torch.tensor([[2, 0], [3, 1]], dtype=torch.int32, device=cuda)
+    x = torch.ones((4, 2, 32), dtype=torch.bfloat16, device=cuda)
+    status = torch.zeros(2, dtype=torch.int32, device=cuda)
+    _native.kv_write(x, x, cache, tab, torch.zeros(2, dtype=torch.int32, device=cuda), torch.tensor([0, 1, 3], dtype=torch.int32, device=cuda),
+                     2, status=status)                                # request 1 would end at row 5
+    assert status.tolist() == [0, _native.ST_BAD_OFFSETS]
+    gk, _ = P.held(cache)
+    assert (gk[2, :, :2] == 1).all() and (gk[3] == 0).all() and (gk[[0, 1]] == 0).all()
+    out = torch.full((5, 2, 32), 7.0, device=cuda)
+    status.zero_()
+    _native.kv_read(cache, tab, torch.tensor([0, 2, 6], dtype=torch.int64, device=cuda), 2, out, None, status=status)
+    assert status.tolist() == [0, _native.ST_BAD_OFFSETS]
+    assert (out[:2] == 1).all() and (out[2:] == 7).all()

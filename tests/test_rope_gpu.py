@@ -215,3 +215,13 @@ def test_a_capacity_far_beyond_the_rows(cuda, dim):
     pos = np.array([cached[b] + j for b, j in ref.owners(cu, 3)])
     check(P.host(out)[:12], P.host(x)[:12], pos, ref.frequencies(dim)[0], "f32", False, 1.0)
     assert (out[12:] == 7).all()
+
+
+def test_rows_behind_the_capacity_are_refused(cuda):
+    """Offsets that name more rows than x has: the request's rows are left as they were, as a malformed one's are."""
+    import torch
+
+    x, out = torch.ones((4, 1, 16), device=cuda), torch.full((4, 1, 16), 7.0, device=cuda)
+    _native.rope(x, out, _native.rope_frequencies(16)[0].to(cuda), 16, cu_num_draft=torch.tensor([0, 1, 3], dtype=torch.int32, device=cuda),
+                 cached_len=torch.tensor([0, 0], dtype=torch.int32, device=cuda), B=2)           # request 1 would end at row 5
+    assert (out[0] == 1).all() and not (out[1] == 7).any() and (out[2:] == 7).all()

@@ -334,10 +334,13 @@ def _status(status, B: int, device: int):
 
 
 def _heads(name: str, t):
-    """(shape, strides) of t, [rows, heads, head_dim] with the elements of a head contiguous."""
+    """(shape, strides) of t, [rows, heads, head_dim] with the elements of a head contiguous. A stride that is never taken
+    (one row, one head) counts as 0."""
     shape, stride = t.shape, t.stride()
     if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1):
         raise ValueError(f"{name} must be [rows, heads, head_dim] with the elements of a head contiguous")
+    if shape[0] == 1 or shape[1] == 1:
+        stride = (0 if shape[0] == 1 else stride[0], 0 if shape[1] == 1 else stride[1], 1)
     return shape, stride
 
 

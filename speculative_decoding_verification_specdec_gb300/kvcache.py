@@ -29,9 +29,11 @@ class PagedCache:
                  torch.float8_e4m3fn: _native.SPECDEC_E4M3, torch.uint8: _native.SPECDEC_E4M3}
         if self.k.dtype not in types or self.v.dtype != self.k.dtype:
             raise _native.SpecdecError(_native.SPECDEC_ERR_UNSUPPORTED, f"cache types {self.k.dtype}, {self.v.dtype}")
-        if self.k.dim() != 4 or self.k.shape != self.v.shape or self.k.stride() != self.v.stride():
+        # (a stride that is never taken counts as 0)
+        stride, v_stride = (tuple(s if n > 1 else 0 for n, s in zip(t.shape, t.stride())) for t in (self.k, self.v))
+        if self.k.dim() != 4 or self.k.shape != self.v.shape or stride != v_stride:
             raise ValueError("k and v must be [num_pages, num_kv_heads, page_size, head_dim] of the same strides")
-        if self.k.stride(3) != 1:
+        if stride[3] != 1:
             raise ValueError("the elements of a head must be contiguous")
         dtype = types[self.k.dtype]
         quantised = dtype == _native.SPECDEC_E4M3
@@ -45,7 +47,6 @@ class PagedCache:
                 raise ValueError("the cache's tensors must be on one device")
 
         n, heads, page, dim = self.k.shape
-        stride = self.k.stride()
         struct = _native.KVCacheStruct(*(None if t is None else t.data_ptr() for t in (self.k, self.v, self.k_exp, self.v_exp)),
                                        dtype, n, page, heads, dim, stride[0], stride[1], stride[2])
         # the description is made once: the fields are frozen (the tensors' contents are not)

@@ -495,3 +495,19 @@ def test_value_scales_that_rise_where_some_columns_scores_do(cuda, kind, dim, k,
     rows = (torch.arange((k + 1) * group) // 32 == block).view(1, k + 1, 1, group)
     s.q[: s.T, :, 0] = torch.where(rows, 32.0, 0.0).expand(B, -1, heads, -1).reshape(s.T, -1).to(s.q.dtype).to(cuda)
     s.run().check()
+
+
+def test_one_row_of_one_head_with_any_strides(cuda):
+    """A single row, head and request out of tensors whose row and head strides fit no alignment: they are never taken."""
+    import torch
+
+    s = Step(cuda, [0], [40], 1, 1, 32)
+    want = s.run().check().out[:1].clone()
+    k = torch.ones((1, 1, 32), dtype=torch.bfloat16, device=cuda)
+    q, out, v = (t.as_strided((1, 1, 32), (77, 33, 1)) for t in (s.q, torch.zeros_like(want), 2 * k))
+    _native.paged_attention(q, s.cache, s.dtab, s.dcached, s.dcu, 1, 0, out, s.ws)
+    assert torch.equal(out, want)
+    _native.kv_write(k, v, s.cache, s.dtab, s.dcached, s.dcu, 1)
+    back = torch.zeros((1, 1, 32), dtype=torch.bfloat16, device=cuda), torch.zeros(200, dtype=torch.bfloat16, device=cuda).as_strided((1, 1, 32), (5, 7, 1))
+    _native.kv_read(s.cache, s.dtab, torch.tensor([0, 1], dtype=torch.int64, device=cuda), 1, *back, first=s.dcached)
+    assert (back[0] == 1).all() and (back[1] == 2).all()

@@ -178,3 +178,36 @@ def test_frequencies_that_are_no_number_are_refused(scaling):
     with pytest.raises(_native.SpecdecError):
         _native.rope_frequencies(32, scaling=scaling, factor=5e-324, original_len=1)
     _native.rope_frequencies(32, scaling=scaling, factor=1e-300, original_len=1)
+
+
+def odd_strides(t, **at):
+    """t with the strides of the given dimensions, all of size one, set to numbers that nothing else has."""
+    s = list(t.stride())
+    for d, x in at.items():
+        assert t.shape[int(d[1:])] == 1
+        s[int(d[1:])] = x
+    return t.as_strided(t.shape, s)
+
+
+def test_strides_that_are_never_taken_do_not_matter(lib):
+    """Tensors of one row, one head, one page: the stride of a dimension of size one may be anything, in k and v alike. (On
+    host tensors, whose device is what is refused once their shapes and strides have been taken.)"""
+    import torch
+
+    i, tab = torch.zeros(5, dtype=torch.int32), torch.zeros((1, 1), dtype=torch.int32)
+    for rows, heads in ((1, 2), (3, 1), (1, 1)):
+        k = torch.zeros((rows, heads, 32), dtype=torch.bfloat16)
+        v = odd_strides(k, **({"d0": 777} if rows == 1 else {}), **({"d1": 333} if heads == 1 else {}))
+        c = kvcache.PagedCache(torch.zeros((4, heads, 16, 32), dtype=torch.bfloat16), torch.zeros((4, heads, 16, 32), dtype=torch.bfloat16))
+        assert k.stride() != v.stride()
+        with pytest.raises(ValueError, match="device"):
+            _native.kv_write(k, v, c, tab, i, i, 1)
+        with pytest.raises(ValueError, match="device"):
+            _native.kv_read(c, tab, i.long(), 1, k, v)
+        assert _native._heads("v", v)[1] == (0 if rows == 1 else heads * 32, 0 if heads == 1 else 32, 1)
+    k = torch.zeros((1, 1, 16, 32), dtype=torch.float8_e4m3fn)
+    e = torch.zeros((1, 1, 16), dtype=torch.uint8)
+    s = kvcache.PagedCache(k, odd_strides(k, d0=777, d1=333), e, e).struct()
+    assert (s.page_stride, s.head_stride, s.slot_stride) == (0, 0, 32)
+    with pytest.raises(ValueError):                                  # a stride that is taken has to agree
+        kvcache.PagedCache(torch.zeros((2, 1, 16, 32)).bfloat16(), torch.zeros((2, 2, 16, 32)).bfloat16()[:, :1])

@@ -463,8 +463,8 @@ specdec_status_t specdec_kv_read(const specdec_kv_cache_t* cache, const int32_t*
  *                head, by which partial results over other keys can be joined.
  *   max_k        every k_b must be <= max_k <= SPECDEC_KMAX; it chooses the kernel's row tile.
  *   scale        finite.  window >= 0.
- *   workspace    specdec_paged_attention_workspace_size(...) bytes, 16-byte aligned, no
- *                initialisation; it holds nothing between calls, and calls (or captured graphs) that
+ *   workspace    specdec_paged_attention_workspace_size(...) bytes (0 for sizes that the call refuses),
+ *                16-byte aligned, no initialisation; it holds nothing between calls, and calls (or captured graphs) that
  *                share one must not overlap in time.
  *   wait_limit_us -1: 2 s; 0..2000000: the limit of every wait inside the kernel, after which the
  *                requests concerned get SPECDEC_ST_DEVICE_TIMEOUT and undefined outputs; nothing

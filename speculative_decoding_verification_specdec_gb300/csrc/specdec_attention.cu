@@ -1233,7 +1233,7 @@ int sm_count()
 
 int row_tile(int32_t max_k, int32_t group)
 {
-    const int64_t rows = (int64_t)(max_k + 1) * group;
+    const int64_t rows = ((int64_t)max_k + 1) * group;
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 96 ? 96 : 128;
 }
 
@@ -1334,8 +1334,10 @@ template <typename T> specdec_status_t launch_type(const Args& a, int N, cudaStr
 extern "C" size_t specdec_paged_attention_workspace_size(int32_t B, int32_t max_k, int32_t num_heads,
                                                          int32_t num_kv_heads, int32_t head_dim)
 {
-    if (B <= 0 || max_k < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0) return 0;
-    const int P = sm_count(), group = (num_heads + num_kv_heads - 1) / num_kv_heads, DP = head_dim <= 64 ? 64 : 128;
+    if (B <= 0 || max_k < 0 || max_k > SPECDEC_KMAX || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
+        !cache_head_dim(head_dim))
+        return 0;
+    const int P = sm_count(), group = num_heads / num_kv_heads, DP = head_dim <= 64 ? 64 : 128;
     return split_bytes(P) + (size_t)2 * P * row_tile(max_k, group) * (DP + 2) * sizeof(float);
 }
 

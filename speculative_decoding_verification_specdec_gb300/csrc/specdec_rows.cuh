@@ -34,13 +34,15 @@ inline specdec_status_t check_rope(const specdec_rope_t* r, int32_t head_dim)
     return SPECDEC_OK;
 }
 
+inline bool cache_head_dim(int32_t d) { return d >= 16 && d <= 128 && d % 16 == 0; }
+
 inline specdec_status_t check_cache(const specdec_kv_cache_t* c)
 {
     if (!c) return SPECDEC_ERR_INVALID_ARG;
     if (c->dtype != SPECDEC_BF16 && c->dtype != SPECDEC_F16 && c->dtype != SPECDEC_E4M3) return SPECDEC_ERR_UNSUPPORTED;
     const int ps = c->page_size, es = (int)elem_bytes(c->dtype);
     if (ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256) return SPECDEC_ERR_UNSUPPORTED;
-    if (c->head_dim < 16 || c->head_dim > 128 || c->head_dim % 16 != 0) return SPECDEC_ERR_UNSUPPORTED;
+    if (!cache_head_dim(c->head_dim)) return SPECDEC_ERR_UNSUPPORTED;
     if (!c->k || !c->v || !aligned_to(c->k, 16) || !aligned_to(c->v, 16) || c->num_pages < 1 || c->num_kv_heads < 1)
         return SPECDEC_ERR_INVALID_ARG;
     const int64_t st[3] = {c->page_stride, c->head_stride, c->slot_stride};

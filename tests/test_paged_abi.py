@@ -211,3 +211,10 @@ def test_strides_that_are_never_taken_do_not_matter(lib):
     assert (s.page_stride, s.head_stride, s.slot_stride) == (0, 0, 32)
     with pytest.raises(ValueError):                                  # a stride that is taken has to agree
         kvcache.PagedCache(torch.zeros((2, 1, 16, 32)).bfloat16(), torch.zeros((2, 2, 16, 32)).bfloat16()[:, :1])
+
+
+def test_workspace_size_of_what_the_call_refuses_is_0(lib):
+    size = _native.paged_attention_workspace_size
+    assert size(4, 32, 8, 2, 128) > 0
+    for bad in ((4, 33, 8, 2, 64), (4, 2 ** 31 - 1, 8, 2, 64), (4, 3, 7, 2, 64), (4, 3, 8, 3, 64), (4, 3, 8, 2, 8), (4, 3, 8, 2, 72), (4, 3, 8, 2, 144)):
+        assert size(*bad) == 0, bad

@@ -294,6 +294,13 @@ def _lazy_torch():
     return _torch
 
 
+def _int32(name: str, x) -> int:
+    """x as it is; ctypes would take a number beyond 32 bits modulo 2^32."""
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{name} = {x} is beyond 32 bits")
+    return x
+
+
 def _stream(stream, device: int) -> int:
     if stream is None:
         return _torch._C._cuda_getCurrentRawStream(device)
@@ -373,6 +380,9 @@ def rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: Optional[str
     torch = _lazy_torch()
     if scaling not in ROPE_SCALINGS:
         raise SpecdecError(SPECDEC_ERR_INVALID_ARG, f"rope scaling {scaling!r}")
+    _int32("rot_dim", rot_dim)
+    if not -2 ** 63 <= original_len < 2 ** 63:
+        raise ValueError(f"original_len = {original_len} is beyond 64 bits")
     table = torch.zeros(max(int(rot_dim) // 2, 1), dtype=torch.int64)
     amplitude = ctypes.c_float()
     rc = load().specdec_rope_frequencies(int(rot_dim), float(theta), ROPE_SCALINGS[scaling], float(factor), int(original_len),
@@ -456,7 +466,8 @@ def kv_read(cache, block_table, cu_len, B: int, out_k, out_v, first=None, status
 
 
 def paged_attention_workspace_size(B: int, max_k: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
-    return int(load().specdec_paged_attention_workspace_size(int(B), int(max_k), int(num_heads), int(num_kv_heads), int(head_dim)))
+    sizes = dict(B=B, max_k=max_k, num_heads=num_heads, num_kv_heads=num_kv_heads, head_dim=head_dim)
+    return int(load().specdec_paged_attention_workspace_size(*(int(_int32(name, x)) for name, x in sizes.items())))
 
 
 def paged_attention(q, cache, block_table, cached_len, cu_num_draft, B: int, max_k: int, out, workspace,
@@ -474,6 +485,10 @@ def paged_attention(q, cache, block_table, cached_len, cu_num_draft, B: int, max
         raise ValueError(f"lse must be a contiguous float32 tensor of shape {tuple(shape[:2])}")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
+    _int32("max_k", max_k)
+    _int32("window", window)
+    if wait_limit_us is not None:
+        _int32("wait_limit_us", wait_limit_us)
     current = torch._C._cuda_getDevice() if device >= 0 else -2
     i32 = torch.int32
     table, max_blocks, block_stride = _table(block_table, B, current)

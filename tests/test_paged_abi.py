@@ -218,3 +218,27 @@ def test_workspace_size_of_what_the_call_refuses_is_0(lib):
     assert size(4, 32, 8, 2, 128) > 0
     for bad in ((4, 33, 8, 2, 64), (4, 2 ** 31 - 1, 8, 2, 64), (4, 3, 7, 2, 64), (4, 3, 8, 3, 64), (4, 3, 8, 2, 8), (4, 3, 8, 2, 72), (4, 3, 8, 2, 144)):
         assert size(*bad) == 0, bad
+
+
+def host_step():
+    import torch
+
+    x, i = torch.zeros((4, 2, 32), dtype=torch.bfloat16), torch.zeros(5, dtype=torch.int32)
+    c = kvcache.PagedCache(*(torch.zeros((4, 2, 16, 32), dtype=torch.bfloat16) for _ in range(2)))
+    return x, c, torch.zeros((4, 1), dtype=torch.int32), i
+
+
+def test_numbers_beyond_32_bits_are_refused(lib):
+    """Not taken modulo 2^32 (a window of 2^32 + 5 would be one of 5)."""
+    x, c, tab, i = host_step()
+    for name, value in (("window", 2 ** 32), ("window", 2 ** 32 + 5), ("window", 2 ** 31), ("max_k", 2 ** 32 + 3), ("wait_limit_us", 2 ** 32 + 1)):
+        kw = dict(max_k=3)
+        kw[name] = value
+        with pytest.raises((ValueError, E.SpecdecError), match=name):
+            _native.paged_attention(x, c, tab, i, i, 4, out=x, workspace=x, **kw)
+    for args in ((2 ** 32 + 4, 3, 8, 2, 64), (4, 2 ** 32 + 3, 8, 2, 64), (4, 3, 2 ** 32 + 8, 2, 64)):
+        with pytest.raises(ValueError):
+            _native.paged_attention_workspace_size(*args)
+    for kw in (dict(rot_dim=2 ** 32 + 64), dict(rot_dim=64, scaling="by_parts", factor=8.0, original_len=2 ** 64 + 4096)):
+        with pytest.raises(ValueError):
+            _native.rope_frequencies(**kw)

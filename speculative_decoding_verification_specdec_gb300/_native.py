@@ -335,7 +335,7 @@ def _ints(name: str, t, dtype, rows: int, device: int):
 def _status(status, B: int, device: int):
     if status is None:
         return None
-    if status.element_size() != 4 or status.dim() != 1 or status.shape[0] < B or not status.is_contiguous():
+    if status.dtype not in (_torch.int32, _torch.uint32) or status.dim() != 1 or status.shape[0] < B or not status.is_contiguous():
         raise ValueError("status must be a contiguous 32-bit integer tensor of B elements")
     return _at("status", status, device)
 

@@ -242,3 +242,18 @@ def test_numbers_beyond_32_bits_are_refused(lib):
     for kw in (dict(rot_dim=2 ** 32 + 64), dict(rot_dim=64, scaling="by_parts", factor=8.0, original_len=2 ** 64 + 4096)):
         with pytest.raises(ValueError):
             _native.rope_frequencies(**kw)
+
+
+def test_status_must_hold_whole_numbers(lib):
+    """Status bits OR-ed into a tensor of another 32-bit type would read as something else."""
+    import torch
+
+    x, c, tab, i = host_step()
+    for calls in (lambda st: _native.kv_write(x, x, c, tab, i, i, 4, status=st), lambda st: _native.kv_read(c, tab, i.long(), 4, x, x, status=st),
+                  lambda st: _native.paged_attention(x, c, tab, i, i, 4, 0, x, x, status=st)):
+        with pytest.raises(ValueError):
+            calls(torch.zeros(4))
+    with pytest.raises(ValueError, match="status must"):
+        _native._status(torch.zeros(4), 4, -1)
+    for fine in (torch.int32, torch.uint32):
+        assert _native._status(torch.zeros(4, dtype=fine), 4, -1)

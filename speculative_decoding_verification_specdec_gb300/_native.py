@@ -397,7 +397,7 @@ def _rope_struct(device: int, freqs, rot_dim: int, interleaved: bool = False, am
 
 
 def rope(x, out, freqs, rot_dim: int, interleaved: bool = False, amplitude: float = 1.0, inverse: bool = False,
-         positions=None, cu_num_draft=None, cached_len=None, B: int = 0, stream=None) -> None:
+         positions=None, cu_num_draft=None, cached_len=None, B: Optional[int] = None, stream=None) -> None:
     """Queue specdec_rope: x rotated into out (which may be x), both [rows, heads, head_dim] with any row and
     head strides. Positions are given for every row, or follow from cu_num_draft, cached_len and B."""
     torch = _lazy_torch()
@@ -405,8 +405,10 @@ def rope(x, out, freqs, rot_dim: int, interleaved: bool = False, amplitude: floa
     shape, xs = _heads("x", x)
     os_ = _like("out", out, shape, x.dtype)
     i32 = torch.int32
-    if positions is None and (cu_num_draft is None or cached_len is None):
-        raise ValueError("rope needs positions, or cu_num_draft and cached_len")
+    if positions is None and (cu_num_draft is None or cached_len is None or B is None):
+        raise ValueError("rope needs positions, or cu_num_draft, cached_len and B")
+    if B is None:
+        B = 0
     current = torch._C._cuda_getDevice() if device >= 0 else -2
     r = _rope_struct(current, freqs, rot_dim, interleaved, amplitude)
     rc = load().specdec_rope(_at("x", x, current), _at("out", out, current), _dtype_of(x), shape[0], shape[1], shape[2], xs[0], xs[1],

@@ -257,3 +257,13 @@ def test_status_must_hold_whole_numbers(lib):
         _native._status(torch.zeros(4), 4, -1)
     for fine in (torch.int32, torch.uint32):
         assert _native._status(torch.zeros(4, dtype=fine), 4, -1)
+
+
+def test_rope_over_ragged_rows_names_their_number(lib):
+    """Without B, cu_num_draft and cached_len described no request, and the call did nothing."""
+    x, _, _, i = host_step()
+    table, _ = _native.rope_frequencies(32)
+    with pytest.raises(ValueError, match="and B"):
+        _native.rope(x, x, table, 32, cu_num_draft=i, cached_len=i)
+    with pytest.raises(ValueError, match="current device"):          # (a host tensor; the arguments themselves are complete)
+        _native.rope(x, x, table, 32, cu_num_draft=i, cached_len=i, B=0)

@@ -472,8 +472,9 @@ specdec_status_t specdec_kv_read(const specdec_kv_cache_t* cache, const int32_t*
  * Equal calls give equal bits; where the batch's work is cut among the SMs (which depends on all of its
  * lengths) a request's result may differ in its last bits. Scores, maxima, sums and the output are
  * accumulated in fp32. The weights exp(s - m) are rounded to the cache's 16-bit type before their product
- * with V; over an E4M3 cache to F16, times their token's scale relative to the largest scale so far, so
- * a weight whose product falls 2^24 below that is lost. There Q is taken as a sum of two (BF16) or three
+ * with V; over an E4M3 cache to F16, times their token's scale relative to the largest scale so far of tokens
+ * that all rows of a block see (a head of zeros has 2^0), so a weight whose product falls 2^24 below that is
+ * lost; values that only some of those rows see, of a scale 2^100 above it or more, may come out infinite. There Q is taken as a sum of two (BF16) or three
  * (F16) e4m3 numbers an element, exact but for elements under 2^-9 (BF16) or 2^-6 (F16) of the row's
  * largest, which are off by at most 2^-17 of it; an infinity in Q counts as NaN there.
  * Keys and values that a row does not see do not reach it, whatever they hold (infinities, NaN, pages

@@ -47,6 +47,8 @@ namespace {
 using namespace specdec;
 
 constexpr int kTile = 128;                               // tokens
+constexpr int kNone = -100000, kUnset = 100000;          // no exponent: below, above every other
+constexpr int kPartly = 4096;                            // added to the exponent of a token that some rows do not see
 constexpr int kItem = 3;                                 // what starting and ending an item costs, in tiles
 constexpr float kLazy = 8.f;                             // how far (log2) a score may pass the reference
 constexpr uint32_t kWaitNs = 2000000000u;                // a wait's default limit
@@ -259,7 +261,14 @@ template <typename S> struct Misc {
     alignas(16) float red[S::kPar][4][S::N];             // a column's value in each warp of its group
     alignas(16) float fac[S::kPar][S::N];
     float ref[S::kPar][S::N];
-    int red_e[4 * S::kGroups], ref_e[S::kGroups];        // (the values' exponent is a group's own, as its votes are)
+    int red_e[2][4 * S::kGroups], ref_e[S::kPar];
+    // E, the exponent that a group takes the values' scales by, and that which a token's must pass to raise it. E follows from
+    // the scales alone, so that the groups of a tile agree on it, and from tokens that every row sees: one that some rows
+    // do not see would cost these rows' weights their bits if its scale were far above theirs, so above E + 4 it is
+    // added by hand (heavy). Until a tile holds a token that every row sees, E is the smallest scale so far and
+    // lift_over below all. (Here and not in registers, where they cost spills: 314 us where 321 for 128 requests of up to
+    // 8000 tokens, 24 rows a key head.)
+    int scale_e[S::kGroups], lift_over[S::kGroups];
     alignas(16) int32_t last[2][S::N];                   // last token that a column sees (-1: no column)
     alignas(16) int2 place[2][S::N];                     // a column's row of q and out, and its query head (row -1: no column)
     alignas(16) int64_t out_at[2][S::N];                 // and where it lies in out
@@ -322,6 +331,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         }
         bar_init(bar(ms.drained), 2);
         ms.expired = 0;
+        for (int i = 0; i < S::kGroups; ++i) ms.scale_e[i] = kUnset, ms.lift_over[i] = kNone;
         for (int i = 0; i < 8; ++i) ms.poison[i >> 2][i & 3] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -749,7 +759,6 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
             float m[NC / 4], l[NC / 4];
 #pragma unroll
             for (int i = 0; i < NC / 4; ++i) m[i] = -FLT_MAX, l[i] = 0.f;
-            int E = -100000;                                             // e4m3: exponent that the values' scales are taken by
             // One tile; kMasked: it holds a token that some row does not see.
             auto tile = [&](auto masked, const int t) {
                 constexpr bool kMasked = decltype(masked)::value;
@@ -771,7 +780,10 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                         kscale[i] = exp_value(ms.scales[0][n & 15][tok]) * a.scale_log2;
                         ve[i] = (int)ms.scales[1][n & 15][tok] - 127;
                         // a token that no row sees may hold anything
-                        if (kMasked && (token0 + tok > seen_any || token0 + tok < from_any)) ve[i] = -100000;
+                        if constexpr (kMasked) {
+                            if (token0 + tok > seen_any || token0 + tok < from_any) ve[i] = kNone;
+                            else if (token0 + tok > seen_all || token0 + tok < from_all) ve[i] += kPartly;
+                        }
                     }
                     __syncwarp();
                     if (lane == 0) {                                     // the scales are read: the slots may go
@@ -779,6 +791,10 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                         bar_arrive(bar(ms.empty[vs]));
                     }
                 }
+                // the exponent by which token i may raise E; that which it has; whether one is heavy
+                [[maybe_unused]] auto lift = [&](int i) { return ve[i] >= 128 ? kNone : ve[i]; };
+                [[maybe_unused]] auto own = [&](int i) { return kMasked && ve[i] > kPartly - 200 ? ve[i] - kPartly : ve[i]; };
+                [[maybe_unused]] auto heavy = [&](int e) { return kMasked && e > ms.scale_e[grp] + 4 && e < 128; };
                 wait(ms.s_full[n & 1], n >> 1);
                 tmem_after();
                 const uint32_t s_at = t_s + (n & 1) * N + quarter + col0;
@@ -831,10 +847,12 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 bool move = over > kLazy;
                 if constexpr (S::kFp8) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) move = move || (ve[i] > E + 4 && ve[i] < 128);
+                    for (int i = 0; i < 4; ++i)
+                        move = move || lift(i) > ms.lift_over[grp] ||
+                               (kMasked && ms.lift_over[grp] == kNone && own(i) > kNone && own(i) < min(ms.scale_e[grp], 128));
                 }
                 if (barrier_or(id, 128, move)) {
-                    // the references move to the columns' maxima so far (and E to the values' largest exponent)
+                    // the references move to the columns' maxima so far, and E to the values' largest exponent if one passes it
                     fetch();
                     float top[NC / 4];
 #pragma unroll
@@ -852,21 +870,43 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
 #pragma unroll
                         for (int i = 0; i < NC / 4; ++i) ms.red[par][wq][col0 + 8 * (i >> 1) + cq + (i & 1)] = top[i];
                     }
-                    [[maybe_unused]] int e_new = E;
                     if constexpr (S::kFp8) {
-                        int et = -100000;
+                        int et = kNone, low = kUnset;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) et = ve[i] < 128 ? max(et, ve[i]) : et;
+                        for (int i = 0; i < 4; ++i) {
+                            et = max(et, lift(i));
+                            if (kMasked && own(i) > kNone && own(i) < 128) low = min(low, own(i));
+                        }
                         et = __reduce_max_sync(0xffffffffu, et);
-                        if (lane == 0) ms.red_e[4 * grp + wq] = et;
+                        if constexpr (kMasked) low = __reduce_min_sync(0xffffffffu, low);
+                        if (lane == 0) {
+                            ms.red_e[0][4 * grp + wq] = et;
+                            if constexpr (kMasked) ms.red_e[1][4 * grp + wq] = low;
+                        }
                     }
                     barrier_sync(id, 128);
                     float e_fac = 1.f;
                     if constexpr (S::kFp8) {
+                        const int E = ms.scale_e[grp], lift_over = ms.lift_over[grp];
+                        int et = kNone, low = E;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) e_new = max(e_new, max(ms.red_e[4 * grp + i], -126));
-                        e_fac = E - e_new < -126 ? 0.f : __uint_as_float((uint32_t)(127 + E - e_new) << 23);
-                        E = e_new;
+                        for (int i = 0; i < 4; ++i) {
+                            et = max(et, ms.red_e[0][4 * grp + i]);
+                            if constexpr (kMasked) low = min(low, ms.red_e[1][4 * grp + i]);
+                        }
+                        const bool firm = et > lift_over;
+                        int to = E;
+                        if (firm) to = max(et, -126);
+                        else if (kMasked && lift_over == kNone) to = max(low, -126);
+                        if (to != E) {
+                            const int d = min(E - to, 127);
+                            e_fac = E == kUnset || d < -126 ? 0.f : __uint_as_float((uint32_t)(127 + d) << 23);
+                        }
+                        barrier_sync(id, 128);
+                        if (gt == 0) {
+                            ms.scale_e[grp] = to;
+                            if (firm) ms.lift_over[grp] = to + 4;
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < NC / 4; ++i) {
@@ -908,8 +948,8 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 if constexpr (S::kFp8) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int de = ve[i] - E;
-                        vw[i] = ve[i] >= 128 ? __int_as_float(0x7fffffff) : de < -126 ? 0.f : __uint_as_float((uint32_t)(127 + de) << 23);
+                        const int e = own(i), de = e - ms.scale_e[grp];
+                        vw[i] = e >= 128 ? __int_as_float(0x7fffffff) : heavy(e) ? 1.f : de < -126 ? 0.f : __uint_as_float((uint32_t)(127 + de) << 23);
                     }
                 }
 #pragma unroll
@@ -947,7 +987,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 uint32_t* const pz = ms.poison[n & 1];
                 if constexpr (kMasked) {
                     // values of tokens that no row sees become zeros (a weight of zero times NaN is NaN); those that some
-                    // rows see and others do not, and that are not finite, become zeros here and are added by hand below
+                    // rows see and others do not, and that are heavy or not finite, become zeros here and are added by hand below
                     unsigned char* vt;
                     if constexpr (S::kFp8) {
                         wait(ms.v16_full[n & 1], n >> 1);
@@ -961,6 +1001,7 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                         const bool none = tok > seen_any || tok < from_any, some = tok > seen_all || tok < from_all;
                         bool clear = none;
                         if (!none && some) {
+                            if constexpr (S::kFp8) clear = heavy((int)ms.scales[1][n & 15][gt] - 127);
 #pragma unroll 2
                             for (int ch = 0; ch < DP / 8; ++ch) {
                                 const uint4 v4 = *reinterpret_cast<const uint4*>(vt + (ch / 8) * (kTile * 128) + gt * 128 + (((ch % 8) ^ (gt & 7)) * 16));
@@ -994,7 +1035,11 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                             float v = 0.f;
                             if (d < c.head_dim && page >= 0 && page < c.num_pages) {
                                 const int64_t at = page * c.page_stride + w.h * c.head_stride + tok % c.page_size * c.slot_stride + d;
-                                if constexpr (S::kFp8) v = to_float<__nv_fp8_e4m3>(static_cast<const __nv_fp8_e4m3*>(c.v)[at]);
+                                if constexpr (S::kFp8) {
+                                    const int e = (int)ms.scales[1][n & 15][tk] - 127;
+                                    v = to_float<__nv_fp8_e4m3>(static_cast<const __nv_fp8_e4m3*>(c.v)[at]);
+                                    if (heavy(e)) v = ldexpf(v, e - ms.scale_e[grp]);  // (its weights are without their scale)
+                                }
                                 else v = to_float<M>(static_cast<const M*>(c.v)[at]);
                             }
 #pragma unroll 1
@@ -1043,10 +1088,14 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                     if (wq == 0) ms.ref[par][col] = m[i];
                 }
             }
-            if (S::kFp8 && gt == 0) ms.ref_e[grp] = E;
+            if (S::kFp8 && cg == 0 && gt == 0) ms.ref_e[par] = ms.scale_e[grp];
             const bool whole = w.begin && w.end;
             float* const part = a.parts + (int64_t)(2 * blockIdx.x + (w.begin ? 1 : 0)) * S::kSlotFloats;
             barrier_sync(7, 128 * S::kGroups);
+            if (S::kFp8 && gt == 0) {                                    // (all have read them)
+                ms.scale_e[grp] = kUnset;
+                ms.lift_over[grp] = kNone;
+            }
             if (tid < N) {
                 // the column's sum, over both sets of tiles at one reference, and each set's factor for O
                 float ref = ms.ref[0][tid], sum = 0.f, f[S::kPar];
@@ -1062,8 +1111,8 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 for (int p = 0; p < S::kPar; ++p) {
                     float y = f[p];
                     if constexpr (S::kFp8) {
-                        const int e = ms.ref_e[p * S::kCol + tid / NC];
-                        if (e >= -126) y *= __uint_as_float((uint32_t)(127 + e) << 23);
+                        const int e = ms.ref_e[p];
+                        if (e != kUnset) y *= __uint_as_float((uint32_t)(127 + e) << 23);
                     }
                     ms.fac[p][tid] = !any ? 0.f : whole ? y * __frcp_rn(sum) : y;
                 }

@@ -511,3 +511,65 @@ def test_one_row_of_one_head_with_any_strides(cuda):
     back = torch.zeros((1, 1, 32), dtype=torch.bfloat16, device=cuda), torch.zeros(200, dtype=torch.bfloat16, device=cuda).as_strided((1, 1, 32), (5, 7, 1))
     _native.kv_read(s.cache, s.dtab, torch.tensor([0, 1], dtype=torch.int64, device=cuda), 1, *back, first=s.dcached)
     assert (back[0] == 1).all() and (back[1] == 2).all()
+
+
+@pytest.mark.parametrize("kind,dim,group,by", [("bf16", 64, 4, 5), ("bf16", 64, 4, 30), ("bf16", 128, 16, 12), ("bf16", 128, 16, 90),
+                                               ("f16", 128, 4, 5), ("f16", 128, 4, 12)])
+@pytest.mark.parametrize("cached", [0, 124, 125, 128, 130, 900])
+def test_a_scale_that_is_large_stays_in_the_rows_that_see_it(cuda, kind, dim, group, by, cached):
+    """The values of one of the last two drafts 2^by times the others' (f16 outputs hold 448 * 2^(121 - 127 + 12), not 2^30),
+    then those of the oldest token of the first row's window: the rows that do not see them give the same bits as
+    without, those that do are exact. Tiles that some or most rows see nothing of, first and later ones."""
+    import torch
+
+    s = Step(cuda, [4, 0], [cached, 3000], 2, group, dim, kind, "e4m3", 16)
+    want = s.run().check().out.clone()
+    for j in (4, 3):
+        p, sl = s.tab[0, (cached + j) // 16], (cached + j) % 16
+        keep = s.cache.v_exp[p, :, sl].clone()
+        s.cache.v_exp[p, :, sl] = keep + by
+        s.run().check()
+        assert torch.equal(s.out[:j], want[:j]) and torch.equal(s.out[5:], want[5:])
+        assert not torch.equal(s.out[j], want[j]) and (s.status == 0).all()
+        s.cache.v_exp[p, :, sl] = keep
+    for window in (100, 128, 700):
+        if window > cached:
+            continue
+        want = s.run(window=window).check(window=window).out.clone()
+        first = cached - window + 1                                  # the first row alone sees it
+        p1, s1 = s.tab[0, first // 16], first % 16
+        keep1 = s.cache.v_exp[p1, :, s1].clone()
+        s.cache.v_exp[p1, :, s1] = keep1 + by
+        s.run(window=window).check(window=window)
+        assert torch.equal(s.out[1:], want[1:]) and not torch.equal(s.out[0], want[0])
+        s.cache.v_exp[p1, :, s1] = keep1
+
+
+@pytest.mark.parametrize("kind,dim,group", [("bf16", 64, 4), ("bf16", 128, 8), ("f16", 32, 16)])
+@pytest.mark.parametrize("window", [1, 2, 4, 100])
+@pytest.mark.parametrize("cached", [0, 121, 124, 127, 700])
+def test_scales_of_rows_that_share_no_token(cuda, kind, dim, group, window, cached):
+    """Windows under the step's own rows, or that begin at the end of a tile: no token of a tile may be seen by every row, and
+    the rows' own scales rise or fall by up to 2^24 (f16: 2^12) from one to the next. Each row is exact by its own values."""
+    import torch
+
+    k, step = 8, 3 if kind == "bf16" else 1
+    for sign in (1, -1):
+        s = Step(cuda, [k, 0], [cached, 260], 2, group, dim, kind, "e4m3", 16)
+        for i in range(cached + k + 1):
+            s.cache.v_exp[s.tab[0, i // 16], :, i % 16] = 112 + sign * step * (i % 9 - 4)
+        s.run(window=window)
+        torch.cuda.synchronize()
+        gk, gv = P.held(s.cache)
+        kk, vv = P.tokens(gk, s.tab[0], cached + k + 1, 16), P.tokens(gv, s.tab[0], cached + k + 1, 16)
+        q, out = P.host(s.q), P.host(s.out)
+        for j in range(k + 1):                       # row by row: its tolerance is by what it sees itself, not by the largest scale
+            n = cached + j + 1
+            first = max(0, n - window)
+            want, _, spread = ref.attention(q[j: j + 1], kk[:n], vv[:n], n - 1, dim ** -0.5, window)
+            score = dim ** -0.5 * np.abs(q[j]).sum(-1) * np.abs(kk[:n]).max() * (dim + 4) * 2.0 ** -23
+            tiny = np.abs(vv[first: n]).max() * 2.0 ** -24 * min(n - first, 64)
+            tol = (2.0 ** -11 + 2 * score[:, None] + 2.0 ** -20) * spread[0] + tiny
+            tol = tol + P.HALF[kind] * (np.abs(want[0]) + tol) + (2.0 ** -25 if kind == "f16" else 2.0 ** -134)
+            assert np.all(np.abs(out[j] - want[0]) <= tol), (j, (np.abs(out[j] - want[0]) / tol).max())
+        assert (s.status == 0).all()

@@ -571,14 +571,14 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                 ++t;
             }
             if constexpr (S::kFp8) {
-                const Ahead& y = x[2];                   // tile k - 2: 16 of its scales a lane (1 where there is no page)
+                const Ahead& y = x[2];                   // tile k - 2: 16 of its scales a lane (without a page the smallest: zeros raise no exponent)
                 if (y.used > 0 && lane < 8) {
                     const int pg = ms.pages[is_v][(k - 2) & 7][(lane << 4) >> row_bits];
                     uint8_t* const to = &ms.scales[is_v][(k - 2) & 15][lane * 16];
                     if (pg >= 0 && pg < c.num_pages)
                         async_copy_16(smem_u32(to), (is_v ? c.v_exp : c.k_exp) + ((((int64_t)pg * H + y.h) << bits) + y.slot0 + ((lane << 4) & (rows - 1))), 16);
                     else
-                        *reinterpret_cast<uint4*>(to) = make_uint4(0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f, 0x7f7f7f7f);
+                        *reinterpret_cast<uint4*>(to) = make_uint4(0x01010101, 0x01010101, 0x01010101, 0x01010101);
                 }
             }
             async_copy_commit();

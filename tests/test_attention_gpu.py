@@ -573,3 +573,17 @@ def test_scales_of_rows_that_share_no_token(cuda, kind, dim, group, window, cach
             tol = tol + P.HALF[kind] * (np.abs(want[0]) + tol) + (2.0 ** -25 if kind == "f16" else 2.0 ** -134)
             assert np.all(np.abs(out[j] - want[0]) <= tol), (j, (np.abs(out[j] - want[0]) / tol).max())
         assert (s.status == 0).all()
+
+
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 256)])
+def test_a_bad_page_of_a_quantised_cache_reads_as_zeros(cuda, dim, page):
+    """Its tokens have no scale: the others' weights keep their bits, small as their values are (scales of 2^-22 and less)."""
+    s = Step(cuda, [2, 0], [900, 700], 2, 4, dim, "bf16", "e4m3", page)
+    s.cache.v_exp.copy_(s.cache.v_exp - 14)
+    s.dtab[0, 1], s.dtab[1, 0] = s.cache.num_pages, -5
+    s.run()
+    assert s.status.tolist() == [_native.ST_BAD_PAGE] * 2
+    free = [p for p in range(s.cache.num_pages) if p not in s.tab][0]
+    s.cache.k[free], s.cache.v[free] = 0, 0
+    s.tab[0, 1], s.tab[1, 0] = free, free
+    s.check()

@@ -196,7 +196,8 @@ template <typename M> __device__ __forceinline__ uint32_t not_finite(uint32_t tw
     return ((two & 0x7fff7fffu) + kOne) & 0x80008000u;
 }
 
-// ln of the sum of a column's weights: log2's approximation is off by 2^-22 at most
+// ln of the sum of a column's weights: log2's approximation is off by 2^-22 near a sum of one, else by two units in its
+// own last place, and so of the size of the other roundings of a long sum
 __device__ __forceinline__ float lse_of(bool any, float ref, float sum)
 {
     return any ? (ref + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
@@ -261,20 +262,20 @@ template <typename S> struct Misc {
     alignas(16) float red[S::kPar][4][S::N];             // a column's value in each warp of its group
     alignas(16) float fac[S::kPar][S::N];
     float ref[S::kPar][S::N];
-    int red_e[2][4 * S::kGroups], ref_e[S::kPar];
-    // E, the exponent that a group takes the values' scales by, and that which a token's must pass to raise it. E follows from
-    // the scales alone, so that the groups of a tile agree on it, and from tokens that every row sees: one that some rows
-    // do not see would cost these rows' weights their bits if its scale were far above theirs, so above E + 4 it is
-    // added by hand (heavy). Until a tile holds a token that every row sees, E is the smallest scale so far and
-    // lift_over below all. (Here and not in registers, where they cost spills: 314 us where 321 for 128 requests of up to
-    // 8000 tokens, 24 rows a key head.)
-    int scale_e[S::kGroups], lift_over[S::kGroups];
+    int red_e[4 * S::kGroups], ref_e[S::kPar];
     alignas(16) int32_t last[2][S::N];                   // last token that a column sees (-1: no column)
     alignas(16) int2 place[2][S::N];                     // a column's row of q and out, and its query head (row -1: no column)
     alignas(16) int64_t out_at[2][S::N];                 // and where it lies in out
     alignas(16) float qscale[2][S::kFp8 ? S::N : 4];
     alignas(16) int32_t pages[2][8][8];                  // of keys and of values: page ids of the tiles looked ahead to
     alignas(16) uint8_t scales[2][S::kFp8 ? 16 : 1][kTile];              // and exponents of their e4m3 keys and values
+    // E, the exponent that a group takes the values' scales by, and that which a token's must pass to raise it. E follows from
+    // the scales alone, so that the groups of a tile agree on it, and from tokens that every row sees: one that some rows
+    // do not see would cost these rows' weights their bits if its scale were far above theirs, so above E + 4 it is
+    // added by hand (heavy). Until a tile holds a token that every row sees, E is the smallest scale so far and
+    // lift_over below all. (Here and not in registers, where they cost spills: 314 us where 321 for 128 requests of up to
+    // 8000 tokens, 24 rows a key head.)
+    int scale_e[S::kGroups], lift_over[S::kGroups], red_low[4 * S::kGroups];
 };
 
 // ---------------------------------------------------------------- the kernel
@@ -331,7 +332,8 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
         }
         bar_init(bar(ms.drained), 2);
         ms.expired = 0;
-        for (int i = 0; i < S::kGroups; ++i) ms.scale_e[i] = kUnset, ms.lift_over[i] = kNone;
+        if constexpr (S::kFp8)
+            for (int i = 0; i < S::kGroups; ++i) ms.scale_e[i] = kUnset, ms.lift_over[i] = kNone;
         for (int i = 0; i < 8; ++i) ms.poison[i >> 2][i & 3] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -880,8 +882,8 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                         et = __reduce_max_sync(0xffffffffu, et);
                         if constexpr (kMasked) low = __reduce_min_sync(0xffffffffu, low);
                         if (lane == 0) {
-                            ms.red_e[0][4 * grp + wq] = et;
-                            if constexpr (kMasked) ms.red_e[1][4 * grp + wq] = low;
+                            ms.red_e[4 * grp + wq] = et;
+                            if constexpr (kMasked) ms.red_low[4 * grp + wq] = low;
                         }
                     }
                     barrier_sync(id, 128);
@@ -891,8 +893,8 @@ specdec_paged_attention_kernel(const Args a, const __grid_constant__ CUtensorMap
                         int et = kNone, low = E;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            et = max(et, ms.red_e[0][4 * grp + i]);
-                            if constexpr (kMasked) low = min(low, ms.red_e[1][4 * grp + i]);
+                            et = max(et, ms.red_e[4 * grp + i]);
+                            if constexpr (kMasked) low = min(low, ms.red_low[4 * grp + i]);
                         }
                         const bool firm = et > lift_over;
                         int to = E;

@@ -242,7 +242,7 @@ template <typename T, typename C> specdec_status_t launch_write(WriteArgs a, cud
     const int64_t per = 16 / (int64_t)sizeof(T);
     const bool wide = rot % 16 == 0 && aligned_to(a.k, 16) && aligned_to(a.v, 16) && a.row_stride % per == 0 &&
                       a.head_stride % per == 0;
-    // rows of one wave of CTAs (four on each of 152 SMs), up to eight heads a group; never fewer than fill a CTA
+    // rows for 608 CTAs (four on each of 152 SMs), up to eight heads a group; never fewer than fill a CTA
     const int groups = wide ? kThreads / 8 : kThreads / 32, heads = 2 * c.num_kv_heads, batch = 8 * groups;
     if (heads >= 1 << 24) return SPECDEC_ERR_UNSUPPORTED;          // (32-bit places within a CTA's rows)
     const int64_t wave = ((int64_t)a.rows + 607) / 608, most = (batch + heads - 1) / heads, fill = (groups + heads - 1) / heads;

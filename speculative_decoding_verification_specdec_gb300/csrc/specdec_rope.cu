@@ -120,7 +120,8 @@ specdec_status_t launch_rope(RopeArgs a, cudaStream_t stream)
     a.units = a.head_dim / (2 * V);
     const int64_t row_units = (int64_t)a.heads * a.units;
     if (row_units >= 1 << 24) return SPECDEC_ERR_UNSUPPORTED;      // (32-bit places within a CTA's rows)
-    // rows of one wave of CTAs (four on each of 152 SMs), up to a batch of units a thread; never fewer than fill a CTA
+    // rows for 608 CTAs (four on each of 152 SMs; 79 registers let three run at once, the rest of so small a grid follows
+    // as they end), up to a batch of units a thread; never fewer than fill a CTA
     const int64_t wave = ((int64_t)a.rows + 607) / 608, batch = (kBatch * kThreads + row_units - 1) / row_units,
                   fill = (kThreads + row_units - 1) / row_units;
     int64_t rpc = wave < batch ? wave : batch;

@@ -7,9 +7,10 @@
  * then rotate the heads in 32-byte units. Bound by HBM: every element is read and written once.
  *
  * A thread has four units in flight and reads the first of them before the rows' places are known; few rows
- * are spread over one wave of CTAs. Measured on one GB300, calls through the binding: a prompt whose floor at the
- * copy rate is 29.8 us takes 41.1 (72 %, 4.9 TB/s). Those choices took 1280 query rows from 10.2 to
- * 8.2 us; called without the binding they take 4 to 6, so the host bounds small calls.
+ * are spread over many CTAs. Measured on one GB300, calls through the binding: a prompt whose floor at the
+ * copy rate is 29.8 us takes 41.7 (71 %, 4.8 TB/s). The look at the requests' total before the first read, which keeps
+ * rows behind it unread, costs 0.5 us of it (1.0 before the first requests' offsets were read beside it). Four units
+ * and many CTAs took 1280 query rows from 10.2 to 8.2 us; without the binding they take 4 to 6: the host bounds small calls.
  */
 #include <cmath>
 
@@ -46,6 +47,8 @@ __global__ void __launch_bounds__(kThreads, 3) specdec_rope_kernel(const RopeArg
     const int64_t row0 = (int64_t)blockIdx.x * a.rows_per_cta;
     const int n = (int)min((int64_t)a.rows_per_cta, a.rows - row0);
     const int row_units = a.heads * a.units, total = n * row_units;
+    auto start = [&](int i) { return (int64_t)__ldg(a.cu + i) + i; };
+    const int64_t first_start = !a.positions && tid < a.B ? start(tid) : 0;        // (on its way beside the offsets' total)
     const int there = a.positions ? total : rows_there(a.cu, a.B, row0, n) * row_units;
     Raw<T, V> v[kBatch][2];
     const Place step(kThreads, a.heads, a.units);
@@ -63,7 +66,7 @@ __global__ void __launch_bounds__(kThreads, 3) specdec_rope_kernel(const RopeArg
     };
     fetch(tid);
     int b = 0;
-    if (!a.positions) b = owner_of<kThreads>(a.B, row0, [&](int i) { return (int64_t)__ldg(a.cu + i) + i; });
+    if (!a.positions) b = owner_of<kThreads>(a.B, row0, first_start, start);
     if (tid < n) {
         const int64_t t = row0 + tid;
         if (a.positions) {
@@ -120,7 +123,7 @@ specdec_status_t launch_rope(RopeArgs a, cudaStream_t stream)
     a.units = a.head_dim / (2 * V);
     const int64_t row_units = (int64_t)a.heads * a.units;
     if (row_units >= 1 << 24) return SPECDEC_ERR_UNSUPPORTED;      // (32-bit places within a CTA's rows)
-    // rows for 608 CTAs (four on each of 152 SMs; 79 registers let three run at once, the rest of so small a grid follows
+    // rows for 608 CTAs (four on each of 152 SMs; 80 registers let three run at once, the rest of so small a grid follows
     // as they end), up to a batch of units a thread; never fewer than fill a CTA
     const int64_t wave = ((int64_t)a.rows + 607) / 608, batch = (kBatch * kThreads + row_units - 1) / row_units,
                   fill = (kThreads + row_units - 1) / row_units;

@@ -101,16 +101,22 @@ __device__ __forceinline__ int rows_there(const int32_t* cu, int32_t B, int64_t 
 
 // The request that owns row t, by counting the requests that start at or before it (every thread
 // of the CTA calls it; one round of independent loads per 256 requests, where a search would
-// wait out a chain of them). The caller checks that the request really holds the row.
+// wait out a chain of them). `first` is start(threadIdx.x), which the
+// caller may have read ahead. The caller checks that the request really holds the row.
 template <int kThreads, typename Start>
-__device__ __forceinline__ int owner_of(int32_t B, int64_t t, Start start)
+__device__ __forceinline__ int owner_of(int32_t B, int64_t t, int64_t first, Start start)
 {
     int n = 0;
     for (int base = 0; base < B; base += kThreads) {
         const int b = base + (int)threadIdx.x;
-        n += __syncthreads_count(b < B && start(b) <= t);
+        n += __syncthreads_count(b < B && (base == 0 ? first : start(b)) <= t);
     }
     return n - 1;
+}
+template <int kThreads, typename Start>
+__device__ __forceinline__ int owner_of(int32_t B, int64_t t, Start start)
+{
+    return owner_of<kThreads>(B, t, (int)threadIdx.x < B ? start((int)threadIdx.x) : 0, start);
 }
 
 // cos and sin of position * freq (units of 2^-64 turn): the product wraps modulo one turn, the

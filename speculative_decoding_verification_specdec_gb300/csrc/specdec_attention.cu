@@ -26,7 +26,7 @@
  * 427 us where this takes 355 (128 requests of up to 8000 tokens, 24 rows a key head).
  *
  * Bound by HBM: every visible key and value is read once per row block. Measured on one GB300: 64 requests of 1000
- * to 32000 bf16 tokens, up to 72 rows a key head (4.8 GB): 716 us, 6.7 TB/s, 99 % of the measured copy rate.
+ * to 32000 bf16 tokens, up to 72 rows a key head (4.8 GB): 716 to 725 us by the card, 6.7 TB/s, 98 to 99 % of the measured copy rate.
  * Over e4m3 a tile is 32 KB and takes 0.84 us with 16 columns (the copy rate would be 0.74) and 1.07 with 32, by the
  * latency of the chain scores - weights - product of a tile; with short contexts an item costs 4 to 9 us to start
  * and end, most of it instructions that are run once an item and not in the instruction cache.

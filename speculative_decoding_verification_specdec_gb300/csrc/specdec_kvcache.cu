@@ -8,9 +8,9 @@
  * e4m3's three mantissa bits (relative error at most 2^-4), and the scale takes one byte.
  *
  * Both kernels only move data: bound by HBM. Measured on one GB300, calls through the binding: a prompt
- * into a bf16 cache 40.5 us where the copy rate would take 32.2 (80 %); prefixes out of an e4m3 cache 123.5 us for
+ * into a bf16 cache 40.6 us where the copy rate would take 32.2 (79 %); prefixes out of an e4m3 cache 123.6 us for
  * 109.6 (89 %; 139 before four units a thread were in flight). A step's rows into an e4m3 cache take 4 us on
- * the GPU and 15.3 through the binding: small calls are bound by the host.
+ * the GPU and 15.2 through the binding: small calls are bound by the host.
  */
 #include "specdec_rows.cuh"
 

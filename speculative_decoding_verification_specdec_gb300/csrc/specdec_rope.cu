@@ -8,7 +8,7 @@
  *
  * A thread has four units in flight and reads the first of them before the rows' places are known; few rows
  * are spread over many CTAs. Measured on one GB300, calls through the binding: a prompt whose floor at the
- * copy rate is 29.8 us takes 41.7 (71 %, 4.8 TB/s). The look at the requests' total before the first read, which keeps
+ * copy rate is 29.8 us takes 41.6 (72 %, 4.9 TB/s). The look at the requests' total before the first read, which keeps
  * rows behind it unread, costs 0.5 us of it (1.0 before the first requests' offsets were read beside it). Four units
  * and many CTAs took 1280 query rows from 10.2 to 8.2 us; without the binding they take 4 to 6: the host bounds small calls.
  */

@@ -464,8 +464,8 @@ specdec_status_t specdec_kv_read(const specdec_kv_cache_t* cache, const int32_t*
  *   max_k        every k_b must be <= max_k <= SPECDEC_KMAX; it chooses the kernel's row tile.
  *   scale        finite.  window >= 0.
  *   workspace    specdec_paged_attention_workspace_size(...) bytes (0 for sizes that the call refuses),
- *                16-byte aligned, no initialisation; it holds nothing between calls, and calls (or captured graphs) that
- *                share one must not overlap in time.
+ *                16-byte aligned, no initialisation; it holds nothing between calls, and calls (or
+ *                captured graphs) that share one must not overlap in time.
  *   wait_limit_us -1: 2 s; 0..2000000: the limit of every wait inside the kernel, after which the
  *                requests concerned get SPECDEC_ST_DEVICE_TIMEOUT and undefined outputs; nothing
  *                hangs or traps.
@@ -473,14 +473,16 @@ specdec_status_t specdec_kv_read(const specdec_kv_cache_t* cache, const int32_t*
  * lengths) a request's result may differ in its last bits. Scores, maxima, sums and the output are
  * accumulated in fp32. The weights exp(s - m) are rounded to the cache's 16-bit type before their product
  * with V; over an E4M3 cache to F16, times their token's scale relative to the largest scale so far of tokens
- * that all rows of a block see (a head of zeros has 2^0), so a weight whose product falls 2^24 below that is
- * lost; values that only some of those rows see, of a scale 2^100 above it or more, may come out infinite. There Q is taken as a sum of two (BF16) or three
- * (F16) e4m3 numbers an element, exact but for elements under 2^-9 (BF16) or 2^-6 (F16) of the row's
- * largest, which are off by at most 2^-17 of it; an infinity in Q counts as NaN there.
+ * that all rows computed together see (a head of zeros has 2^0), so a weight whose product falls 2^24 below that
+ * is lost; values that only some of those rows see, of a scale 2^100 above it or more, may come out infinite.
+ * There Q is taken as a sum of two (BF16) or three (F16) e4m3 numbers an element, exact but for elements under
+ * 2^-9 (BF16) or 2^-6 (F16) of the row's largest, which are off by at most 2^-17 of it; an infinity in Q counts
+ * as NaN there.
  * Keys and values that a row does not see do not reach it, whatever they hold (infinities, NaN, pages
  * never written; with a window, block_table entries of pages that lie wholly before it are not read).
  * A row that sees no finite score gets zeros and lse = -inf.
- * status: K_TOO_LARGE, BAD_OFFSETS (rows unknown: not written), BAD_LENGTH (both others: zeros, lse -inf in its rows; also 2^31 - 128 tokens or more),
+ * status: K_TOO_LARGE, BAD_OFFSETS (rows unknown: not written), BAD_LENGTH (both others: zeros, lse -inf in
+ * its rows; also 2^31 - 128 tokens or more),
  * BAD_PAGE (its tokens read as zeros), DEVICE_TIMEOUT.
  * Errors: INVALID_ARG for a NULL required pointer, a bad size or stride, num_heads not a multiple of
  * num_kv_heads, a workspace too small or misaligned; UNSUPPORTED for types, page_size or head_dim

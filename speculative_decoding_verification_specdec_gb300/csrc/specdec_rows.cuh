@@ -101,8 +101,8 @@ __device__ __forceinline__ int rows_there(const int32_t* cu, int32_t B, int64_t 
 
 // The request that owns row t, by counting the requests that start at or before it (every thread
 // of the CTA calls it; one round of independent loads per 256 requests, where a search would
-// wait out a chain of them). `first` is start(threadIdx.x), which the
-// caller may have read ahead. The caller checks that the request really holds the row.
+// wait out a chain of them). `first` is start(threadIdx.x), which the caller may have read ahead.
+// The caller checks that the request really holds the row.
 template <int kThreads, typename Start>
 __device__ __forceinline__ int owner_of(int32_t B, int64_t t, int64_t first, Start start)
 {

@@ -68,6 +68,10 @@ typedef enum { SPECDEC_F32 = 0, SPECDEC_BF16 = 1, SPECDEC_F16 = 2, SPECDEC_E4M3 
 /* Set by the cache operators (with K_TOO_LARGE, BAD_OFFSETS and DEVICE_TIMEOUT above). */
 #define SPECDEC_ST_BAD_LENGTH    128u   /* a negative length, or one past the request's row of block_table: skipped */
 #define SPECDEC_ST_BAD_PAGE      256u   /* a page id outside [0, num_pages): nothing written there, zeros read */
+/* Set by the operators on rows of logits beside the verify (with EMPTY_MASK_ROW above, here also a row without
+ * any logit above -infinity). */
+#define SPECDEC_ST_BAD_SCORE     512u   /* a beam's score, or a logit of its row, is NaN or +infinity: no candidates */
+#define SPECDEC_ST_BAD_TARGET   1024u   /* a listed id outside [-1, V) or listed before, or no log-probability: not counted */
 
 /*
  * specdec_verify -- verify one batch (stream-ordered, asynchronous).
@@ -499,6 +503,140 @@ specdec_status_t specdec_paged_attention(const void* q, specdec_dtype_t dtype, i
                                          int64_t out_head_stride, float* lse, uint32_t* status,
                                          void* workspace, size_t workspace_bytes, int32_t wait_limit_us,
                                          void* stream);
+
+/*
+ * specdec_kv_fork -- new rows of block tables whose requests go on from other rows' tokens: the paged cache's part of a
+ * beam step (specdec_beam_select's out_rows are the parents), or of a prompt that several requests share. Row i
+ * takes over the lengths[parent[i]] tokens of its parent. Pages that those fill are shared: their ids are copied. The page that the
+ * next token goes to becomes fresh[i], and the tokens that the parent already has there (length modulo page_size of them) are
+ * copied into it, keys, values and scales as they are held.
+ *
+ *   block_table  [sources, max_blocks] of the parents, rows block_stride apart;  lengths [sources].
+ *   parent       [n]: 0 .. sources - 1, or -1: an empty row (no pages, length 0).
+ *   fresh        [n] or NULL: a page that no row reads or writes and that no other entry names. -1 (NULL: every row): the
+ *                parent's page goes on being used, as it does, uncopied, where fresh[i] is that page itself. What is
+ *                read of a page that another entry writes is undefined.
+ *   out_table    [n, max_blocks] rows out_stride apart, -1 behind each row's last page; it must not overlap block_table.
+ *                NULL: not written (the other layers of a model whose caches share one table: with fresh given, only
+ *                the tokens are copied).
+ *   out_lengths  [n] or NULL; it must not overlap lengths.
+ * status, [n] here: BAD_OFFSETS (a parent outside [-1, sources)) and BAD_LENGTH (a negative length, or one past
+ * max_blocks pages): an empty row; BAD_PAGE (fresh[i], or the page to be copied, outside [0, num_pages)): nothing is
+ * copied and the parent's page stays (-1 where it has none). A length that fills all max_blocks pages leaves no place for fresh[i].
+ * Errors: INVALID_ARG for a NULL required pointer (block_table, lengths, parent; one of out_table and fresh), a bad size or
+ * stride; UNSUPPORTED for types, page_size or head_dim outside those above; CUDA.
+ */
+specdec_status_t specdec_kv_fork(const specdec_kv_cache_t* cache, const int32_t* block_table, int32_t max_blocks,
+                                 int64_t block_stride, const int32_t* lengths, int32_t sources, const int32_t* parent,
+                                 const int32_t* fresh, int32_t n, int32_t* out_table, int64_t out_stride,
+                                 int32_t* out_lengths, uint32_t* status, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Rows of logits beside the verify: the best ids of every row, the distillation of a drafter from such a record of
+ * its target, and a beam step's selection. The operators are this library's, from their formulas.
+ *
+ * Rows are [rows, V] of dtype F32, BF16 or F16, row_stride elements apart (at least V; any alignment of an element's), V
+ * up to 2^30. Pointers, status bits (OR-ed in, never cleared) and streams are as the cache operators', and calls may
+ * be captured: everything but sizes is read on the device. temperature (host) is in [1e-4, 1e4]; sums of exponentials
+ * are of z / temperature, of which what lies beyond 2 10^38 either way counts as infinite (the lowest finite logit of
+ * a masked place as -infinity; ids are still ordered by the logits themselves).
+ * ------------------------------------------------------------------------------------------ */
+#define SPECDEC_TOP_MAX 128       /* largest n, and the most beams of a request */
+
+/*
+ * specdec_top_logits -- the n largest logits of every row: their ids, and their log-probabilities in the softmax of
+ * z / temperature over all allowed ids.
+ *
+ *   bitmask      [rows, W] as the verify's, or NULL (all ids allowed).
+ *   out_ids      [rows, n]: largest logit first, the lower id first among equals. -infinity and NaN are never listed;
+ *                behind the last id come -1, with log-probability -infinity.
+ *   out_logprobs [rows, n] fp32.
+ *   lse          [rows] fp32 or NULL: ln(sum exp(z / temperature)) over the allowed ids (-infinity for none). A NaN or
+ *                +infinity among them makes it and the row's log-probabilities NaN; the ids stand.
+ *   workspace    specdec_top_logits_workspace_size(...) bytes (0 for sizes that the call refuses), 16-byte aligned,
+ *                no initialisation; it holds nothing between calls, and calls (or captured graphs) that share one must not overlap in time.
+ * status, [rows] here: EMPTY_MASK_ROW where nothing is listed. Equal rows of one alignment give equal bits wherever they stand.
+ * Sums are held in fp32 over 64 elements or fewer a thread and in 64 bits from there on.
+ * Errors: INVALID_ARG for a NULL required pointer, n outside [1, SPECDEC_TOP_MAX], a bad size, stride or temperature, a
+ * workspace too small or misaligned; UNSUPPORTED for a type or V outside those above, or more than 2^31 units of 4 KB; CUDA.
+ */
+size_t specdec_top_logits_workspace_size(int32_t rows, int32_t V, specdec_dtype_t dtype);
+specdec_status_t specdec_top_logits(const void* logits, specdec_dtype_t dtype, int32_t rows, int32_t V, int64_t row_stride,
+                                    const int32_t* bitmask, double temperature, int32_t n, int32_t* out_ids,
+                                    float* out_logprobs, float* lse, uint32_t* status, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
+ * specdec_distill -- the loss of a drafter's rows of logits against the top log-probabilities of its target, and its
+ * gradient. With s = softmax(z / temperature), t_i = exp(top_logprobs_i) for the ids listed and w = weight[row]:
+ *
+ *   rest = 1   r = max(0, 1 - sum t) is left to all other ids together, one more category, of which the drafter
+ *              gives rho = the sum of s outside the list:
+ *              loss = w (sum t_i (ln t_i - ln s_i) + r (ln r - ln rho))
+ *              grad_j = w / temperature (M s_j - t_j) on the list, w / temperature (M s_j - r s_j / rho) outside, M = sum t + r
+ *   rest = 0   the t_i are divided by their sum, and r = 0.
+ * One listed id of log-probability 0 makes it the cross entropy of a label.
+ *
+ *   top_ids      [rows, n] contiguous, 1 <= n <= SPECDEC_TOP_MAX, in any order; -1 is no entry.
+ *   top_logprobs [rows, n] contiguous fp32: at the same temperature as the loss (specdec_top_logits').
+ *   weight       [rows] fp32 or NULL (1): a row's factor. A row of weight 0 is not read: its loss and stats are 0, its gradient zeros.
+ *   loss         [rows] fp32.
+ *   stats        [rows, 2] fp32 contiguous or NULL: ln(sum exp(z / temperature)) over all ids and over those not listed,
+ *                which specdec_distill_backward takes.
+ *   grad         [rows, V] of the logits' type, rows grad_row_stride elements apart, or NULL (the loss alone). It may be
+ *                logits itself (with its stride), and must not overlap it otherwise.
+ * Where the drafter leaves nothing to the other ids (none is there, or all are -infinity), r does not count (it is taken as 0).
+ * A row without a finite logit: loss +infinity, gradient zeros. A row whose list asks for nothing (rest = 0 and no entry): zeros. NaN or
+ * +infinity in a row makes its loss and gradient NaN.
+ * status, [rows] here: BAD_TARGET (an id outside [-1, V), one listed before, a log-probability that is NaN or +infinity: that entry does not
+ * count); EMPTY_MASK_ROW (no finite logit).
+ * Sums over the row are held in fp32 by a thread and in 64 bits across them; targets, listed exponentials and the loss in 64
+ * bits; an element of the gradient is one fp32 exponential times one factor, rounded once to its type. Equal calls give equal bits.
+ * Errors: INVALID_ARG for a NULL required pointer, n, a size, a stride or a temperature outside those above, rest not 0 or 1;
+ * UNSUPPORTED for a type or V outside those above, or more than 2^31 CTAs; CUDA.
+ */
+specdec_status_t specdec_distill(const void* logits, specdec_dtype_t dtype, int32_t rows, int32_t V, int64_t row_stride,
+                                 const int32_t* top_ids, const float* top_logprobs, int32_t n, double temperature,
+                                 int32_t rest, const float* weight, float* loss, float* stats, void* grad,
+                                 int64_t grad_row_stride, uint32_t* status, void* stream);
+
+/*
+ * specdec_distill_backward -- the gradient alone, where the loss's own gradient is known only after the forward pass:
+ * grad as above with w = grad_loss[row] (times the forward call's weight, if it had one), from the stats that
+ * specdec_distill kept for the same rows, list, temperature and rest. grad may be logits itself. grad_loss NULL: 1.
+ * status: BAD_TARGET. Errors as specdec_distill's.
+ */
+specdec_status_t specdec_distill_backward(const void* logits, specdec_dtype_t dtype, int32_t rows, int32_t V,
+                                          int64_t row_stride, const int32_t* top_ids, const float* top_logprobs, int32_t n,
+                                          double temperature, int32_t rest, const float* stats, const float* grad_loss,
+                                          void* grad, int64_t grad_row_stride, uint32_t* status, void* stream);
+
+/*
+ * specdec_beam_select -- the n best continuations of each of B requests with `beams` beams: of beam w (row b * beams + w) and
+ * every allowed id v, score = scores[b, w] + ln softmax(z)[v] (over the allowed ids). A finished beam has one
+ * continuation, end_token at its own score, and its row is not read; a beam of score -infinity (not begun yet) has none.
+ *
+ *   bitmask      [B * beams, W] or NULL.   scores [B, beams] fp32.   finished [B, beams] uint8 or NULL (none).
+ *   end_token    the id that ends a beam, -1: none (finished must be NULL then).
+ *   out_rows     [B, n] int32: the row b * beams + w that each continuation goes on from (specdec_kv_fork's parent), best score
+ *                first, the lower row and then the lower id first among equals; behind the last, -1.
+ *   out_tokens   [B, n] int32: its id (-1).   out_scores [B, n] fp32 (-infinity).
+ *   out_finished [B, n] uint8 or NULL: whether it is finished now (it was, or its id is end_token).
+ *   n            1 .. SPECDEC_TOP_MAX, beams up to SPECDEC_TOP_MAX, beams * n <= 4096.
+ *   workspace    specdec_beam_select_workspace_size(...) bytes, as specdec_top_logits'.
+ * scores may be out_scores and finished out_finished where n = beams. Scores compete in 64 bits (the row's sum of exponentials is held
+ * as specdec_top_logits holds it: differences under 10^-6 may fall either way); out_scores is their value in fp32.
+ * status, [B] here: BAD_SCORE (a score, or a row's logit, that is NaN or +infinity: that beam has no continuation), EMPTY_MASK_ROW (a
+ * beam whose row allows nothing). Equal calls give equal bits.
+ * Errors: INVALID_ARG for a NULL required pointer, a bad size or stride, end_token outside [-1, V) or -1 with finished, a
+ * workspace too small or misaligned; UNSUPPORTED for a type or V outside those above or beams * n > 4096; CUDA.
+ */
+size_t specdec_beam_select_workspace_size(int32_t B, int32_t beams, int32_t V, specdec_dtype_t dtype, int32_t n);
+specdec_status_t specdec_beam_select(const void* logits, specdec_dtype_t dtype, int32_t B, int32_t beams, int32_t V,
+                                     int64_t row_stride, const int32_t* bitmask, const float* scores, const uint8_t* finished,
+                                     int32_t end_token, int32_t n, int32_t* out_rows, int32_t* out_tokens, float* out_scores,
+                                     uint8_t* out_finished, uint32_t* status, void* workspace, size_t workspace_bytes,
+                                     void* stream);
 
 /*
  * specdec_wait -- block the calling host thread until all work queued on `stream` has

@@ -8,6 +8,11 @@ from ._native import (  # noqa: F401
     SPECDEC_F32,
     SPECDEC_KMAX,
     SpecdecError,
+    beam_select,
+    beam_select_workspace_size,
+    distill,
+    distill_backward,
+    kv_fork,
     kv_read,
     kv_write,
     launch_config,
@@ -19,6 +24,8 @@ from ._native import (  # noqa: F401
     specdec_verify,
     specdec_wait,
     status_string,
+    top_logits,
+    top_logits_workspace_size,
 )
 from .kvcache import PagedCache  # noqa: F401
 from .metrics import acceptance_rates, mean_acceptance_length  # noqa: F401

@@ -32,12 +32,16 @@ ST_DEVICE_TIMEOUT = 32
 ST_BAD_TOP_P = 64
 ST_BAD_LENGTH = 128
 ST_BAD_PAGE = 256
+ST_BAD_SCORE = 512
+ST_BAD_TARGET = 1024
 
 EXPORTED = ("specdec_verify", "specdec_verify_noalloc", "specdec_wait", "specdec_status_string",
             "specdec_launch_config", "specdec_workspace_size", "specdec_ngram_propose",
             "specdec_bitmask_scatter", "specdec_set_launch_options", "specdec_rope_frequencies",
             "specdec_rope", "specdec_kv_write", "specdec_kv_read", "specdec_paged_attention_workspace_size",
-            "specdec_paged_attention")
+            "specdec_paged_attention", "specdec_kv_fork", "specdec_top_logits_workspace_size", "specdec_top_logits",
+            "specdec_distill", "specdec_distill_backward", "specdec_beam_select_workspace_size", "specdec_beam_select")
+TOP_MAX = 128                           # SPECDEC_TOP_MAX
 NGRAM_MAX_N = 64                        # SPECDEC_NGRAM_MAX_N
 NOALLOC_MAX_REQUESTS = 16384            # SPECDEC_NOALLOC_MAX_REQUESTS
 
@@ -109,6 +113,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.specdec_paged_attention.restype = ctypes.c_int
     lib.specdec_paged_attention.argtypes = [vp, ctypes.c_int, i32, i32, i64, i64, vp, vp, i32, i64, vp, vp, i32, i32,
                                             ctypes.c_float, i32, vp, i64, i64, vp, vp, vp, ctypes.c_size_t, i32, vp]
+    lib.specdec_kv_fork.restype = ctypes.c_int
+    lib.specdec_kv_fork.argtypes = [vp, vp, i32, i64, vp, i32, vp, vp, i32, vp, i64, vp, vp, vp]
+    lib.specdec_top_logits_workspace_size.restype = ctypes.c_size_t
+    lib.specdec_top_logits_workspace_size.argtypes = [i32, i32, ctypes.c_int]
+    lib.specdec_top_logits.restype = ctypes.c_int
+    lib.specdec_top_logits.argtypes = [vp, ctypes.c_int, i32, i32, i64, vp, f64, i32, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.specdec_distill.restype = ctypes.c_int
+    lib.specdec_distill.argtypes = [vp, ctypes.c_int, i32, i32, i64, vp, vp, i32, f64, i32, vp, vp, vp, vp, i64, vp, vp]
+    lib.specdec_distill_backward.restype = ctypes.c_int
+    lib.specdec_distill_backward.argtypes = [vp, ctypes.c_int, i32, i32, i64, vp, vp, i32, f64, i32, vp, vp, vp, i64, vp, vp]
+    lib.specdec_beam_select_workspace_size.restype = ctypes.c_size_t
+    lib.specdec_beam_select_workspace_size.argtypes = [i32, i32, i32, ctypes.c_int, i32]
+    lib.specdec_beam_select.restype = ctypes.c_int
+    lib.specdec_beam_select.argtypes = [vp, ctypes.c_int, i32, i32, i32, i64, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
     _lib = lib
     return lib
 
@@ -504,3 +522,178 @@ def paged_attention(q, cache, block_table, cached_len, cu_num_draft, B: int, max
                                         _stream(stream, current))
     if rc != SPECDEC_OK:
         raise SpecdecError(rc, "specdec_paged_attention")
+
+
+def kv_fork(cache, block_table, lengths, parent, fresh, out_table, out_lengths=None, status=None, stream=None) -> None:
+    """Queue specdec_kv_fork: row i of out_table [n, max_blocks] and out_lengths [n] go on from row parent[i] of block_table
+    and lengths (-1: an empty row), with the begun page copied to page fresh[i] (-1, or fresh None: shared). out_table None:
+    the tokens alone, for the further caches of one table."""
+    torch = _lazy_torch()
+    i32 = torch.int32
+    device = parent.get_device()
+    n = parent.shape[0] if parent.dim() == 1 else -1
+    current = torch._C._cuda_getDevice() if device >= 0 else -2
+    sources = lengths.shape[0] if lengths.dim() == 1 else -1
+    table, max_blocks, block_stride = _table(block_table, max(sources, 0), current)
+    to, out_stride = None, max_blocks
+    if out_table is not None:
+        to, width, out_stride = _table(out_table, max(n, 0), current)
+        if width != max_blocks:
+            raise ValueError(f"out_table has {width} pages a row, block_table {max_blocks}")
+    rc = load().specdec_kv_fork(ctypes.byref(_cache_of(cache, current)), table, max_blocks, block_stride,
+                                _ints("lengths", lengths, i32, sources, current), sources, _ints("parent", parent, i32, n, current),
+                                _ints("fresh", fresh, i32, n, current), n, to, out_stride,
+                                _ints("out_lengths", out_lengths, i32, n, current), _status(status, n, current), _stream(stream, current))
+    if rc != SPECDEC_OK:
+        raise SpecdecError(rc, "specdec_kv_fork")
+
+
+# ------------------------------------------------------------------ rows of logits beside the verify
+
+
+def _row_stride(name: str, t) -> int:
+    """Row stride of t [rows, V] with the elements of a row contiguous."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be [rows, V] with the elements of a row contiguous")
+    return stride[0] if shape[0] > 1 else shape[1]
+
+
+def _rows_of(logits):
+    """(rows, V, row stride)"""
+    stride = _row_stride("logits", logits)
+    rows, V = logits.shape
+    if rows > 0x7fffffff or V > 0x7fffffff:
+        raise ValueError(f"logits of shape {tuple(logits.shape)}: a size is beyond 32 bits")
+    return rows, V, stride
+
+
+def _matrix(name: str, t, dtype, shape, device: int):
+    """Address of a contiguous tensor of that type and shape (None: none)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    return _at(name, t, device)
+
+
+def _workspace(t, device: int):
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return _at("workspace", t, device), t.numel() * t.element_size()
+
+
+def _number_of(dtype) -> int:
+    _lazy_torch()
+    n = _FLOATS.get(dtype)
+    if n is None:
+        raise SpecdecError(SPECDEC_ERR_UNSUPPORTED, f"dtype {dtype}")
+    return n
+
+
+def top_logits_workspace_size(rows: int, V: int, dtype) -> int:
+    """Bytes of workspace for logits of that torch type."""
+    return int(load().specdec_top_logits_workspace_size(_int32("rows", rows), _int32("V", V), _number_of(dtype)))
+
+
+def top_logits(logits, out_ids, out_logprobs, workspace, bitmask=None, temperature: float = 1.0, lse=None, status=None,
+               stream=None) -> None:
+    """Queue specdec_top_logits: the n best ids of every row of logits [rows, V], into out_ids int32 and out_logprobs float32
+    [rows, n]. workspace: a CUDA tensor of at least top_logits_workspace_size(...) bytes."""
+    torch = _lazy_torch()
+    device = logits.get_device()
+    rows, V, stride = _rows_of(logits)
+    current = torch._C._cuda_getDevice() if device >= 0 else -2
+    n = out_ids.shape[1] if out_ids.dim() == 2 else -1
+    space, size = _workspace(workspace, current)
+    rc = load().specdec_top_logits(_at("logits", logits, current), _dtype_of(logits), rows, V, stride,
+                                   _matrix("bitmask", bitmask, torch.int32, (rows, (V + 31) // 32), current), temperature, n,
+                                   _matrix("out_ids", out_ids, torch.int32, (rows, n), current),
+                                   _matrix("out_logprobs", out_logprobs, torch.float32, (rows, n), current),
+                                   _matrix("lse", lse, torch.float32, (rows,), current), _status(status, rows, current), space, size,
+                                   _stream(stream, current))
+    if rc != SPECDEC_OK:
+        raise SpecdecError(rc, "specdec_top_logits")
+
+
+def distill(logits, top_ids, top_logprobs, loss, weight=None, temperature: float = 1.0, rest: bool = True, stats=None, grad=None,
+            status=None, stream=None) -> None:
+    """Queue specdec_distill: the loss [rows] of the drafter's logits [rows, V] against top_ids and top_logprobs [rows, n]
+    (top_logits' outputs on the target's rows), with the gradient into grad [rows, V] (which may be logits) where it is given,
+    and stats [rows, 2] for distill_backward. rest: whether the mass that the list leaves is a category."""
+    torch = _lazy_torch()
+    device = logits.get_device()
+    rows, V, stride = _rows_of(logits)
+    current = torch._C._cuda_getDevice() if device >= 0 else -2
+    n = top_ids.shape[1] if top_ids.dim() == 2 else -1
+    to, to_stride = _gradient(logits, grad, current)
+    rc = load().specdec_distill(_at("logits", logits, current), _dtype_of(logits), rows, V, stride,
+                                _matrix("top_ids", top_ids, torch.int32, (rows, n), current),
+                                _matrix("top_logprobs", top_logprobs, torch.float32, (rows, n), current), n, temperature,
+                                1 if rest else 0, _matrix("weight", weight, torch.float32, (rows,), current),
+                                _matrix("loss", loss, torch.float32, (rows,), current),
+                                _matrix("stats", stats, torch.float32, (rows, 2), current), to, to_stride,
+                                _status(status, rows, current), _stream(stream, current))
+    if rc != SPECDEC_OK:
+        raise SpecdecError(rc, "specdec_distill")
+
+
+def _gradient(logits, grad, device: int):
+    if grad is None:
+        return None, 0
+    if grad.shape != logits.shape or grad.dtype is not logits.dtype:
+        raise ValueError(f"grad has shape {tuple(grad.shape)} {grad.dtype}, {tuple(logits.shape)} {logits.dtype} is needed")
+    return _at("grad", grad, device), _row_stride("grad", grad)
+
+
+def distill_backward(logits, top_ids, top_logprobs, stats, grad_loss, grad, temperature: float = 1.0, rest: bool = True, status=None,
+                     stream=None) -> None:
+    """Queue specdec_distill_backward: the gradient of distill's loss alone, times grad_loss [rows] (None: 1), from its stats."""
+    torch = _lazy_torch()
+    device = logits.get_device()
+    rows, V, stride = _rows_of(logits)
+    current = torch._C._cuda_getDevice() if device >= 0 else -2
+    n = top_ids.shape[1] if top_ids.dim() == 2 else -1
+    to, to_stride = _gradient(logits, grad, current)
+    rc = load().specdec_distill_backward(_at("logits", logits, current), _dtype_of(logits), rows, V, stride,
+                                         _matrix("top_ids", top_ids, torch.int32, (rows, n), current),
+                                         _matrix("top_logprobs", top_logprobs, torch.float32, (rows, n), current), n, temperature,
+                                         1 if rest else 0, _matrix("stats", stats, torch.float32, (rows, 2), current),
+                                         _matrix("grad_loss", grad_loss, torch.float32, (rows,), current), to, to_stride,
+                                         _status(status, rows, current), _stream(stream, current))
+    if rc != SPECDEC_OK:
+        raise SpecdecError(rc, "specdec_distill_backward")
+
+
+def beam_select_workspace_size(B: int, beams: int, V: int, dtype, n: int) -> int:
+    """Bytes of workspace for logits of that torch type."""
+    return int(load().specdec_beam_select_workspace_size(_int32("B", B), _int32("beams", beams), _int32("V", V), _number_of(dtype),
+                                                         _int32("n", n)))
+
+
+def beam_select(logits, scores, out_rows, out_tokens, out_scores, workspace, bitmask=None, finished=None, end_token: int = -1,
+                out_finished=None, status=None, stream=None) -> None:
+    """Queue specdec_beam_select: the n best continuations (out_rows, out_tokens, out_scores [B, n]) of the beams of every
+    request: logits [B * beams, V], scores [B, beams]. workspace: a CUDA tensor of at least
+    beam_select_workspace_size(...) bytes."""
+    torch = _lazy_torch()
+    device = logits.get_device()
+    rows, V, stride = _rows_of(logits)
+    if scores.dim() != 2 or out_rows.dim() != 2:
+        raise ValueError("scores must be [B, beams], out_rows [B, n]")
+    (B, beams), n = scores.shape, out_rows.shape[1]
+    if rows != B * beams:
+        raise ValueError(f"{rows} rows of logits for {B} requests of {beams} beams")
+    current = torch._C._cuda_getDevice() if device >= 0 else -2
+    space, size = _workspace(workspace, current)
+    rc = load().specdec_beam_select(_at("logits", logits, current), _dtype_of(logits), B, beams, V, stride,
+                                    _matrix("bitmask", bitmask, torch.int32, (rows, (V + 31) // 32), current),
+                                    _matrix("scores", scores, torch.float32, (B, beams), current),
+                                    _matrix("finished", finished, torch.uint8, (B, beams), current), _int32("end_token", end_token), n,
+                                    _matrix("out_rows", out_rows, torch.int32, (B, n), current),
+                                    _matrix("out_tokens", out_tokens, torch.int32, (B, n), current),
+                                    _matrix("out_scores", out_scores, torch.float32, (B, n), current),
+                                    _matrix("out_finished", out_finished, torch.uint8, (B, n), current), _status(status, B, current),
+                                    space, size, _stream(stream, current))
+    if rc != SPECDEC_OK:
+        raise SpecdecError(rc, "specdec_beam_select")

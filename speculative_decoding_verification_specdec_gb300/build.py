@@ -10,8 +10,9 @@ import tempfile
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", f) for f in ("specdec_verify.cu", "specdec_ngram.cu", "specdec_bitmask.cu",
-                                                  "specdec_rope.cu", "specdec_kvcache.cu", "specdec_attention.cu")]
-HEADERS = [os.path.join(PKG, "csrc", f) for f in ("specdec_rows.cuh", "specdec_tensor.cuh")] + [os.path.join(ROOT, "include", "specdec.h")]
+                                                  "specdec_rope.cu", "specdec_kvcache.cu", "specdec_attention.cu",
+                                                  "specdec_top.cu", "specdec_distill.cu")]
+HEADERS = [os.path.join(PKG, "csrc", f) for f in ("specdec_rows.cuh", "specdec_tensor.cuh", "specdec_logits.cuh")] + [os.path.join(ROOT, "include", "specdec.h")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libspecdec.so")
 

@@ -1,7 +1,7 @@
 /*
  * specdec_kvcache.cu -- the paged key-value cache for GB300 (sm_103a): rows of a step written into
- * their pages (keys rotated, heads quantised on the way) and tokens read back; C-ABI entry points
- * in include/specdec.h.
+ * their pages (keys rotated, heads quantised on the way), tokens read back, and requests forked; C-ABI entry
+ * points in include/specdec.h.
  *
  * Quantisation: an e4m3 head (one token, one head) carries the power of two 2^e with
  * max |x| in (224, 448] 2^e. Scaling by a power of two is exact, so the only rounding is the one to
@@ -386,6 +386,89 @@ template <typename C> specdec_status_t launch_read_to(const ReadArgs& a, specdec
     return launch_read<C, __half>(a, stream);
 }
 
+struct ForkArgs {
+    specdec_kv_cache_t cache;
+    const int32_t* block_table;
+    int64_t block_stride;
+    int32_t max_blocks, sources;
+    const int32_t *lengths, *parent, *fresh;
+    int32_t* out_table;
+    int64_t out_stride;
+    int32_t* out_lengths;
+    uint32_t* status;
+};
+
+constexpr int kForkBytes = 32 * 1024;              // a CTA's share of a page: 8 units of 16 bytes a thread
+
+// A CTA row i of the new tables and, as far as its share goes, the tokens of the page that the parent has begun:
+// blockIdx.y numbers the shares (units of 16 bytes; K and V, head by head, slot by slot).
+__global__ void __launch_bounds__(kThreads) specdec_kv_fork_kernel(const ForkArgs a)
+{
+    after_predecessor();
+    const specdec_kv_cache_t& c = a.cache;
+    const int tid = threadIdx.x;
+    const int64_t i = blockIdx.x;
+    const int32_t parent = __ldg(a.parent + i);
+    uint32_t fault = parent < -1 || parent >= a.sources ? SPECDEC_ST_BAD_OFFSETS : 0u;
+    int32_t length = 0;
+    if (parent >= 0 && !fault) {
+        length = __ldg(a.lengths + parent);
+        if (length < 0 || !fits(c, Table{a.block_table, a.block_stride, a.max_blocks}, length)) {
+            fault = SPECDEC_ST_BAD_LENGTH;
+            length = 0;
+        }
+    }
+    const bool there = parent >= 0 && !fault;
+    const int32_t full = length / c.page_size, begun = length % c.page_size;
+    const int32_t* const from = a.block_table + (there ? parent : 0) * a.block_stride;
+    // the page that the next token goes to: `fresh`, or where the row names none the parent's own
+    const int32_t fresh = there && a.fresh ? __ldg(a.fresh + i) : -1;
+    const int32_t old = begun ? __ldg(from + full) : -1;
+    int32_t next = old;
+    if (fresh >= 0 && full < a.max_blocks) {
+        if (fresh >= c.num_pages || (begun && (old < 0 || old >= c.num_pages))) fault |= SPECDEC_ST_BAD_PAGE;
+        else next = fresh;
+    }
+    if (blockIdx.y == 0) {
+        if (a.out_table)
+            for (int32_t k = tid; k < a.max_blocks; k += kThreads)
+                a.out_table[i * a.out_stride + k] = k < full ? __ldg(from + k) : k == full && there ? next : -1;
+        if (tid == 0) {
+            if (a.out_lengths) a.out_lengths[i] = length;
+            if (a.status && fault) atomicOr(a.status + i, fault);
+        }
+    }
+    if (!begun || next == old) return;
+    const int es = c.dtype == SPECDEC_E4M3 ? 1 : 2, slot_units = c.head_dim * es / 16, H = c.num_kv_heads;
+    const int total = 2 * H * begun * slot_units;
+    const int share = kForkBytes / 16, first = blockIdx.y * share, last = min(first + share, total);
+    const Place step(kThreads, begun, slot_units);
+    Place at(first + tid, begun, slot_units);                        // r: head of K, then of V; h: slot; u: unit
+    for (int base = first + tid; base < last; base += kReadBatch * kThreads) {
+        uint4 x[kReadBatch];
+        uint4* to[kReadBatch];
+#pragma unroll
+        for (int q = 0; q < kReadBatch; ++q, at.move(step, begun, slot_units)) {
+            to[q] = nullptr;
+            if (base + q * kThreads >= last) continue;
+            const int is_v = at.r >= H, h = at.r - is_v * H;
+            char* const pool = static_cast<char*>(is_v ? c.v : c.k);
+            const int64_t within = h * c.head_stride + at.h * c.slot_stride;
+            x[q] = *reinterpret_cast<const uint4*>(pool + (old * c.page_stride + within) * es + at.u * 16);
+            to[q] = reinterpret_cast<uint4*>(pool + (next * c.page_stride + within) * es + at.u * 16);
+        }
+#pragma unroll
+        for (int q = 0; q < kReadBatch; ++q)
+            if (to[q]) *to[q] = x[q];
+    }
+    if (c.dtype == SPECDEC_E4M3 && blockIdx.y == 0)
+        for (int k = tid; k < 2 * H * begun; k += kThreads) {
+            const int head = k / begun, slot = k - head * begun, is_v = head >= H, h = head - is_v * H;
+            uint8_t* const pool = is_v ? c.v_exp : c.k_exp;
+            pool[((int64_t)next * H + h) * c.page_size + slot] = pool[((int64_t)old * H + h) * c.page_size + slot];
+        }
+}
+
 }  // namespace
 
 extern "C" specdec_status_t specdec_kv_write(const void* k, const void* v, specdec_dtype_t dtype, int32_t rows,
@@ -436,4 +519,26 @@ extern "C" specdec_status_t specdec_kv_read(const specdec_kv_cache_t* cache, con
     if (cache->dtype == SPECDEC_BF16) return launch_read_to<__nv_bfloat16>(a, out_dtype, (cudaStream_t)stream);
     if (cache->dtype == SPECDEC_F16) return launch_read_to<__half>(a, out_dtype, (cudaStream_t)stream);
     return launch_read_to<__nv_fp8_e4m3>(a, out_dtype, (cudaStream_t)stream);
+}
+
+extern "C" specdec_status_t specdec_kv_fork(const specdec_kv_cache_t* cache, const int32_t* block_table, int32_t max_blocks,
+                                            int64_t block_stride, const int32_t* lengths, int32_t sources, const int32_t* parent,
+                                            const int32_t* fresh, int32_t n, int32_t* out_table, int64_t out_stride,
+                                            int32_t* out_lengths, uint32_t* status, void* stream)
+{
+    const specdec_status_t rc = check_cache(cache);
+    if (rc != SPECDEC_OK) return rc;
+    if (n < 0 || sources < 0 || max_blocks < 0 || block_stride < 0 || out_stride < 0 || (n > 1 && out_stride < max_blocks))
+        return SPECDEC_ERR_INVALID_ARG;
+    if (n == 0) return SPECDEC_OK;
+    if (!block_table || !lengths || !parent || (!out_table && !fresh)) return SPECDEC_ERR_INVALID_ARG;
+    if (!aligned_to(block_table, 4) || !aligned_to(lengths, 4) || !aligned_to(parent, 4) || !aligned_to(fresh, 4) ||
+        !aligned_to(out_table, 4) || !aligned_to(out_lengths, 4) || !aligned_to(status, 4))
+        return SPECDEC_ERR_INVALID_ARG;
+    const int64_t page_bytes = (int64_t)2 * cache->num_kv_heads * (cache->page_size - 1) * cache->head_dim * (int64_t)elem_bytes(cache->dtype);
+    const int64_t shares = fresh ? (page_bytes + kForkBytes - 1) / kForkBytes : 1;
+    if (shares > 65535) return SPECDEC_ERR_UNSUPPORTED;
+    const ForkArgs a = {*cache, block_table, block_stride, max_blocks, sources, lengths, parent, fresh, out_table, out_stride, out_lengths, status};
+    const cudaError_t e = launch_dependent(specdec_kv_fork_kernel, dim3((unsigned)n, (unsigned)shares), kThreads, 0, (cudaStream_t)stream, a);
+    return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }

@@ -59,11 +59,10 @@ def distill(z, ids, logprobs, temperature=1.0, rest=True, weight=1.0):
     outside = np.ones(V, dtype=bool)
     outside[ids] = False
     every, others = log_sum(z), log_sum(z[outside])
+    if not rest and lps.size and lps.max() > -np.inf:
+        lps = lps - log_sum(lps)
     t = np.exp(lps)
     r = max(0.0, 1.0 - t.sum()) if rest else 0.0
-    if not rest and t.sum() > 0:
-        lps = lps - math.log(t.sum())
-        t = t / t.sum()
     asks = t.sum() + r > 0
     if others == -np.inf:
         r = 0.0

@@ -15,6 +15,7 @@
  * A row is held by a cluster of CTAs, a slice each, in shared memory: it is read from HBM once, for the sums and for the gradient.
  */
 #include <atomic>
+#include <cmath>
 
 #include "specdec_logits.cuh"
 
@@ -34,8 +35,8 @@ struct Args {
     const int32_t* ids;                            // [rows, n]
     const float* logprobs;                         // [rows, n]
     int32_t n;
-    float scale, scale_low;                        // log2(e) / temperature as a sum of two
-    double inverse;                                // 1 / temperature
+    float scale, scale_low;                        // log2(e) / temperature as a sum of two positive numbers
+    float inverse;                                 // 1 / temperature
     int32_t rest;                                  // 1: what the list leaves is a category; 0: the list is renormalised
     const float* weight;                           // [rows] (backward: the loss's gradient) or nullptr
     float* loss;
@@ -48,17 +49,23 @@ struct Args {
 
 constexpr double kLn2 = 0.69314718055994530941723;
 
-// NaN stays; -infinity becomes the lowest number, so that its product with the scale's small part is no NaN.
-__device__ __forceinline__ float not_below_lowest(float x)
-{
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-3.402823466e38f));
-    return y;
-}
+// z log2(e) / temperature - ref: scale and scale_low are both positive, so that -infinity stays what it is.
 __device__ __forceinline__ float exponent(float z, const Args& a, float ref)
 {
     return fmaf(z, a.scale_low, fmaf(z, a.scale, -ref));
 }
+// 2 to that, two at a time; kLow: with scale_low.
+template <bool kLow> struct Exponentials {
+    Pair c, low, less;
+    __device__ __forceinline__ Exponentials(const Args& a, float ref)
+        : c(pair_of(a.scale, a.scale)), low(pair_of(a.scale_low, a.scale_low)), less(pair_of(-ref, -ref))
+    {
+    }
+    __device__ __forceinline__ Pair operator()(Pair z) const
+    {
+        return exp2_2(kLow ? fma_2(z, low, fma_2(z, c, less)) : fma_2(z, c, less));
+    }
+};
 
 // Thread i's entry of the list: id, -1 where there is none or it does not count.
 struct Entry {
@@ -89,59 +96,92 @@ __device__ __forceinline__ Entry read_entry(const Args& a, int64_t r, int32_t* i
     return e;
 }
 
-// Sums over the CTA of a double a thread; every thread gets it. Two barriers.
-__device__ __forceinline__ double sum_64(double x, double* part, int threads)
+template <typename F> __device__ __forceinline__ F warp_sum(F x)
 {
-    const int warps = (threads + 31) / 32, warp = threadIdx.x >> 5;
-    if (warp < warps) {
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if ((threadIdx.x & 31) == 0) part[warp] = x;
-    }
-    __syncthreads();
-    double sum = 0.0;
-    for (int w = 0; w < warps; ++w) sum += part[w];
-    __syncthreads();
-    return sum;
+    for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
 }
-
-struct Targets {
-    double r, mass;                                // what is left to the rest; the sum of all
-    double t;                                      // this thread's
-    double log_t;                                  // and its logarithm
-};
-
-__device__ __forceinline__ Targets targets_of(const Args& a, const Entry& e, double* part)
+__device__ __forceinline__ float warp_max(float x)
 {
-    Targets t;
-    t.log_t = (double)e.lp;
-    t.t = e.id >= 0 ? exp((double)e.lp) : 0.0;
-    const double sum = sum_64(t.t, part, a.n);
-    t.r = 0.0;
-    t.mass = sum;
-    if (a.rest) {
-        t.r = fmax(0.0, 1.0 - sum);
-        t.mass = sum + t.r;
-    } else if (sum > 0.0) {
-        t.t /= sum;
-        t.log_t -= log(sum);
-        t.mass = 1.0;
-    }
-    return t;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
 }
+
+constexpr int kListWarps = SPECDEC_TOP_MAX / 32;   // the warps that hold entries
+
+// 2^y to 2^-43 relative in some fifteen 64-bit operations (this part has few of them): y = k + f with k whole, v = f ln 2 / 8,
+// exp(v) by its series (|v| < 0.044: from the fourth power on in fp32, whose 2^-24 is 2^-46 of the sum), squared three times.
+__device__ __forceinline__ double exp2_64(double y)
+{
+    if (!(y > -1000.0)) return y != y ? y : 0.0;
+    const double shifted = y + 0x1.8p52, k = shifted - 0x1.8p52;
+    const double v = (y - k) * (kLn2 / 8.0), square = v * v;
+    const float x = (float)v;
+    const float series = fmaf(fmaf(fmaf(x, 1.f / 5040.f, 1.f / 720.f), x, 1.f / 120.f), x, 1.f / 24.f);
+    double e = fma(fma(square, (double)series, fma(v, 1.0 / 6.0, 0.5)), square, v) + 1.0;
+    e *= e;
+    e *= e;
+    e *= e;
+    return e * __hiloint2double((1023 + (int)fmin(k, 1023.0)) << 20, 0);
+}
+
+// What the list asks for. A target is exp(lp - shift) * norm; where the list is renormalised, shift is its largest log-probability,
+// so that a list of small ones keeps its shares.
+struct Asked {
+    float shift, norm, listed, rest;               // listed, rest: the masses of the targets and of what is left
+};
+struct ListPart {
+    double sum;                                    // in 64 bits: the rest is what it leaves of one
+    float shift;
+};
+constexpr double kLog2e = 1.4426950408889634073599;
+__device__ __forceinline__ double target_64(const Entry& e, float shift) { return e.id >= 0 ? exp2_64(((double)e.lp - (double)shift) * kLog2e) : 0.0; }
+__device__ __forceinline__ ListPart list_part(const Entry& e, int has_rest)       // a warp's
+{
+    float shift = 0.f;
+    if (!has_rest) {
+        shift = warp_max(e.id >= 0 ? e.lp : -INFINITY);
+        if (shift == -INFINITY) shift = 0.f;
+    }
+    return ListPart{warp_sum(target_64(e, shift)), shift};
+}
+__device__ __forceinline__ Asked asked_of(const ListPart* parts, int n, int has_rest)
+{
+    Asked a = {0.f, 1.f, 0.f, 0.f};
+    const int warps = (n + 31) / 32;
+    if (has_rest) {
+        double sum = 0.0;
+        for (int i = 0; i < warps; ++i) sum += parts[i].sum;
+        a.listed = (float)sum;
+        a.rest = (float)fmax(0.0, 1.0 - sum);
+        return a;
+    }
+    float shift = -INFINITY, sum = 0.f;
+    for (int i = 0; i < warps; ++i)
+        if (parts[i].sum > 0.0) shift = fmaxf(shift, parts[i].shift);
+    for (int i = 0; i < warps; ++i)
+        if (parts[i].sum > 0.0) sum += (float)parts[i].sum * expf(parts[i].shift - shift);
+    if (sum > 0.f) {
+        a.shift = shift;
+        a.norm = 1.f / sum;
+        a.listed = 1.f;
+    }
+    return a;
+}
+__device__ __forceinline__ float target_of(const Entry& e, const Asked& a) { return expf(e.lp - a.shift) * a.norm; }
 
 // Store of a vector's elements, those inside the row.
-template <typename T> __device__ __forceinline__ void store_vector(const Row<T>& row, T* to, bool aligned, int32_t v, const float* x)
+template <typename T> __device__ __forceinline__ void store_vector(const Row<T>& row, T* to, bool aligned, int32_t v, const Raw<T, kPer<T>>& x)
 {
     const int32_t at = row.first(v);
-    Raw<T, kPer<T>> y;
-    y.from(x);
     if (aligned && row.whole(at)) {
-        *reinterpret_cast<uint4*>(to + at) = *reinterpret_cast<const uint4*>(y.e);
+        *reinterpret_cast<uint4*>(to + at) = *reinterpret_cast<const uint4*>(x.e);
     } else {
 #pragma unroll
         for (int i = 0; i < kPer<T>; ++i)
-            if (at + i >= 0 && at + i < row.V) to[at + i] = y.e[i];
+            if (at + i >= 0 && at + i < row.V) to[at + i] = x.e[i];
     }
 }
 
@@ -159,6 +199,7 @@ __device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
     return a;
 }
+__device__ __forceinline__ void put_32(uint32_t to, float x) { asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(x) : "memory"); }
 __device__ __forceinline__ void put_64(uint32_t to, double x) { asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(x) : "memory"); }
 __device__ __forceinline__ void cluster_barrier()
 {
@@ -167,15 +208,17 @@ __device__ __forceinline__ void cluster_barrier()
 }
 
 struct Shared {
-    double part[kWarps];
-    double peer_S[kMaxCluster], peer_ref[kMaxCluster];
-    double inverse_all, each;                      // M over the sum of all at all_ref; weight / temperature
+    double peer_S[kMaxCluster];
+    float peer_ref[kMaxCluster];
     float refs[kWarps], sums[kWarps];
-    float factor, all_ref;
+    float top_ref[kListWarps], top_sum[kListWarps];
+    ListPart list[kListWarps];
+    Asked asked;
+    double list_64[kListWarps][3];
     int32_t ids[SPECDEC_TOP_MAX];
 };
 
-template <typename T, bool kGrad> __global__ void __launch_bounds__(kThreads) specdec_distill_kernel(const Args a)
+template <typename T, bool kGrad> __global__ void __launch_bounds__(kThreads, 4) specdec_distill_kernel(const Args a)
 {
     extern __shared__ __align__(16) unsigned char held[];
     __shared__ Shared s;
@@ -191,7 +234,7 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__(kThreads) sp
     const bool aligned = kGrad && same_grid(z, g);
     if (w == 0.f) {
         if (kGrad) {
-            const float zero[kPer<T>] = {};
+            const Raw<T, kPer<T>> zero = {};
             for (int32_t v = v0 + tid; v < v1; v += kThreads) store_vector(row, g, aligned, v, zero);
         }
         if (rank == 0 && tid == 0) {
@@ -220,22 +263,18 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__(kThreads) sp
     // the list: targets, and the student's logits there, which every CTA of the cluster reads before any of them writes
     const Entry e = read_entry(a, r, s.ids);
     float top = e.id >= 0 ? to_float<T>(z[e.id]) : -INFINITY;
-    float top_ref = ceilf(top * a.scale);
-    if (top_ref == -INFINITY) top = -INFINITY;                        // (the lowest numbers, where masks put them)
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top_ref = fmaxf(top_ref, __shfl_xor_sync(0xffffffffu, top_ref, o));
-    if (lane == 0) s.refs[warp] = top_ref;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) top_ref = fmaxf(top_ref, s.refs[i]);
-    // Every CTA takes the targets and the listed exponentials in 64 bits: a loss near zero is a small difference of their logarithms.
-    const Targets t = targets_of(a, e, s.part);
-    const double scale = (double)a.scale + (double)a.scale_low;
-    const double up = top == -INFINITY ? -INFINITY : (double)top * scale - (double)top_ref;
-    const double S_top = sum_64(exp2(up), s.part, a.n);
-    double cross = 0.0;                            // sum of t_i (ln t_i - (z_i / temperature - top_ref ln 2))
-    if (rank == 0) cross = sum_64(t.t > 0.0 ? t.t * (t.log_t - up * kLn2) : 0.0, s.part, a.n);
-    const bool any = t.mass > 0.0;                 // (an empty list that leaves nothing asks for nothing)
+    if (warp < kListWarps) {
+        float ref = ceilf(top * a.scale);
+        if (ref == -INFINITY) top = -INFINITY;                        // (the lowest numbers, where masks put them)
+        ref = warp_max(ref);
+        const float sum = warp_sum(top == -INFINITY ? 0.f : exp2_fast(exponent(top, a, ref)));
+        const ListPart part = list_part(e, a.rest);
+        if (lane == 0) {
+            s.top_ref[warp] = ref;
+            s.top_sum[warp] = sum;
+            s.list[warp] = part;
+        }
+    }
 
     // the sums over this CTA's part of the row without the listed
     float ref = -INFINITY, S = 0.f;
@@ -254,17 +293,15 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__(kThreads) sp
             const Raw<T, kPer<T>> x = mine[v];
             const float m = vector_max(x);
             if (m * a.scale > ref) {
-                const float up_ref = ceilf(m * a.scale);
-                S *= reference_step(ref, up_ref);
-                ref = up_ref;
+                const float up = ceilf(m * a.scale);
+                S *= reference_step(ref, up);
+                ref = up;
             }
-            float f[kPer<T>];
-            x.to(f);
-            const float base = ref == -INFINITY ? 0.f : ref;
-            float part = 0.f;
+            const Exponentials<true> e2(a, ref == -INFINITY ? 0.f : ref);
+            Pair part = e2(elements(x, 0));
 #pragma unroll
-            for (int i = 0; i < kPer<T>; ++i) part += exp2_fast(exponent(not_below_lowest(f[i]), a, base));
-            S += part;
+            for (int i = 1; i < kPer<T> / 2; ++i) part = add_2(part, e2(elements(x, i)));
+            S += both(part).x + both(part).y;
         }
     }
     warp_join(ref, S);
@@ -274,92 +311,128 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__(kThreads) sp
     }
     __syncthreads();
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-    if (tid < (int)size) {
-        // every CTA gets every CTA's sum: thread i writes into CTA i
-        float top_all = -INFINITY;
+    if (warp == 0) {
+        const Asked asked = asked_of(s.list, a.n, a.rest);
+        if (lane == 0) s.asked = asked;
+        // every CTA gets every CTA's sum: lane i writes into CTA i
+        const float one = s.refs[lane % kWarps], all = warp_max(one);
+        double sum = (double)s.sums[lane % kWarps] * reference_step_64(one, all);
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) top_all = fmaxf(top_all, s.refs[i]);
-        double sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) sum += (double)s.sums[i] * reference_step_64(s.refs[i], top_all);
-        put_64(in_cta(&s.peer_S[rank], tid), sum);
-        put_64(in_cta(&s.peer_ref[rank], tid), (double)top_all);
+        for (int o = kWarps / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane < (int)size) {
+            put_64(in_cta(&s.peer_S[rank], lane), sum);
+            put_32(in_cta(&s.peer_ref[rank], lane), all);
+        }
     }
     cluster_barrier();
 
-    float rest_ref = -INFINITY;
-    for (uint32_t i = 0; i < size; ++i) rest_ref = fmaxf(rest_ref, (float)s.peer_ref[i]);
-    if (tid == 0) {
-        double S_rest = 0.0;
-        for (uint32_t i = 0; i < size; ++i) S_rest += s.peer_S[i] * reference_step_64((float)s.peer_ref[i], rest_ref);
-        const float all_ref = fmaxf(rest_ref, top_ref);
-        const double S_all = S_rest * reference_step_64(rest_ref, all_ref) + S_top * reference_step_64(top_ref, all_ref);
-        // Where the student leaves nothing to the rest there is no such category.
-        const bool tail = S_rest > 0.0 || S_rest != S_rest;
-        const double left = tail ? t.r : 0.0, mass = tail ? t.mass : t.mass - t.r;
-        const bool none = !(S_all > 0.0) && S_all == S_all;           // no finite logit
-        const bool still = none || !any;                              // no gradient
-        s.each = still ? 0.0 : (double)w * a.inverse;
-        s.inverse_all = none ? 0.0 : mass / S_all;
-        s.all_ref = none ? 0.f : all_ref;
-        s.factor = still ? 0.f : (float)((s.inverse_all * reference_step_64(rest_ref, all_ref) - (tail ? left / S_rest : 0.0)) * s.each);
-        if (rank == 0) {
-            const double log_all = log(S_all) + (double)all_ref * kLn2, log_rest = log(S_rest) + (double)rest_ref * kLn2;
-            double loss = 0.0;
-            if (none) {
-                loss = any ? INFINITY : 0.0;
-            } else if (any) {
-                const double sum = t.mass - t.r;
-                loss = cross + (sum > 0.0 ? sum * (log_all - (double)top_ref * kLn2) : 0.0);
-                if (left > 0.0) loss += left * (log(left) - (log_rest - log_all));
-            }
-            a.loss[r] = (float)((double)w * loss);
-            if (a.stats) {
-                a.stats[2 * r] = (float)log_all;
-                a.stats[2 * r + 1] = (float)log_rest;
-            }
-        }
-    }
-    if (rank == 0 && a.status) {
-        const uint32_t empty = tid == 0 && !(fmaxf(rest_ref, top_ref) > -INFINITY) ? SPECDEC_ST_EMPTY_MASK_ROW : 0u;
-        if (e.fault | empty) atomicOr(a.status + r, e.fault | empty);
-    }
-    if constexpr (!kGrad) return;
-    __syncthreads();
-    const float factor = s.factor, base = rest_ref == -INFINITY ? 0.f : rest_ref;
-    for (int32_t from = v0; from < v1; from += a.tile) {
-        const int32_t to = min(from + a.tile, v1);
-        if (a.tile < a.slice) {
-            __syncthreads();
-            fetch(from, to);
-            async_copy_wait();
-            __syncthreads();
-        }
-        for (int32_t v = tid; v < to - from; v += kThreads) {
-            float f[kPer<T>];
-            mine[v].to(f);
+    float rest_ref = -INFINITY, top_ref = -INFINITY, S_rest = 0.f, S_top = 0.f;
+    for (uint32_t i = 0; i < size; ++i) rest_ref = fmaxf(rest_ref, s.peer_ref[i]);
+    for (uint32_t i = 0; i < size; ++i) S_rest += (float)s.peer_S[i] * reference_step(s.peer_ref[i], rest_ref);
 #pragma unroll
-            for (int i = 0; i < kPer<T>; ++i) f[i] = exp2_fast(exponent(not_below_lowest(f[i]), a, base)) * factor;
-            store_vector(row, g, aligned, from + v, f);
+    for (int i = 0; i < kListWarps; ++i) top_ref = fmaxf(top_ref, s.top_ref[i]);
+#pragma unroll
+    for (int i = 0; i < kListWarps; ++i) S_top += s.top_sum[i] * reference_step(s.top_ref[i], top_ref);
+    const Asked asked = s.asked;
+    const bool asks = asked.listed + asked.rest > 0.f;                // (an empty list that leaves nothing asks for nothing)
+    const float all_ref = fmaxf(rest_ref, top_ref);
+    const float S_rest_all = S_rest * reference_step(rest_ref, all_ref), S_top_all = S_top * reference_step(top_ref, all_ref);
+    const float S_all = S_rest_all + S_top_all;
+    const bool none = all_ref == -INFINITY && !(S_all != S_all);      // no finite logit
+    // Where the student leaves nothing to the rest there is no such category.
+    const bool tail = !(S_rest == 0.f);
+    const float left = tail ? asked.rest : 0.f;
+
+    if constexpr (kGrad) {
+        // outside the list: e_j (M / S - r / S_rest), which is (S_rest sum t - r S_top) / (S S_rest) without the cancellation of M and r
+        const float each = none || !asks ? 0.f : w * a.inverse, mass = asked.listed + left, per_all = none ? 0.f : mass / S_all;
+        const float base = rest_ref == -INFINITY ? 0.f : rest_ref;
+        const float factor = tail ? ((asked.listed * S_rest_all - left * S_top_all) / S_all) / S_rest * each : 0.f;
+        const Exponentials<sizeof(T) == 4> e2(a, base);
+        const Pair factors = pair_of(factor, factor);
+        for (int32_t from = v0; from < v1; from += a.tile) {
+            const int32_t to = min(from + a.tile, v1);
+            if (a.tile < a.slice) {
+                __syncthreads();
+                fetch(from, to);
+                async_copy_wait();
+                __syncthreads();
+            }
+            for (int32_t v = tid; v < to - from; v += kThreads) {
+                Raw<T, kPer<T>> x = mine[v];
+#pragma unroll
+                for (int i = 0; i < kPer<T> / 2; ++i) put_elements(x, i, mul_2(e2(elements(x, i)), factors));
+                store_vector(row, g, aligned, from + v, x);
+            }
+        }
+        __syncthreads();
+        if (e.id >= 0 && e.id >= row.first(v0) && e.id < row.first(v1)) {
+            const float share = top == -INFINITY ? 0.f : exp2_fast(exponent(top, a, all_ref)) * per_all;
+            g[e.id] = from_float<T>((share - target_of(e, asked)) * each);
+        }
+    }
+    if (rank != 0) return;
+
+    // The loss in 64 bits: near zero it is a small difference of logarithms.
+    if (a.status && (e.fault || (tid == 0 && none))) atomicOr(a.status + r, e.fault | (tid == 0 && none ? SPECDEC_ST_EMPTY_MASK_ROW : 0u));
+    if (warp < kListWarps) {
+        const double up = top == -INFINITY ? -INFINITY : (double)top * ((double)a.scale + (double)a.scale_low) - (double)top_ref;
+        const double t = target_64(e, asked.shift), sum = warp_sum(t), listed = warp_sum(exp2_64(up)), cross = warp_sum(t > 0.0 ? t * ((double)e.lp - up * kLn2) : 0.0);
+        if (lane == 0) {
+            s.list_64[warp][0] = sum;
+            s.list_64[warp][1] = listed;
+            s.list_64[warp][2] = cross;
         }
     }
     __syncthreads();
-    if (e.id >= 0 && e.id >= row.first(v0) && e.id < row.first(v1)) {
-        const double share = top == -INFINITY ? 0.0 : exp2((double)top * scale - (double)s.all_ref) * s.inverse_all;
-        g[e.id] = from_float<T>((float)((share - t.t) * s.each));
+    if (tid == 0) {
+        double sum = 0.0, listed = 0.0, cross = 0.0, others = 0.0;
+        for (int i = 0; i < kListWarps; ++i) {
+            sum += s.list_64[i][0];
+            listed += s.list_64[i][1];
+            cross += s.list_64[i][2];
+        }
+        for (uint32_t i = 0; i < size; ++i) others += s.peer_S[i] * reference_step_64(s.peer_ref[i], rest_ref);
+        const double log_all = log(others * reference_step_64(rest_ref, all_ref) + listed * reference_step_64(top_ref, all_ref)) + (double)all_ref * kLn2;
+        const double log_rest = log(others) + (double)rest_ref * kLn2;
+        double loss = 0.0;
+        if (none) {
+            loss = asks ? INFINITY : 0.0;
+        } else if (asks) {
+            const double r_64 = a.rest && tail ? fmax(0.0, 1.0 - sum) : 0.0;
+            if (sum > 0.0) {
+                // sum of t_i (ln t_i - ln s_i) where t_i = exp(lp_i), and where they are renormalised
+                loss = cross + sum * (log_all - (double)top_ref * kLn2);
+                if (!a.rest) loss = loss / sum - log(sum) - (double)asked.shift;
+            }
+            if (r_64 > 0.0) loss += r_64 * (log(r_64) - (log_rest - log_all));
+        }
+        a.loss[r] = (float)((double)w * loss);
+        if (a.stats) {
+            a.stats[2 * r] = (float)log_all;
+            a.stats[2 * r + 1] = (float)log_rest;
+        }
     }
 }
 
-// The gradient from the sums that a forward pass kept: element by element, a CTA a chunk of a row.
+// log2(e) x = whole - less, whole a whole number (x's, rounded up) and 0 <= less <= 1 without the product's rounding.
+__device__ __forceinline__ void in_octaves(float x, float* whole, float* less)
+{
+    constexpr float kHigh = 1.44269504f, kLow = (float)(1.4426950408889634073599 - (double)kHigh);
+    const float p = x * kHigh;
+    *whole = ceilf(p);
+    *less = (*whole - p) - fmaf(x, kHigh, -p) - x * kLow;
+}
+
+// The gradient from the sums that a forward pass kept: element by element, a CTA a chunk of a row. All in fp32: the sums come in fp32.
 constexpr int kChunk = 8;                          // vectors a thread
 
 template <typename T> __global__ void __launch_bounds__(kThreads) specdec_distill_backward_kernel(const Args a, const int32_t chunks)
 {
-    __shared__ double part[kWarps];
+    __shared__ ListPart parts[kListWarps];
     __shared__ int32_t ids[SPECDEC_TOP_MAX];
-    __shared__ float s_factor;
     after_predecessor();
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t r = blockIdx.x / (uint32_t)chunks;
     const int32_t v0 = (int32_t)(blockIdx.x - r * chunks) * (kChunk * kThreads);
     const T* const z = static_cast<const T*>(a.logits) + r * a.row_stride;
@@ -369,7 +442,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) specdec_distil
     const bool aligned = same_grid(z, g);
     const float w = a.weight ? a.weight[r] : 1.f;
     if (w == 0.f) {
-        const float zero[kPer<T>] = {};
+        const Raw<T, kPer<T>> zero = {};
 #pragma unroll
         for (int i = 0; i < kChunk; ++i)
             if (v0 + i * kThreads + tid < row.vectors) store_vector(row, g, aligned, v0 + i * kThreads + tid, zero);
@@ -386,37 +459,37 @@ template <typename T> __global__ void __launch_bounds__(kThreads) specdec_distil
             for (int k = 0; k < kPer<T>; ++k) x[i].e[k] = at + k >= 0 && at + k < a.V ? z[at + k] : neg_inf<T>();
         }
     }
+    const float lse = a.stats[2 * r], lse_rest = a.stats[2 * r + 1];
     const Entry e = read_entry(a, r, ids);
-    const Targets t = targets_of(a, e, part);
-    const double each = (double)w * a.inverse;
-    const double log_all = (double)a.stats[2 * r], log_rest = (double)a.stats[2 * r + 1];
-    // the exponentials of this kernel are taken at the rest's sum, or where there is none at that of all
-    const bool tail = !(log_rest == -INFINITY), none = log_all == -INFINITY || !(t.mass > 0.0);
-    const double left = tail ? t.r : 0.0, mass = tail ? t.mass : t.mass - t.r;
-    const float ref = (float)ceil((tail ? log_rest : none ? 0.0 : log_all) / kLn2);
-    if (tid == 0) {
-        const double rest = tail ? left * exp((double)ref * kLn2 - log_rest) : 0.0;
-        s_factor = none ? 0.f : (float)((mass * exp((double)ref * kLn2 - log_all) - rest) * each);
+    const bool here = e.id >= 0 && e.id >= row.first(v0) && e.id < row.first(min(v0 + kChunk * kThreads, row.vectors));
+    const float top = here ? to_float<T>(z[e.id]) : 0.f;              // (before the row is written: the gradient may lie over it)
+    if (warp < kListWarps) {
+        const ListPart part = list_part(e, a.rest);
+        if (lane == 0) parts[warp] = part;
     }
-    const int32_t at = e.id;
-    const bool here = at >= 0 && at >= row.first(v0) && at < row.first(min(v0 + kChunk * kThreads, row.vectors));
-    const float top = here ? to_float<T>(z[at]) : 0.f;                // (before the row is written: the gradient may lie over it)
     __syncthreads();
-    const float factor = s_factor;
+    const Asked asked = asked_of(parts, a.n, a.rest);
+    // the exponentials of this kernel are taken at the rest's sum; where there is none, no element is outside the list
+    const bool tail = !(lse_rest == -INFINITY), none = lse == -INFINITY || !(asked.listed + asked.rest > 0.f);
+    const float left = tail ? asked.rest : 0.f, each = none ? 0.f : w * a.inverse;
+    float all, all_less, ref, ref_less;
+    in_octaves(none ? 0.f : lse, &all, &all_less);
+    in_octaves(tail ? lse_rest : 0.f, &ref, &ref_less);
+    const float factor = tail ? ((asked.listed + left) * exp2f(ref - all + all_less) - left * exp2f(ref_less)) * each : 0.f;
+    const Exponentials<sizeof(T) == 4> e2(a, ref);
+    const Pair factors = pair_of(factor, factor);
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) {
         const int32_t v = v0 + i * kThreads + tid;
         if (v >= row.vectors) continue;
-        float f[kPer<T>];
-        x[i].to(f);
 #pragma unroll
-        for (int k = 0; k < kPer<T>; ++k) f[k] = exp2_fast(exponent(not_below_lowest(f[k]), a, ref)) * factor;
-        store_vector(row, g, aligned, v, f);
+        for (int k = 0; k < kPer<T> / 2; ++k) put_elements(x[i], k, mul_2(e2(elements(x[i], k)), factors));
+        store_vector(row, g, aligned, v, x[i]);
     }
     __syncthreads();
     if (here) {
-        const double share = top == -INFINITY ? 0.0 : mass * exp((double)top * ((double)a.scale + (double)a.scale_low) * kLn2 - log_all);
-        g[at] = from_float<T>(none ? 0.f : (float)((share - t.t) * each));
+        const float share = exp2f(exponent(top, a, all) + all_less) * (asked.listed + left);
+        g[e.id] = from_float<T>((share - target_of(e, asked)) * each);
     }
     if (v0 == 0 && a.status && e.fault) atomicOr(a.status + r, e.fault);
 }
@@ -510,8 +583,10 @@ Args args_of(const void* logits, int32_t rows, int32_t V, int64_t row_stride, co
              double temperature, int32_t rest, const float* weight, float* loss, float* stats, void* grad, int64_t grad_row_stride,
              uint32_t* status)
 {
+    // (the first rounded towards zero and the second at least a little above it: the kernels rely on their signs)
     const double c = scale_of(temperature);
-    return Args{logits, row_stride, V, rows, top_ids, top_logprobs, n, (float)c, (float)(c - (double)(float)c), 1.0 / temperature, rest,
+    const float high = std::nextafterf((float)c, 0.f), low = std::fmax((float)(c - (double)high), 1e-30f);
+    return Args{logits, row_stride, V, rows, top_ids, top_logprobs, n, high, low, (float)(1.0 / temperature), rest,
                 weight, loss, stats, grad, grad_row_stride, status, 0, 0};
 }
 

@@ -107,6 +107,73 @@ __device__ __forceinline__ double reference_step_64(float a, float b)
     return d == -1023 ? 0.0 : __hiloint2double((1023 + d) << 20, 0);
 }
 
+// Two fp32 numbers in a register pair: one instruction adds or multiplies both.
+typedef unsigned long long Pair;
+__device__ __forceinline__ Pair pair_of(float x, float y)
+{
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ float2 both(Pair p)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ Pair fma_2(Pair a, Pair b, Pair c)
+{
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ Pair add_2(Pair a, Pair b)
+{
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair mul_2(Pair a, Pair b)
+{
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair exp2_2(Pair a)
+{
+    const float2 f = both(a);
+    return pair_of(exp2_fast(f.x), exp2_fast(f.y));
+}
+
+// Elements 2 i and 2 i + 1 of a vector.
+__device__ __forceinline__ Pair elements(const Raw<float, 4>& x, int i) { return pair_of(x.e[2 * i], x.e[2 * i + 1]); }
+__device__ __forceinline__ Pair elements(const Raw<__nv_bfloat16, 8>& x, int i)
+{
+    const uint32_t w = reinterpret_cast<const uint32_t*>(x.e)[i];
+    return pair_of(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ Pair elements(const Raw<__half, 8>& x, int i)
+{
+    const float2 f = __half22float2(reinterpret_cast<const __half2*>(x.e)[i]);
+    return pair_of(f.x, f.y);
+}
+__device__ __forceinline__ void put_elements(Raw<float, 4>& x, int i, Pair p)
+{
+    const float2 f = both(p);
+    x.e[2 * i] = f.x;
+    x.e[2 * i + 1] = f.y;
+}
+__device__ __forceinline__ void put_elements(Raw<__nv_bfloat16, 8>& x, int i, Pair p)
+{
+    const float2 f = both(p);
+    reinterpret_cast<__nv_bfloat162*>(x.e)[i] = __floats2bfloat162_rn(f.x, f.y);
+}
+__device__ __forceinline__ void put_elements(Raw<__half, 8>& x, int i, Pair p)
+{
+    const float2 f = both(p);
+    reinterpret_cast<__half2*>(x.e)[i] = __floats2half2_rn(f.x, f.y);
+}
+
 // Joins the lanes' sums; every lane gets the warp's.
 __device__ __forceinline__ void warp_join(float& ref, float& S)
 {

@@ -80,15 +80,16 @@ template <typename T, bool kMasked> __global__ void __launch_bounds__(kThreads) 
     if (!(m > -INFINITY)) m = -INFINITY;           // (nothing but NaN)
     float ref = m == -INFINITY ? m : whole_reference(m, a.scale), S = 0.f;
     const float from = m == -INFINITY ? 0.f : ref;
+    const Pair c = pair_of(a.scale, a.scale), less = pair_of(-from, -from);
+    Pair sum = pair_of(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kLaneVectors; ++i) {
-        float f[kPer<T>];
-        x[i].to(f);
-        float part = 0.f;
+        Pair part = exp2_2(fma_2(elements(x[i], 0), c, less));
 #pragma unroll
-        for (int e = 0; e < kPer<T>; ++e) part += exp2_fast(fmaf(f[e], a.scale, -from));
-        S += part;
+        for (int e = 1; e < kPer<T> / 2; ++e) part = add_2(part, exp2_2(fma_2(elements(x[i], e), c, less)));
+        sum = add_2(sum, part);
     }
+    S = both(sum).x + both(sum).y;
     static_cast<T*>(a.maxima)[unit * 32 + lane] = from_float<T>(m);
     warp_join(ref, S);
     if (lane == 0) a.sums[unit] = make_float2(ref, S);

@@ -89,7 +89,7 @@ class Case:
                 s = np.exp(self.z[r] / tau - every) if np.isfinite(every) else np.zeros(self.V)
             ids, lps, _ = ref.entries(self.ids[r], self.lps[r], self.V)
             size = s * (2 + ratio)
-            size[ids] += np.exp(lps) / (1 if self.rest else max(np.exp(lps).sum(), 1e-300))
+            size[ids] += np.exp(lps) if self.rest or not lps.size else np.exp(lps - ref.log_sum(lps))
             err = rel * size * w / tau
             assert np.all(np.abs(g[r] - want) <= err + P.HALF[kind] * (np.abs(want) + err) + TINY[kind]), r
 
@@ -205,6 +205,26 @@ def test_sure_students(cuda):
     c.check_loss(loss, stats)
     c.check_grad(grad, "f32")
     assert (loss[1:] - loss[:-1] > 1.0).all()
+
+
+def test_small_targets_keep_their_shares(cuda):
+    """A renormalised list whose log-probabilities are all far below fp32's smallest exponential, in every warp that holds one."""
+    import torch
+
+    rng = np.random.default_rng(14)
+    x, z = L.rows(rng, 2, 800, "f32")
+    ids = np.stack([rng.permutation(800)[:100] for _ in range(2)]).astype(np.int32)
+    lps = (-300 - rng.uniform(0, 4, (2, 100))).astype(np.float32)
+    lps[1, 50:] -= 2000
+    c = Case(x, ids, lps, 1.0, False)
+    grad = torch.empty_like(x)
+    loss, stats, _ = c.forward(grad=grad)
+    c.check_loss(loss, stats)
+    _, _, want, _ = zip(*c.want)
+    # the targets' exponents are below 2050 in size: fp32 holds their differences to 2^-13 at worst, in the second row's last ones
+    assert np.all(np.abs(P.host(grad) - np.array(want)) <= 2.0 ** -14)
+    _native.distill_backward(x, c.dids, c.dlps, stats, None, grad, rest=False)
+    assert np.all(np.abs(P.host(grad) - np.array(want)) <= 2.0 ** -14)
 
 
 def test_entries_that_do_not_count(cuda):

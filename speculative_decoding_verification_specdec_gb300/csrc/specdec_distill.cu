@@ -23,8 +23,9 @@ namespace {
 
 using namespace specdec;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBackThreads = 256;
 constexpr int kMaxCluster = 8;
 constexpr int kTileBytes = 100 * 1024;             // the most of a row that a CTA holds at once: two CTAs an SM
 
@@ -85,10 +86,15 @@ __device__ __forceinline__ Entry read_entry(const Args& a, int64_t r, int32_t* i
         ids[tid] = e.id;
     }
     __syncthreads();
-    if (tid < a.n && e.id != -1) {
-        bool bad = e.id < 0 || e.id >= a.V || !(e.lp < INFINITY);
-        for (int j = 0; j < tid; ++j) bad |= ids[j] == e.id;
-        if (bad) {
+    if (tid < (a.n + 31) / 32 * 32) {                                 // (whole warps)
+        const uint32_t same = __match_any_sync(0xffffffffu, e.id);
+        bool bad = e.id < -1 || e.id >= a.V || !(e.lp < INFINITY) || (same & ((1u << (tid & 31)) - 1u)) != 0;
+        const int4* before = reinterpret_cast<const int4*>(ids);
+        for (int j = 0; j < tid / 32 * 8; ++j) {
+            const int4 four = before[j];
+            bad |= four.x == e.id || four.y == e.id || four.z == e.id || four.w == e.id;
+        }
+        if (bad && e.id != -1) {
             e.id = -1;
             e.fault = SPECDEC_ST_BAD_TARGET;
         }
@@ -215,10 +221,10 @@ struct Shared {
     ListPart list[kListWarps];
     Asked asked;
     double list_64[kListWarps][3];
-    int32_t ids[SPECDEC_TOP_MAX];
+    alignas(16) int32_t ids[SPECDEC_TOP_MAX];
 };
 
-template <typename T, bool kGrad> __global__ void __launch_bounds__(kThreads, 4) specdec_distill_kernel(const Args a)
+template <typename T, bool kGrad> __global__ void __launch_bounds__(kThreads, 2) specdec_distill_kernel(const Args a)
 {
     extern __shared__ __align__(16) unsigned char held[];
     __shared__ Shared s;
@@ -245,17 +251,14 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__(kThreads, 4)
     }
     asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");     // (waited for before any CTA writes to another)
     Raw<T, kPer<T>>* const mine = reinterpret_cast<Raw<T, kPer<T>>*>(held);
+    // (but for the row's first and last vector, every vector lies inside it)
+    const int32_t whole0 = row.lead ? 1 : 0, whole1 = (row.lead + a.V) / kPer<T>;
     auto fetch = [&](int32_t from, int32_t to) {
-        for (int32_t v = from + tid; v < to; v += kThreads) {
-            const int32_t at = row.first(v);
-            if (row.whole(at)) {
-                async_copy_16(smem_u32(mine + (v - from)), z + at, 16);
-            } else {
-                Raw<T, kPer<T>> x;
-#pragma unroll
-                for (int i = 0; i < kPer<T>; ++i) x.e[i] = at + i >= 0 && at + i < a.V ? z[at + i] : neg_inf<T>();
-                mine[v - from] = x;
-            }
+        const int32_t end = min(to, whole1);
+        for (int32_t v = max(from, whole0) + tid; v < end; v += kThreads) async_copy_16(smem_u32(mine + (v - from)), z + row.first(v), 16);
+        if (tid < 2) {
+            const int32_t v = tid == 0 ? 0 : row.vectors - 1;
+            if ((v < whole0 || v >= whole1) && v >= from && v < to) load_vector(row, v, mine[v - from]);
         }
     };
     fetch(v0, min(v0 + a.tile, v1));
@@ -291,7 +294,7 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__(kThreads, 4)
         __syncthreads();
         for (int32_t v = tid; v < to - from; v += kThreads) {
             const Raw<T, kPer<T>> x = mine[v];
-            const float m = vector_max(x);
+            const float m = Maximum<T>::of(x).value();
             if (m * a.scale > ref) {
                 const float up = ceilf(m * a.scale);
                 S *= reference_step(ref, up);
@@ -358,11 +361,24 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__(kThreads, 4)
                 async_copy_wait();
                 __syncthreads();
             }
-            for (int32_t v = tid; v < to - from; v += kThreads) {
-                Raw<T, kPer<T>> x = mine[v];
+            auto change = [&](int32_t v) {
+                Raw<T, kPer<T>> x = mine[v - from];
 #pragma unroll
                 for (int i = 0; i < kPer<T> / 2; ++i) put_elements(x, i, mul_2(e2(elements(x, i)), factors));
-                store_vector(row, g, aligned, from + v, x);
+                return x;
+            };
+            if (aligned) {
+                const int32_t end = min(to, whole1);
+                for (int32_t v = max(from, whole0) + tid; v < end; v += kThreads) {
+                    const Raw<T, kPer<T>> x = change(v);
+                    *reinterpret_cast<uint4*>(g + row.first(v)) = *reinterpret_cast<const uint4*>(x.e);
+                }
+                if (tid < 2) {
+                    const int32_t v = tid == 0 ? 0 : row.vectors - 1;
+                    if ((v < whole0 || v >= whole1) && v >= from && v < to) store_vector(row, g, false, v, change(v));
+                }
+            } else {
+                for (int32_t v = from + tid; v < to; v += kThreads) store_vector(row, g, false, v, change(v));
             }
         }
         __syncthreads();
@@ -427,14 +443,14 @@ __device__ __forceinline__ void in_octaves(float x, float* whole, float* less)
 // The gradient from the sums that a forward pass kept: element by element, a CTA a chunk of a row. All in fp32: the sums come in fp32.
 constexpr int kChunk = 8;                          // vectors a thread
 
-template <typename T> __global__ void __launch_bounds__(kThreads) specdec_distill_backward_kernel(const Args a, const int32_t chunks)
+template <typename T> __global__ void __launch_bounds__(kBackThreads) specdec_distill_backward_kernel(const Args a, const int32_t chunks)
 {
     __shared__ ListPart parts[kListWarps];
-    __shared__ int32_t ids[SPECDEC_TOP_MAX];
+    __shared__ __align__(16) int32_t ids[SPECDEC_TOP_MAX];
     after_predecessor();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t r = blockIdx.x / (uint32_t)chunks;
-    const int32_t v0 = (int32_t)(blockIdx.x - r * chunks) * (kChunk * kThreads);
+    const int32_t v0 = (int32_t)(blockIdx.x - r * chunks) * (kChunk * kBackThreads);
     const T* const z = static_cast<const T*>(a.logits) + r * a.row_stride;
     T* const g = static_cast<T*>(a.grad) + r * a.grad_stride;
     const Row<T> row(z, a.V);
@@ -445,13 +461,13 @@ template <typename T> __global__ void __launch_bounds__(kThreads) specdec_distil
         const Raw<T, kPer<T>> zero = {};
 #pragma unroll
         for (int i = 0; i < kChunk; ++i)
-            if (v0 + i * kThreads + tid < row.vectors) store_vector(row, g, aligned, v0 + i * kThreads + tid, zero);
+            if (v0 + i * kBackThreads + tid < row.vectors) store_vector(row, g, aligned, v0 + i * kBackThreads + tid, zero);
         return;
     }
     Raw<T, kPer<T>> x[kChunk];
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) {
-        const int32_t v = v0 + i * kThreads + tid, at = row.first(v);
+        const int32_t v = v0 + i * kBackThreads + tid, at = row.first(v);
         if (v < row.vectors && row.whole(at)) {
             *reinterpret_cast<uint4*>(x[i].e) = *reinterpret_cast<const uint4*>(z + at);
         } else {
@@ -461,7 +477,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) specdec_distil
     }
     const float lse = a.stats[2 * r], lse_rest = a.stats[2 * r + 1];
     const Entry e = read_entry(a, r, ids);
-    const bool here = e.id >= 0 && e.id >= row.first(v0) && e.id < row.first(min(v0 + kChunk * kThreads, row.vectors));
+    const bool here = e.id >= 0 && e.id >= row.first(v0) && e.id < row.first(min(v0 + kChunk * kBackThreads, row.vectors));
     const float top = here ? to_float<T>(z[e.id]) : 0.f;              // (before the row is written: the gradient may lie over it)
     if (warp < kListWarps) {
         const ListPart part = list_part(e, a.rest);
@@ -480,7 +496,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) specdec_distil
     const Pair factors = pair_of(factor, factor);
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) {
-        const int32_t v = v0 + i * kThreads + tid;
+        const int32_t v = v0 + i * kBackThreads + tid;
         if (v >= row.vectors) continue;
 #pragma unroll
         for (int k = 0; k < kPer<T> / 2; ++k) put_elements(x[i], k, mul_2(e2(elements(x[i], k)), factors));
@@ -500,14 +516,14 @@ struct Shape {
     int32_t cluster, slice, tile;
 };
 
-// A row goes to the fewest CTAs that keep three of them on an SM (64 KB each), more where the rows alone do not
+// A row goes to the fewest CTAs that keep two of them on an SM, more where the rows alone do not
 // fill the GPU; what is longer than eight times kTileBytes is read a second time for the gradient.
 template <typename T> Shape shape_of(int32_t rows, int32_t V)
 {
     const int32_t vectors = most_vectors<T>(V);
     int32_t cluster = 1;
     auto slice = [&] { return (vectors + cluster - 1) / cluster; };
-    while (cluster < kMaxCluster && (slice() > 64 * 1024 / 16 || ((int64_t)rows * cluster < 304 && slice() > 8 * 1024 / 16))) cluster *= 2;
+    while (cluster < kMaxCluster && (slice() > kTileBytes / 16 || ((int64_t)rows * cluster < 304 && slice() > 8 * 1024 / 16))) cluster *= 2;
     const int32_t s = (slice() + 7) / 8 * 8;
     return Shape{cluster, s, s < kTileBytes / 16 ? s : kTileBytes / 16};
 }
@@ -558,9 +574,9 @@ template <typename T> specdec_status_t launch_forward(Args a, cudaStream_t strea
 
 template <typename T> specdec_status_t launch_backward(const Args& a, cudaStream_t stream)
 {
-    const int32_t chunks = (most_vectors<T>(a.V) + kChunk * kThreads - 1) / (kChunk * kThreads);
+    const int32_t chunks = (most_vectors<T>(a.V) + kChunk * kBackThreads - 1) / (kChunk * kBackThreads);
     if ((int64_t)a.rows * chunks > 0x7fffffff) return SPECDEC_ERR_UNSUPPORTED;
-    const cudaError_t e = launch_dependent(specdec_distill_backward_kernel<T>, (unsigned)((int64_t)a.rows * chunks), kThreads, 0, stream, a, chunks);
+    const cudaError_t e = launch_dependent(specdec_distill_backward_kernel<T>, (unsigned)((int64_t)a.rows * chunks), kBackThreads, 0, stream, a, chunks);
     return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 

@@ -186,23 +186,54 @@ __device__ __forceinline__ void warp_join(float& ref, float& S)
     ref = top;
 }
 
-// Largest element of a vector (NaN is passed over).
-__device__ __forceinline__ float vector_max(const Raw<float, 4>& x)
-{
-    return fmaxf(fmaxf(x.e[0], x.e[1]), fmaxf(x.e[2], x.e[3]));
-}
-__device__ __forceinline__ float vector_max(const Raw<__nv_bfloat16, 8>& x)
-{
-    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(x.e);
-    const __nv_bfloat162 m = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
-    return fmaxf(__bfloat162float(m.x), __bfloat162float(m.y));
-}
-__device__ __forceinline__ float vector_max(const Raw<__half, 8>& x)
-{
-    const __half2* p = reinterpret_cast<const __half2*>(x.e);
-    const __half2 m = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
-    return fmaxf(__half2float(__low2half(m)), __half2float(__high2half(m)));
-}
+// Maxima of vectors as they are kept on the way: a float, or a pair of 16-bit numbers whose larger one counts. NaN is passed over.
+template <typename T> struct Maximum;
+template <> struct Maximum<float> {
+    float x;
+    __device__ __forceinline__ static Maximum of(const Raw<float, 4>& v) { return {fmaxf(fmaxf(v.e[0], v.e[1]), fmaxf(v.e[2], v.e[3]))}; }
+    __device__ __forceinline__ friend Maximum larger(Maximum a, Maximum b) { return {fmaxf(a.x, b.x)}; }
+    __device__ __forceinline__ float value() const { return x; }
+    __device__ __forceinline__ uint32_t bits() const { return __float_as_uint(x); }
+    __device__ __forceinline__ static Maximum from(uint32_t b) { return {__uint_as_float(b)}; }
+};
+template <> struct Maximum<__nv_bfloat16> {
+    uint32_t x;
+    __device__ __forceinline__ friend Maximum larger(Maximum a, Maximum b)
+    {
+        Maximum m;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(m.x) : "r"(a.x), "r"(b.x));
+        return m;
+    }
+    __device__ __forceinline__ static Maximum of(const Raw<__nv_bfloat16, 8>& v)
+    {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(v.e);
+        return larger(larger(Maximum{p[0]}, Maximum{p[1]}), larger(Maximum{p[2]}, Maximum{p[3]}));
+    }
+    __device__ __forceinline__ float value() const { return fmaxf(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)); }
+    __device__ __forceinline__ uint32_t bits() const { return x; }
+    __device__ __forceinline__ static Maximum from(uint32_t b) { return {b}; }
+};
+template <> struct Maximum<__half> {
+    uint32_t x;
+    __device__ __forceinline__ friend Maximum larger(Maximum a, Maximum b)
+    {
+        Maximum m;
+        asm("max.f16x2 %0, %1, %2;" : "=r"(m.x) : "r"(a.x), "r"(b.x));
+        return m;
+    }
+    __device__ __forceinline__ static Maximum of(const Raw<__half, 8>& v)
+    {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(v.e);
+        return larger(larger(Maximum{p[0]}, Maximum{p[1]}), larger(Maximum{p[2]}, Maximum{p[3]}));
+    }
+    __device__ __forceinline__ float value() const
+    {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+        return fmaxf(f.x, f.y);
+    }
+    __device__ __forceinline__ uint32_t bits() const { return x; }
+    __device__ __forceinline__ static Maximum from(uint32_t b) { return {b}; }
+};
 
 inline specdec_status_t check_logits(const void* logits, specdec_dtype_t dtype, int64_t rows, int32_t V, int64_t row_stride)
 {

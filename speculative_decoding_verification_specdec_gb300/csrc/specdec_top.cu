@@ -5,10 +5,10 @@
  * Two kernels for the rows, a third for the beams:
  *
  *   stream   reads every row once. A warp takes a unit of 256 vectors (4 KB), a lane 8 of them, 512 bytes apart: their sum of
- *            exponentials goes into the unit's (reference, sum) pair, and their largest element is kept as the
- *            maximum of that group of elements.
+ *            exponentials goes into the unit's (reference, sum) pair, and the largest element of every 128 bytes (a
+ *            group) is kept.
  *   select   a CTA a row: joins the sums, and finds the n best elements through the groups' maxima. The n-th largest of 256
- *            numbers, each the largest maximum of every 256th group, is a lower bound of the n-th best element, so that only
+ *            numbers, each the largest of some groups' maxima, is a lower bound of the n-th best element, so that only
  *            the groups that reach it (about n) are read again.
  *   merge    a CTA a request: the beams' lists hold everything that can survive; a candidate's rank is its place in its
  *            own list plus, by bisection, how many entries of each other list come before it.
@@ -19,10 +19,12 @@ namespace {
 
 using namespace specdec;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;                      // of the stream and the merge
 constexpr int kUnitVectors = 256;                  // a warp's: 8 a lane
-constexpr int kLaneVectors = kUnitVectors / 32;
-constexpr int kMaxGroups = 1024, kMaxFound = 2048;
+constexpr int kLaneVectors = kUnitVectors / 32, kGroupVectors = kUnitVectors / 32;
+constexpr int kSelectThreads = 128;
+constexpr int kBounds = 256;                       // the numbers of which the n-th largest bounds the n-th best element
+constexpr int kMaxGroups = 1024, kMaxFound = 1024;
 constexpr int kMaxMerge = 4096;                    // candidates of one request
 
 struct StreamArgs {
@@ -74,9 +76,13 @@ template <typename T, bool kMasked> __global__ void __launch_bounds__(kThreads) 
 #pragma unroll
         for (int i = 0; i < kLaneVectors; ++i) load_vector(row, v0 + i * 32, x[i]);
     }
-    float m = vector_max(x[0]);
+    Maximum<T> part[kLaneVectors];
 #pragma unroll
-    for (int i = 1; i < kLaneVectors; ++i) m = fmaxf(m, vector_max(x[i]));
+    for (int i = 0; i < kLaneVectors; ++i) part[i] = Maximum<T>::of(x[i]);
+    Maximum<T> own = part[0];
+#pragma unroll
+    for (int i = 1; i < kLaneVectors; ++i) own = larger(own, part[i]);
+    float m = own.value();
     if (!(m > -INFINITY)) m = -INFINITY;           // (nothing but NaN)
     float ref = m == -INFINITY ? m : whole_reference(m, a.scale), S = 0.f;
     const float from = m == -INFINITY ? 0.f : ref;
@@ -90,7 +96,17 @@ template <typename T, bool kMasked> __global__ void __launch_bounds__(kThreads) 
         sum = add_2(sum, part);
     }
     S = both(sum).x + both(sum).y;
-    static_cast<T*>(a.maxima)[unit * 32 + lane] = from_float<T>(m);
+    // The maxima of 8 neighbouring lanes' i-th vectors, 128 bytes, meet in the i-th of those lanes: three exchanges, of 4, 2 and 1.
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) {
+        const bool high = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const Maximum<T> kept = high ? part[i + o] : part[i], given = high ? part[i] : part[i + o];
+            part[i] = larger(kept, Maximum<T>::from(__shfl_xor_sync(0xffffffffu, given.bits(), o)));
+        }
+    }
+    static_cast<T*>(a.maxima)[unit * 32 + (lane & 7) * 4 + (lane >> 3)] = from_float<T>(part[0].value());
     warp_join(ref, S);
     if (lane == 0) a.sums[unit] = make_float2(ref, S);
 }
@@ -106,7 +122,7 @@ struct SelectArgs {
     double* sums;                                  // beams: ln of the sum of exp, [rows]
 };
 
-// The largest t, a multiple of 2^low, with at least n of the CTA's numbers (count(t) of them here) at or above it.
+// The largest t, a multiple of 2^low, with at least n of some numbers (count(t) of them) at or above it.
 template <typename Count> __device__ __forceinline__ uint32_t nth_largest(int n, int low, Count count)
 {
     uint32_t t = 0;
@@ -118,14 +134,14 @@ template <typename Count> __device__ __forceinline__ uint32_t nth_largest(int n,
 }
 
 // The sum of one number a thread, the same in every thread; two barriers.
-__device__ __forceinline__ int block_sum(int x, int* part)
+template <int kCount> __device__ __forceinline__ int block_sum(int x, int* part)
 {
     x = __reduce_add_sync(0xffffffffu, x);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
     __syncthreads();
     int sum = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) sum += part[w];
+    for (int w = 0; w < kCount / 32; ++w) sum += part[w];
     __syncthreads();
     return sum;
 }
@@ -163,12 +179,15 @@ __device__ __forceinline__ unsigned long long composite(uint32_t key, int32_t at
     return (unsigned long long)key << 32 | (uint32_t)~at;
 }
 
-template <typename T> __global__ void __launch_bounds__(kThreads) specdec_rows_select_kernel(const SelectArgs a)
+template <typename T> __global__ void __launch_bounds__(kSelectThreads) specdec_rows_select_kernel(const SelectArgs a)
 {
+    constexpr int kWarps = kSelectThreads / 32, kMine = kMaxFound / kSelectThreads, kSides = kBounds / kSelectThreads;
     __shared__ unsigned long long found[kMaxFound];
     __shared__ int32_t groups[kMaxGroups];
+    __shared__ uint32_t bounds[kBounds];
     __shared__ double row_sum;
-    __shared__ int counts[kThreads / 32];
+    __shared__ uint32_t bound;
+    __shared__ int counts[kWarps];
     __shared__ int num_groups, num_found;
     after_predecessor();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.n;
@@ -177,8 +196,35 @@ template <typename T> __global__ void __launch_bounds__(kThreads) specdec_rows_s
     const Select<T> sel(a, r);
     if (tid == 0) num_groups = num_found = 0;
 
-    // the row's sum, in 64 bits and always in the same order: the first warp's
+    // the largest maxima of 256 sets of groups (a set is every 256th vector of them)
+    const T* const maxima = static_cast<const T*>(a.s.maxima) + r * a.s.units * 32;
+    const int32_t vectors = a.s.units * 32 / kPer<T>;
+    auto largest = [&](int32_t v) {
+        Raw<T, kPer<T>> x;
+        x.load(maxima + v * kPer<T>);
+        return order_key(Maximum<T>::of(x).value());
+    };
+#pragma unroll
+    for (int side = 0; side < kSides; ++side) {
+        uint32_t top = 0;
+        for (int32_t v = tid + side * kSelectThreads; v < vectors; v += kBounds) top = max(top, largest(v));
+        bounds[tid + side * kSelectThreads] = top;
+    }
+    __syncthreads();
     if (warp == 0) {
+        // the n-th largest of them, its upper 16 bits (a lower bound of a lower bound)
+        uint32_t mine[kBounds / 32];
+#pragma unroll
+        for (int i = 0; i < kBounds / 32; ++i) mine[i] = bounds[lane + i * 32];
+        const uint32_t t = nth_largest(n, 16, [&](uint32_t t) {
+            int c = 0;
+#pragma unroll
+            for (int i = 0; i < kBounds / 32; ++i) c += mine[i] >= t;
+            return (int)__reduce_add_sync(0xffffffffu, c);
+        });
+        if (lane == 0) bound = max(t, 1u);
+    } else if (warp == 1) {
+        // the row's sum, in 64 bits and always in the same order
         const float2* sums = a.s.sums + r * a.s.units;
         float ref = -INFINITY;
         for (int u = lane; u < a.s.units; u += 32) ref = fmaxf(ref, sums[u].x);
@@ -190,31 +236,29 @@ template <typename T> __global__ void __launch_bounds__(kThreads) specdec_rows_s
         for (int o = 16; o >= 1; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
         if (lane == 0) row_sum = (double)ref + log2(S);               // in units of the exponents
     }
-
-    // the largest maximum of every 256th group
-    const T* maxima = static_cast<const T*>(a.s.maxima) + r * a.s.units * 32;
-    const int32_t all = a.s.units * 32;
-    uint32_t top = 0;
-    for (int32_t g = tid; g < all; g += kThreads) top = max(top, order_key(to_float<T>(maxima[g])));
-    const uint32_t least = max(1u, nth_largest(n, kKeyLow<T>, [&](uint32_t t) { return __syncthreads_count(top >= t); }));
-
-    for (int32_t g = tid; g < all; g += kThreads)
-        if (order_key(to_float<T>(maxima[g])) >= least) {
-            const int at = atomicAdd(&num_groups, 1);
-            if (at < kMaxGroups) groups[at] = g;
-        }
+    __syncthreads();
+    const uint32_t least = bound;
+    for (int32_t v = tid; v < vectors; v += kSelectThreads) {
+        Raw<T, kPer<T>> x;
+        x.load(maxima + v * kPer<T>);
+        if (order_key(Maximum<T>::of(x).value()) < least) continue;
+#pragma unroll
+        for (int e = 0; e < kPer<T>; ++e)
+            if (order_key(to_float<T>(x.e[e])) >= least) {
+                const int at = atomicAdd(&num_groups, 1);
+                if (at < kMaxGroups) groups[at] = v * kPer<T> + e;
+            }
+    }
     __syncthreads();
     const int want = num_groups;
     if (want <= kMaxGroups) {
-        for (int i = tid; i < want * kLaneVectors; i += kThreads) {
-            const int32_t g = groups[i / kLaneVectors];
-            sel.each((g / 32) * kUnitVectors + (i % kLaneVectors) * 32 + g % 32, [&](uint32_t key, int32_t at) {
+        for (int i = tid; i < want * kGroupVectors; i += kSelectThreads)
+            sel.each(groups[i / kGroupVectors] * kGroupVectors + i % kGroupVectors, [&](uint32_t key, int32_t at) {
                 if (key >= least) {
                     const int to = atomicAdd(&num_found, 1);
                     if (to < kMaxFound) found[to] = composite(key, at);
                 }
             });
-        }
     }
     __syncthreads();
     int have = num_found;
@@ -225,17 +269,17 @@ template <typename T> __global__ void __launch_bounds__(kThreads) specdec_rows_s
         if (tid == 0) num_found = 0;
         const uint32_t nth = max(1u, nth_largest(n, kKeyLow<T>, [&](uint32_t t) {
             int mine = 0;
-            for (int32_t v = tid; v < sel.row.vectors; v += kThreads) sel.each(v, [&](uint32_t key, int32_t) { mine += key >= t; });
-            return block_sum(mine, counts);
+            for (int32_t v = tid; v < sel.row.vectors; v += kSelectThreads) sel.each(v, [&](uint32_t key, int32_t) { mine += key >= t; });
+            return block_sum<kSelectThreads>(mine, counts);
         }));
         const uint32_t above = nth | ((1u << kKeyLow<T>) - 1u);       // (a key's low bits follow from the others)
-        for (int32_t v = tid; v < sel.row.vectors; v += kThreads)
+        for (int32_t v = tid; v < sel.row.vectors; v += kSelectThreads)
             sel.each(v, [&](uint32_t key, int32_t at) {
                 if (key > above) found[atomicAdd(&num_found, 1)] = composite(key, at);
             });
         __syncthreads();
         have = num_found;
-        for (int32_t v0 = 0; v0 < sel.row.vectors && have < n; v0 += kThreads) {
+        for (int32_t v0 = 0; v0 < sel.row.vectors && have < n; v0 += kSelectThreads) {
             int mine = 0;
             if (v0 + tid < sel.row.vectors) sel.each(v0 + tid, [&](uint32_t key, int32_t) { mine += key >= nth && key <= above; });
             int before = mine;
@@ -248,7 +292,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) specdec_rows_s
             __syncthreads();
             int to = have + before - mine, sum = 0;
 #pragma unroll
-            for (int w = 0; w < kThreads / 32; ++w) {
+            for (int w = 0; w < kWarps; ++w) {
                 if (w < warp) to += counts[w];
                 sum += counts[w];
             }
@@ -261,19 +305,19 @@ template <typename T> __global__ void __launch_bounds__(kThreads) specdec_rows_s
         }
     } else if (have > 384) {
         // few rows come here (wide ties, small vocabularies): the n-th largest first, so that ranks are counted among few
-        unsigned long long mine[kMaxFound / kThreads];
+        unsigned long long mine[kMine];
 #pragma unroll
-        for (int i = 0; i < kMaxFound / kThreads; ++i) mine[i] = tid + i * kThreads < have ? found[tid + i * kThreads] : 0;
+        for (int i = 0; i < kMine; ++i) mine[i] = tid + i * kSelectThreads < have ? found[tid + i * kSelectThreads] : 0;
         const uint32_t nth = max(1u, nth_largest(n, kKeyLow<T>, [&](uint32_t t) {
             int c = 0;
 #pragma unroll
-            for (int i = 0; i < kMaxFound / kThreads; ++i) c += (uint32_t)(mine[i] >> 32) >= t;
-            return block_sum(c, counts);
+            for (int i = 0; i < kMine; ++i) c += (uint32_t)(mine[i] >> 32) >= t;
+            return block_sum<kSelectThreads>(c, counts);
         }));
         if (tid == 0) num_found = 0;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kMaxFound / kThreads; ++i)
+        for (int i = 0; i < kMine; ++i)
             if ((uint32_t)(mine[i] >> 32) >= nth) found[atomicAdd(&num_found, 1)] = mine[i];
         __syncthreads();
         have = num_found;
@@ -282,7 +326,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) specdec_rows_s
     // ranks among what was found: they are the places, whatever the order of the finding was
     const double log_sum = row_sum;
     constexpr double kLn2 = 0.69314718055994530941723;
-    for (int i = tid; i < have; i += kThreads) {
+    for (int i = tid; i < have; i += kSelectThreads) {
         const unsigned long long me = found[i];
         int rank = 0;
         for (int j = 0; j < have; ++j) rank += found[j] > me;
@@ -292,7 +336,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) specdec_rows_s
         if (a.values) a.values[r * n + rank] = z;
         if (a.logprobs) a.logprobs[r * n + rank] = log_sum == -INFINITY ? -INFINITY : (float)(((double)z * a.s.scale - log_sum) * kLn2);
     }
-    for (int i = have + tid; i < n; i += kThreads) {
+    for (int i = have + tid; i < n; i += kSelectThreads) {
         a.ids[r * n + i] = -1;
         if (a.values) a.values[r * n + i] = -INFINITY;
         if (a.logprobs) a.logprobs[r * n + i] = -INFINITY;
@@ -360,7 +404,7 @@ __global__ void __launch_bounds__(kThreads) specdec_beam_merge_kernel(const Merg
         valid += key != kNone;
     }
     if (a.status && bad) atomicOr(a.status + b, bad);
-    valid = block_sum(valid, counts);                                // (its barriers also publish the keys)
+    valid = block_sum<kThreads>(valid, counts);                                // (its barriers also publish the keys)
     for (int i = tid; i < total; i += kThreads) {
         const int w = i / n, k = i - w * n;
         const long long key = keys[i];
@@ -434,7 +478,7 @@ template <typename T> specdec_status_t launch_rows(const StreamArgs& s, const Se
     const unsigned grid = (unsigned)((units + kThreads / 32 - 1) / (kThreads / 32));
     cudaError_t e = s.bitmask ? launch_dependent(specdec_rows_stream_kernel<T, true>, grid, kThreads, 0, stream, s)
                               : launch_dependent(specdec_rows_stream_kernel<T, false>, grid, kThreads, 0, stream, s);
-    if (e == cudaSuccess) e = launch_dependent(specdec_rows_select_kernel<T>, (unsigned)s.rows, kThreads, 0, stream, a);
+    if (e == cudaSuccess) e = launch_dependent(specdec_rows_select_kernel<T>, (unsigned)s.rows, kSelectThreads, 0, stream, a);
     return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 

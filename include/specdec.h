@@ -593,7 +593,8 @@ specdec_status_t specdec_top_logits(const void* logits, specdec_dtype_t dtype, i
  * Sums over the row are held in fp32 by a thread and in 64 bits across them; targets, listed exponentials and the loss in 64
  * bits; an element of the gradient is one fp32 exponential times one factor, rounded once to its type. Equal calls give equal bits.
  * Errors: INVALID_ARG for a NULL required pointer, n, a size, a stride or a temperature outside those above, rest not 0 or 1;
- * UNSUPPORTED for a type or V outside those above, or more than 2^31 CTAs; CUDA.
+ * UNSUPPORTED for a type or V outside those above, a row of more than 3,276,768 bytes (it is held on chip; the backward call
+ * has no such limit, but one of 2^31 CTAs of 32 KB); CUDA.
  */
 specdec_status_t specdec_distill(const void* logits, specdec_dtype_t dtype, int32_t rows, int32_t V, int64_t row_stride,
                                  const int32_t* top_ids, const float* top_logprobs, int32_t n, double temperature,

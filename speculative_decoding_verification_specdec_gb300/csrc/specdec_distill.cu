@@ -12,10 +12,11 @@
  * elements are taken out of the row in shared memory. Outside the list the gradient is one exponential times one number,
  * e_j (M / S - r / S_rest).
  *
- * A row is held by a cluster of CTAs, a slice each, in shared memory: it is read from HBM once, for the sums and for the gradient.
+ * A row is held by a cluster of CTAs, a part each, in shared memory: it is read from HBM once, for the sums and for the gradient.
  */
 #include <atomic>
 #include <cmath>
+#include <cstddef>
 
 #include "specdec_logits.cuh"
 
@@ -23,11 +24,12 @@ namespace {
 
 using namespace specdec;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kRowWarps = 8;                       // of a CTA, at most, without the list's
+constexpr int kLaneVectors = 10;                   // of a thread, where that many warps are enough
 constexpr int kBackThreads = 256;
-constexpr int kMaxCluster = 8;
-constexpr int kTileBytes = 100 * 1024;             // the most of a row that a CTA holds at once: two CTAs an SM
+constexpr int kMaxCluster = 16;
+constexpr int kSliceBytes = 40 * 1024;             // of a row in a CTA: four CTAs an SM
+constexpr int kMostBytes = 200 * 1024;             // and where sixteen CTAs hold the row only so
 
 struct Args {
     const void* logits;
@@ -45,10 +47,8 @@ struct Args {
     void* grad;
     int64_t grad_stride;
     uint32_t* status;
-    int32_t slice, tile;                           // vectors of a CTA, and of what it holds at once (the slice, or a part)
+    int32_t slice;                                 // vectors of a row in a CTA
 };
-
-constexpr double kLn2 = 0.69314718055994530941723;
 
 // z log2(e) / temperature - ref: scale and scale_low are both positive, so that -infinity stays what it is.
 __device__ __forceinline__ float exponent(float z, const Args& a, float ref)
@@ -68,46 +68,6 @@ template <bool kLow> struct Exponentials {
     }
 };
 
-// Thread i's entry of the list: id, -1 where there is none or it does not count.
-struct Entry {
-    int32_t id;
-    float lp;
-    uint32_t fault;
-};
-
-// `ids` is filled for the CTA; a barrier is inside.
-__device__ __forceinline__ Entry read_entry(const Args& a, int64_t r, int32_t* ids)
-{
-    const int tid = threadIdx.x;
-    Entry e = {-1, -INFINITY, 0};
-    if (tid < a.n) {
-        e.id = __ldg(a.ids + r * a.n + tid);
-        e.lp = __ldg(a.logprobs + r * a.n + tid);
-        ids[tid] = e.id;
-    }
-    __syncthreads();
-    if (tid < (a.n + 31) / 32 * 32) {                                 // (whole warps)
-        const uint32_t same = __match_any_sync(0xffffffffu, e.id);
-        bool bad = e.id < -1 || e.id >= a.V || !(e.lp < INFINITY) || (same & ((1u << (tid & 31)) - 1u)) != 0;
-        const int4* before = reinterpret_cast<const int4*>(ids);
-        for (int j = 0; j < tid / 32 * 8; ++j) {
-            const int4 four = before[j];
-            bad |= four.x == e.id || four.y == e.id || four.z == e.id || four.w == e.id;
-        }
-        if (bad && e.id != -1) {
-            e.id = -1;
-            e.fault = SPECDEC_ST_BAD_TARGET;
-        }
-    }
-    return e;
-}
-
-template <typename F> __device__ __forceinline__ F warp_sum(F x)
-{
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
 __device__ __forceinline__ float warp_max(float x)
 {
 #pragma unroll
@@ -115,68 +75,56 @@ __device__ __forceinline__ float warp_max(float x)
     return x;
 }
 
-constexpr int kListWarps = SPECDEC_TOP_MAX / 32;   // the warps that hold entries
+constexpr int kEntries = SPECDEC_TOP_MAX / 32;     // of a lane of the warp that holds the list
 
-// 2^y to 2^-43 relative in some fifteen 64-bit operations (this part has few of them): y = k + f with k whole, v = f ln 2 / 8,
-// exp(v) by its series (|v| < 0.044: from the fourth power on in fp32, whose 2^-24 is 2^-46 of the sum), squared three times.
-__device__ __forceinline__ double exp2_64(double y)
-{
-    if (!(y > -1000.0)) return y != y ? y : 0.0;
-    const double shifted = y + 0x1.8p52, k = shifted - 0x1.8p52;
-    const double v = (y - k) * (kLn2 / 8.0), square = v * v;
-    const float x = (float)v;
-    const float series = fmaf(fmaf(fmaf(x, 1.f / 5040.f, 1.f / 720.f), x, 1.f / 120.f), x, 1.f / 24.f);
-    double e = fma(fma(square, (double)series, fma(v, 1.0 / 6.0, 0.5)), square, v) + 1.0;
-    e *= e;
-    e *= e;
-    e *= e;
-    return e * __hiloint2double((1023 + (int)fmin(k, 1023.0)) << 20, 0);
-}
+// The list as one warp holds it: entry lane + 32 c in a lane's c-th place.
+struct List {
+    int32_t ids[kEntries];
+    float lps[kEntries];
+    __device__ __forceinline__ void read(const Args& a, int64_t r)
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int c = 0; c < kEntries; ++c) {
+            const int j = lane + 32 * c;
+            ids[c] = j < a.n ? __ldg(a.ids + r * a.n + j) : -1;
+            lps[c] = j < a.n ? __ldg(a.logprobs + r * a.n + j) : -INFINITY;
+        }
+    }
+    // Entries that do not count become -1; the status bit of this lane's.
+    __device__ __forceinline__ uint32_t check(const Args& a)
+    {
+        const int lane = threadIdx.x & 31;
+        int32_t given[kEntries];
+        uint32_t fault = 0;
+#pragma unroll
+        for (int c = 0; c < kEntries; ++c) given[c] = ids[c];
+#pragma unroll
+        for (int c = 0; c < kEntries; ++c) {
+            if (32 * c >= a.n) continue;
+            const uint32_t same = __match_any_sync(0xffffffffu, given[c]);
+            bool bad = (same & ((1u << lane) - 1u)) != 0 || given[c] < -1 || given[c] >= a.V || !(lps[c] < INFINITY);
+#pragma unroll
+            for (int b = 0; b < c; ++b)
+                for (int l = 0; l < 32; ++l) bad |= __shfl_sync(0xffffffffu, given[b], l) == given[c];
+            if (bad && given[c] != -1) {
+                ids[c] = -1;
+                fault = SPECDEC_ST_BAD_TARGET;
+            }
+        }
+        return fault;
+    }
+};
 
-// What the list asks for. A target is exp(lp - shift) * norm; where the list is renormalised, shift is its largest log-probability,
-// so that a list of small ones keeps its shares.
-struct Asked {
-    float shift, norm, listed, rest;               // listed, rest: the masses of the targets and of what is left
-};
-struct ListPart {
-    double sum;                                    // in 64 bits: the rest is what it leaves of one
-    float shift;
-};
-constexpr double kLog2e = 1.4426950408889634073599;
-__device__ __forceinline__ double target_64(const Entry& e, float shift) { return e.id >= 0 ? exp2_64(((double)e.lp - (double)shift) * kLog2e) : 0.0; }
-__device__ __forceinline__ ListPart list_part(const Entry& e, int has_rest)       // a warp's
+// exp(lp - shift), a target (0 from 2^-125 down, -infinity among it).
+__device__ __forceinline__ Two target_of(float lp, float shift)
 {
-    float shift = 0.f;
-    if (!has_rest) {
-        shift = warp_max(e.id >= 0 ? e.lp : -INFINITY);
-        if (shift == -INFINITY) shift = 0.f;
-    }
-    return ListPart{warp_sum(target_64(e, shift)), shift};
+    return lp - shift < -90.f ? Two{0.f, 0.f} : exp2_two(two_sum(lp, -shift) * SPECDEC_TWO(kLog2e));
 }
-__device__ __forceinline__ Asked asked_of(const ListPart* parts, int n, int has_rest)
-{
-    Asked a = {0.f, 1.f, 0.f, 0.f};
-    const int warps = (n + 31) / 32;
-    if (has_rest) {
-        double sum = 0.0;
-        for (int i = 0; i < warps; ++i) sum += parts[i].sum;
-        a.listed = (float)sum;
-        a.rest = (float)fmax(0.0, 1.0 - sum);
-        return a;
-    }
-    float shift = -INFINITY, sum = 0.f;
-    for (int i = 0; i < warps; ++i)
-        if (parts[i].sum > 0.0) shift = fmaxf(shift, parts[i].shift);
-    for (int i = 0; i < warps; ++i)
-        if (parts[i].sum > 0.0) sum += (float)parts[i].sum * expf(parts[i].shift - shift);
-    if (sum > 0.f) {
-        a.shift = shift;
-        a.norm = 1.f / sum;
-        a.listed = 1.f;
-    }
-    return a;
-}
-__device__ __forceinline__ float target_of(const Entry& e, const Asked& a) { return expf(e.lp - a.shift) * a.norm; }
+// Targets add up as whole numbers of 2^-56, so that what they leave of one is exact.
+constexpr float kFixed = 0x1p56f;
+__device__ __forceinline__ long long fixed_of(Two x) { return __float2ll_rn(x.hi * kFixed) + __float2ll_rn(x.lo * kFixed); }
+__device__ __forceinline__ float from_fixed(long long x) { return __ll2float_rn(x) * (1.f / kFixed); }
 
 // Store of a vector's elements, those inside the row.
 template <typename T> __device__ __forceinline__ void store_vector(const Row<T>& row, T* to, bool aligned, int32_t v, const Raw<T, kPer<T>>& x)
@@ -205,236 +153,331 @@ __device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
     return a;
 }
-__device__ __forceinline__ void put_32(uint32_t to, float x) { asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(x) : "memory"); }
-__device__ __forceinline__ void put_64(uint32_t to, double x) { asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(x) : "memory"); }
+__device__ __forceinline__ void put_64(uint32_t to, long long x) { asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(to), "l"(x) : "memory"); }
 __device__ __forceinline__ void cluster_barrier()
 {
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// ---------------------------------------------------------------- forward
+
+// Persistent clusters, row after row. All warps but a CTA's last hold its part of the row in shared memory, each thread its own
+// vectors, and fetch the next row's into their places as they finish with them. The last warp holds the list: it takes the listed elements
+// out of the row, sums their part in 64 bits, exchanges the CTAs' sums and works the loss out while the others write the
+// gradient. What a CTA knows of a row meets the others' by distributed shared memory and one cluster barrier a row.
+// What one CTA of a cluster knows of a row.
+struct Part {
+    long long fixed;                               // the sum of the targets in 2^-56 (rest = 1)
+    Two rest, top, targets, cross;                 // sums of exponentials outside and on the list; of the targets; of t (ln t - z / temperature)
+    float rest_ref, top_ref, shift;
+    int32_t endless;                               // whether a target lies where the student has -infinity
+};
+constexpr int kPartWords = sizeof(Part) / 8;
+// An entry that lies in this CTA's part of the row.
+struct Own {
+    int32_t id;
+    float lp, top;                                 // top: the student's logit
+};
 struct Shared {
-    double peer_S[kMaxCluster];
-    float peer_ref[kMaxCluster];
-    float refs[kWarps], sums[kWarps];
-    float top_ref[kListWarps], top_sum[kListWarps];
-    ListPart list[kListWarps];
-    Asked asked;
-    double list_64[kListWarps][3];
-    alignas(16) int32_t ids[SPECDEC_TOP_MAX];
+    Part peer[2][kMaxCluster];                     // two rows': a CTA may be one ahead
+    Part part;
+    float refs[kRowWarps], sums[kRowWarps];
+    Own own[SPECDEC_TOP_MAX];
 };
 
-template <typename T, bool kGrad> __global__ void __launch_bounds__(kThreads, 2) specdec_distill_kernel(const Args a)
+// The parts of all CTAs together: the lanes of each half of a warp hold one each.
+__device__ __forceinline__ float half_max(float x)
+{
+#pragma unroll
+    for (int o = kMaxCluster / 2; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+template <typename F> __device__ __forceinline__ F half_sum(F x)
+{
+#pragma unroll
+    for (int o = kMaxCluster / 2; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+__device__ __forceinline__ Two half_sum(Two x)
+{
+#pragma unroll
+    for (int o = kMaxCluster / 2; o >= 1; o >>= 1) x = x + shuffle_xor(x, o);
+    return x;
+}
+
+template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps + 1) * 32, 4) specdec_distill_kernel(const Args a)
 {
     extern __shared__ __align__(16) unsigned char held[];
     __shared__ Shared s;
     after_predecessor();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x - 32;
+    const bool lists = tid >= threads;
     const uint32_t rank = cluster_rank(), size = cluster_size();
-    const int64_t r = blockIdx.x / size;
-    const T* const z = static_cast<const T*>(a.logits) + r * a.row_stride;
-    T* const g = static_cast<T*>(a.grad) + r * a.grad_stride;
-    const Row<T> row(z, a.V);
-    const int32_t v0 = min((int32_t)rank * a.slice, row.vectors), v1 = min(v0 + a.slice, row.vectors);
-    const float w = a.weight ? a.weight[r] : 1.f;
-    const bool aligned = kGrad && same_grid(z, g);
-    if (w == 0.f) {
-        if (kGrad) {
-            const Raw<T, kPer<T>> zero = {};
-            for (int32_t v = v0 + tid; v < v1; v += kThreads) store_vector(row, g, aligned, v, zero);
-        }
-        if (rank == 0 && tid == 0) {
-            a.loss[r] = 0.f;
-            if (a.stats) a.stats[2 * r] = a.stats[2 * r + 1] = 0.f;
-        }
-        return;
-    }
-    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");     // (waited for before any CTA writes to another)
+    const int32_t clusters = gridDim.x / size;
     Raw<T, kPer<T>>* const mine = reinterpret_cast<Raw<T, kPer<T>>*>(held);
-    // (but for the row's first and last vector, every vector lies inside it)
-    const int32_t whole0 = row.lead ? 1 : 0, whole1 = (row.lead + a.V) / kPer<T>;
-    auto fetch = [&](int32_t from, int32_t to) {
-        const int32_t end = min(to, whole1);
-        for (int32_t v = max(from, whole0) + tid; v < end; v += kThreads) async_copy_16(smem_u32(mine + (v - from)), z + row.first(v), 16);
-        if (tid < 2) {
-            const int32_t v = tid == 0 ? 0 : row.vectors - 1;
-            if ((v < whole0 || v >= whole1) && v >= from && v < to) load_vector(row, v, mine[v - from]);
+    auto row_of = [&](int64_t r) { return Row<T>(static_cast<const T*>(a.logits) + r * a.row_stride, a.V); };
+    auto first_of = [&](const Row<T>& row) { return min((int32_t)rank * a.slice, row.vectors); };
+    auto last_of = [&](const Row<T>& row) { return min((int32_t)(rank + 1) * a.slice, row.vectors); };
+    auto weight_of = [&](int64_t r) { return a.weight ? a.weight[r] : 1.f; };
+    // Row r or the next of this cluster that has a weight; those before it get zeros.
+    auto next_live = [&](int64_t r) {
+        for (; r < a.rows && weight_of(r) == 0.f; r += clusters) {
+            if (rank == 0 && tid == 0) {
+                a.loss[r] = 0.f;
+                if (a.stats) a.stats[2 * r] = a.stats[2 * r + 1] = 0.f;
+            }
+            if (kGrad && !lists) {
+                const Row<T> row = row_of(r);
+                T* const g = static_cast<T*>(a.grad) + r * a.grad_stride;
+                const bool aligned = same_grid(row.p, g);
+                const Raw<T, kPer<T>> zero = {};
+                for (int32_t v = first_of(row) + tid, end = last_of(row); v < end; v += threads) store_vector(row, g, aligned, v, zero);
+            }
         }
+        return r;
     };
-    fetch(v0, min(v0 + a.tile, v1));
+    // The copy of vector v of a row into place i, by the thread that will use it.
+    auto fetch = [&](const Row<T>& row, int32_t v, int32_t i) {
+        const int32_t at = row.first(v);
+        if (row.whole(at)) async_copy_16(smem_u32(mine + i), row.p + at, 16);
+        else load_vector(row, v, mine[i]);
+    };
 
-    // the list: targets, and the student's logits there, which every CTA of the cluster reads before any of them writes
-    const Entry e = read_entry(a, r, s.ids);
-    float top = e.id >= 0 ? to_float<T>(z[e.id]) : -INFINITY;
-    if (warp < kListWarps) {
-        float ref = ceilf(top * a.scale);
-        if (ref == -INFINITY) top = -INFINITY;                        // (the lowest numbers, where masks put them)
-        ref = warp_max(ref);
-        const float sum = warp_sum(top == -INFINITY ? 0.f : exp2_fast(exponent(top, a, ref)));
-        const ListPart part = list_part(e, a.rest);
-        if (lane == 0) {
-            s.top_ref[warp] = ref;
-            s.top_sum[warp] = sum;
-            s.list[warp] = part;
-        }
+    // the list's warp: the next row's list, and what is written over a row's vectors once all of them are
+    List list;
+    T* late = nullptr;
+    int owned = 0;
+    auto write_late = [&] {
+        if (late)
+            for (int j = lane; j < owned; j += 32) late[s.own[j].id] = from_float<T>(s.own[j].top);
+    };
+
+    int64_t r = next_live(blockIdx.x / size);
+    if (r >= a.rows) return;                                          // (the whole cluster)
+    if (lists) {
+        list.read(a, r);
+    } else {
+        const Row<T> row = row_of(r);
+        const int32_t v0 = first_of(row), count = last_of(row) - v0;
+        for (int32_t i = tid; i < count; i += threads) fetch(row, v0 + i, i);
     }
+    cluster_barrier();                                                // (no CTA writes to one that has not started)
+    for (int turn = 0; r < a.rows; turn ^= 1) {
+        const Row<T> row = row_of(r);
+        const int32_t v0 = first_of(row), count = last_of(row) - v0;
+        const float w = weight_of(r);
+        T* const g = static_cast<T*>(a.grad) + r * a.grad_stride;
+        const int64_t after = next_live(r + clusters);
+        const Row<T> next = row_of(after < a.rows ? after : r);
+        const int32_t next0 = first_of(next), next_count = after < a.rows ? last_of(next) - next0 : 0;
 
-    // the sums over this CTA's part of the row without the listed
-    float ref = -INFINITY, S = 0.f;
-    for (int32_t from = v0; from < v1; from += a.tile) {
-        const int32_t to = min(from + a.tile, v1);
-        if (from != v0) {
-            __syncthreads();
-            fetch(from, to);
-        }
-        async_copy_wait();
+        uint32_t fault = 0;
+        if (lists) fault = list.check(a);
+        else async_copy_wait();
         __syncthreads();
-        const int32_t at = e.id - row.first(from);
-        if (e.id >= 0 && at >= 0 && at < (to - from) * kPer<T>) reinterpret_cast<T*>(held)[at] = neg_inf<T>();
-        __syncthreads();
-        for (int32_t v = tid; v < to - from; v += kThreads) {
-            const Raw<T, kPer<T>> x = mine[v];
-            const float m = Maximum<T>::of(x).value();
-            if (m * a.scale > ref) {
-                const float up = ceilf(m * a.scale);
-                S *= reference_step(ref, up);
-                ref = up;
+        if (lists) {
+            if (kGrad) write_late();
+            __syncwarp();
+            // the entries that lie here, side by side, and their elements out of the row
+            owned = 0;
+#pragma unroll
+            for (int c = 0; c < kEntries; ++c) {
+                if (32 * c >= a.n) continue;
+                const int32_t at = list.ids[c] - row.first(v0);
+                const bool here = list.ids[c] >= 0 && at >= 0 && at < count * kPer<T>;
+                const uint32_t all = __ballot_sync(0xffffffffu, here);
+                if (here) {
+                    T* const e = reinterpret_cast<T*>(held) + at;
+                    const float top = to_float<T>(*e);
+                    // (the lowest numbers, where masks put them, count as -infinity)
+                    s.own[owned + __popc(all & ((1u << lane) - 1u))] = Own{list.ids[c], list.lps[c], top * a.scale == -INFINITY ? -INFINITY : top};
+                    *e = neg_inf<T>();
+                }
+                owned += __popc(all);
             }
-            const Exponentials<true> e2(a, ref == -INFINITY ? 0.f : ref);
-            Pair part = e2(elements(x, 0));
-#pragma unroll
-            for (int i = 1; i < kPer<T> / 2; ++i) part = add_2(part, e2(elements(x, i)));
-            S += both(part).x + both(part).y;
         }
-    }
-    warp_join(ref, S);
-    if (lane == 0) {
-        s.refs[warp] = ref;
-        s.sums[warp] = S;
-    }
-    __syncthreads();
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-    if (warp == 0) {
-        const Asked asked = asked_of(s.list, a.n, a.rest);
-        if (lane == 0) s.asked = asked;
-        // every CTA gets every CTA's sum: lane i writes into CTA i
-        const float one = s.refs[lane % kWarps], all = warp_max(one);
-        double sum = (double)s.sums[lane % kWarps] * reference_step_64(one, all);
+        __syncthreads();
+
+        float ref = -INFINITY;
+        if (!lists) {
+            Pair sum = pair_of(0.f, 0.f);
+            for (int32_t i = tid; i < count; i += threads) {
+                const Raw<T, kPer<T>> x = mine[i];
+                const float m = Maximum<T>::of(x).value() * a.scale;
+                if (m > ref) {
+                    const float up = ceilf(m), step = reference_step(ref, up);
+                    sum = mul_2(sum, pair_of(step, step));
+                    ref = up;
+                }
+                const Exponentials<true> e2(a, ref == -INFINITY ? 0.f : ref);
+                Pair some = e2(elements(x, 0));
 #pragma unroll
-        for (int o = kWarps / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane < (int)size) {
-            put_64(in_cta(&s.peer_S[rank], lane), sum);
-            put_32(in_cta(&s.peer_ref[rank], lane), all);
+                for (int k = 1; k < kPer<T> / 2; ++k) some = add_2(some, e2(elements(x, k)));
+                sum = add_2(sum, some);
+                if (!kGrad && i < next_count) fetch(next, next0 + i, i);
+            }
+            if (!kGrad)                                               // (a row off the 16-byte grid may have one vector more than this one)
+                for (int32_t i = tid + (count - tid + threads - 1) / threads * threads; i < next_count; i += threads) fetch(next, next0 + i, i);
+            float S = both(sum).x + both(sum).y;
+            warp_join(ref, S);
+            if (lane == 0) {
+                s.refs[warp] = ref;
+                s.sums[warp] = S;
+            }
+        } else {
+            if (after < a.rows) list.read(a, after);
+            Part part = {0, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, -INFINITY, -INFINITY, a.rest ? 0.f : -INFINITY, 0};
+            for (int j = lane; j < owned; j += 32) {
+                part.top_ref = fmaxf(part.top_ref, ceilf(s.own[j].top * a.scale));
+                if (!a.rest) part.shift = fmaxf(part.shift, s.own[j].lp);
+            }
+            part.top_ref = warp_max(part.top_ref);
+            part.shift = warp_max(part.shift);
+            const float base = part.top_ref == -INFINITY ? 0.f : part.top_ref, shift = part.shift == -INFINITY ? 0.f : part.shift;
+            for (int j0 = 0; j0 < owned; j0 += 32) {
+                const bool in = j0 + lane < owned;
+                const Own o = s.own[in ? j0 + lane : 0];
+                const bool number = o.top > -INFINITY || o.top != o.top;
+                // z log2(e) / temperature
+                const Two up = two_product(o.top, a.scale) + Two{o.top * a.scale_low, 0.f};
+                const Two target = target_of(o.lp, shift);
+                if (in && number) part.top = part.top + exp2_two(up + Two{-base, 0.f});
+                if (in) {
+                    part.targets = part.targets + target;
+                    part.fixed += fixed_of(target);
+                    if (target.hi > 0.f && number) part.cross = part.cross + target * (Two{o.lp, 0.f} - up * SPECDEC_TWO(kLn2));
+                    else if (target.hi > 0.f) part.endless = 1;
+                }
+            }
+            part.top = warp_sum(part.top);
+            part.targets = warp_sum(part.targets);
+            part.cross = warp_sum(part.cross);
+            part.endless = __any_sync(0xffffffffu, part.endless);
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) part.fixed += __shfl_xor_sync(0xffffffffu, part.fixed, o);
+            if (lane == 0) s.part = part;
         }
+        __syncthreads();
+        if (lists) {
+            const bool there = lane < threads / 32;
+            const float one = there ? s.refs[lane] : -INFINITY, rest_ref = warp_max(one);
+            const Two rest = warp_sum(Two{there ? s.sums[lane] * reference_step(one, rest_ref) : 0.f, 0.f});
+            if (lane == 0) {
+                s.part.rest = rest;
+                s.part.rest_ref = rest_ref;
+            }
+            __syncwarp();
+            // to every CTA, eight bytes a lane at a time
+            for (int i = lane; i < kPartWords * (int)size; i += 32) {
+                const int word = i % kPartWords, to = i / kPartWords;
+                put_64(in_cta(&s.peer[turn][rank], to) + word * 8, reinterpret_cast<const long long*>(&s.part)[word]);
+            }
+        }
+        cluster_barrier();
+
+        // all of the row
+        const bool there = lane % kMaxCluster < (int)size;
+        const Part* const one = &s.peer[turn][there ? lane % kMaxCluster : 0];
+        const float one_rest = there ? one->rest_ref : -INFINITY, one_top = there ? one->top_ref : -INFINITY;
+        const float rest_ref = half_max(one_rest), top_ref = half_max(one_top), all_ref = fmaxf(rest_ref, top_ref);
+        const float S_rest = half_sum(there ? one->rest.hi * reference_step(one_rest, rest_ref) : 0.f);
+        const float S_top_all = half_sum(there ? one->top.hi * reference_step(one_top, all_ref) : 0.f);
+        const float S_rest_all = S_rest * reference_step(rest_ref, all_ref), S_all = S_rest_all + S_top_all;
+        float listed, left_over = 0.f;             // the masses of the targets and of what they leave
+        if (a.rest) {
+            const long long fixed = half_sum(there ? one->fixed : 0ll), unit = (long long)kFixed;
+            listed = from_fixed(fixed);
+            left_over = fixed < unit ? from_fixed(unit - fixed) : 0.f;
+        } else {
+            listed = half_max(there && one->targets.hi > 0.f ? 1.f : 0.f);
+        }
+        const bool none = all_ref == -INFINITY && !(S_all != S_all), asks = listed + left_over > 0.f;
+        const bool tail = !(S_rest == 0.f);        // (where the student leaves nothing to the rest there is no such category)
+        const float left = tail ? left_over : 0.f, each = none || !asks ? 0.f : w * a.inverse;
+        if (!lists) {
+            if constexpr (kGrad) {
+                // outside the list: e_j (M / S - r / S_rest), which is (S_rest sum t - r S_top) / (S S_rest) without the cancellation of M and r
+                const float factor = tail ? ((listed * S_rest_all - left * S_top_all) / S_all) / S_rest * each : 0.f;
+                const Exponentials<sizeof(T) == 4> e2(a, rest_ref == -INFINITY ? 0.f : rest_ref);
+                const Pair factors = pair_of(factor, factor);
+                const bool aligned = same_grid(row.p, g);
+                for (int32_t i = tid; i < max(count, next_count); i += threads) {
+                    if (i < count) {
+                        Raw<T, kPer<T>> x = mine[i];
+#pragma unroll
+                        for (int k = 0; k < kPer<T> / 2; ++k) put_elements(x, k, mul_2(e2(elements(x, k)), factors));
+                        store_vector(row, g, aligned, v0 + i, x);
+                    }
+                    if (i < next_count) fetch(next, next0 + i, i);
+                }
+            }
+        } else {
+            float norm = 1.f, shift = 0.f;
+            if (!a.rest && asks) {
+                const float some = there && one->targets.hi > 0.f ? one->shift : -INFINITY;
+                shift = half_max(some);
+                norm = 1.f / half_sum(some == -INFINITY ? 0.f : one->targets.hi * expf(some - shift));
+            }
+            if constexpr (kGrad) {
+                const float per_all = none ? 0.f : (listed + left) / S_all;
+                late = g;
+                for (int j = lane; j < owned; j += 32) {
+                    const Own o = s.own[j];
+                    const float share = o.top == -INFINITY ? 0.f : exp2_fast(exponent(o.top, a, all_ref)) * per_all;
+                    s.own[j].top = (share - expf(o.lp - shift) * norm) * each;
+                }
+            }
+            if (a.status && rank == 0 && (fault || (lane == 0 && none)))
+                atomicOr(a.status + r, fault | (lane == 0 && none ? SPECDEC_ST_EMPTY_MASK_ROW : 0u));
+            if (rank == 0) {
+                // The loss in pairs of floats: near zero it is a small difference of logarithms.
+                const Two zero = {0.f, 0.f};
+                const Two rest = half_sum(there ? times(one->rest, reference_step(one_rest, rest_ref)) : zero);
+                const Two top = half_sum(there ? times(one->top, reference_step(one_top, all_ref)) : zero);
+                const Two by = there && !a.rest && one->targets.hi > 0.f ? target_of(one->shift, shift) : Two{a.rest ? 1.f : 0.f, 0.f};
+                const Two sum = half_sum(there && one->targets.hi > 0.f ? one->targets * by : zero);
+                const Two cross = half_sum(there && one->targets.hi > 0.f ? one->cross * by : zero);
+                const bool endless = __any_sync(0xffffffffu, there && one->endless);
+                const Two remains = a.rest && tail ? Two{1.f, 0.f} - sum : zero;
+                const Two logs = log2_two(lane == 0 ? times(rest, reference_step(rest_ref, all_ref)) + top : lane == 1 ? rest : lane == 2 ? remains : sum);
+                auto log_of = [&](int l, float ref) {                 // natural; what is no number stays so
+                    const Two x = {__shfl_sync(0xffffffffu, logs.hi, l), __shfl_sync(0xffffffffu, logs.lo, l)};
+                    return x.hi - x.hi == 0.f ? (x + Two{ref, 0.f}) * SPECDEC_TWO(kLn2) : Two{x.hi, 0.f};
+                };
+                const Two log_all = log_of(0, all_ref), log_rest = log_of(1, rest_ref), log_r = log_of(2, 0.f), log_sum = log_of(3, 0.f);
+                if (lane == 0) {
+                    Two loss = zero;
+                    if (asks && !none) {
+                        // sum of t_i (ln t_i - ln s_i) where t_i = exp(lp_i), and where they are renormalised
+                        if (sum.hi > 0.f) {
+                            loss = cross + sum * log_all;
+                            if (!a.rest) loss = loss * reciprocal(sum) - log_sum - Two{shift, 0.f};
+                        }
+                        if (remains.hi > 0.f) loss = loss + remains * (log_r - (log_rest - log_all));
+                    }
+                    a.loss[r] = asks && (none || endless) ? w * INFINITY : w * loss.hi;
+                    if (a.stats) {
+                        a.stats[2 * r] = log_all.hi;
+                        a.stats[2 * r + 1] = log_rest.hi;
+                    }
+                }
+            }
+        }
+        r = after;
     }
-    cluster_barrier();
-
-    float rest_ref = -INFINITY, top_ref = -INFINITY, S_rest = 0.f, S_top = 0.f;
-    for (uint32_t i = 0; i < size; ++i) rest_ref = fmaxf(rest_ref, s.peer_ref[i]);
-    for (uint32_t i = 0; i < size; ++i) S_rest += (float)s.peer_S[i] * reference_step(s.peer_ref[i], rest_ref);
-#pragma unroll
-    for (int i = 0; i < kListWarps; ++i) top_ref = fmaxf(top_ref, s.top_ref[i]);
-#pragma unroll
-    for (int i = 0; i < kListWarps; ++i) S_top += s.top_sum[i] * reference_step(s.top_ref[i], top_ref);
-    const Asked asked = s.asked;
-    const bool asks = asked.listed + asked.rest > 0.f;                // (an empty list that leaves nothing asks for nothing)
-    const float all_ref = fmaxf(rest_ref, top_ref);
-    const float S_rest_all = S_rest * reference_step(rest_ref, all_ref), S_top_all = S_top * reference_step(top_ref, all_ref);
-    const float S_all = S_rest_all + S_top_all;
-    const bool none = all_ref == -INFINITY && !(S_all != S_all);      // no finite logit
-    // Where the student leaves nothing to the rest there is no such category.
-    const bool tail = !(S_rest == 0.f);
-    const float left = tail ? asked.rest : 0.f;
-
     if constexpr (kGrad) {
-        // outside the list: e_j (M / S - r / S_rest), which is (S_rest sum t - r S_top) / (S S_rest) without the cancellation of M and r
-        const float each = none || !asks ? 0.f : w * a.inverse, mass = asked.listed + left, per_all = none ? 0.f : mass / S_all;
-        const float base = rest_ref == -INFINITY ? 0.f : rest_ref;
-        const float factor = tail ? ((asked.listed * S_rest_all - left * S_top_all) / S_all) / S_rest * each : 0.f;
-        const Exponentials<sizeof(T) == 4> e2(a, base);
-        const Pair factors = pair_of(factor, factor);
-        for (int32_t from = v0; from < v1; from += a.tile) {
-            const int32_t to = min(from + a.tile, v1);
-            if (a.tile < a.slice) {
-                __syncthreads();
-                fetch(from, to);
-                async_copy_wait();
-                __syncthreads();
-            }
-            auto change = [&](int32_t v) {
-                Raw<T, kPer<T>> x = mine[v - from];
-#pragma unroll
-                for (int i = 0; i < kPer<T> / 2; ++i) put_elements(x, i, mul_2(e2(elements(x, i)), factors));
-                return x;
-            };
-            if (aligned) {
-                const int32_t end = min(to, whole1);
-                for (int32_t v = max(from, whole0) + tid; v < end; v += kThreads) {
-                    const Raw<T, kPer<T>> x = change(v);
-                    *reinterpret_cast<uint4*>(g + row.first(v)) = *reinterpret_cast<const uint4*>(x.e);
-                }
-                if (tid < 2) {
-                    const int32_t v = tid == 0 ? 0 : row.vectors - 1;
-                    if ((v < whole0 || v >= whole1) && v >= from && v < to) store_vector(row, g, false, v, change(v));
-                }
-            } else {
-                for (int32_t v = from + tid; v < to; v += kThreads) store_vector(row, g, false, v, change(v));
-            }
-        }
         __syncthreads();
-        if (e.id >= 0 && e.id >= row.first(v0) && e.id < row.first(v1)) {
-            const float share = top == -INFINITY ? 0.f : exp2_fast(exponent(top, a, all_ref)) * per_all;
-            g[e.id] = from_float<T>((share - target_of(e, asked)) * each);
-        }
-    }
-    if (rank != 0) return;
-
-    // The loss in 64 bits: near zero it is a small difference of logarithms.
-    if (a.status && (e.fault || (tid == 0 && none))) atomicOr(a.status + r, e.fault | (tid == 0 && none ? SPECDEC_ST_EMPTY_MASK_ROW : 0u));
-    if (warp < kListWarps) {
-        const double up = top == -INFINITY ? -INFINITY : (double)top * ((double)a.scale + (double)a.scale_low) - (double)top_ref;
-        const double t = target_64(e, asked.shift), sum = warp_sum(t), listed = warp_sum(exp2_64(up)), cross = warp_sum(t > 0.0 ? t * ((double)e.lp - up * kLn2) : 0.0);
-        if (lane == 0) {
-            s.list_64[warp][0] = sum;
-            s.list_64[warp][1] = listed;
-            s.list_64[warp][2] = cross;
-        }
-    }
-    __syncthreads();
-    if (tid == 0) {
-        double sum = 0.0, listed = 0.0, cross = 0.0, others = 0.0;
-        for (int i = 0; i < kListWarps; ++i) {
-            sum += s.list_64[i][0];
-            listed += s.list_64[i][1];
-            cross += s.list_64[i][2];
-        }
-        for (uint32_t i = 0; i < size; ++i) others += s.peer_S[i] * reference_step_64(s.peer_ref[i], rest_ref);
-        const double log_all = log(others * reference_step_64(rest_ref, all_ref) + listed * reference_step_64(top_ref, all_ref)) + (double)all_ref * kLn2;
-        const double log_rest = log(others) + (double)rest_ref * kLn2;
-        double loss = 0.0;
-        if (none) {
-            loss = asks ? INFINITY : 0.0;
-        } else if (asks) {
-            const double r_64 = a.rest && tail ? fmax(0.0, 1.0 - sum) : 0.0;
-            if (sum > 0.0) {
-                // sum of t_i (ln t_i - ln s_i) where t_i = exp(lp_i), and where they are renormalised
-                loss = cross + sum * (log_all - (double)top_ref * kLn2);
-                if (!a.rest) loss = loss / sum - log(sum) - (double)asked.shift;
-            }
-            if (r_64 > 0.0) loss += r_64 * (log(r_64) - (log_rest - log_all));
-        }
-        a.loss[r] = (float)((double)w * loss);
-        if (a.stats) {
-            a.stats[2 * r] = (float)log_all;
-            a.stats[2 * r + 1] = (float)log_rest;
-        }
+        if (lists) write_late();
     }
 }
+
+// ---------------------------------------------------------------- backward
 
 // log2(e) x = whole - less, whole a whole number (x's, rounded up) and 0 <= less <= 1 without the product's rounding.
 __device__ __forceinline__ void in_octaves(float x, float* whole, float* less)
 {
-    constexpr float kHigh = 1.44269504f, kLow = (float)(1.4426950408889634073599 - (double)kHigh);
+    constexpr float kHigh = (float)kLog2e, kLow = (float)(kLog2e - (double)kHigh);
     const float p = x * kHigh;
     *whole = ceilf(p);
     *less = (*whole - p) - fmaf(x, kHigh, -p) - x * kLow;
@@ -445,8 +488,8 @@ constexpr int kChunk = 8;                          // vectors a thread
 
 template <typename T> __global__ void __launch_bounds__(kBackThreads) specdec_distill_backward_kernel(const Args a, const int32_t chunks)
 {
-    __shared__ ListPart parts[kListWarps];
-    __shared__ __align__(16) int32_t ids[SPECDEC_TOP_MAX];
+    __shared__ Own own[SPECDEC_TOP_MAX];           // of the list, what lies in this chunk
+    __shared__ float s_listed, s_left, s_shift, s_norm;
     after_predecessor();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t r = blockIdx.x / (uint32_t)chunks;
@@ -476,22 +519,56 @@ template <typename T> __global__ void __launch_bounds__(kBackThreads) specdec_di
         }
     }
     const float lse = a.stats[2 * r], lse_rest = a.stats[2 * r + 1];
-    const Entry e = read_entry(a, r, ids);
-    const bool here = e.id >= 0 && e.id >= row.first(v0) && e.id < row.first(min(v0 + kChunk * kBackThreads, row.vectors));
-    const float top = here ? to_float<T>(z[e.id]) : 0.f;              // (before the row is written: the gradient may lie over it)
-    if (warp < kListWarps) {
-        const ListPart part = list_part(e, a.rest);
-        if (lane == 0) parts[warp] = part;
+    int owned = 0;
+    if (warp == 0) {
+        List list;
+        list.read(a, r);
+        const uint32_t fault = list.check(a);
+        if (a.status && v0 == 0 && fault) atomicOr(a.status + r, fault);
+        float shift = a.rest ? 0.f : -INFINITY, sum = 0.f;
+        long long fixed = 0;
+        if (!a.rest) {
+#pragma unroll
+            for (int c = 0; c < kEntries; ++c)
+                if (list.ids[c] >= 0) shift = fmaxf(shift, list.lps[c]);
+            shift = warp_max(shift);
+            if (shift == -INFINITY) shift = 0.f;
+        }
+        const int32_t begin = row.first(v0), end = row.first(min(v0 + kChunk * kBackThreads, row.vectors));
+#pragma unroll
+        for (int c = 0; c < kEntries; ++c) {
+            if (32 * c >= a.n) continue;
+            const int32_t id = list.ids[c];
+            if (a.rest) fixed += id >= 0 ? fixed_of(target_of(list.lps[c], 0.f)) : 0;
+            else sum += id >= 0 ? expf(list.lps[c] - shift) : 0.f;
+            const bool here = id >= 0 && id >= begin && id < end;
+            const uint32_t all = __ballot_sync(0xffffffffu, here);
+            // (the student's logit is read before the row is written: the gradient may lie over it)
+            if (here) own[owned + __popc(all & ((1u << lane) - 1u))] = Own{id, list.lps[c], to_float<T>(z[id])};
+            owned += __popc(all);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+            fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        }
+        if (lane == 0) {
+            const long long unit = (long long)kFixed;
+            s_listed = a.rest ? from_fixed(fixed) : sum > 0.f ? 1.f : 0.f;
+            s_left = a.rest && fixed < unit ? from_fixed(unit - fixed) : 0.f;
+            s_shift = shift;
+            s_norm = a.rest || !(sum > 0.f) ? 1.f : 1.f / sum;
+        }
     }
     __syncthreads();
-    const Asked asked = asked_of(parts, a.n, a.rest);
+    const float listed = s_listed, left_over = s_left;
     // the exponentials of this kernel are taken at the rest's sum; where there is none, no element is outside the list
-    const bool tail = !(lse_rest == -INFINITY), none = lse == -INFINITY || !(asked.listed + asked.rest > 0.f);
-    const float left = tail ? asked.rest : 0.f, each = none ? 0.f : w * a.inverse;
+    const bool tail = !(lse_rest == -INFINITY), none = lse == -INFINITY || !(listed + left_over > 0.f);
+    const float left = tail ? left_over : 0.f, each = none ? 0.f : w * a.inverse;
     float all, all_less, ref, ref_less;
     in_octaves(none ? 0.f : lse, &all, &all_less);
     in_octaves(tail ? lse_rest : 0.f, &ref, &ref_less);
-    const float factor = tail ? ((asked.listed + left) * exp2f(ref - all + all_less) - left * exp2f(ref_less)) * each : 0.f;
+    const float factor = tail ? ((listed + left) * exp2f(ref - all + all_less) - left * exp2f(ref_less)) * each : 0.f;
     const Exponentials<sizeof(T) == 4> e2(a, ref);
     const Pair factors = pair_of(factor, factor);
 #pragma unroll
@@ -503,58 +580,84 @@ template <typename T> __global__ void __launch_bounds__(kBackThreads) specdec_di
         store_vector(row, g, aligned, v, x[i]);
     }
     __syncthreads();
-    if (here) {
-        const float share = exp2f(exponent(top, a, all) + all_less) * (asked.listed + left);
-        g[e.id] = from_float<T>((share - target_of(e, asked)) * each);
+    for (int j = tid; warp == 0 && j < owned; j += 32) {
+        const Own o = own[j];
+        const float share = exp2f(exponent(o.top, a, all) + all_less) * (listed + left);
+        g[o.id] = from_float<T>((share - expf(o.lp - s_shift) * s_norm) * each);
     }
-    if (v0 == 0 && a.status && e.fault) atomicOr(a.status + r, e.fault);
 }
 
 // ---------------------------------------------------------------- host
 
 struct Shape {
-    int32_t cluster, slice, tile;
+    int32_t cluster, slice, threads;
 };
 
-// A row goes to the fewest CTAs that keep two of them on an SM, more where the rows alone do not
-// fill the GPU; what is longer than eight times kTileBytes is read a second time for the gradient.
+// A row goes to the fewest CTAs that keep four of them on an SM, more where the rows alone do not fill the GPU, and at
+// most to sixteen; each has as many warps as its part takes.
 template <typename T> Shape shape_of(int32_t rows, int32_t V)
 {
     const int32_t vectors = most_vectors<T>(V);
     int32_t cluster = 1;
     auto slice = [&] { return (vectors + cluster - 1) / cluster; };
-    while (cluster < kMaxCluster && (slice() > kTileBytes / 16 || ((int64_t)rows * cluster < 304 && slice() > 8 * 1024 / 16))) cluster *= 2;
-    const int32_t s = (slice() + 7) / 8 * 8;
-    return Shape{cluster, s, s < kTileBytes / 16 ? s : kTileBytes / 16};
+    while (cluster < kMaxCluster && (slice() > kSliceBytes / 16 || ((int64_t)rows * cluster < 152 && slice() > 8 * 1024 / 16))) cluster *= 2;
+    const int32_t warps = (slice() + 32 * kLaneVectors - 1) / (32 * kLaneVectors);
+    return Shape{cluster, slice(), ((warps < kRowWarps ? warps : kRowWarps) + 1) * 32};
 }
 
-cudaError_t launch_clusters(void (*kernel)(Args), const Args& a, const Shape& shape, std::atomic<uint64_t>& allowed, cudaStream_t stream)
+// What a kernel remembers: the devices on which it may have its shared memory and clusters of sixteen, and how many clusters of the
+// shape last asked for are resident at once (the shape in the upper half).
+struct Memory {
+    std::atomic<uint64_t> allowed{0}, resident{0};
+};
+
+cudaError_t launch_clusters(void (*kernel)(Args), const Args& a, const Shape& shape, Memory& memory, cudaStream_t stream)
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     const uint64_t bit = 1ull << (dev & 63);
-    for (int attempt = allowed.load() & bit ? 0 : 1; e == cudaSuccess; ++attempt) {
+    for (int attempt = memory.allowed.load() & bit ? 0 : 1; e == cudaSuccess; ++attempt) {
         // (once a device; again where a launch fails, for a device may have been reset)
-        if (attempt > 0) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileBytes);
-        if (e != cudaSuccess) break;
+        if (attempt > 0) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostBytes);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) break;
+        }
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)((int64_t)a.rows * shape.cluster));
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = (size_t)shape.tile * 16;
+        cfg.gridDim = dim3((unsigned)shape.cluster);
+        cfg.blockDim = dim3((unsigned)shape.threads);
+        cfg.dynamicSmemBytes = (size_t)shape.slice * 16;
         cfg.stream = stream;
         cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim = {(unsigned)shape.cluster, 1, 1};
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {(unsigned)shape.cluster, 1, 1};
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const uint64_t key = (uint64_t)(dev & 63) << 58 | (uint64_t)shape.cluster << 52 | (uint64_t)(shape.threads / 32) << 47 | (uint64_t)shape.slice << 32;
+        uint64_t known = memory.resident.load();
+        if ((known >> 32) != (key >> 32)) {
+            int clusters = 0;
+            e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+            if (e != cudaSuccess || clusters < 1) {
+                (void)cudaGetLastError();
+                if (e == cudaSuccess || attempt > 0) return e != cudaSuccess ? e : cudaErrorInvalidConfiguration;
+                e = cudaSuccess;
+                continue;
+            }
+            known = key | (uint32_t)clusters;
+            memory.resident = known;
+        }
+        const uint32_t clusters = (uint32_t)known;
         cfg.numAttrs = 2;
+        cfg.gridDim = dim3((clusters < (uint32_t)a.rows ? clusters : (uint32_t)a.rows) * (unsigned)shape.cluster);
         if (cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess) {
-            allowed |= bit;
+            memory.allowed |= bit;
             return cudaSuccess;
         }
-        if (attempt > 0) e = cudaErrorUnknown;
         (void)cudaGetLastError();
+        if (attempt > 0) e = cudaErrorUnknown;
     }
     (void)cudaGetLastError();
     return e;
@@ -562,13 +665,12 @@ cudaError_t launch_clusters(void (*kernel)(Args), const Args& a, const Shape& sh
 
 template <typename T> specdec_status_t launch_forward(Args a, cudaStream_t stream)
 {
-    static std::atomic<uint64_t> allowed[2];
+    static Memory memory[2];
     const Shape shape = shape_of<T>(a.rows, a.V);
-    if ((int64_t)a.rows * shape.cluster > 0x7fffffff) return SPECDEC_ERR_UNSUPPORTED;
+    if (shape.slice > kMostBytes / 16) return SPECDEC_ERR_UNSUPPORTED;
     a.slice = shape.slice;
-    a.tile = shape.tile;
-    const cudaError_t e = a.grad ? launch_clusters(specdec_distill_kernel<T, true>, a, shape, allowed[1], stream)
-                                 : launch_clusters(specdec_distill_kernel<T, false>, a, shape, allowed[0], stream);
+    const cudaError_t e = a.grad ? launch_clusters(specdec_distill_kernel<T, true>, a, shape, memory[1], stream)
+                                 : launch_clusters(specdec_distill_kernel<T, false>, a, shape, memory[0], stream);
     return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }
 
@@ -603,7 +705,7 @@ Args args_of(const void* logits, int32_t rows, int32_t V, int64_t row_stride, co
     const double c = scale_of(temperature);
     const float high = std::nextafterf((float)c, 0.f), low = std::fmax((float)(c - (double)high), 1e-30f);
     return Args{logits, row_stride, V, rows, top_ids, top_logprobs, n, high, low, (float)(1.0 / temperature), rest,
-                weight, loss, stats, grad, grad_row_stride, status, 0, 0};
+                weight, loss, stats, grad, grad_row_stride, status, 0};
 }
 
 }  // namespace

@@ -95,16 +95,92 @@ inline double scale_of(double temperature) { return 1.4426950408889634073599 / t
 // beyond fp32: the reference stays finite, and their terms are 0.)
 __device__ __forceinline__ float whole_reference(float m, float c) { return ceilf(fmaxf(m * c, -3.0e38f)); }
 
-// 2^(a - b) for references a <= b: exact, and 0 where a is an empty sum's or the power is under the type's normal numbers.
+// 2^(a - b) for references a <= b: exact, and 0 where a is an empty sum's or the power is under fp32's normal numbers.
 __device__ __forceinline__ float reference_step(float a, float b)
 {
     const int d = (int)fmaxf(a - b, -127.f);
     return d == -127 ? 0.f : __int_as_float((127 + d) << 23);
 }
-__device__ __forceinline__ double reference_step_64(float a, float b)
+
+// A number as the sum of two floats, |lo| at most half an ulp of hi: 2^-46 or so from additions and products by fp32's own
+// instructions. This part has few 64-bit ones: a warp's takes an SM some 16 clocks.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two two_ordered(float a, float b)         // |a| >= |b|, or a = 0
 {
-    const int d = (int)fmaxf(a - b, -1023.f);
-    return d == -1023 ? 0.0 : __hiloint2double((1023 + d) << 20, 0);
+    const float s = __fadd_rn(a, b);
+    return Two{s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Two two_sum(float a, float b)
+{
+    const float s = __fadd_rn(a, b), c = __fsub_rn(s, a);
+    return Two{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, c)), __fsub_rn(b, c))};
+}
+__device__ __forceinline__ Two two_product(float a, float b)
+{
+    const float p = __fmul_rn(a, b);
+    return Two{p, __fmaf_rn(a, b, -p)};
+}
+__device__ __forceinline__ Two operator+(Two a, Two b)
+{
+    const Two s = two_sum(a.hi, b.hi);
+    return two_ordered(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ Two operator-(Two a) { return Two{-a.hi, -a.lo}; }
+__device__ __forceinline__ Two operator-(Two a, Two b) { return a + -b; }
+__device__ __forceinline__ Two operator*(Two a, Two b)
+{
+    const Two p = two_product(a.hi, b.hi);
+    return two_ordered(p.hi, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, p.lo)));
+}
+__device__ __forceinline__ Two times(Two a, float power_of_two) { return Two{a.hi * power_of_two, a.lo * power_of_two}; }
+// A constant, to 48 bits.
+#define SPECDEC_TWO(x) (::specdec::Two{(float)(x), (float)((x) - (double)(float)(x))})
+constexpr double kLn2 = 0.69314718055994530941723, kLog2e = 1.4426950408889634073599;
+
+// 2^y to 2^-42: y = k + f with k whole, v = f ln 2 / 8, exp(v) by its series (|v| < 0.044: from the fourth power on in fp32),
+// squared three times. 0 below 2^-125.
+__device__ __forceinline__ Two exp2_two(Two y)
+{
+    if (!(y.hi > -125.f)) return Two{y.hi != y.hi ? y.hi : 0.f, 0.f};
+    const float k = rintf(y.hi);
+    const Two v = two_ordered(__fsub_rn(y.hi, k), y.lo) * SPECDEC_TWO(kLn2 / 8.0), square = v * v;
+    const float x = v.hi, fourth = square.hi * square.hi;
+    const float series = fmaf(fmaf(fmaf(x, 1.f / 5040.f, 1.f / 720.f), x, 1.f / 120.f), x, 1.f / 24.f) * fourth;
+    Two e = square * (v * SPECDEC_TWO(1.0 / 6.0) + Two{0.5f, 0.f}) + v + Two{series, 0.f};
+    e = Two{1.f, 0.f} + e;
+    e = e * e;
+    e = e * e;
+    e = e * e;
+    return times(times(e, __int_as_float((127 + (int)k / 2) << 23)), __int_as_float((127 + (int)k - (int)k / 2) << 23));
+}
+// log2 x, x > 0 and no subnormal: fp32's, put right by one step of Newton's method (-infinity for 0; infinity and NaN stay).
+__device__ __forceinline__ Two log2_two(Two x)
+{
+    if (!(x.hi > 0.f) || x.hi == INFINITY) return Two{x.hi == 0.f ? -INFINITY : x.hi, 0.f};
+    const int e = (__float_as_int(x.hi) >> 23) - 127;
+    const float down = __int_as_float((127 - e / 2) << 23), more = __int_as_float((127 - (e - e / 2)) << 23);
+    const Two m = times(times(x, down), more);
+    const float y = log2f(m.hi);
+    const Two d = m * exp2_two(Two{-y, 0.f}) + Two{-1.f, 0.f};
+    return two_sum((float)e, y) + d * SPECDEC_TWO(kLog2e) + Two{-0.5f * (float)kLog2e * d.hi * d.hi, 0.f};
+}
+__device__ __forceinline__ Two shuffle_xor(Two x, int o)
+{
+    return Two{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)};
+}
+__device__ __forceinline__ Two reciprocal(Two x)
+{
+    const float r = 1.f / x.hi;
+    return Two{r, 0.f} + (Two{1.f, 0.f} - x * Two{r, 0.f}) * Two{r, 0.f};
+}
+// The sum of one number a lane, the same in every lane.
+__device__ __forceinline__ Two warp_sum(Two x)
+{
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) x = x + shuffle_xor(x, o);
+    return x;
 }
 
 // Two fp32 numbers in a register pair: one instruction adds or multiplies both.

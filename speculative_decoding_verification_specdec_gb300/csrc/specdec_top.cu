@@ -173,6 +173,13 @@ template <typename T> struct Select {
     }
 };
 
+// (z scale - log_sum) ln 2
+__device__ __forceinline__ float log_probability(float z, float scale, Two log_sum)
+{
+    const Two zc = two_product(z, scale);
+    return ((zc.hi - log_sum.hi) + (zc.lo - log_sum.lo)) * (float)kLn2;
+}
+
 // An element as one number: by value, then the lower index first. Never 0.
 __device__ __forceinline__ unsigned long long composite(uint32_t key, int32_t at)
 {
@@ -185,7 +192,7 @@ template <typename T> __global__ void __launch_bounds__(kSelectThreads) specdec_
     __shared__ unsigned long long found[kMaxFound];
     __shared__ int32_t groups[kMaxGroups];
     __shared__ uint32_t bounds[kBounds];
-    __shared__ double row_sum;
+    __shared__ Two row_sum;
     __shared__ uint32_t bound;
     __shared__ int counts[kWarps];
     __shared__ int num_groups, num_found;
@@ -224,17 +231,17 @@ template <typename T> __global__ void __launch_bounds__(kSelectThreads) specdec_
         });
         if (lane == 0) bound = max(t, 1u);
     } else if (warp == 1) {
-        // the row's sum, in 64 bits and always in the same order
+        // the row's sum, in pairs of floats and always in the same order
         const float2* sums = a.s.sums + r * a.s.units;
         float ref = -INFINITY;
         for (int u = lane; u < a.s.units; u += 32) ref = fmaxf(ref, sums[u].x);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
-        double S = 0.0;
-        for (int u = lane; u < a.s.units; u += 32) S += (double)sums[u].y * reference_step_64(sums[u].x, ref);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
-        if (lane == 0) row_sum = (double)ref + log2(S);               // in units of the exponents
+        Two S = {0.f, 0.f};
+        for (int u = lane; u < a.s.units; u += 32) S = S + Two{sums[u].y * reference_step(sums[u].x, ref), 0.f};
+        S = log2_two(warp_sum(S));
+        // in units of the exponents
+        if (lane == 0) row_sum = S.hi - S.hi == 0.f && ref > -INFINITY ? Two{ref, 0.f} + S : Two{S.hi + ref, 0.f};
     }
     __syncthreads();
     const uint32_t least = bound;
@@ -324,8 +331,7 @@ template <typename T> __global__ void __launch_bounds__(kSelectThreads) specdec_
     }
 
     // ranks among what was found: they are the places, whatever the order of the finding was
-    const double log_sum = row_sum;
-    constexpr double kLn2 = 0.69314718055994530941723;
+    const Two log_sum = row_sum;
     for (int i = tid; i < have; i += kSelectThreads) {
         const unsigned long long me = found[i];
         int rank = 0;
@@ -334,7 +340,7 @@ template <typename T> __global__ void __launch_bounds__(kSelectThreads) specdec_
         const float z = key_value((uint32_t)(me >> 32));
         a.ids[r * n + rank] = (int32_t)~(uint32_t)me;
         if (a.values) a.values[r * n + rank] = z;
-        if (a.logprobs) a.logprobs[r * n + rank] = log_sum == -INFINITY ? -INFINITY : (float)(((double)z * a.s.scale - log_sum) * kLn2);
+        if (a.logprobs) a.logprobs[r * n + rank] = log_sum.hi == -INFINITY ? -INFINITY : log_probability(z, a.s.scale, log_sum);
     }
     for (int i = have + tid; i < n; i += kSelectThreads) {
         a.ids[r * n + i] = -1;
@@ -342,8 +348,10 @@ template <typename T> __global__ void __launch_bounds__(kSelectThreads) specdec_
         if (a.logprobs) a.logprobs[r * n + i] = -INFINITY;
     }
     if (tid == 0) {
-        if (a.lse) a.lse[r] = (float)(log_sum * kLn2);
-        if (a.sums) a.sums[r] = log_sum / a.s.scale;
+        const bool number = log_sum.hi - log_sum.hi == 0.f;
+        const Two natural = number ? log_sum * SPECDEC_TWO(kLn2) : log_sum;
+        if (a.lse) a.lse[r] = natural.hi;
+        if (a.sums) a.sums[r] = number ? ((double)log_sum.hi + (double)log_sum.lo) / (double)a.s.scale : (double)log_sum.hi;
         if (a.status && have == 0) atomicOr(a.status + r, SPECDEC_ST_EMPTY_MASK_ROW);
     }
 }

@@ -67,7 +67,7 @@ def test_distill_refusals(lib, call):
         assert call(lib, rows=1, loss=None) == E.SPECDEC_ERR_INVALID_ARG and call(lib, rows=1, loss=P + 2) == E.SPECDEC_ERR_INVALID_ARG
     else:
         assert call(lib, rows=1, stats=None) == E.SPECDEC_ERR_INVALID_ARG and call(lib, rows=1, grad=None) == E.SPECDEC_ERR_INVALID_ARG
-    assert call(lib, rows=2 ** 31 - 1, V=2 ** 20, stride=2 ** 20, grad=P, gs=2 ** 20) == E.SPECDEC_ERR_UNSUPPORTED
+    assert call(lib, rows=2 ** 31 - 1, V=2 ** 21, stride=2 ** 21, grad=P, gs=2 ** 21) == E.SPECDEC_ERR_UNSUPPORTED
 
 
 def call_beam(lib, **o):

@@ -176,7 +176,8 @@ def test_many_rows_on_a_stream_and_in_a_graph(cuda):
 
 
 def test_equal_rows_give_equal_bits(cuda):
-    x, _ = L.rows(np.random.default_rng(3), 9, 20001, "f32")
+    """Rows of one alignment (another one groups a row's terms differently)."""
+    x, _ = L.rows(np.random.default_rng(3), 9, 20001, "f32", extra=3)
     x[:] = x[0].clone()
     ids, lps, lse, _ = top(x, 64)
     assert (ids == ids[0]).all() and (lps == lps[0]).all() and (lse == lse[0]).all()

@@ -91,30 +91,71 @@ struct List {
             lps[c] = j < a.n ? __ldg(a.logprobs + r * a.n + j) : -INFINITY;
         }
     }
-    // Entries that do not count become -1; the status bit of this lane's.
-    __device__ __forceinline__ uint32_t check(const Args& a)
-    {
-        const int lane = threadIdx.x & 31;
-        int32_t given[kEntries];
-        uint32_t fault = 0;
-#pragma unroll
-        for (int c = 0; c < kEntries; ++c) given[c] = ids[c];
-#pragma unroll
-        for (int c = 0; c < kEntries; ++c) {
-            if (32 * c >= a.n) continue;
-            const uint32_t same = __match_any_sync(0xffffffffu, given[c]);
-            bool bad = (same & ((1u << lane) - 1u)) != 0 || given[c] < -1 || given[c] >= a.V || !(lps[c] < INFINITY);
-#pragma unroll
-            for (int b = 0; b < c; ++b)
-                for (int l = 0; l < 32; ++l) bad |= __shfl_sync(0xffffffffu, given[b], l) == given[c];
-            if (bad && given[c] != -1) {
-                ids[c] = -1;
-                fault = SPECDEC_ST_BAD_TARGET;
-            }
-        }
-        return fault;
-    }
 };
+
+// An entry that lies in one part of a row.
+struct Own {
+    int32_t id;
+    float lp, top;                                 // top: the student's logit
+};
+// The entries that lie in elements begin .. end - 1, side by side in own, but for those that do not count: a repeated id (which lies
+// in the same part as its first listing), or no log-probability. One warp; returns how many, and the status bits of this lane's
+// entries (ids outside the vocabulary lie in no part: they count for the first).
+__device__ __forceinline__ int own_entries(const Args& a, const List& list, int32_t begin, int32_t end, Own* own, uint32_t* fault)
+{
+    const int lane = threadIdx.x & 31;
+    const uint32_t below = (1u << lane) - 1u;
+    int found = 0;
+    *fault = 0;
+#pragma unroll
+    for (int c = 0; c < kEntries; ++c) {
+        if (32 * c >= a.n) continue;
+        const int32_t id = list.ids[c];
+        if ((id < -1 || id >= a.V) && begin <= 0) *fault = SPECDEC_ST_BAD_TARGET;
+        const bool here = id >= max(begin, 0) && id < min(end, a.V);
+        const uint32_t all = __ballot_sync(0xffffffffu, here);
+        if (here) own[found + __popc(all & below)] = Own{id, list.lps[c], 0.f};
+        found += __popc(all);
+    }
+    __syncwarp();
+    int kept = 0;
+    for (int j0 = 0; j0 < found; j0 += 32) {
+        const int j = j0 + lane;
+        const Own o = own[j < found ? j : 0];
+        bool counts = j < found;
+        if (counts) {
+            counts = o.lp < INFINITY;
+            for (int k = 0; k < j; ++k) counts &= own[k].id != o.id;
+            if (!counts) *fault = SPECDEC_ST_BAD_TARGET;
+        }
+        if (found <= 32) {                         // (the usual case: nothing has to be looked at again)
+            const uint32_t all = __ballot_sync(0xffffffffu, counts);
+            __syncwarp();
+            if (counts) own[__popc(all & below)] = o;
+            kept = __popc(all);
+        } else {
+            // marked, for later entries still look at them
+            __syncwarp();
+            if (j < found) own[j].top = counts ? 0.f : 1.f;
+            kept = found;
+        }
+    }
+    __syncwarp();
+    if (found > 32) {
+        kept = 0;
+        for (int j0 = 0; j0 < found; j0 += 32) {
+            const int j = j0 + lane;
+            const Own o = own[j < found ? j : 0];
+            const bool counts = j < found && o.top == 0.f;
+            const uint32_t all = __ballot_sync(0xffffffffu, counts);
+            __syncwarp();
+            if (counts) own[kept + __popc(all & below)] = o;      // (never behind where it is read)
+            kept += __popc(all);
+            __syncwarp();
+        }
+    }
+    return kept;
+}
 
 // exp(lp - shift), a target (0 from 2^-125 down, -infinity among it).
 __device__ __forceinline__ Two target_of(float lp, float shift)
@@ -154,36 +195,34 @@ __device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank)
     return a;
 }
 __device__ __forceinline__ void put_64(uint32_t to, long long x) { asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(to), "l"(x) : "memory"); }
-__device__ __forceinline__ void cluster_barrier()
-{
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
+// (A thread that has written nothing for others: a release would wait for its own copies and stores in flight.)
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // ---------------------------------------------------------------- forward
 
-// Persistent clusters, row after row. All warps but a CTA's last hold its part of the row in shared memory, each thread its own
-// vectors, and fetch the next row's into their places as they finish with them. The last warp holds the list: it takes the listed elements
-// out of the row, sums their part in 64 bits, exchanges the CTAs' sums and works the loss out while the others write the
-// gradient. What a CTA knows of a row meets the others' by distributed shared memory and one cluster barrier a row.
+// Persistent clusters, row after row. All warps of a CTA but two hold its part of the row in shared memory, each thread its own
+// vectors, and fetch the next row's into their places as they finish with them. One warp holds the list: it takes the listed
+// elements out of the row, sums their part and exchanges the CTAs' sums. Another works the loss out while the others go on. What
+// a CTA knows of a row meets the others' by distributed shared memory and one cluster barrier a row.
 // What one CTA of a cluster knows of a row.
 struct Part {
     long long fixed;                               // the sum of the targets in 2^-56 (rest = 1)
     Two rest, top, targets, cross;                 // sums of exponentials outside and on the list; of the targets; of t (ln t - z / temperature)
     float rest_ref, top_ref, shift;
     int32_t endless;                               // whether a target lies where the student has -infinity
+    long long unused;
 };
 constexpr int kPartWords = sizeof(Part) / 8;
-// An entry that lies in this CTA's part of the row.
-struct Own {
-    int32_t id;
-    float lp, top;                                 // top: the student's logit
-};
+static_assert(kPartWords == 8, "a power of two");
 struct Shared {
     Part peer[2][kMaxCluster];                     // two rows': a CTA may be one ahead
     Part part;
+    int64_t after;                                 // the cluster's next row that has a weight
     float refs[kRowWarps], sums[kRowWarps];
-    Own own[SPECDEC_TOP_MAX];
+    float factor, base;                            // of the gradient outside the list: e_j relative to base, times factor
+    Own own[2][SPECDEC_TOP_MAX];                   // of this row and of the one before, or after
 };
 
 // The parts of all CTAs together: the lanes of each half of a warp hold one each.
@@ -206,269 +245,385 @@ __device__ __forceinline__ Two half_sum(Two x)
     return x;
 }
 
-template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps + 1) * 32, 4) specdec_distill_kernel(const Args a)
+// All CTAs' parts together, by one warp.
+struct Total {
+    float rest_ref, all_ref, S_rest, S_rest_all, S_top_all, S_all, listed, left;      // listed, left: the masses of the targets and of the rest
+    bool none, asks, tail;                         // no finite logit; whether anything is asked for; whether there is a rest
+    __device__ __forceinline__ Total(const Args& a, const Part* peer, uint32_t size)
+    {
+        const int i = threadIdx.x % kMaxCluster;
+        const bool there = i < (int)size;
+        const Part& one = peer[there ? i : 0];
+        const float one_rest = there ? one.rest_ref : -INFINITY, one_top = there ? one.top_ref : -INFINITY;
+        rest_ref = half_max(one_rest);
+        all_ref = fmaxf(rest_ref, half_max(one_top));
+        S_rest = half_sum(there ? one.rest.hi * reference_step(one_rest, rest_ref) : 0.f);
+        S_top_all = half_sum(there ? one.top.hi * reference_step(one_top, all_ref) : 0.f);
+        S_rest_all = S_rest * reference_step(rest_ref, all_ref);
+        S_all = S_rest_all + S_top_all;
+        tail = !(S_rest == 0.f);                   // (where the student leaves nothing to the rest there is no such category)
+        left = 0.f;
+        if (a.rest) {
+            const long long fixed = half_sum(there ? one.fixed : 0ll), unit = (long long)kFixed;
+            listed = from_fixed(fixed);
+            if (fixed < unit) left = from_fixed(unit - fixed);
+        } else {
+            listed = half_max(there && one.targets.hi > 0.f ? 1.f : 0.f);
+        }
+        asks = listed + left > 0.f;
+        if (!tail) left = 0.f;
+        none = all_ref == -INFINITY && !(S_all != S_all);
+    }
+    // The largest log-probability of a list that is renormalised, and one over the sum of exp(lp - shift).
+    __device__ __forceinline__ float shift(const Args& a, const Part* peer, uint32_t size) const
+    {
+        if (a.rest || !asks) return 0.f;
+        const int i = threadIdx.x % kMaxCluster;
+        return half_max(i < (int)size && peer[i].targets.hi > 0.f ? peer[i].shift : -INFINITY);
+    }
+    __device__ __forceinline__ float norm(const Args& a, const Part* peer, uint32_t size, float shift) const
+    {
+        if (a.rest || !asks) return 1.f;
+        const int i = threadIdx.x % kMaxCluster;
+        return 1.f / half_sum(i < (int)size && peer[i].targets.hi > 0.f ? peer[i].targets.hi * expf(peer[i].shift - shift) : 0.f);
+    }
+};
+
+// A CTA's part of a row: vectors begin .. begin + count - 1, of which those from number `whole` on, `wholes` of them, lie in it as a whole.
+template <typename T> struct Slice {
+    Row<T> row;
+    int32_t begin, count, whole, wholes;
+    __device__ __forceinline__ Slice(const Args& a, int64_t r, int32_t rank)
+        : row(static_cast<const T*>(a.logits) + r * a.row_stride, a.V)
+    {
+        begin = min(rank * a.slice, row.vectors);
+        count = min(begin + a.slice, row.vectors) - begin;
+        whole = max(row.lead ? 1 : 0, begin) - begin;
+        wholes = max(min((row.lead + a.V) / kPer<T>, begin + count) - begin - whole, 0);
+    }
+    __device__ __forceinline__ bool is_whole(int32_t i) const { return (uint32_t)(i - whole) < (uint32_t)wholes; }
+    __device__ __forceinline__ const T* at(int32_t i) const { return row.p + row.first(begin + i); }
+};
+
+template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps + 2) * 32, 4) specdec_distill_kernel(const Args a)
 {
     extern __shared__ __align__(16) unsigned char held[];
     __shared__ Shared s;
     after_predecessor();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x - 32;
-    const bool lists = tid >= threads;
+    constexpr int kPairs = kPer<T> / 2;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x - 64;
     const uint32_t rank = cluster_rank(), size = cluster_size();
-    const int32_t clusters = gridDim.x / size;
-    Raw<T, kPer<T>>* const mine = reinterpret_cast<Raw<T, kPer<T>>*>(held);
-    auto row_of = [&](int64_t r) { return Row<T>(static_cast<const T*>(a.logits) + r * a.row_stride, a.V); };
-    auto first_of = [&](const Row<T>& row) { return min((int32_t)rank * a.slice, row.vectors); };
-    auto last_of = [&](const Row<T>& row) { return min((int32_t)(rank + 1) * a.slice, row.vectors); };
+    const int64_t clusters = gridDim.x / size;
     auto weight_of = [&](int64_t r) { return a.weight ? a.weight[r] : 1.f; };
-    // Row r or the next of this cluster that has a weight; those before it get zeros.
-    auto next_live = [&](int64_t r) {
-        for (; r < a.rows && weight_of(r) == 0.f; r += clusters) {
-            if (rank == 0 && tid == 0) {
-                a.loss[r] = 0.f;
-                if (a.stats) a.stats[2 * r] = a.stats[2 * r + 1] = 0.f;
-            }
-            if (kGrad && !lists) {
-                const Row<T> row = row_of(r);
-                T* const g = static_cast<T*>(a.grad) + r * a.grad_stride;
-                const bool aligned = same_grid(row.p, g);
-                const Raw<T, kPer<T>> zero = {};
-                for (int32_t v = first_of(row) + tid, end = last_of(row); v < end; v += threads) store_vector(row, g, aligned, v, zero);
-            }
-        }
-        return r;
+    // the cluster's first row, and what follows a row: the next with a weight
+    int64_t r = blockIdx.x / size;
+    // (every thread arrives at the cluster's barrier once at the start and once a row, and waits for each phase)
+    auto next_live = [&](int64_t from) {
+        while (from < a.rows && weight_of(from) == 0.f) from += clusters;
+        return from;
     };
-    // The copy of vector v of a row into place i, by the thread that will use it.
-    auto fetch = [&](const Row<T>& row, int32_t v, int32_t i) {
-        const int32_t at = row.first(v);
-        if (row.whole(at)) async_copy_16(smem_u32(mine + i), row.p + at, 16);
-        else load_vector(row, v, mine[i]);
-    };
+    const int64_t first = next_live(r);
+    auto meet = [&] { barrier_sync(1, threads + 32); };               // the row's warps and the list's
 
-    // the list's warp: the next row's list, and what is written over a row's vectors once all of them are
-    List list;
-    T* late = nullptr;
-    int owned = 0;
-    auto write_late = [&] {
-        if (late)
-            for (int j = lane; j < owned; j += 32) late[s.own[j].id] = from_float<T>(s.own[j].top);
-    };
-
-    int64_t r = next_live(blockIdx.x / size);
-    if (r >= a.rows) return;                                          // (the whole cluster)
-    if (lists) {
-        list.read(a, r);
-    } else {
-        const Row<T> row = row_of(r);
-        const int32_t v0 = first_of(row), count = last_of(row) - v0;
-        for (int32_t i = tid; i < count; i += threads) fetch(row, v0 + i, i);
-    }
-    cluster_barrier();                                                // (no CTA writes to one that has not started)
-    for (int turn = 0; r < a.rows; turn ^= 1) {
-        const Row<T> row = row_of(r);
-        const int32_t v0 = first_of(row), count = last_of(row) - v0;
-        const float w = weight_of(r);
-        T* const g = static_cast<T*>(a.grad) + r * a.grad_stride;
-        const int64_t after = next_live(r + clusters);
-        const Row<T> next = row_of(after < a.rows ? after : r);
-        const int32_t next0 = first_of(next), next_count = after < a.rows ? last_of(next) - next0 : 0;
-
-        uint32_t fault = 0;
-        if (lists) fault = list.check(a);
-        else async_copy_wait();
-        __syncthreads();
-        if (lists) {
-            if (kGrad) write_late();
-            __syncwarp();
-            // the entries that lie here, side by side, and their elements out of the row
-            owned = 0;
-#pragma unroll
-            for (int c = 0; c < kEntries; ++c) {
-                if (32 * c >= a.n) continue;
-                const int32_t at = list.ids[c] - row.first(v0);
-                const bool here = list.ids[c] >= 0 && at >= 0 && at < count * kPer<T>;
-                const uint32_t all = __ballot_sync(0xffffffffu, here);
-                if (here) {
-                    T* const e = reinterpret_cast<T*>(held) + at;
-                    const float top = to_float<T>(*e);
-                    // (the lowest numbers, where masks put them, count as -infinity)
-                    s.own[owned + __popc(all & ((1u << lane) - 1u))] = Own{list.ids[c], list.lps[c], top * a.scale == -INFINITY ? -INFINITY : top};
-                    *e = neg_inf<T>();
+    if (tid < threads) {
+        // ---- the warps that hold the row
+        Raw<T, kPer<T>>* const mine = reinterpret_cast<Raw<T, kPer<T>>*>(held) + tid;
+        const uint32_t mine_at = smem_u32(mine);
+        auto zeros = [&](int64_t from, int64_t to) {                  // the gradients of rows without a weight
+            if (kGrad)
+                for (; from < min(to, (int64_t)a.rows); from += clusters) {
+                    const Slice<T> z(a, from, rank);
+                    T* const g = static_cast<T*>(a.grad) + from * a.grad_stride;
+                    const bool aligned = same_grid(z.row.p, g);
+                    const Raw<T, kPer<T>> zero = {};
+                    for (int32_t i = tid; i < z.count; i += threads) store_vector(z.row, g, aligned, z.begin + i, zero);
                 }
-                owned += __popc(all);
-            }
+        };
+        zeros(r, first);
+        r = first;
+        if (r >= a.rows) return;                                      // (the whole cluster)
+        {
+            const Slice<T> now(a, r, rank);
+            for (int32_t i = tid; i < now.count; i += threads)
+                if (now.is_whole(i)) async_copy_16(mine_at + (i - tid) * 16, now.at(i), 16);
         }
-        __syncthreads();
-
-        float ref = -INFINITY;
-        if (!lists) {
+        cluster_arrive_relaxed();                                     // (no CTA writes to one that has not started)
+        while (true) {
+            const Slice<T> now(a, r, rank);
+            async_copy_wait();
+            meet();                                          // A: the row has landed; the list's warp takes the listed out
+            meet();                                          // B
+            const int64_t after = s.after;
+            const bool more = after < a.rows;
+            const Slice<T> next(a, more ? after : r, rank);
+            const int32_t coming = more ? next.count : 0;
+            const char* const source = reinterpret_cast<const char*>(next.at(0));
+            auto fetch = [&](int32_t i) {                             // vector i of the next row into the place that this thread is done with
+                if (next.is_whole(i)) async_copy_16(mine_at + (i - tid) * 16, source + (int64_t)i * 16, 16);
+            };
+            float ref = -INFINITY;
             Pair sum = pair_of(0.f, 0.f);
-            for (int32_t i = tid; i < count; i += threads) {
-                const Raw<T, kPer<T>> x = mine[i];
-                const float m = Maximum<T>::of(x).value() * a.scale;
+            auto fold = [&](const Raw<T, kPer<T>>& x, const Exponentials<true>& e2) {
+                Pair some = e2(elements(x, 0));
+#pragma unroll
+                for (int k = 1; k < kPairs; ++k) some = add_2(some, e2(elements(x, k)));
+                sum = add_2(sum, some);
+            };
+            auto raise = [&](float m) {
+                m *= a.scale;
                 if (m > ref) {
                     const float up = ceilf(m), step = reference_step(ref, up);
                     sum = mul_2(sum, pair_of(step, step));
                     ref = up;
                 }
+            };
+            int32_t i = tid;
+            for (; i + threads < now.count; i += 2 * threads) {
+                const Raw<T, kPer<T>> x = mine[i - tid], y = mine[i - tid + threads];
+                raise(larger(Maximum<T>::of(x), Maximum<T>::of(y)).value());
                 const Exponentials<true> e2(a, ref == -INFINITY ? 0.f : ref);
-                Pair some = e2(elements(x, 0));
-#pragma unroll
-                for (int k = 1; k < kPer<T> / 2; ++k) some = add_2(some, e2(elements(x, k)));
-                sum = add_2(sum, some);
-                if (!kGrad && i < next_count) fetch(next, next0 + i, i);
+                fold(x, e2);
+                fold(y, e2);
+                if (!kGrad) {
+                    if (i < coming) fetch(i);
+                    if (i + threads < coming) fetch(i + threads);
+                }
             }
-            if (!kGrad)                                               // (a row off the 16-byte grid may have one vector more than this one)
-                for (int32_t i = tid + (count - tid + threads - 1) / threads * threads; i < next_count; i += threads) fetch(next, next0 + i, i);
+            if (i < now.count) {
+                const Raw<T, kPer<T>> x = mine[i - tid];
+                raise(Maximum<T>::of(x).value());
+                fold(x, Exponentials<true>(a, ref == -INFINITY ? 0.f : ref));
+            }
+            // (a row off the 16-byte grid may have one vector more or less than the next)
+            if (!kGrad)
+                for (; i < coming; i += threads) fetch(i);
             float S = both(sum).x + both(sum).y;
             warp_join(ref, S);
             if (lane == 0) {
                 s.refs[warp] = ref;
                 s.sums[warp] = S;
             }
-        } else {
-            if (after < a.rows) list.read(a, after);
-            Part part = {0, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, -INFINITY, -INFINITY, a.rest ? 0.f : -INFINITY, 0};
-            for (int j = lane; j < owned; j += 32) {
-                part.top_ref = fmaxf(part.top_ref, ceilf(s.own[j].top * a.scale));
-                if (!a.rest) part.shift = fmaxf(part.shift, s.own[j].lp);
-            }
-            part.top_ref = warp_max(part.top_ref);
-            part.shift = warp_max(part.shift);
-            const float base = part.top_ref == -INFINITY ? 0.f : part.top_ref, shift = part.shift == -INFINITY ? 0.f : part.shift;
-            for (int j0 = 0; j0 < owned; j0 += 32) {
-                const bool in = j0 + lane < owned;
-                const Own o = s.own[in ? j0 + lane : 0];
-                const bool number = o.top > -INFINITY || o.top != o.top;
-                // z log2(e) / temperature
-                const Two up = two_product(o.top, a.scale) + Two{o.top * a.scale_low, 0.f};
-                const Two target = target_of(o.lp, shift);
-                if (in && number) part.top = part.top + exp2_two(up + Two{-base, 0.f});
-                if (in) {
-                    part.targets = part.targets + target;
-                    part.fixed += fixed_of(target);
-                    if (target.hi > 0.f && number) part.cross = part.cross + target * (Two{o.lp, 0.f} - up * SPECDEC_TWO(kLn2));
-                    else if (target.hi > 0.f) part.endless = 1;
-                }
-            }
-            part.top = warp_sum(part.top);
-            part.targets = warp_sum(part.targets);
-            part.cross = warp_sum(part.cross);
-            part.endless = __any_sync(0xffffffffu, part.endless);
+            meet();                                          // D: the sums are there
+            cluster_wait();                                           // (the phase before: the list's warp has waited for it)
+            cluster_arrive_relaxed();
+            if constexpr (kGrad) {
+                T* const g = static_cast<T*>(a.grad) + r * a.grad_stride;
+                const bool aligned = same_grid(now.row.p, g);
+                T* const to = g + now.row.first(now.begin);
+                meet();                                      // E: the factor is there
+                const Exponentials<sizeof(T) == 4> e2(a, s.base);
+                const Pair factors = pair_of(s.factor, s.factor);
+                for (i = tid; i < now.count; i += threads) {
+                    Raw<T, kPer<T>> x = mine[i - tid];
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) part.fixed += __shfl_xor_sync(0xffffffffu, part.fixed, o);
-            if (lane == 0) s.part = part;
-        }
-        __syncthreads();
-        if (lists) {
-            const bool there = lane < threads / 32;
-            const float one = there ? s.refs[lane] : -INFINITY, rest_ref = warp_max(one);
-            const Two rest = warp_sum(Two{there ? s.sums[lane] * reference_step(one, rest_ref) : 0.f, 0.f});
-            if (lane == 0) {
-                s.part.rest = rest;
-                s.part.rest_ref = rest_ref;
+                    for (int k = 0; k < kPairs; ++k) put_elements(x, k, mul_2(e2(elements(x, k)), factors));
+                    if (i < coming) fetch(i);
+                    if (aligned && now.is_whole(i)) *reinterpret_cast<uint4*>(to + (int64_t)i * kPer<T>) = *reinterpret_cast<const uint4*>(x.e);
+                    else store_vector(now.row, g, false, now.begin + i, x);
+                }
+                for (; i < coming; i += threads) fetch(i);
+                zeros(r + clusters, after);
             }
+            r = after;
+            if (!more) break;
+        }
+        if (kGrad) meet();                                   // F: the row is written, the listed may go over it
+        cluster_wait();
+        return;
+    }
+
+    if (first >= a.rows && tid < threads + 32) return;
+    List list;
+    if (tid < threads + 32) {
+        // ---- the list's warp
+        list.read(a, first);
+        // The row's ends, where a vector lies partly outside it: an element a lane, the first vector's and the last one's.
+        T end_element;
+        auto read_ends = [&](const Slice<T>& z) {
+            const int32_t v = lane < kPer<T> ? 0 : z.row.vectors - 1, at = z.row.first(v) + lane % kPer<T>;
+            end_element = lane < 2 * kPer<T> && at >= 0 && at < a.V ? z.row.p[at] : neg_inf<T>();
+        };
+        auto put_ends = [&](const Slice<T>& z) {
+            const int32_t i = (lane < kPer<T> ? 0 : z.row.vectors - 1) - z.begin;
+            if (lane < 2 * kPer<T> && i >= 0 && i < z.count && !z.is_whole(i)) reinterpret_cast<T*>(held)[i * kPer<T> + lane % kPer<T>] = end_element;
+        };
+        // the entries of a row that lie here
+        auto own_of = [&](int64_t row, Own* own) {
+            const Slice<T> z(a, row, rank);
+            read_ends(z);
+            uint32_t fault;
+            const int n = own_entries(a, list, z.row.first(z.begin), z.row.first(z.begin + z.count), own, &fault);
+            if (a.status && fault) atomicOr(a.status + row, fault);
+            return n;
+        };
+        r = first;
+        int owned = own_of(r, s.own[0]), late_count = 0;
+        T* late = nullptr;                                            // where the listed elements' gradients go once all others are written
+        auto write_late = [&](const Own* own) {
+            for (int j = lane; j < late_count; j += 32) late[own[j].id] = from_float<T>(own[j].top);
+            __syncwarp();
+        };
+        int64_t after = next_live(r + clusters);
+        cluster_arrive();
+        int turn = 0;
+        for (;; turn ^= 1) {
+            Own* const own = s.own[turn];
+            const Slice<T> now(a, r, rank);
+            const float w = weight_of(r);
+            if (lane == 0) s.after = after;
+            meet();                                                   // A
+            const int32_t begin = now.row.first(now.begin);
+            put_ends(now);
+            __syncwarp();
+            for (int j = lane; j < owned; j += 32) {
+                T* const e = reinterpret_cast<T*>(held) + (own[j].id - begin);
+                const float top = to_float<T>(*e);
+                own[j].top = top * a.scale == -INFINITY ? -INFINITY : top;    // (the lowest numbers, where masks put them)
+                *e = neg_inf<T>();
+            }
+            meet();                                                   // B
+            if (kGrad) write_late(s.own[turn ^ 1]);
+            if (after < a.rows) list.read(a, after);
+            Part part = {0, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, -INFINITY, -INFINITY, a.rest ? 0.f : -INFINITY, 0, 0};
+            if (owned) {
+                for (int j = lane; j < owned; j += 32) {
+                    part.top_ref = fmaxf(part.top_ref, ceilf(own[j].top * a.scale));
+                    if (!a.rest) part.shift = fmaxf(part.shift, own[j].lp);
+                }
+                part.top_ref = warp_max(part.top_ref);
+                if (!a.rest) part.shift = warp_max(part.shift);
+                const float base = part.top_ref == -INFINITY ? 0.f : part.top_ref, origin = part.shift == -INFINITY ? 0.f : part.shift;
+                for (int j0 = 0; j0 < owned; j0 += 32) {
+                    const bool in = j0 + lane < owned;
+                    const Own o = own[in ? j0 + lane : 0];
+                    const bool number = o.top > -INFINITY || o.top != o.top;
+                    // z log2(e) / temperature
+                    const Two up = two_product(o.top, a.scale) + Two{o.top * a.scale_low, 0.f};
+                    const Two target = target_of(o.lp, origin);
+                    if (in && number) part.top = part.top + exp2_two(up + Two{-base, 0.f});
+                    if (in) {
+                        part.targets = part.targets + target;
+                        part.fixed += fixed_of(target);
+                        if (target.hi > 0.f && number) part.cross = part.cross + target * (Two{o.lp, 0.f} - up * SPECDEC_TWO(kLn2));
+                        else if (target.hi > 0.f) part.endless = 1;
+                    }
+                }
+                part.top = warp_sum(part.top);
+                part.targets = warp_sum(part.targets);
+                part.cross = warp_sum(part.cross);
+                part.endless = __any_sync(0xffffffffu, part.endless);
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) part.fixed += __shfl_xor_sync(0xffffffffu, part.fixed, o);
+            }
+            if (!kGrad) cluster_wait();                               // (the phase before)
+            else if (!late) cluster_wait();                           // (with a gradient: the first)
+            meet();                                                   // D
+            {
+                const bool holds = lane < threads / 32;
+                const float one = holds ? s.refs[lane] : -INFINITY;
+                part.rest_ref = half_max(one);                        // (both of the lower half's lanes)
+                part.rest = half_sum(Two{holds ? s.sums[lane] * reference_step(one, part.rest_ref) : 0.f, 0.f});
+            }
+            if (lane == 0) s.part = part;
             __syncwarp();
             // to every CTA, eight bytes a lane at a time
-            for (int i = lane; i < kPartWords * (int)size; i += 32) {
-                const int word = i % kPartWords, to = i / kPartWords;
-                put_64(in_cta(&s.peer[turn][rank], to) + word * 8, reinterpret_cast<const long long*>(&s.part)[word]);
-            }
-        }
-        cluster_barrier();
-
-        // all of the row
-        const bool there = lane % kMaxCluster < (int)size;
-        const Part* const one = &s.peer[turn][there ? lane % kMaxCluster : 0];
-        const float one_rest = there ? one->rest_ref : -INFINITY, one_top = there ? one->top_ref : -INFINITY;
-        const float rest_ref = half_max(one_rest), top_ref = half_max(one_top), all_ref = fmaxf(rest_ref, top_ref);
-        const float S_rest = half_sum(there ? one->rest.hi * reference_step(one_rest, rest_ref) : 0.f);
-        const float S_top_all = half_sum(there ? one->top.hi * reference_step(one_top, all_ref) : 0.f);
-        const float S_rest_all = S_rest * reference_step(rest_ref, all_ref), S_all = S_rest_all + S_top_all;
-        float listed, left_over = 0.f;             // the masses of the targets and of what they leave
-        if (a.rest) {
-            const long long fixed = half_sum(there ? one->fixed : 0ll), unit = (long long)kFixed;
-            listed = from_fixed(fixed);
-            left_over = fixed < unit ? from_fixed(unit - fixed) : 0.f;
-        } else {
-            listed = half_max(there && one->targets.hi > 0.f ? 1.f : 0.f);
-        }
-        const bool none = all_ref == -INFINITY && !(S_all != S_all), asks = listed + left_over > 0.f;
-        const bool tail = !(S_rest == 0.f);        // (where the student leaves nothing to the rest there is no such category)
-        const float left = tail ? left_over : 0.f, each = none || !asks ? 0.f : w * a.inverse;
-        if (!lists) {
+            for (int i = lane; i < kPartWords * (int)size; i += 32)
+                put_64(in_cta(&s.peer[turn][rank], i / kPartWords) + i % kPartWords * 8, reinterpret_cast<const long long*>(&s.part)[i % kPartWords]);
+            cluster_arrive();
             if constexpr (kGrad) {
+                cluster_wait();
+                const Total all(a, s.peer[turn], size);
+                const float each = all.none || !all.asks ? 0.f : w * a.inverse;
                 // outside the list: e_j (M / S - r / S_rest), which is (S_rest sum t - r S_top) / (S S_rest) without the cancellation of M and r
-                const float factor = tail ? ((listed * S_rest_all - left * S_top_all) / S_all) / S_rest * each : 0.f;
-                const Exponentials<sizeof(T) == 4> e2(a, rest_ref == -INFINITY ? 0.f : rest_ref);
-                const Pair factors = pair_of(factor, factor);
-                const bool aligned = same_grid(row.p, g);
-                for (int32_t i = tid; i < max(count, next_count); i += threads) {
-                    if (i < count) {
-                        Raw<T, kPer<T>> x = mine[i];
-#pragma unroll
-                        for (int k = 0; k < kPer<T> / 2; ++k) put_elements(x, k, mul_2(e2(elements(x, k)), factors));
-                        store_vector(row, g, aligned, v0 + i, x);
-                    }
-                    if (i < next_count) fetch(next, next0 + i, i);
-                }
-            }
-        } else {
-            float norm = 1.f, shift = 0.f;
-            if (!a.rest && asks) {
-                const float some = there && one->targets.hi > 0.f ? one->shift : -INFINITY;
-                shift = half_max(some);
-                norm = 1.f / half_sum(some == -INFINITY ? 0.f : one->targets.hi * expf(some - shift));
-            }
-            if constexpr (kGrad) {
-                const float per_all = none ? 0.f : (listed + left) / S_all;
-                late = g;
-                for (int j = lane; j < owned; j += 32) {
-                    const Own o = s.own[j];
-                    const float share = o.top == -INFINITY ? 0.f : exp2_fast(exponent(o.top, a, all_ref)) * per_all;
-                    s.own[j].top = (share - expf(o.lp - shift) * norm) * each;
-                }
-            }
-            if (a.status && rank == 0 && (fault || (lane == 0 && none)))
-                atomicOr(a.status + r, fault | (lane == 0 && none ? SPECDEC_ST_EMPTY_MASK_ROW : 0u));
-            if (rank == 0) {
-                // The loss in pairs of floats: near zero it is a small difference of logarithms.
-                const Two zero = {0.f, 0.f};
-                const Two rest = half_sum(there ? times(one->rest, reference_step(one_rest, rest_ref)) : zero);
-                const Two top = half_sum(there ? times(one->top, reference_step(one_top, all_ref)) : zero);
-                const Two by = there && !a.rest && one->targets.hi > 0.f ? target_of(one->shift, shift) : Two{a.rest ? 1.f : 0.f, 0.f};
-                const Two sum = half_sum(there && one->targets.hi > 0.f ? one->targets * by : zero);
-                const Two cross = half_sum(there && one->targets.hi > 0.f ? one->cross * by : zero);
-                const bool endless = __any_sync(0xffffffffu, there && one->endless);
-                const Two remains = a.rest && tail ? Two{1.f, 0.f} - sum : zero;
-                const Two logs = log2_two(lane == 0 ? times(rest, reference_step(rest_ref, all_ref)) + top : lane == 1 ? rest : lane == 2 ? remains : sum);
-                auto log_of = [&](int l, float ref) {                 // natural; what is no number stays so
-                    const Two x = {__shfl_sync(0xffffffffu, logs.hi, l), __shfl_sync(0xffffffffu, logs.lo, l)};
-                    return x.hi - x.hi == 0.f ? (x + Two{ref, 0.f}) * SPECDEC_TWO(kLn2) : Two{x.hi, 0.f};
-                };
-                const Two log_all = log_of(0, all_ref), log_rest = log_of(1, rest_ref), log_r = log_of(2, 0.f), log_sum = log_of(3, 0.f);
                 if (lane == 0) {
-                    Two loss = zero;
-                    if (asks && !none) {
-                        // sum of t_i (ln t_i - ln s_i) where t_i = exp(lp_i), and where they are renormalised
-                        if (sum.hi > 0.f) {
-                            loss = cross + sum * log_all;
-                            if (!a.rest) loss = loss * reciprocal(sum) - log_sum - Two{shift, 0.f};
-                        }
-                        if (remains.hi > 0.f) loss = loss + remains * (log_r - (log_rest - log_all));
-                    }
-                    a.loss[r] = asks && (none || endless) ? w * INFINITY : w * loss.hi;
-                    if (a.stats) {
-                        a.stats[2 * r] = log_all.hi;
-                        a.stats[2 * r + 1] = log_rest.hi;
-                    }
+                    s.factor = all.tail ? ((all.listed * all.S_rest_all - all.left * all.S_top_all) / all.S_all) / all.S_rest * each : 0.f;
+                    s.base = all.rest_ref == -INFINITY ? 0.f : all.rest_ref;
                 }
+                meet();                                               // E
+                const float shift = all.shift(a, s.peer[turn], size), norm = all.norm(a, s.peer[turn], size, shift);
+                const float per_all = all.none ? 0.f : (all.listed + all.left) / all.S_all;
+                late = static_cast<T*>(a.grad) + r * a.grad_stride;
+                late_count = owned;
+                for (int j = lane; j < owned; j += 32) {
+                    const Own o = own[j];
+                    const float share = o.top == -INFINITY ? 0.f : exp2_fast(exponent(o.top, a, all.all_ref)) * per_all;
+                    own[j].top = (share - expf(o.lp - shift) * norm) * each;
+                }
+            }
+            if (after >= a.rows) break;
+            owned = own_of(after, s.own[turn ^ 1]);
+            r = after;
+            after = next_live(r + clusters);
+        }
+        if constexpr (kGrad) {
+            meet();                                                   // F
+            write_late(s.own[turn]);
+        } else {
+            cluster_wait();
+        }
+        return;
+    }
+
+    // ---- the loss's warp
+    auto no_weight = [&](int64_t from, int64_t to) {
+        if (rank == 0)
+            for (from += lane * clusters; from < min(to, (int64_t)a.rows); from += 32 * clusters) {
+                a.loss[from] = 0.f;
+                if (a.stats) a.stats[2 * from] = a.stats[2 * from + 1] = 0.f;
+            }
+    };
+    no_weight(r, first);
+    if (first >= a.rows) return;
+    cluster_arrive_relaxed();
+    cluster_wait();
+    cluster_arrive_relaxed();
+    r = first;
+    for (int turn = 0;; turn ^= 1) {
+        const int64_t after = next_live(r + clusters);
+        const float w = weight_of(r);
+        no_weight(r + clusters, after);
+        cluster_wait();
+        const bool there = lane % kMaxCluster < (int)size;
+        const Part one = s.peer[turn][there ? lane % kMaxCluster : 0];
+        const Total all(a, s.peer[turn], size);
+        const float shift = all.shift(a, s.peer[turn], size);
+        if (after < a.rows) cluster_arrive_relaxed();                 // (nothing of the row is read behind this)
+        if (rank == 0) {
+            // The loss in pairs of floats: near zero it is a small difference of logarithms.
+            const Two zero = {0.f, 0.f};
+            const bool some = there && one.targets.hi > 0.f;
+            const Two rest = half_sum(there ? times(one.rest, reference_step(one.rest_ref, all.rest_ref)) : zero);
+            const Two top = half_sum(there ? times(one.top, reference_step(one.top_ref, all.all_ref)) : zero);
+            const Two by = !some ? zero : a.rest ? Two{1.f, 0.f} : target_of(one.shift, shift);
+            const Two sum = half_sum(some ? one.targets * by : zero), cross = half_sum(some ? one.cross * by : zero);
+            const bool endless = __any_sync(0xffffffffu, there && one.endless);
+            const Two remains = a.rest && all.tail ? Two{1.f, 0.f} - sum : zero;
+            const Two logs = log2_two(lane == 0 ? times(rest, reference_step(all.rest_ref, all.all_ref)) + top : lane == 1 ? rest : lane == 2 ? remains : sum);
+            auto log_of = [&](int l, float ref) {                     // natural; what is no number stays so
+                const Two x = {__shfl_sync(0xffffffffu, logs.hi, l), __shfl_sync(0xffffffffu, logs.lo, l)};
+                return x.hi - x.hi == 0.f ? (x + Two{ref, 0.f}) * SPECDEC_TWO(kLn2) : Two{x.hi, 0.f};
+            };
+            const Two log_all = log_of(0, all.all_ref), log_rest = log_of(1, all.rest_ref), log_r = log_of(2, 0.f), log_sum = log_of(3, 0.f);
+            if (lane == 0) {
+                Two loss = zero;
+                if (all.asks && !all.none) {
+                    // sum of t_i (ln t_i - ln s_i) where t_i = exp(lp_i), and where they are renormalised
+                    if (sum.hi > 0.f) {
+                        loss = cross + sum * log_all;
+                        if (!a.rest) loss = loss * reciprocal(sum) - log_sum - Two{shift, 0.f};
+                    }
+                    if (remains.hi > 0.f) loss = loss + remains * (log_r - (log_rest - log_all));
+                }
+                a.loss[r] = all.asks && (all.none || endless) ? w * INFINITY : w * loss.hi;
+                if (a.stats) {
+                    a.stats[2 * r] = log_all.hi;
+                    a.stats[2 * r + 1] = log_rest.hi;
+                }
+                if (a.status && all.none) atomicOr(a.status + r, SPECDEC_ST_EMPTY_MASK_ROW);
             }
         }
+        if (after >= a.rows) break;
         r = after;
-    }
-    if constexpr (kGrad) {
-        __syncthreads();
-        if (lists) write_late();
     }
 }
 
@@ -523,29 +678,32 @@ template <typename T> __global__ void __launch_bounds__(kBackThreads) specdec_di
     if (warp == 0) {
         List list;
         list.read(a, r);
-        const uint32_t fault = list.check(a);
+        uint32_t fault;
+        // targets are summed over the whole list: every entry that counts, wherever it lies
+        const int32_t begin = row.first(v0), end = row.first(min(v0 + kChunk * kBackThreads, row.vectors));
+        const int all_owned = own_entries(a, list, 0, a.V, own, &fault);
         if (a.status && v0 == 0 && fault) atomicOr(a.status + r, fault);
         float shift = a.rest ? 0.f : -INFINITY, sum = 0.f;
         long long fixed = 0;
         if (!a.rest) {
-#pragma unroll
-            for (int c = 0; c < kEntries; ++c)
-                if (list.ids[c] >= 0) shift = fmaxf(shift, list.lps[c]);
+            for (int j = lane; j < all_owned; j += 32) shift = fmaxf(shift, own[j].lp);
             shift = warp_max(shift);
             if (shift == -INFINITY) shift = 0.f;
         }
-        const int32_t begin = row.first(v0), end = row.first(min(v0 + kChunk * kBackThreads, row.vectors));
-#pragma unroll
-        for (int c = 0; c < kEntries; ++c) {
-            if (32 * c >= a.n) continue;
-            const int32_t id = list.ids[c];
-            if (a.rest) fixed += id >= 0 ? fixed_of(target_of(list.lps[c], 0.f)) : 0;
-            else sum += id >= 0 ? expf(list.lps[c] - shift) : 0.f;
-            const bool here = id >= 0 && id >= begin && id < end;
+        for (int j0 = 0; j0 < all_owned; j0 += 32) {
+            const bool in = j0 + lane < all_owned;
+            Own o = own[in ? j0 + lane : 0];
+            if (a.rest) fixed += in ? fixed_of(target_of(o.lp, 0.f)) : 0;
+            else sum += in ? expf(o.lp - shift) : 0.f;
+            const bool here = in && o.id >= begin && o.id < end;
             const uint32_t all = __ballot_sync(0xffffffffu, here);
             // (the student's logit is read before the row is written: the gradient may lie over it)
-            if (here) own[owned + __popc(all & ((1u << lane) - 1u))] = Own{id, list.lps[c], to_float<T>(z[id])};
+            if (here) {
+                o.top = to_float<T>(z[o.id]);
+                own[owned + __popc(all & ((1u << lane) - 1u))] = o;  // (never behind where it is read)
+            }
             owned += __popc(all);
+            __syncwarp();
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) {
@@ -602,7 +760,7 @@ template <typename T> Shape shape_of(int32_t rows, int32_t V)
     auto slice = [&] { return (vectors + cluster - 1) / cluster; };
     while (cluster < kMaxCluster && (slice() > kSliceBytes / 16 || ((int64_t)rows * cluster < 152 && slice() > 8 * 1024 / 16))) cluster *= 2;
     const int32_t warps = (slice() + 32 * kLaneVectors - 1) / (32 * kLaneVectors);
-    return Shape{cluster, slice(), ((warps < kRowWarps ? warps : kRowWarps) + 1) * 32};
+    return Shape{cluster, slice(), ((warps < kRowWarps ? warps : kRowWarps) + 2) * 32};
 }
 
 // What a kernel remembers: the devices on which it may have its shared memory and clusters of sixteen, and how many clusters of the

@@ -24,11 +24,12 @@ namespace {
 
 using namespace specdec;
 
-constexpr int kRowWarps = 8;                       // of a CTA, at most, without the list's
-constexpr int kLaneVectors = 10;                   // of a thread, where that many warps are enough
+constexpr int kRowWarps = 8;                       // of a CTA, at most, that hold its part of a row
+constexpr int kLaneVectors = 20;                   // of a thread, where that many warps are enough
 constexpr int kBackThreads = 256;
 constexpr int kMaxCluster = 16;
-constexpr int kSliceBytes = 40 * 1024;             // of a row in a CTA: four CTAs an SM
+constexpr int kSliceBytes = 70 * 1024;             // of a row in a CTA: three CTAs an SM
+constexpr int kSmallBytes = 44 * 1024;             // five of them, of four warps
 constexpr int kMostBytes = 200 * 1024;             // and where sixteen CTAs hold the row only so
 
 struct Args {
@@ -118,41 +119,28 @@ __device__ __forceinline__ int own_entries(const Args& a, const List& list, int3
         found += __popc(all);
     }
     __syncwarp();
+    // (from the last 32 to the first, so that those before are still as they were listed)
+    for (int j0 = (found - 1) / 32 * 32; found > 0 && j0 >= 0; j0 -= 32) {
+        const int j = j0 + lane;
+        const Own o = own[j < found ? j : 0];
+        bool counts = (__match_any_sync(0xffffffffu, j < found ? o.id : -2 - lane) & below) == 0 && o.lp < INFINITY;
+        for (int k = 0; k < j0; ++k) counts &= own[k].id != o.id;
+        if (j < found && !counts) {
+            own[j].top = 1.f;                      // marked
+            *fault = SPECDEC_ST_BAD_TARGET;
+        }
+    }
+    if (!__any_sync(0xffffffffu, *fault)) return found;
     int kept = 0;
     for (int j0 = 0; j0 < found; j0 += 32) {
         const int j = j0 + lane;
         const Own o = own[j < found ? j : 0];
-        bool counts = j < found;
-        if (counts) {
-            counts = o.lp < INFINITY;
-            for (int k = 0; k < j; ++k) counts &= own[k].id != o.id;
-            if (!counts) *fault = SPECDEC_ST_BAD_TARGET;
-        }
-        if (found <= 32) {                         // (the usual case: nothing has to be looked at again)
-            const uint32_t all = __ballot_sync(0xffffffffu, counts);
-            __syncwarp();
-            if (counts) own[__popc(all & below)] = o;
-            kept = __popc(all);
-        } else {
-            // marked, for later entries still look at them
-            __syncwarp();
-            if (j < found) own[j].top = counts ? 0.f : 1.f;
-            kept = found;
-        }
-    }
-    __syncwarp();
-    if (found > 32) {
-        kept = 0;
-        for (int j0 = 0; j0 < found; j0 += 32) {
-            const int j = j0 + lane;
-            const Own o = own[j < found ? j : 0];
-            const bool counts = j < found && o.top == 0.f;
-            const uint32_t all = __ballot_sync(0xffffffffu, counts);
-            __syncwarp();
-            if (counts) own[kept + __popc(all & below)] = o;      // (never behind where it is read)
-            kept += __popc(all);
-            __syncwarp();
-        }
+        const bool counts = j < found && o.top == 0.f;
+        const uint32_t all = __ballot_sync(0xffffffffu, counts);
+        __syncwarp();
+        if (counts) own[kept + __popc(all & below)] = o;              // (never behind where it is read)
+        kept += __popc(all);
+        __syncwarp();
     }
     return kept;
 }
@@ -209,7 +197,7 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // What one CTA of a cluster knows of a row.
 struct Part {
     long long fixed;                               // the sum of the targets in 2^-56 (rest = 1)
-    Two rest, top, targets, cross;                 // sums of exponentials outside and on the list; of the targets; of t (ln t - z / temperature)
+    Two rest, top, targets, cross;                 // sums of exponentials outside and on the list; of the targets (rest = 0); of t (ln t - z / temperature)
     float rest_ref, top_ref, shift;
     int32_t endless;                               // whether a target lies where the student has -infinity
     long long unused;
@@ -305,7 +293,7 @@ template <typename T> struct Slice {
     __device__ __forceinline__ const T* at(int32_t i) const { return row.p + row.first(begin + i); }
 };
 
-template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps + 2) * 32, 4) specdec_distill_kernel(const Args a)
+template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps + 2) * 32, 3) specdec_distill_kernel(const Args a)
 {
     extern __shared__ __align__(16) unsigned char held[];
     __shared__ Shared s;
@@ -484,6 +472,8 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps +
             meet();                                                   // B
             if (kGrad) write_late(s.own[turn ^ 1]);
             if (after < a.rows) list.read(a, after);
+            const int64_t later = after + clusters;                   // (read well before it is asked)
+            const float later_weight = later < a.rows ? weight_of(later) : 1.f;
             Part part = {0, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, -INFINITY, -INFINITY, a.rest ? 0.f : -INFINITY, 0, 0};
             if (owned) {
                 for (int j = lane; j < owned; j += 32) {
@@ -502,18 +492,19 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps +
                     const Two target = target_of(o.lp, origin);
                     if (in && number) part.top = part.top + exp2_two(up + Two{-base, 0.f});
                     if (in) {
-                        part.targets = part.targets + target;
-                        part.fixed += fixed_of(target);
+                        if (a.rest) part.fixed += fixed_of(target);
+                        else part.targets = part.targets + target;
                         if (target.hi > 0.f && number) part.cross = part.cross + target * (Two{o.lp, 0.f} - up * SPECDEC_TWO(kLn2));
                         else if (target.hi > 0.f) part.endless = 1;
                     }
                 }
                 part.top = warp_sum(part.top);
-                part.targets = warp_sum(part.targets);
                 part.cross = warp_sum(part.cross);
                 part.endless = __any_sync(0xffffffffu, part.endless);
+                if (a.rest)
 #pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) part.fixed += __shfl_xor_sync(0xffffffffu, part.fixed, o);
+                    for (int o = 16; o >= 1; o >>= 1) part.fixed += __shfl_xor_sync(0xffffffffu, part.fixed, o);
+                else part.targets = warp_sum(part.targets);
             }
             if (!kGrad) cluster_wait();                               // (the phase before)
             else if (!late) cluster_wait();                           // (with a gradient: the first)
@@ -553,7 +544,7 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps +
             if (after >= a.rows) break;
             owned = own_of(after, s.own[turn ^ 1]);
             r = after;
-            after = next_live(r + clusters);
+            after = later_weight == 0.f ? next_live(later + clusters) : later;
         }
         if constexpr (kGrad) {
             meet();                                                   // F
@@ -591,11 +582,13 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps +
         if (rank == 0) {
             // The loss in pairs of floats: near zero it is a small difference of logarithms.
             const Two zero = {0.f, 0.f};
-            const bool some = there && one.targets.hi > 0.f;
+            const bool some = there && (a.rest ? one.fixed > 0 : one.targets.hi > 0.f);
+            const long long whole = (long long)(one.fixed >> 32) << 32;       // (its upper half is exact in fp32)
+            const Two given = a.rest ? two_sum(from_fixed(whole), from_fixed(one.fixed - whole)) : one.targets;
             const Two rest = half_sum(there ? times(one.rest, reference_step(one.rest_ref, all.rest_ref)) : zero);
             const Two top = half_sum(there ? times(one.top, reference_step(one.top_ref, all.all_ref)) : zero);
             const Two by = !some ? zero : a.rest ? Two{1.f, 0.f} : target_of(one.shift, shift);
-            const Two sum = half_sum(some ? one.targets * by : zero), cross = half_sum(some ? one.cross * by : zero);
+            const Two sum = half_sum(some ? given * by : zero), cross = half_sum(some ? one.cross * by : zero);
             const bool endless = __any_sync(0xffffffffu, there && one.endless);
             const Two remains = a.rest && all.tail ? Two{1.f, 0.f} - sum : zero;
             const Two logs = log2_two(lane == 0 ? times(rest, reference_step(all.rest_ref, all.all_ref)) + top : lane == 1 ? rest : lane == 2 ? remains : sum);
@@ -751,16 +744,18 @@ struct Shape {
     int32_t cluster, slice, threads;
 };
 
-// A row goes to the fewest CTAs that keep four of them on an SM, more where the rows alone do not fill the GPU, and at
-// most to sixteen; each has as many warps as its part takes.
+// A row goes to the fewest CTAs that keep three of them on an SM, more where the rows alone do not fill the GPU, and at most to
+// sixteen. A part of up to 44 KB has four warps or fewer, so that five CTAs share an SM: while some wait for the others of their
+// cluster, the rest read and write. Measured, 2048 bf16 rows against 64 ids with the gradient: V = 151936 (38 KB parts) 267 us with
+// four warps, 416 with eight; V = 128256 (64 KB parts) 276 and 217.
 template <typename T> Shape shape_of(int32_t rows, int32_t V)
 {
     const int32_t vectors = most_vectors<T>(V);
     int32_t cluster = 1;
     auto slice = [&] { return (vectors + cluster - 1) / cluster; };
     while (cluster < kMaxCluster && (slice() > kSliceBytes / 16 || ((int64_t)rows * cluster < 152 && slice() > 8 * 1024 / 16))) cluster *= 2;
-    const int32_t warps = (slice() + 32 * kLaneVectors - 1) / (32 * kLaneVectors);
-    return Shape{cluster, slice(), ((warps < kRowWarps ? warps : kRowWarps) + 2) * 32};
+    const int32_t most = slice() > kSmallBytes / 16 ? kRowWarps : 4, warps = (slice() + 32 * kLaneVectors - 1) / (32 * kLaneVectors);
+    return Shape{cluster, slice(), ((slice() > kSmallBytes / 16 || warps > most ? most : warps) + 2) * 32};
 }
 
 // What a kernel remembers: the devices on which it may have its shared memory and clusters of sixteen, and how many clusters of the

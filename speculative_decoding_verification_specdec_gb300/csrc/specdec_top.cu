@@ -45,7 +45,7 @@ __device__ __forceinline__ bool live_beam(const float* scores, const uint8_t* fi
     return !scores || (isfinite(__ldg(scores + row)) && !(finished && __ldg(finished + row)));
 }
 
-template <typename T, bool kMasked> __global__ void __launch_bounds__(kThreads) specdec_rows_stream_kernel(const StreamArgs a)
+template <typename T> __global__ void __launch_bounds__(kThreads) specdec_rows_stream_kernel(const StreamArgs a)
 {
     after_predecessor();
     const int lane = threadIdx.x & 31;
@@ -56,26 +56,8 @@ template <typename T, bool kMasked> __global__ void __launch_bounds__(kThreads) 
     const Row<T> row(static_cast<const T*>(a.logits) + r * a.row_stride, a.V);
     const int v0 = u * kUnitVectors + lane;
     Raw<T, kPer<T>> x[kLaneVectors];
-    if constexpr (kMasked) {
-        const int32_t* words = a.bitmask + r * a.words;
-        uint32_t bits[kLaneVectors];
 #pragma unroll
-        for (int i = 0; i < kLaneVectors; ++i) bits[i] = vector_bits(row, words, v0 + i * 32);
-#pragma unroll
-        for (int i = 0; i < kLaneVectors; ++i) {
-            if (bits[i]) {
-                load_vector(row, v0 + i * 32, x[i]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < kPer<T>; ++e) x[i].e[e] = neg_inf<T>();
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kLaneVectors; ++i) apply_bits<T>(x[i], bits[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kLaneVectors; ++i) load_vector(row, v0 + i * 32, x[i]);
-    }
+    for (int i = 0; i < kLaneVectors; ++i) load_vector(row, v0 + i * 32, x[i]);
     Maximum<T> part[kLaneVectors];
 #pragma unroll
     for (int i = 0; i < kLaneVectors; ++i) part[i] = Maximum<T>::of(x[i]);
@@ -90,10 +72,10 @@ template <typename T, bool kMasked> __global__ void __launch_bounds__(kThreads) 
     Pair sum = pair_of(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kLaneVectors; ++i) {
-        Pair part = exp2_2(fma_2(elements(x[i], 0), c, less));
+        Pair some = exp2_2(fma_2(elements(x[i], 0), c, less));
 #pragma unroll
-        for (int e = 1; e < kPer<T> / 2; ++e) part = add_2(part, exp2_2(fma_2(elements(x[i], e), c, less)));
-        sum = add_2(sum, part);
+        for (int e = 1; e < kPer<T> / 2; ++e) some = add_2(some, exp2_2(fma_2(elements(x[i], e), c, less)));
+        sum = add_2(sum, some);
     }
     S = both(sum).x + both(sum).y;
     // The maxima of 8 neighbouring lanes' i-th vectors, 128 bytes, meet in the i-th of those lanes: three exchanges, of 4, 2 and 1.
@@ -107,6 +89,94 @@ template <typename T, bool kMasked> __global__ void __launch_bounds__(kThreads) 
         }
     }
     static_cast<T*>(a.maxima)[unit * 32 + (lane & 7) * 4 + (lane >> 3)] = from_float<T>(part[0].value());
+    warp_join(ref, S);
+    if (lane == 0) a.sums[unit] = make_float2(ref, S);
+}
+
+// The same under a bitmask. A lane takes the mask of one group; the vectors in which an id is allowed are listed side by side
+// for the warp, and only those are loaded, a lane one. (Where 5 % of the ids are allowed that is a twelfth of fp32's vectors and an eighth
+// of the 16-bit types'; with all allowed the list is the whole unit.)
+template <typename T> __global__ void __launch_bounds__(kThreads) specdec_rows_stream_masked_kernel(const StreamArgs a)
+{
+    constexpr int kWords = 8 * kPer<T> / 32;       // of a group's mask
+    __shared__ uint16_t listed[kThreads / 32][kUnitVectors];
+    __shared__ uint32_t best[kThreads / 32][32];
+    after_predecessor();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + warp;
+    const int64_t r = unit / a.units;
+    if (r >= a.rows || !live_beam(a.scores, a.finished, r)) return;
+    const int u = (int)(unit - r * a.units);
+    const Row<T> row(static_cast<const T*>(a.logits) + r * a.row_stride, a.V);
+    const int32_t* const words = a.bitmask + r * a.words;
+    // bits of the group's elements first .. first + 32 kWords - 1; what lies outside the row is 0
+    const int32_t v0 = u * kUnitVectors, first = row.first(v0 + lane * kGroupVectors);
+    uint32_t bits[kWords + 1];
+#pragma unroll
+    for (int i = 0; i <= kWords; ++i) {
+        const int32_t w = (first >> 5) + i;        // (first may be negative: the first group of a row off the grid)
+        bits[i] = w >= 0 && w < a.words && (i < kWords || (first & 31)) ? (uint32_t)__ldg(words + w) : 0u;
+    }
+    best[warp][lane] = 0;
+    uint32_t some[kWords];                         // a bit for each vector with one
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        bits[i] = __funnelshift_r(bits[i], bits[i + 1], first & 31);
+        const int32_t at = first + i * 32;
+        if (at < 0) bits[i] &= at > -32 ? 0xffffffffu << -at : 0u;
+        if (at + 32 > a.V) bits[i] &= at < a.V ? (1u << (a.V - at)) - 1u : 0u;
+        uint32_t t = bits[i] | bits[i] >> 1;
+        t |= t >> 2;
+        if (kPer<T> == 8) t |= t >> 4;
+        some[i] = t & (kPer<T> == 8 ? 0x01010101u : 0x11111111u);
+        mine += __popc(some[i]);
+    }
+    int to = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, to, o);
+        if (lane >= o) to += y;
+    }
+    const int count = __shfl_sync(0xffffffffu, to, 31);
+    to -= mine;
+#pragma unroll
+    for (int i = 0; i < kGroupVectors; ++i) {
+        const int bit = i * kPer<T> % 32, word = i * kPer<T> / 32;
+        if (some[word] >> bit & 1) listed[warp][to++] = (uint16_t)(lane * kGroupVectors + i | (bits[word] >> bit & ((1u << kPer<T>) - 1u)) << 8);
+    }
+    __syncwarp();
+    float ref = -INFINITY;
+    Pair sum = pair_of(0.f, 0.f);
+    const Pair c = pair_of(a.scale, a.scale);
+    for (int j = lane; j < count; j += 32) {
+        const uint32_t entry = listed[warp][j];
+        const int i = entry & 255;
+        Raw<T, kPer<T>> x;
+        load_vector(row, v0 + i, x);
+        apply_bits<T>(x, entry >> 8);
+        const float m = Maximum<T>::of(x).value();
+        const uint32_t key = order_key(m);
+        if (key) {
+            atomicMax(&best[warp][i / kGroupVectors], key);
+            const float up = whole_reference(m, a.scale);
+            if (up > ref) {
+                const float step = reference_step(ref, up);
+                sum = mul_2(sum, pair_of(step, step));
+                ref = up;
+            }
+        }
+        const float from = ref == -INFINITY ? 0.f : ref;
+        const Pair less = pair_of(-from, -from);
+        Pair part = exp2_2(fma_2(elements(x, 0), c, less));
+#pragma unroll
+        for (int e = 1; e < kPer<T> / 2; ++e) part = add_2(part, exp2_2(fma_2(elements(x, e), c, less)));
+        sum = add_2(sum, part);
+    }
+    __syncwarp();
+    const uint32_t key = best[warp][lane];
+    static_cast<T*>(a.maxima)[unit * 32 + lane] = from_float<T>(key ? key_value(key) : -INFINITY);
+    float S = both(sum).x + both(sum).y;
     warp_join(ref, S);
     if (lane == 0) a.sums[unit] = make_float2(ref, S);
 }
@@ -484,8 +554,8 @@ template <typename T> specdec_status_t launch_rows(const StreamArgs& s, const Se
 {
     const int64_t units = s.rows * s.units;
     const unsigned grid = (unsigned)((units + kThreads / 32 - 1) / (kThreads / 32));
-    cudaError_t e = s.bitmask ? launch_dependent(specdec_rows_stream_kernel<T, true>, grid, kThreads, 0, stream, s)
-                              : launch_dependent(specdec_rows_stream_kernel<T, false>, grid, kThreads, 0, stream, s);
+    cudaError_t e = s.bitmask ? launch_dependent(specdec_rows_stream_masked_kernel<T>, grid, kThreads, 0, stream, s)
+                              : launch_dependent(specdec_rows_stream_kernel<T>, grid, kThreads, 0, stream, s);
     if (e == cudaSuccess) e = launch_dependent(specdec_rows_select_kernel<T>, (unsigned)s.rows, kSelectThreads, 0, stream, a);
     return e == cudaSuccess ? SPECDEC_OK : SPECDEC_ERR_CUDA;
 }

@@ -207,7 +207,6 @@ static_assert(kPartWords == 8, "a power of two");
 struct Shared {
     Part peer[2][kMaxCluster];                     // two rows': a CTA may be one ahead
     Part part;
-    int64_t after;                                 // the cluster's next row that has a weight
     float refs[kRowWarps], sums[kRowWarps];
     float factor, base;                            // of the gradient outside the list: e_j relative to base, times factor
     Own own[2][SPECDEC_TOP_MAX];                   // of this row and of the one before, or after
@@ -303,48 +302,31 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps +
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int64_t clusters = gridDim.x / size;
     auto weight_of = [&](int64_t r) { return a.weight ? a.weight[r] : 1.f; };
-    // the cluster's first row, and what follows a row: the next with a weight
-    int64_t r = blockIdx.x / size;
-    // (every thread arrives at the cluster's barrier once at the start and once a row, and waits for each phase)
-    auto next_live = [&](int64_t from) {
-        while (from < a.rows && weight_of(from) == 0.f) from += clusters;
-        return from;
-    };
-    const int64_t first = next_live(r);
+    const int64_t first = blockIdx.x / size;       // the cluster's rows: from this one on, `clusters` apart
+    // Every thread goes through every row's barriers, whether the row has a weight or not, so that no weight that changes under
+    // the call can part them; it arrives at the cluster's barrier once at the start and once a row, and waits for each phase.
     auto meet = [&] { barrier_sync(1, threads + 32); };               // the row's warps and the list's
 
     if (tid < threads) {
         // ---- the warps that hold the row
         Raw<T, kPer<T>>* const mine = reinterpret_cast<Raw<T, kPer<T>>*>(held) + tid;
         const uint32_t mine_at = smem_u32(mine);
-        auto zeros = [&](int64_t from, int64_t to) {                  // the gradients of rows without a weight
-            if (kGrad)
-                for (; from < min(to, (int64_t)a.rows); from += clusters) {
-                    const Slice<T> z(a, from, rank);
-                    T* const g = static_cast<T*>(a.grad) + from * a.grad_stride;
-                    const bool aligned = same_grid(z.row.p, g);
-                    const Raw<T, kPer<T>> zero = {};
-                    for (int32_t i = tid; i < z.count; i += threads) store_vector(z.row, g, aligned, z.begin + i, zero);
-                }
-        };
-        zeros(r, first);
-        r = first;
-        if (r >= a.rows) return;                                      // (the whole cluster)
-        {
-            const Slice<T> now(a, r, rank);
+        bool live = weight_of(first) != 0.f;
+        if (live) {
+            const Slice<T> now(a, first, rank);
             for (int32_t i = tid; i < now.count; i += threads)
                 if (now.is_whole(i)) async_copy_16(mine_at + (i - tid) * 16, now.at(i), 16);
         }
         cluster_arrive_relaxed();                                     // (no CTA writes to one that has not started)
-        while (true) {
+        for (int64_t r = first; r < a.rows; r += clusters) {
             const Slice<T> now(a, r, rank);
+            const int64_t after = min(r + clusters, (int64_t)a.rows - 1);
+            const bool next_live = r + clusters < a.rows && weight_of(after) != 0.f;
             async_copy_wait();
-            meet();                                          // A: the row has landed; the list's warp takes the listed out
-            meet();                                          // B
-            const int64_t after = s.after;
-            const bool more = after < a.rows;
-            const Slice<T> next(a, more ? after : r, rank);
-            const int32_t coming = more ? next.count : 0;
+            meet();                                                   // A: the row has landed; the list's warp takes the listed out
+            meet();                                                   // B
+            const Slice<T> next(a, after, rank);
+            const int32_t count = live ? now.count : 0, coming = next_live ? next.count : 0;
             const char* const source = reinterpret_cast<const char*>(next.at(0));
             auto fetch = [&](int32_t i) {                             // vector i of the next row into the place that this thread is done with
                 if (next.is_whole(i)) async_copy_16(mine_at + (i - tid) * 16, source + (int64_t)i * 16, 16);
@@ -366,7 +348,7 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps +
                 }
             };
             int32_t i = tid;
-            for (; i + threads < now.count; i += 2 * threads) {
+            for (; i + threads < count; i += 2 * threads) {
                 const Raw<T, kPer<T>> x = mine[i - tid], y = mine[i - tid + threads];
                 raise(larger(Maximum<T>::of(x), Maximum<T>::of(y)).value());
                 const Exponentials<true> e2(a, ref == -INFINITY ? 0.f : ref);
@@ -377,7 +359,7 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps +
                     if (i + threads < coming) fetch(i + threads);
                 }
             }
-            if (i < now.count) {
+            if (i < count) {
                 const Raw<T, kPer<T>> x = mine[i - tid];
                 raise(Maximum<T>::of(x).value());
                 fold(x, Exponentials<true>(a, ref == -INFINITY ? 0.f : ref));
@@ -391,39 +373,39 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps +
                 s.refs[warp] = ref;
                 s.sums[warp] = S;
             }
-            meet();                                          // D: the sums are there
+            meet();                                                   // D: the sums are there
             cluster_wait();                                           // (the phase before: the list's warp has waited for it)
             cluster_arrive_relaxed();
             if constexpr (kGrad) {
                 T* const g = static_cast<T*>(a.grad) + r * a.grad_stride;
                 const bool aligned = same_grid(now.row.p, g);
                 T* const to = g + now.row.first(now.begin);
-                meet();                                      // E: the factor is there
+                meet();                                               // E: the factor is there
                 const Exponentials<sizeof(T) == 4> e2(a, s.base);
                 const Pair factors = pair_of(s.factor, s.factor);
                 for (i = tid; i < now.count; i += threads) {
-                    Raw<T, kPer<T>> x = mine[i - tid];
+                    Raw<T, kPer<T>> x = {};
+                    if (live) {
+                        x = mine[i - tid];
 #pragma unroll
-                    for (int k = 0; k < kPairs; ++k) put_elements(x, k, mul_2(e2(elements(x, k)), factors));
+                        for (int k = 0; k < kPairs; ++k) put_elements(x, k, mul_2(e2(elements(x, k)), factors));
+                    }
                     if (i < coming) fetch(i);
                     if (aligned && now.is_whole(i)) *reinterpret_cast<uint4*>(to + (int64_t)i * kPer<T>) = *reinterpret_cast<const uint4*>(x.e);
                     else store_vector(now.row, g, false, now.begin + i, x);
                 }
                 for (; i < coming; i += threads) fetch(i);
-                zeros(r + clusters, after);
             }
-            r = after;
-            if (!more) break;
+            live = next_live;
         }
-        if (kGrad) meet();                                   // F: the row is written, the listed may go over it
+        if (kGrad) meet();                                            // F: the row is written, the listed may go over it
         cluster_wait();
         return;
     }
 
-    if (first >= a.rows && tid < threads + 32) return;
-    List list;
     if (tid < threads + 32) {
         // ---- the list's warp
+        List list;
         list.read(a, first);
         // The row's ends, where a vector lies partly outside it: an element a lane, the first vector's and the last one's.
         T end_element;
@@ -435,8 +417,9 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps +
             const int32_t i = (lane < kPer<T> ? 0 : z.row.vectors - 1) - z.begin;
             if (lane < 2 * kPer<T> && i >= 0 && i < z.count && !z.is_whole(i)) reinterpret_cast<T*>(held)[i * kPer<T> + lane % kPer<T>] = end_element;
         };
-        // the entries of a row that lie here
-        auto own_of = [&](int64_t row, Own* own) {
+        // the entries of a row that lie here; none of a row without a weight
+        auto own_of = [&](int64_t row, float w, Own* own) {
+            if (w == 0.f) return 0;
             const Slice<T> z(a, row, rank);
             read_ends(z);
             uint32_t fault;
@@ -444,24 +427,22 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps +
             if (a.status && fault) atomicOr(a.status + row, fault);
             return n;
         };
-        r = first;
-        int owned = own_of(r, s.own[0]), late_count = 0;
+        float w = weight_of(first);
+        int owned = own_of(first, w, s.own[0]), late_count = 0;
         T* late = nullptr;                                            // where the listed elements' gradients go once all others are written
         auto write_late = [&](const Own* own) {
             for (int j = lane; j < late_count; j += 32) late[own[j].id] = from_float<T>(own[j].top);
             __syncwarp();
         };
-        int64_t after = next_live(r + clusters);
         cluster_arrive();
+        cluster_wait();                                               // (every CTA has started)
         int turn = 0;
-        for (;; turn ^= 1) {
+        for (int64_t r = first; r < a.rows; r += clusters, turn ^= 1) {
             Own* const own = s.own[turn];
             const Slice<T> now(a, r, rank);
-            const float w = weight_of(r);
-            if (lane == 0) s.after = after;
             meet();                                                   // A
             const int32_t begin = now.row.first(now.begin);
-            put_ends(now);
+            if (w != 0.f) put_ends(now);
             __syncwarp();
             for (int j = lane; j < owned; j += 32) {
                 T* const e = reinterpret_cast<T*>(held) + (own[j].id - begin);
@@ -471,9 +452,12 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps +
             }
             meet();                                                   // B
             if (kGrad) write_late(s.own[turn ^ 1]);
-            if (after < a.rows) list.read(a, after);
-            const int64_t later = after + clusters;                   // (read well before it is asked)
-            const float later_weight = later < a.rows ? weight_of(later) : 1.f;
+            const int64_t after = r + clusters;
+            float next_w = 0.f;
+            if (after < a.rows) {                                     // (read well before they are asked)
+                next_w = weight_of(after);
+                list.read(a, after);
+            }
             Part part = {0, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, -INFINITY, -INFINITY, a.rest ? 0.f : -INFINITY, 0, 0};
             if (owned) {
                 for (int j = lane; j < owned; j += 32) {
@@ -506,8 +490,7 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps +
                     for (int o = 16; o >= 1; o >>= 1) part.fixed += __shfl_xor_sync(0xffffffffu, part.fixed, o);
                 else part.targets = warp_sum(part.targets);
             }
-            if (!kGrad) cluster_wait();                               // (the phase before)
-            else if (!late) cluster_wait();                           // (with a gradient: the first)
+            if (!kGrad && r != first) cluster_wait();                 // (the phase before)
             meet();                                                   // D
             {
                 const bool holds = lane < threads / 32;
@@ -541,14 +524,12 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps +
                     own[j].top = (share - expf(o.lp - shift) * norm) * each;
                 }
             }
-            if (after >= a.rows) break;
-            owned = own_of(after, s.own[turn ^ 1]);
-            r = after;
-            after = later_weight == 0.f ? next_live(later + clusters) : later;
+            if (after < a.rows) owned = own_of(after, next_w, s.own[turn ^ 1]);
+            w = next_w;
         }
         if constexpr (kGrad) {
             meet();                                                   // F
-            write_late(s.own[turn]);
+            write_late(s.own[turn ^ 1]);
         } else {
             cluster_wait();
         }
@@ -556,30 +537,22 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps +
     }
 
     // ---- the loss's warp
-    auto no_weight = [&](int64_t from, int64_t to) {
-        if (rank == 0)
-            for (from += lane * clusters; from < min(to, (int64_t)a.rows); from += 32 * clusters) {
-                a.loss[from] = 0.f;
-                if (a.stats) a.stats[2 * from] = a.stats[2 * from + 1] = 0.f;
-            }
-    };
-    no_weight(r, first);
-    if (first >= a.rows) return;
     cluster_arrive_relaxed();
     cluster_wait();
     cluster_arrive_relaxed();
-    r = first;
-    for (int turn = 0;; turn ^= 1) {
-        const int64_t after = next_live(r + clusters);
+    int turn = 0;
+    for (int64_t r = first; r < a.rows; r += clusters, turn ^= 1) {
         const float w = weight_of(r);
-        no_weight(r + clusters, after);
         cluster_wait();
         const bool there = lane % kMaxCluster < (int)size;
         const Part one = s.peer[turn][there ? lane % kMaxCluster : 0];
         const Total all(a, s.peer[turn], size);
         const float shift = all.shift(a, s.peer[turn], size);
-        if (after < a.rows) cluster_arrive_relaxed();                 // (nothing of the row is read behind this)
-        if (rank == 0) {
+        if (r + clusters < a.rows) cluster_arrive_relaxed();          // (nothing of the row is read behind this)
+        if (rank == 0 && w == 0.f) {
+            if (lane == 0) a.loss[r] = 0.f;
+            if (lane < 2 && a.stats) a.stats[2 * r + lane] = 0.f;
+        } else if (rank == 0) {
             // The loss in pairs of floats: near zero it is a small difference of logarithms.
             const Two zero = {0.f, 0.f};
             const bool some = there && (a.rest ? one.fixed > 0 : one.targets.hi > 0.f);
@@ -615,8 +588,6 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps +
                 if (a.status && all.none) atomicOr(a.status + r, SPECDEC_ST_EMPTY_MASK_ROW);
             }
         }
-        if (after >= a.rows) break;
-        r = after;
     }
 }
 

@@ -170,6 +170,40 @@ def test_whole_vocabularies_in_place(cuda, kind, V, rows):
     part.check_grad(back[some], kind, more=80 * L.U + 2 * L.U * 20)
 
 
+@pytest.mark.parametrize("share", [0.0, 0.2, 0.9, 1.0])
+@pytest.mark.parametrize("V", [700, 40003])
+def test_rows_without_weight_are_not_read(cuda, share, V):
+    """More rows than are in flight at once, that share of them with a weight; the others hold NaN, their lists anything."""
+    import torch
+
+    rng = np.random.default_rng([V, int(10 * share)])
+    rows = 2500 if V < 1000 else 600
+    some = np.sort(rng.permutation(rows)[:6])
+    weight = np.where(rng.random(rows) < share, 0.25, 0.0).astype(np.float32)
+    x, _ = L.rows(rng, rows, V, "bf16")
+    x[L.dev(weight) == 0] = torch.nan
+    ids, lps = rng.integers(-5, V + 5, (rows, 9)).astype(np.int32), np.full((rows, 9), -3.0, dtype=np.float32)
+    ids[some] = np.stack([rng.permutation(V)[:9] for _ in some])
+    loss, stats, grad = torch.full((rows,), 7.0, device=cuda), torch.full((rows, 2), 7.0, device=cuda), torch.full_like(x, 7.0)
+    _native.distill(x, L.dev(ids), L.dev(lps), loss, weight=L.dev(weight), stats=stats, grad=grad)
+    alone = torch.full((rows,), 7.0, device=cuda)
+    _native.distill(x, L.dev(ids), L.dev(lps), alone, weight=L.dev(weight))
+    back = torch.full_like(x, 7.0)
+    _native.distill_backward(x, L.dev(ids), L.dev(lps), stats, L.dev(weight), back)
+    none = torch.from_numpy(weight == 0).to(cuda)
+    for t in (loss, stats, grad, alone, back):
+        assert (t[none] == 0).all() and torch.isfinite(t[~none].float()).all()
+    part = Case(x[torch.from_numpy(some).to(cuda)], ids[some], lps[some], weight=weight[some])
+    for r, (want, _, _, _) in enumerate(part.want):
+        err = 0 if weight[some[r]] == 0 else L.loss_error(part.z[r], 1.0, weight[some[r]], 2.0)
+        assert abs(float(loss[some[r]]) - want) <= err + L.U * abs(want) and abs(float(alone[some[r]]) - want) <= err + L.U * abs(want)
+    keep = weight[some] != 0
+    if keep.any():
+        sub = Case(x[torch.from_numpy(some[keep]).to(cuda)], ids[some[keep]], lps[some[keep]], weight=weight[some[keep]])
+        sub.check_grad(grad[torch.from_numpy(some[keep]).to(cuda)], "bf16")
+        sub.check_grad(back[torch.from_numpy(some[keep]).to(cuda)], "bf16", more=2 * L.U * 20)
+
+
 def test_gradient_against_differences(cuda):
     """Along a direction of at most 1 an element: a central difference of step h is off by both losses' errors over 2 h and by
     h^2 / 6 times a third derivative, which is at most 16 for a softmax and its part (third moments of what lies in [-1, 1])."""

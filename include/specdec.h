@@ -556,7 +556,7 @@ specdec_status_t specdec_kv_fork(const specdec_kv_cache_t* cache, const int32_t*
  *   workspace    specdec_top_logits_workspace_size(...) bytes (0 for sizes that the call refuses), 16-byte aligned,
  *                no initialisation; it holds nothing between calls, and calls (or captured graphs) that share one must not overlap in time.
  * status, [rows] here: EMPTY_MASK_ROW where nothing is listed. Equal rows of one alignment give equal bits wherever they stand.
- * Sums are held in fp32 over 64 elements or fewer a thread and in 64 bits from there on.
+ * Sums are held in fp32 over 4 KB of a row, by a warp, and in pairs of fp32 numbers (some 46 bits) from there on.
  * Errors: INVALID_ARG for a NULL required pointer, n outside [1, SPECDEC_TOP_MAX], a bad size, stride or temperature, a
  * workspace too small or misaligned; UNSUPPORTED for a type or V outside those above, or more than 2^31 units of 4 KB; CUDA.
  */
@@ -590,11 +590,12 @@ specdec_status_t specdec_top_logits(const void* logits, specdec_dtype_t dtype, i
  * +infinity in a row makes its loss and gradient NaN.
  * status, [rows] here: BAD_TARGET (an id outside [-1, V), one listed before, a log-probability that is NaN or +infinity: that entry does not
  * count); EMPTY_MASK_ROW (no finite logit).
- * Sums over the row are held in fp32 by a thread and in 64 bits across them; targets, listed exponentials and the loss in 64
- * bits; an element of the gradient is one fp32 exponential times one factor, rounded once to its type. Equal calls give equal bits.
+ * Sums over the row are held in fp32 by a warp, and in pairs of fp32 numbers (some 46 bits) across them, as are targets, listed
+ * exponentials and the loss; an element of the gradient is one fp32 exponential times one factor, rounded once to its type. Equal
+ * calls give equal bits.
  * Errors: INVALID_ARG for a NULL required pointer, n, a size, a stride or a temperature outside those above, rest not 0 or 1;
- * UNSUPPORTED for a type or V outside those above, a row of more than 3,276,768 bytes (it is held on chip; the backward call
- * has no such limit, but one of 2^31 CTAs of 32 KB); CUDA.
+ * UNSUPPORTED for a type or V outside those above, a row of more than 3,276,784 bytes (it is held on chip; the backward call
+ * has no such limit, but one of 2^31 CTAs of 32 KB each); CUDA.
  */
 specdec_status_t specdec_distill(const void* logits, specdec_dtype_t dtype, int32_t rows, int32_t V, int64_t row_stride,
                                  const int32_t* top_ids, const float* top_logprobs, int32_t n, double temperature,
@@ -626,7 +627,8 @@ specdec_status_t specdec_distill_backward(const void* logits, specdec_dtype_t dt
  *   n            1 .. SPECDEC_TOP_MAX, beams up to SPECDEC_TOP_MAX, beams * n <= 4096.
  *   workspace    specdec_beam_select_workspace_size(...) bytes, as specdec_top_logits'.
  * scores may be out_scores and finished out_finished where n = beams. Scores compete in 64 bits (the row's sum of exponentials is held
- * as specdec_top_logits holds it: differences under 10^-6 may fall either way); out_scores is their value in fp32.
+ * as specdec_top_logits holds it: differences under 10^-6 may fall either way); out_scores is their value in fp32. Of a row, no more
+ * than its n best ids are ever candidates; equal logits rank by id.
  * status, [B] here: BAD_SCORE (a score, or a row's logit, that is NaN or +infinity: that beam has no continuation), EMPTY_MASK_ROW (a
  * beam whose row allows nothing). Equal calls give equal bits.
  * Errors: INVALID_ARG for a NULL required pointer, a bad size or stride, end_token outside [-1, V) or -1 with finished, a

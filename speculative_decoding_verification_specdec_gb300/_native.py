@@ -572,9 +572,11 @@ def _matrix(name: str, t, dtype, shape, device: int):
     """Address of a contiguous tensor of that type and shape (None: none)."""
     if t is None:
         return None
-    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
-    return _at(name, t, device)
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+    return t.data_ptr()
 
 
 def _workspace(t, device: int):

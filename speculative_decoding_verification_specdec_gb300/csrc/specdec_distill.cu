@@ -88,8 +88,8 @@ struct List {
 #pragma unroll
         for (int c = 0; c < kEntries; ++c) {
             const int j = lane + 32 * c;
-            ids[c] = j < a.n ? __ldg(a.ids + r * a.n + j) : -1;
-            lps[c] = j < a.n ? __ldg(a.logprobs + r * a.n + j) : -INFINITY;
+            ids[c] = j < a.n ? a.ids[r * a.n + j] : -1;
+            lps[c] = j < a.n ? a.logprobs[r * a.n + j] : -INFINITY;
         }
     }
 };

@@ -37,7 +37,7 @@ template <typename T> inline __host__ __device__ int32_t most_vectors(int32_t V)
 __device__ __forceinline__ uint4 load_once(const void* p)
 {
     uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
     return r;
 }
 
@@ -58,7 +58,7 @@ template <typename T> __device__ __forceinline__ uint32_t vector_bits(const Row<
 {
     const int32_t at = row.first(v), lo = max(at, 0), hi = min(at + kPer<T>, row.V) - 1;
     if (hi < lo) return 0;
-    const uint32_t a = (uint32_t)__ldg(words + (lo >> 5)), b = (lo >> 5) == (hi >> 5) ? 0u : (uint32_t)__ldg(words + (hi >> 5));
+    const uint32_t a = (uint32_t)words[lo >> 5], b = (lo >> 5) == (hi >> 5) ? 0u : (uint32_t)words[hi >> 5];
     const uint32_t bits = __funnelshift_r(a, b, lo & 31) & ((2u << (hi - lo)) - 1u);
     return bits << (lo - at);
 }

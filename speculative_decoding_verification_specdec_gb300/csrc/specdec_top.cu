@@ -40,9 +40,11 @@ struct StreamArgs {
     void* maxima;                                  // [rows, units, 32], the logits' type
 };
 
+// (Scores and flags past L1: the call before may have written them in place of its own, a line's parts by several CTAs that had read
+// it, while this kernel had been set up already.)
 __device__ __forceinline__ bool live_beam(const float* scores, const uint8_t* finished, int64_t row)
 {
-    return !scores || (isfinite(__ldg(scores + row)) && !(finished && __ldg(finished + row)));
+    return !scores || (isfinite(__ldcg(scores + row)) && !(finished && __ldcg(finished + row)));
 }
 
 template <typename T> __global__ void __launch_bounds__(kThreads) specdec_rows_stream_kernel(const StreamArgs a)
@@ -115,7 +117,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) specdec_rows_s
 #pragma unroll
     for (int i = 0; i <= kWords; ++i) {
         const int32_t w = (first >> 5) + i;        // (first may be negative: the first group of a row off the grid)
-        bits[i] = w >= 0 && w < a.words && (i < kWords || (first & 31)) ? (uint32_t)__ldg(words + w) : 0u;
+        bits[i] = w >= 0 && w < a.words && (i < kWords || (first & 31)) ? (uint32_t)words[w] : 0u;
     }
     best[warp][lane] = 0;
     uint32_t some[kWords];                         // a bit for each vector with one
@@ -458,8 +460,8 @@ __global__ void __launch_bounds__(kThreads) specdec_beam_merge_kernel(const Merg
     const int tid = threadIdx.x, n = a.n, total = a.beams * n;
     const int64_t b = blockIdx.x, row0 = b * a.beams;
     if (tid < a.beams) {
-        scores[tid] = a.scores[row0 + tid];
-        done[tid] = a.finished && a.finished[row0 + tid];
+        scores[tid] = __ldcg(a.scores + row0 + tid);
+        done[tid] = a.finished && __ldcg(a.finished + row0 + tid);
     }
     __syncthreads();
     int valid = 0;

@@ -132,6 +132,34 @@ def test_scores_and_flags_in_place(cuda):
     check([t.cpu().numpy() for t in (rows, tokens, s, f)] + [None], z, scores, W, finished=finished, end_token=1)
 
 
+def test_steps_that_follow_at_once(cuda):
+    """Captured steps one behind the other over scores and flags in place, many short requests to a line of memory."""
+    import torch
+
+    rng = np.random.default_rng(9)
+    B, W, V, steps = 40, 2, 300, 6
+    xs = [L.rows(rng, B * W, V, "f32") for _ in range(steps)]
+    scores, finished = start(rng, B, W), np.zeros((B, W), dtype=np.uint8)
+    s, f = L.dev(scores), L.dev(finished)
+    rows, tokens = (torch.empty((steps, B, W), dtype=torch.int32, device=cuda) for _ in range(2))
+    ws = torch.empty(_native.beam_select_workspace_size(B, W, V, s.dtype, W), dtype=torch.uint8, device=cuda)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i, (x, _) in enumerate(xs):
+            _native.beam_select(x, s, rows[i], tokens[i], s, ws, finished=f, end_token=5, out_finished=f)
+    for _ in range(20):
+        s.copy_(L.dev(scores))
+        f.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want, done = scores, finished
+        for i, (_, z) in enumerate(xs):
+            got = [ref.beam_select(z.reshape(B, W, V)[b], want[b], W, finished=done[b], end_token=5) for b in range(B)]
+            assert rows[i].tolist() == [[b * W + w for w in g[0]] for b, g in enumerate(got)] and tokens[i].tolist() == [g[1] for g in got]
+            want, done = np.array([g[2] for g in got]).astype(np.float32), np.array([g[3] for g in got], dtype=np.uint8)
+        assert np.abs(s.cpu().numpy() - want).max() <= steps * (L.lse_error(z)[0] + 40 * L.U) and np.array_equal(f.cpu().numpy(), done)
+
+
 # ---------------------------------------------------------------- forks
 
 

@@ -334,3 +334,29 @@ def test_graph_and_stream(cuda):
         c = Case(x, ids.cpu().numpy(), lps.cpu().numpy(), 2.0)
         c.check_loss(loss, stats)
         c.check_grad(grad, "bf16")
+
+
+def test_offsets_beyond_32_bits(cuda):
+    """More than 2^31 elements: the record, the loss with its gradient in place and the backward pass of the last rows."""
+    import torch
+
+    rows, V, n = 15000, 151936, 8
+    x = torch.zeros((rows, V), dtype=torch.bfloat16, device=cuda)
+    last = slice(rows - 3, rows)
+    x[last] = L.rows(np.random.default_rng(15), 3, V, "bf16")[0]
+    z = P.host(x[last])
+    ids, lps = torch.empty((rows, n), dtype=torch.int32, device=cuda), torch.empty((rows, n), device=cuda)
+    ws = torch.empty(_native.top_logits_workspace_size(rows, V, x.dtype), dtype=torch.uint8, device=cuda)
+    _native.top_logits(x, ids, lps, ws)
+    want = [ref.top_logits(r, n)[0] for r in z]
+    assert np.array_equal(ids[last].cpu().numpy(), want) and (ids[:-3] == torch.arange(n, device=cuda)).all()
+    loss, stats = torch.empty(rows, device=cuda), torch.empty((rows, 2), device=cuda)
+    lps -= 0.5
+    c = Case(x[last].clone(), ids[last].cpu().numpy(), lps[last].cpu().numpy())
+    back = x.clone()
+    _native.distill(x, ids, lps, loss, stats=stats, grad=x)
+    _native.distill_backward(back, ids, lps, stats, None, back)
+    torch.cuda.synchronize()
+    c.check_loss(loss[last], stats[last])
+    c.check_grad(x[last], "bf16", more=40 * L.U)
+    c.check_grad(back[last], "bf16", more=40 * L.U + rounded(stats))

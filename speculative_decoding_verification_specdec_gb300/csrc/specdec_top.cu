@@ -275,7 +275,8 @@ template <typename T> __global__ void __launch_bounds__(kSelectThreads) specdec_
     const Select<T> sel(a, r);
     if (tid == 0) num_groups = num_found = 0;
 
-    // the largest maxima of 256 sets of groups (a set is every 256th vector of them)
+    // 256 numbers, each the largest of a set of the row's elements: of every 256th vector of the groups' maxima, where those are
+    // too few of every 256th group, and in rows of fewer than 2 n groups of every 256th vector of the row itself
     const T* const maxima = static_cast<const T*>(a.s.maxima) + r * a.s.units * 32;
     const int32_t vectors = a.s.units * 32 / kPer<T>;
     auto largest = [&](int32_t v) {
@@ -286,7 +287,18 @@ template <typename T> __global__ void __launch_bounds__(kSelectThreads) specdec_
 #pragma unroll
     for (int side = 0; side < kSides; ++side) {
         uint32_t top = 0;
-        for (int32_t v = tid + side * kSelectThreads; v < vectors; v += kBounds) top = max(top, largest(v));
+        const int32_t first = tid + side * kSelectThreads;
+        if (vectors >= kBounds) {
+            for (int32_t v = first; v < vectors; v += kBounds) top = max(top, largest(v));
+        } else if (sel.row.vectors / kGroupVectors >= 2 * n) {
+            for (int32_t g = first; g < vectors * kPer<T>; g += kBounds) top = max(top, order_key(to_float<T>(maxima[g])));
+        } else {
+            for (int32_t v = first; v < sel.row.vectors; v += kBounds) {
+                Raw<T, kPer<T>> x;
+                sel.load(v, x);
+                top = max(top, order_key(Maximum<T>::of(x).value()));
+            }
+        }
         bounds[tid + side * kSelectThreads] = top;
     }
     __syncthreads();
@@ -456,6 +468,7 @@ __global__ void __launch_bounds__(kThreads) specdec_beam_merge_kernel(const Merg
     __shared__ int counts[kThreads / 32];
     __shared__ float scores[SPECDEC_TOP_MAX];                        // read once: the outputs may lie over the inputs
     __shared__ uint8_t done[SPECDEC_TOP_MAX];
+    __shared__ long long least;                                      // the best of the beams' n-th: what is below it has n before it
     after_predecessor();
     const int tid = threadIdx.x, n = a.n, total = a.beams * n;
     const int64_t b = blockIdx.x, row0 = b * a.beams;
@@ -463,6 +476,7 @@ __global__ void __launch_bounds__(kThreads) specdec_beam_merge_kernel(const Merg
         scores[tid] = __ldcg(a.scores + row0 + tid);
         done[tid] = a.finished && __ldcg(a.finished + row0 + tid);
     }
+    if (tid == 0) least = kNone;
     __syncthreads();
     int valid = 0;
     uint32_t bad = 0;
@@ -484,11 +498,13 @@ __global__ void __launch_bounds__(kThreads) specdec_beam_merge_kernel(const Merg
         valid += key != kNone;
     }
     if (a.status && bad) atomicOr(a.status + b, bad);
-    valid = block_sum<kThreads>(valid, counts);                                // (its barriers also publish the keys)
+    valid = block_sum<kThreads>(valid, counts);                      // (its barriers also publish the keys)
+    if (tid < a.beams) atomicMax(&least, keys[tid * n + n - 1]);
+    __syncthreads();
     for (int i = tid; i < total; i += kThreads) {
         const int w = i / n, k = i - w * n;
         const long long key = keys[i];
-        if (key == kNone) continue;
+        if (key == kNone || key < least) continue;
         int rank = k;
         for (int o = 0; o < a.beams && rank < n; ++o) {
             if (o == w) continue;

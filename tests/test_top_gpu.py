@@ -72,6 +72,18 @@ def test_random_rows(cuda, kind, V, n):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("V", [900, 1024, 1025, 2048, 8191, 8192, 16384, 16385, 65536, 131072, 140000])
+@pytest.mark.parametrize("n", [64, 127, 128])
+def test_where_the_bounds_come_from(cuda, kind, V, n):
+    """Sizes on both sides of every way of taking the bound, with clusters of large values beside each other."""
+    rng = np.random.default_rng([V, n])
+    x, _ = L.rows(rng, 3, V, kind)
+    x[1, V // 3: V // 3 + 300] += 6.0
+    x[2, : n + 3] = 30.0
+    check(top(x, n), P.host(x), n)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("extra,shift", [(1, 0), (0, 1), (3, 5), (8, 8)])
 @pytest.mark.parametrize("temperature", [0.3, 4.0])
 def test_strides_and_alignments(cuda, kind, extra, shift, temperature):

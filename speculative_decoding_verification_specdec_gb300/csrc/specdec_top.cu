@@ -22,7 +22,7 @@ using namespace specdec;
 constexpr int kThreads = 256;                      // of the stream and the merge
 constexpr int kUnitVectors = 256;                  // a warp's: 8 a lane
 constexpr int kLaneVectors = kUnitVectors / 32, kGroupVectors = kUnitVectors / 32;
-constexpr int kSelectThreads = 128;
+constexpr int kSelectThreads = 256;
 constexpr int kBounds = 256;                       // the numbers of which the n-th largest bounds the n-th best element
 constexpr int kMaxGroups = 1024, kMaxFound = 1024;
 constexpr int kMaxMerge = 4096;                    // candidates of one request
@@ -258,7 +258,7 @@ __device__ __forceinline__ unsigned long long composite(uint32_t key, int32_t at
     return (unsigned long long)key << 32 | (uint32_t)~at;
 }
 
-template <typename T> __global__ void __launch_bounds__(kSelectThreads) specdec_rows_select_kernel(const SelectArgs a)
+template <typename T> __global__ void __launch_bounds__(kSelectThreads, 8) specdec_rows_select_kernel(const SelectArgs a)
 {
     constexpr int kWarps = kSelectThreads / 32, kMine = kMaxFound / kSelectThreads, kSides = kBounds / kSelectThreads;
     __shared__ unsigned long long found[kMaxFound];

@@ -194,6 +194,9 @@ struct SelectArgs {
     double* sums;                                  // beams: ln of the sum of exp, [rows]
 };
 
+// The value of a bound on keys: of what lies below every key, the lowest number (-infinity and NaN are never at or above it).
+__device__ __forceinline__ float bound_value(uint32_t key) { return key <= 0x00800000u ? -3.402823466e38f : key_value(key); }
+
 // The largest t, a multiple of 2^low, with at least n of some numbers (count(t) of them) at or above it.
 template <typename Count> __device__ __forceinline__ uint32_t nth_largest(int n, int low, Count count)
 {
@@ -234,7 +237,20 @@ template <typename T> struct Select {
         load_vector(row, v, x);
         if (words) apply_bits<T>(x, vector_bits(row, words, v));
     }
-    // Calls f(key, element) for every element of vector v that can be chosen.
+    // Calls f(key, element) for every element of vector v that is at least `bound`.
+    template <typename F> __device__ __forceinline__ void each_from(float bound, int32_t v, F f) const
+    {
+        Raw<T, kPer<T>> x;
+        load(v, x);
+        if (!(Maximum<T>::of(x).value() >= bound)) return;
+        const int32_t at = row.first(v);
+#pragma unroll
+        for (int e = 0; e < kPer<T>; ++e) {
+            const float z = to_float<T>(x.e[e]);
+            if (z >= bound) f(order_key(z), at + e);
+        }
+    }
+    // Calls f(key, element) for every element of vector v (key 0: it cannot be chosen).
     template <typename F> __device__ __forceinline__ void each(int32_t v, F f) const
     {
         Raw<T, kPer<T>> x;
@@ -329,13 +345,14 @@ template <typename T> __global__ void __launch_bounds__(kSelectThreads, 8) specd
     }
     __syncthreads();
     const uint32_t least = bound;
+    const float least_value = bound_value(least);
     for (int32_t v = tid; v < vectors; v += kSelectThreads) {
         Raw<T, kPer<T>> x;
         x.load(maxima + v * kPer<T>);
-        if (order_key(Maximum<T>::of(x).value()) < least) continue;
+        if (!(Maximum<T>::of(x).value() >= least_value)) continue;
 #pragma unroll
         for (int e = 0; e < kPer<T>; ++e)
-            if (order_key(to_float<T>(x.e[e])) >= least) {
+            if (to_float<T>(x.e[e]) >= least_value) {
                 const int at = atomicAdd(&num_groups, 1);
                 if (at < kMaxGroups) groups[at] = v * kPer<T> + e;
             }
@@ -344,11 +361,9 @@ template <typename T> __global__ void __launch_bounds__(kSelectThreads, 8) specd
     const int want = num_groups;
     if (want <= kMaxGroups) {
         for (int i = tid; i < want * kGroupVectors; i += kSelectThreads)
-            sel.each(groups[i / kGroupVectors] * kGroupVectors + i % kGroupVectors, [&](uint32_t key, int32_t at) {
-                if (key >= least) {
-                    const int to = atomicAdd(&num_found, 1);
-                    if (to < kMaxFound) found[to] = composite(key, at);
-                }
+            sel.each_from(least_value, groups[i / kGroupVectors] * kGroupVectors + i % kGroupVectors, [&](uint32_t key, int32_t at) {
+                const int to = atomicAdd(&num_found, 1);
+                if (to < kMaxFound) found[to] = composite(key, at);
             });
     }
     __syncthreads();

@@ -588,8 +588,8 @@ specdec_status_t specdec_top_logits(const void* logits, specdec_dtype_t dtype, i
  * Where the drafter leaves nothing to the other ids (none is there, or all are -infinity), r does not count (it is taken as 0).
  * A row without a finite logit: loss +infinity, gradient zeros. A row whose list asks for nothing (rest = 0 and no entry): zeros. NaN or
  * +infinity in a row makes its loss and gradient NaN.
- * status, [rows] here: BAD_TARGET (an id outside [-1, V), one listed before, a log-probability that is NaN or +infinity: that entry does not
- * count); EMPTY_MASK_ROW (no finite logit).
+ * status, [rows] here: BAD_TARGET (an id outside [-1, V), one listed before, a log-probability that is NaN, +infinity or, with rest = 1, above
+ * 0.5: that entry does not count); EMPTY_MASK_ROW (no finite logit).
  * Sums over the row are held in fp32 by a warp, and in pairs of fp32 numbers (some 46 bits) across them, as are targets, listed
  * exponentials and the loss; an element of the gradient is one fp32 exponential times one factor, rounded once to its type. Equal
  * calls give equal bits.

@@ -35,13 +35,14 @@ def top_logits(z, n, temperature=1.0, mask=None):
     return ids, logprobs, lse
 
 
-def entries(ids, logprobs, V):
-    """The entries of a list that count: (ids, log-probabilities, whether any is at fault)."""
+def entries(ids, logprobs, V, rest=True):
+    """The entries of a list that count: (ids, log-probabilities, whether any is at fault). Where the list is not renormalised, a
+    log-probability above 0.5 is none."""
     got, lps, fault = [], [], False
     for j, (i, lp) in enumerate(zip(ids, logprobs)):
         if i == -1:
             continue
-        if not 0 <= i < V or i in list(ids[:j]) or not lp < np.inf:
+        if not 0 <= i < V or i in list(ids[:j]) or not lp < np.inf or (rest and lp > 0.5):
             fault = True
             continue
         got.append(int(i))
@@ -55,7 +56,7 @@ def distill(z, ids, logprobs, temperature=1.0, rest=True, weight=1.0):
     V = z.shape[0]
     if weight == 0:
         return 0.0, (0.0, 0.0), np.zeros(V), 0.0
-    ids, lps, _ = entries(ids, logprobs, V)
+    ids, lps, _ = entries(ids, logprobs, V, rest)
     outside = np.ones(V, dtype=bool)
     outside[ids] = False
     every, others = log_sum(z), log_sum(z[outside])

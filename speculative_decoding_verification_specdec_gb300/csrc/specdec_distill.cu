@@ -13,6 +13,9 @@
  * e_j (M / S - r / S_rest).
  *
  * A row is held by a cluster of CTAs, a part each, in shared memory: it is read from HBM once, for the sums and for the gradient.
+ * Measured on one GB300: 2048 rows of 151936 bf16 logits against 64 ids, loss and gradient, 270 us, 68 % of what reading and
+ * writing them once takes at the copy rate (a forward and a backward pass of their own: 157 + 185). Its bound is a row's chain of
+ * barriers, which the other CTAs of an SM fill. The backward kernel goes element by element: 700 rows of 128256 fp32 logits in 107.5 us, 98 %.
  */
 #include <atomic>
 #include <cmath>
@@ -77,6 +80,7 @@ __device__ __forceinline__ float warp_max(float x)
 }
 
 constexpr int kEntries = SPECDEC_TOP_MAX / 32;     // of a lane of the warp that holds the list
+constexpr float kMostLogProbability = 0.5f;        // where the list is not renormalised: rounding may bring one above 0, not so far
 
 // The list as one warp holds it: entry lane + 32 c in a lane's c-th place.
 struct List {
@@ -123,7 +127,8 @@ __device__ __forceinline__ int own_entries(const Args& a, const List& list, int3
     for (int j0 = (found - 1) / 32 * 32; found > 0 && j0 >= 0; j0 -= 32) {
         const int j = j0 + lane;
         const Own o = own[j < found ? j : 0];
-        bool counts = (__match_any_sync(0xffffffffu, j < found ? o.id : -2 - lane) & below) == 0 && o.lp < INFINITY;
+        bool counts = (__match_any_sync(0xffffffffu, j < found ? o.id : -2 - lane) & below) == 0 &&
+                      o.lp <= (a.rest ? kMostLogProbability : 3.402823466e38f);
         for (int k = 0; k < j0; ++k) counts &= own[k].id != o.id;
         if (j < found && !counts) {
             own[j].top = 1.f;                      // marked
@@ -150,8 +155,8 @@ __device__ __forceinline__ Two target_of(float lp, float shift)
 {
     return lp - shift < -90.f ? Two{0.f, 0.f} : exp2_two(two_sum(lp, -shift) * SPECDEC_TWO(kLog2e));
 }
-// Targets add up as whole numbers of 2^-56, so that what they leave of one is exact.
-constexpr float kFixed = 0x1p56f;
+// Targets add up as whole numbers of 2^-54, so that what they leave of one is exact (128 of exp(0.5) stay below 2^63 of them).
+constexpr float kFixed = 0x1p54f;
 __device__ __forceinline__ long long fixed_of(Two x) { return __float2ll_rn(x.hi * kFixed) + __float2ll_rn(x.lo * kFixed); }
 __device__ __forceinline__ float from_fixed(long long x) { return __ll2float_rn(x) * (1.f / kFixed); }
 
@@ -194,9 +199,10 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // vectors, and fetch the next row's into their places as they finish with them. One warp holds the list: it takes the listed
 // elements out of the row, sums their part and exchanges the CTAs' sums. Another works the loss out while the others go on. What
 // a CTA knows of a row meets the others' by distributed shared memory and one cluster barrier a row.
+
 // What one CTA of a cluster knows of a row.
 struct Part {
-    long long fixed;                               // the sum of the targets in 2^-56 (rest = 1)
+    long long fixed;                               // the sum of the targets in 2^-54 (rest = 1)
     Two rest, top, targets, cross;                 // sums of exponentials outside and on the list; of the targets (rest = 0); of t (ln t - z / temperature)
     float rest_ref, top_ref, shift;
     int32_t endless;                               // whether a target lies where the student has -infinity

@@ -12,6 +12,13 @@
  *            the groups that reach it (about n) are read again.
  *   merge    a CTA a request: the beams' lists hold everything that can survive; a candidate's rank is its place in its
  *            own list plus, by bisection, how many entries of each other list come before it.
+ *
+ * The stream is bound by HBM: 2048 rows of 128256 bf16 logits in 78.8 us, 98 % of the measured copy rate (eight 16-byte loads a
+ * thread in flight, no shared memory; 3 % of the bytes go into the groups' maxima and their second reading). The selection takes 20 us more of
+ * that call's 97.6, bound by instructions (issue 70 %). 128 threads a row: 102; its 64-bit sums: 106; groups of a lane's own
+ * eight vectors, which are 512 bytes apart: 117, for 64 of them are 32 KB of DRAM bursts a row where 128 contiguous bytes are 8.
+ * Under a bitmask only vectors with an allowed id are loaded: 768 rows of 151936 fp32 logits with 5 % allowed in 48.8 us (157 MB of 467 read),
+ * 105 when every vector was gone through. A beam step over 1024 rows of 128256 fp32 logits: 87.9 us, 88 % of the copy rate.
  */
 #include "specdec_logits.cuh"
 

@@ -87,7 +87,7 @@ class Case:
             rel = 2 * L.loss_error(self.z[r], tau, 1.0) / 3 + 4 * L.U + more
             with np.errstate(invalid="ignore", over="ignore"):
                 s = np.exp(self.z[r] / tau - every) if np.isfinite(every) else np.zeros(self.V)
-            ids, lps, _ = ref.entries(self.ids[r], self.lps[r], self.V)
+            ids, lps, _ = ref.entries(self.ids[r], self.lps[r], self.V, self.rest)
             size = s * (2 + ratio)
             size[ids] += np.exp(lps) if self.rest or not lps.size else np.exp(lps - ref.log_sum(lps))
             err = rel * size * w / tau
@@ -261,14 +261,40 @@ def test_small_targets_keep_their_shares(cuda):
     assert np.all(np.abs(P.host(grad) - np.array(want)) <= 2.0 ** -14)
 
 
+@pytest.mark.parametrize("V", [400, 60001])
+@pytest.mark.parametrize("rest", [False, True])
+def test_long_lists_with_repeated_ids(cuda, V, rest):
+    """Full lists of which many entries repeat, within 32 of each other and further apart, in one part of the row and in several."""
+    import torch
+
+    rng = np.random.default_rng(V)
+    x, _ = L.rows(rng, 4, V, "f32")
+    ids = rng.integers(0, V, (4, 128)).astype(np.int32)
+    ids[0] = rng.integers(0, 90, 128)
+    ids[1, 64:] = ids[1, :64]
+    ids[2, 1::2] = ids[2, ::2]
+    lps = (-5 - rng.uniform(0, 2, (4, 128))).astype(np.float32)
+    lps[3, ::5] = np.nan
+    c = Case(x, ids, lps, 1.0, rest)
+    grad, back = torch.full_like(x, 7.0), torch.full_like(x, 7.0)
+    loss, stats, status = c.forward(grad=grad)
+    _native.distill_backward(x, c.dids, c.dlps, stats, None, back, rest=rest)
+    c.check_loss(loss, stats)
+    c.check_grad(grad, "f32")
+    c.check_grad(back, "f32", more=rounded(stats))
+    assert (status == _native.ST_BAD_TARGET).all()
+
+
 def test_entries_that_do_not_count(cuda):
     """Padding, repeated ids, ids outside the vocabulary, log-probabilities that are none, an empty list."""
     import torch
 
-    x, _ = L.rows(np.random.default_rng(9), 6, 50, "f32")
-    ids = np.array([[3, -1, 7, -1], [3, 3, 7, 3], [50, 3, -2, 7], [3, 7, 9, 11], [-1, -1, -1, -1], [3, 7, 9, 2 ** 31 - 1]], dtype=np.int32)
-    lps = np.full((6, 4), -1.5, dtype=np.float32)
+    x, _ = L.rows(np.random.default_rng(9), 7, 50, "f32")
+    ids = np.array([[3, -1, 7, -1], [3, 3, 7, 3], [50, 3, -2, 7], [3, 7, 9, 11], [-1, -1, -1, -1], [3, 7, 9, 2 ** 31 - 1], [3, 7, 9, 11]],
+                   dtype=np.int32)
+    lps = np.full((7, 4), -1.5, dtype=np.float32)
     lps[0, 1] = np.nan
+    lps[6] = [0.25, 3.0, -4.0, 80.0]              # (no log-probabilities but the first and third, unless they are renormalised)
     lps[3] = [-1.0, np.nan, np.inf, -np.inf]
     for rest in (False, True):
         c = Case(x, ids, lps, 1.0, rest)
@@ -277,11 +303,11 @@ def test_entries_that_do_not_count(cuda):
         c.check_loss(loss, stats)
         c.check_grad(grad, "f32")
         bad = _native.ST_BAD_TARGET
-        assert list(status) == [0, bad, bad, bad, 0, bad]
-        status = torch.zeros(6, dtype=torch.int32, device=cuda)
+        assert list(status) == [0, bad, bad, bad, 0, bad, bad if rest else 0]
+        status = torch.zeros(7, dtype=torch.int32, device=cuda)
         _native.distill_backward(x, c.dids, c.dlps, stats, None, grad, rest=rest, status=status)
         c.check_grad(grad, "f32", more=16 * L.U)
-        assert list(status.cpu().numpy()) == [0, bad, bad, bad, 0, bad]
+        assert list(status.cpu().numpy()) == [0, bad, bad, bad, 0, bad, bad if rest else 0]
 
 
 def test_rows_without_a_number_and_infinities(cuda):

@@ -497,14 +497,17 @@ template <typename T, bool kGrad> __global__ void __launch_bounds__((kRowWarps +
                 else part.targets = warp_sum(part.targets);
             }
             if (!kGrad && r != first) cluster_wait();                 // (the phase before)
+            if (lane == 0) s.part = part;
             meet();                                                   // D
             {
                 const bool holds = lane < threads / 32;
-                const float one = holds ? s.refs[lane] : -INFINITY;
-                part.rest_ref = half_max(one);                        // (both of the lower half's lanes)
-                part.rest = half_sum(Two{holds ? s.sums[lane] * reference_step(one, part.rest_ref) : 0.f, 0.f});
+                const float one = holds ? s.refs[lane] : -INFINITY, rest_ref = half_max(one);      // (of the lower half)
+                const Two rest = half_sum(Two{holds ? s.sums[lane] * reference_step(one, rest_ref) : 0.f, 0.f});
+                if (lane == 0) {
+                    s.part.rest_ref = rest_ref;
+                    s.part.rest = rest;
+                }
             }
-            if (lane == 0) s.part = part;
             __syncwarp();
             // to every CTA, eight bytes a lane at a time
             for (int i = lane; i < kPartWords * (int)size; i += 32)

@@ -362,6 +362,40 @@ def test_graph_and_stream(cuda):
         c.check_grad(grad, "bf16")
 
 
+def test_calls_at_the_same_time(cuda):
+    """Records and losses of different rows on two streams at once, each with its own workspace, equal the same calls alone."""
+    import torch
+
+    streams, work = [torch.cuda.Stream() for _ in range(2)], []
+    for i, (rows, V, kind) in enumerate(((300, 70001, "bf16"), (700, 9000, "f32"))):
+        x, _ = L.rows(np.random.default_rng(20 + i), rows, V, kind)
+        ids, lps = torch.empty((rows, 32), dtype=torch.int32, device=cuda), torch.empty((rows, 32), device=cuda)
+        ws = torch.empty(_native.top_logits_workspace_size(rows, V, x.dtype), dtype=torch.uint8, device=cuda)
+        work.append((x, ids, lps, ws, torch.empty(rows, device=cuda), torch.empty_like(x)))
+
+    def call(w, stream=None):
+        x, ids, lps, ws, loss, grad = w
+        _native.top_logits(x, ids, lps, ws, temperature=2.0, stream=stream)
+        _native.distill(x, ids, lps, loss, temperature=1.5, grad=grad, stream=stream)
+
+    alone = []
+    for w in work:
+        call(w)
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in (w[1], w[2], w[4], w[5])])
+    for _ in range(5):
+        for w in work:
+            for t in (w[1], w[2], w[4], w[5]):
+                t.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for w, s in zip(work, streams):
+                call(w, s)
+        torch.cuda.synchronize()
+        for w, a in zip(work, alone):
+            assert all(torch.equal(t, u) for t, u in zip((w[1], w[2], w[4], w[5]), a))
+
+
 def test_offsets_beyond_32_bits(cuda):
     """More than 2^31 elements: the record, the loss with its gradient in place and the backward pass of the last rows."""
     import torch
